@@ -452,6 +452,127 @@ int32_t mlora_grouped_down_all_noalloc(const mlora_expert_route* route, const vo
                                        const int32_t* sorted_ids, const int32_t* row_adapter,
                                        int32_t top_k, int64_t cap, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The MoE layer around the fold: the router's choice, the sort of its rows  */
+/* by expert, their dispatch and weighted combine, and 4-bit base products.  */
+/* ------------------------------------------------------------------------ */
+/*
+ * What these make is what the folds read: `indices` of the gather fold,
+ * `expert_offsets` and `sorted_ids` of the grouped fold, and base_out. All
+ * enqueue on `stream`, read routing on the device and are capturable in a HIP
+ * graph. dtype is MLORA_BF16 or MLORA_F32 for logits, rows and outputs;
+ * weights and their gradients are fp32; sums are fp32. A row stride (_ld) is
+ * in elements and >= the row's width. Any width works; rows that start on 16
+ * bytes and hold a multiple of 16 bytes move in 16-byte accesses. Results do
+ * not depend on timing: no floating-point atomics. Outputs must not overlap
+ * inputs. Errors: MLORA_ERR_INVALID, MLORA_ERR_CAPACITY (a buffer too small)
+ * and MLORA_ERR_HIP, with nothing enqueued on the first two.
+ * Limits: 1024 experts, top_k 64, 2^30 - 1 (token, slot) rows.
+ */
+
+/* The top_k experts of each token and their weights: indices[t, j] is the
+ * expert of token t's j-th largest logit (ties: the lowest index; a NaN is
+ * above every number), weights[t, j] its softmax probability over all experts,
+ * divided by the sum of the chosen ones if `renormalize`. Masked experts hold
+ * -inf: they are chosen last, with weight 0; a row with nothing but -inf gets
+ * experts 0 .. top_k - 1 with weights of 0.
+ * logits [n_tokens, n_experts] dtype; indices, weights [n_tokens, top_k]. */
+int32_t mlora_router_topk(const void* logits, int64_t logits_ld, int32_t dtype,
+                          int64_t n_tokens, int32_t n_experts, int32_t top_k,
+                          int32_t renormalize, int32_t* indices, float* weights, void* stream);
+
+/* Gradient of the weights with respect to the logits, from the forward's
+ * indices (distinct per token; others are out of the sum): d_logits
+ * [n_tokens, n_experts] is written whole. Rows with nothing but -inf get 0. */
+int32_t mlora_router_topk_backward(const void* logits, int64_t logits_ld, int32_t dtype,
+                                   int64_t n_tokens, int32_t n_experts, int32_t top_k,
+                                   int32_t renormalize, const int32_t* indices,
+                                   const float* d_weights, void* d_logits, int64_t d_logits_ld,
+                                   void* stream);
+
+/* Bytes of workspace mlora_moe_sort needs: 0 for small calls (and for
+ * arguments it refuses). */
+uint64_t mlora_moe_sort_workspace_bytes(int64_t n_slots, int32_t n_experts);
+
+/* Stable sort of the flat (token, slot) rows by expert. ids[i] outside
+ * [0, n_experts) marks a dropped slot (a skipped sequence, a full expert).
+ * Writes expert_offsets [n_experts + 1] (expert e holds sorted rows
+ * expert_offsets[e] .. [e + 1]; the last is the number of live rows L),
+ * sorted_ids [n_slots] (the flat id of each sorted row; -1 from L on) and
+ * slot_rows [n_slots] (the sorted row of each flat id; -1 where dropped).
+ * The workspace's contents need no initialisation and are dead afterwards. */
+int32_t mlora_moe_sort(const int32_t* ids, int64_t n_slots, int32_t n_experts,
+                       int32_t* expert_offsets, int32_t* sorted_ids, int32_t* slot_rows,
+                       void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Token rows to sorted rows: rows[r] = x[sorted_ids[r] / top_k], zeros where
+ * sorted_ids[r] < 0. x [n_tokens, dim], rows [n_tokens * top_k, dim]; the two
+ * maps are mlora_moe_sort's. Its gradient is mlora_moe_combine of the rows'
+ * gradient with weights == NULL. */
+int32_t mlora_moe_dispatch(const void* x, int64_t x_ld, int32_t dtype, int64_t n_tokens,
+                           int64_t dim, int32_t top_k, const int32_t* sorted_ids,
+                           const int32_t* slot_rows, void* rows, int64_t rows_ld, void* stream);
+
+/* out[t] = sum over j of weights[t, j] * rows[slot_rows[t * top_k + j]], in
+ * slot order, rounded once. A negative (or too large) slot row is left out and
+ * its weight not used; a token without rows gets zeros. slot_rows == NULL:
+ * rows are in flat (token, slot) order. weights == NULL: all 1. */
+int32_t mlora_moe_combine(const void* rows, int64_t rows_ld, int64_t n_rows, int32_t dtype,
+                          int64_t n_tokens, int64_t dim, int32_t top_k, const float* weights,
+                          const int32_t* slot_rows, void* out, int64_t out_ld, void* stream);
+
+/* Gradient of mlora_moe_combine: d_rows[slot_rows[t, j]] = weights[t, j] *
+ * d_out[t], rounded once; d_weights[t, j] = <d_out[t], rows[slot_rows[t, j]]>,
+ * 0 for a slot left out. rows, d_rows [n_tokens * top_k, dim]; rows of d_rows
+ * that no slot names are zeros (sorted_ids < 0 marks them; slot_rows and
+ * sorted_ids are given together or both NULL). d_weights == NULL: not
+ * computed, rows not read. weights == NULL: all 1. */
+int32_t mlora_moe_combine_backward(const void* d_out, int64_t d_out_ld, const void* rows,
+                                   int64_t rows_ld, int32_t dtype, int64_t n_tokens, int64_t dim,
+                                   int32_t top_k, const float* weights, const int32_t* slot_rows,
+                                   const int32_t* sorted_ids, void* d_rows, int64_t d_rows_ld,
+                                   float* d_weights, void* stream);
+
+/* Device pointers of 4-bit expert weights as mlora_w4_pack lays them out (the
+ * struct itself lives in host memory). */
+typedef struct mlora_w4_route {
+  const void* weights;
+  const void* scales;
+  const void* zeros;   /* NULL: zero point 8 */
+  int32_t n_experts;
+  int32_t k_in;        /* multiple of 8                              */
+  int32_t n_out;
+  int32_t group;       /* 32, 64 or a multiple of 128                */
+  int32_t dtype;       /* of scales, x and out                       */
+} mlora_w4_route;
+
+/* Bytes of the packed form; 0 for arguments mlora_w4_pack refuses. */
+uint64_t mlora_w4_packed_bytes(int32_t n_experts, int32_t k_in, int32_t n_out, int32_t group,
+                               int32_t dtype, int32_t has_zeros);
+
+/* Lays 4-bit weights out for mlora_w4_gather_gemv, once per weight.
+ *   q       [n_experts, n_out, k_in / 2] bytes, k even in the low half
+ *   scales  [n_experts, n_out, ceil(k_in / group)] dtype
+ *   zeros   the same shape, bytes 0 .. 15 (the low half counts), or NULL
+ *   packed  mlora_w4_packed_bytes bytes, 256-byte aligned, kept while the
+ *           route is used; q, scales and zeros are not needed afterwards
+ * Fills *route. */
+int32_t mlora_w4_pack(const uint8_t* q, const void* scales, const uint8_t* zeros,
+                      int32_t n_experts, int32_t k_in, int32_t n_out, int32_t group,
+                      int32_t dtype, void* packed, uint64_t packed_bytes, mlora_w4_route* route,
+                      void* stream);
+
+/* out[r] = W_e x[row], W_e[n, k] = (q - zero) * scale, e = ids[r]; rows whose
+ * id is outside [0, n_experts) get zeros. ids == NULL: one weight
+ * (n_experts == 1) for every row. x_by_row as in mlora_projection: row r reads
+ * x[r / top_k] or x[r]. x rows start on 16 bytes (x_ld a multiple of 8) and
+ * span at most 4 GiB. Weights enter exactly, sums are fp32, one rounding. A
+ * row of x that is not finite, or above 2^122 in magnitude, gives its own
+ * output row no defined finite values; other rows do not change. */
+int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void* x, int64_t x_rows,
+                             int64_t x_ld, int32_t x_by_row, void* out, int64_t out_ld,
+                             const int32_t* ids, int64_t n_rows, int32_t top_k, void* stream);
+
 /* Reads the MLORA_* launch-shape overrides from the environment again (they
  * are otherwise read once, at the first fold call). For measurement tools and
  * tests that change the environment within one process. Not safe while

@@ -1,9 +1,10 @@
 """Python binding of libmlora.so: the MoE expert-LoRA fold for MI355X (gfx950).
 
 Argument marshalling only. Every function has the name of the C entry point it
-calls (include/mlora.h); host functions take and return NumPy arrays, the two
-device folds take PyTorch tensors (used only for device memory and the current
-stream) and enqueue the library's HIP kernels. There is no fallback path: when
+calls (include/mlora.h); host functions take and return NumPy arrays, the
+device calls (the folds, and the MoE layer's operators around them) take
+PyTorch tensors (used only for device memory and the current stream) and
+enqueue the library's HIP kernels. There is no fallback path: when
 libmlora.so is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
@@ -57,6 +58,16 @@ EXPORTS = (
     "mlora_build_moe_row_adapter_decode_multi",
     "mlora_pack_expert_tables_multi",
     "mlora_gather_bgmv_multi",
+    "mlora_router_topk",
+    "mlora_router_topk_backward",
+    "mlora_moe_sort_workspace_bytes",
+    "mlora_moe_sort",
+    "mlora_moe_dispatch",
+    "mlora_moe_combine",
+    "mlora_moe_combine_backward",
+    "mlora_w4_packed_bytes",
+    "mlora_w4_pack",
+    "mlora_w4_gather_gemv",
 )
 
 
@@ -118,6 +129,21 @@ class Projection(ctypes.Structure):
     ]
 
 
+class W4Route(ctypes.Structure):
+    """``mlora_w4_route``: packed 4-bit expert weights of one projection."""
+
+    _fields_ = [
+        ("weights", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+        ("n_experts", ctypes.c_int32),
+        ("k_in", ctypes.c_int32),
+        ("n_out", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
@@ -176,6 +202,20 @@ def load() -> ctypes.CDLL:
         "mlora_apply_expert_lora_sorted": (i32, [ctypes.POINTER(ExpertRoute), vp, i64, vp, i64,
                                                  vp, _i32p, i32, _u64p, _u64p, vp, vp, i32, vp,
                                                  ctypes.c_uint64, vp]),
+        "mlora_router_topk": (i32, [vp, i64, i32, i64, i32, i32, i32, vp, vp, vp]),
+        "mlora_router_topk_backward": (i32, [vp, i64, i32, i64, i32, i32, i32, vp, vp, vp, i64,
+                                             vp]),
+        "mlora_moe_sort_workspace_bytes": (ctypes.c_uint64, [i64, i32]),
+        "mlora_moe_sort": (i32, [vp, i64, i32, vp, vp, vp, vp, ctypes.c_uint64, vp]),
+        "mlora_moe_dispatch": (i32, [vp, i64, i32, i64, i64, i32, vp, vp, vp, i64, vp]),
+        "mlora_moe_combine": (i32, [vp, i64, i64, i32, i64, i64, i32, vp, vp, vp, i64, vp]),
+        "mlora_moe_combine_backward": (i32, [vp, i64, vp, i64, i32, i64, i64, i32, vp, vp, vp, vp,
+                                             i64, vp, vp]),
+        "mlora_w4_packed_bytes": (ctypes.c_uint64, [i32, i32, i32, i32, i32, i32]),
+        "mlora_w4_pack": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp, ctypes.c_uint64,
+                                ctypes.POINTER(W4Route), vp]),
+        "mlora_w4_gather_gemv": (i32, [ctypes.POINTER(W4Route), vp, i64, i64, i32, vp, i64, vp,
+                                       i64, i32, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -674,3 +714,208 @@ def mlora_gather_bgmv_multi(route: MultiRoute, x, base_out, indices, row_adapter
     if rc != MLORA_OK:
         raise _err(rc)
 
+
+
+# ---------------------------------------------------------------------------
+# the MoE layer around the fold
+# ---------------------------------------------------------------------------
+
+def _f32(t, name):
+    import torch
+    return _dev(t, name, torch.float32)
+
+
+def _i32(t, name):
+    import torch
+    return _dev(t, name, torch.int32)
+
+
+def mlora_router_topk(logits, indices, weights, renormalize: bool = False, stream=None) -> None:
+    """Top-k experts of each row of ``logits`` [n_tokens, n_experts] (bf16 or
+    float32, contiguous rows) into ``indices`` (int32) and ``weights``
+    (float32), both [n_tokens, top_k]."""
+    p, n, ld = _rows_2d(logits, "logits")
+    if indices.dim() != 2 or indices.shape[0] != n or indices.shape != weights.shape:
+        raise ValueError("indices and weights must be [n_tokens, top_k]")
+    rc = load().mlora_router_topk(p, ld, _dtype_code(logits), n, logits.shape[1],
+                                  indices.shape[1], int(bool(renormalize)),
+                                  _i32(indices, "indices"), _f32(weights, "weights"),
+                                  _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)
+
+
+def mlora_router_topk_backward(logits, indices, d_weights, d_logits, renormalize: bool = False,
+                               stream=None) -> None:
+    """Gradient of mlora_router_topk's weights into ``d_logits`` (written whole),
+    from the forward's logits and indices."""
+    p, n, ld = _rows_2d(logits, "logits")
+    dp, dn, dld = _rows_2d(d_logits, "d_logits")
+    if d_logits.dtype != logits.dtype:
+        raise TypeError("d_logits dtype differs from logits'")
+    if dn != n or d_logits.shape[1] != logits.shape[1]:
+        raise ValueError("d_logits must have the shape of logits")
+    if indices.dim() != 2 or indices.shape[0] != n or indices.shape != d_weights.shape:
+        raise ValueError("indices and d_weights must be [n_tokens, top_k]")
+    rc = load().mlora_router_topk_backward(p, ld, _dtype_code(logits), n, logits.shape[1],
+                                           indices.shape[1], int(bool(renormalize)),
+                                           _i32(indices, "indices"),
+                                           _f32(d_weights, "d_weights"), dp, dld,
+                                           _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)
+
+
+def mlora_moe_sort_workspace_bytes(n_slots: int, n_experts: int) -> int:
+    """Workspace bytes of mlora_moe_sort (0 for small calls)."""
+    return int(load().mlora_moe_sort_workspace_bytes(int(n_slots), int(n_experts)))
+
+
+def mlora_moe_sort(ids, n_experts: int, expert_offsets, sorted_ids, slot_rows, workspace=None,
+                   stream=None) -> None:
+    """Stable sort of the flat (token, slot) ids by expert: fills
+    ``expert_offsets`` [n_experts + 1], ``sorted_ids`` and ``slot_rows``
+    (all int32); ids outside [0, n_experts) are dropped (-1)."""
+    n = ids.numel()
+    if expert_offsets.numel() != n_experts + 1:
+        raise ValueError("expert_offsets must have n_experts + 1 entries")
+    if sorted_ids.numel() != n or slot_rows.numel() != n:
+        raise ValueError("sorted_ids and slot_rows must have one entry per id")
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None and workspace.numel():
+        ws_ptr = _dev(workspace, "workspace")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    rc = load().mlora_moe_sort(_i32(ids, "ids"), n, int(n_experts),
+                               _i32(expert_offsets, "expert_offsets"),
+                               _i32(sorted_ids, "sorted_ids"), _i32(slot_rows, "slot_rows"),
+                               ws_ptr, ws_bytes, _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)
+
+
+def mlora_moe_dispatch(x, rows, sorted_ids, slot_rows, top_k: int, stream=None) -> None:
+    """Copies token rows of ``x`` [n_tokens, dim] to their sorted ``rows``
+    [n_tokens * top_k, dim]; rows no slot names get zeros. The maps are
+    mlora_moe_sort's. Its gradient: mlora_moe_combine with no weights."""
+    xp, n, x_ld = _rows_2d(x, "x")
+    rp, n_rows, r_ld = _rows_2d(rows, "rows")
+    if rows.dtype != x.dtype:
+        raise TypeError("rows dtype differs from x's")
+    if rows.shape[1] != x.shape[1] or n_rows != n * top_k:
+        raise ValueError("rows must be [n_tokens * top_k, dim]")
+    if sorted_ids.numel() != n_rows or slot_rows.numel() != n_rows:
+        raise ValueError("sorted_ids and slot_rows must have one entry per row")
+    rc = load().mlora_moe_dispatch(xp, x_ld, _dtype_code(x), n, x.shape[1], int(top_k),
+                                   _i32(sorted_ids, "sorted_ids"), _i32(slot_rows, "slot_rows"),
+                                   rp, r_ld, _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)
+
+
+def mlora_moe_combine(rows, out, top_k: int, weights=None, slot_rows=None, stream=None) -> None:
+    """``out[t]`` = sum over slots of weights[t, j] * rows[slot_rows[t * top_k + j]]
+    (``slot_rows`` None: rows in flat (token, slot) order; ``weights`` None: 1)."""
+    rp, n_rows, r_ld = _rows_2d(rows, "rows")
+    op, n, o_ld = _rows_2d(out, "out")
+    if rows.dtype != out.dtype:
+        raise TypeError("out dtype differs from rows'")
+    if rows.shape[1] != out.shape[1]:
+        raise ValueError("rows and out differ in width")
+    if (weights is not None and weights.numel() != n * top_k) or (
+            slot_rows is not None and slot_rows.numel() != n * top_k):
+        raise ValueError("weights and slot_rows must have n_tokens * top_k entries")
+    rc = load().mlora_moe_combine(rp, r_ld, n_rows, _dtype_code(rows), n, rows.shape[1],
+                                  int(top_k),
+                                  None if weights is None else _f32(weights, "weights"),
+                                  None if slot_rows is None else _i32(slot_rows, "slot_rows"),
+                                  op, o_ld, _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)
+
+
+def mlora_moe_combine_backward(d_out, rows, weights, d_rows, d_weights, top_k: int,
+                               slot_rows=None, sorted_ids=None, stream=None) -> None:
+    """Gradient of mlora_moe_combine into ``d_rows`` [n_tokens * top_k, dim] and
+    ``d_weights`` [n_tokens, top_k] (None: not computed, ``rows`` not read)."""
+    dp, n, d_ld = _rows_2d(d_out, "d_out")
+    op, n_rows, o_ld = _rows_2d(d_rows, "d_rows")
+    if d_rows.dtype != d_out.dtype:
+        raise TypeError("d_rows dtype differs from d_out's")
+    if d_rows.shape[1] != d_out.shape[1] or n_rows != n * top_k:
+        raise ValueError("d_rows must be [n_tokens * top_k, dim]")
+    rp, r_ld = None, 0
+    if d_weights is not None:
+        rp, r_rows, r_ld = _rows_2d(rows, "rows")
+        if rows.dtype != d_out.dtype:
+            raise TypeError("rows dtype differs from d_out's")
+        if rows.shape[1] != d_out.shape[1] or r_rows != n_rows:
+            raise ValueError("rows must have the shape of d_rows")
+    for t in (weights, d_weights, slot_rows, sorted_ids):
+        if t is not None and t.numel() != n_rows:
+            raise ValueError("weights, d_weights and the maps must have one entry per row")
+    rc = load().mlora_moe_combine_backward(
+        dp, d_ld, rp, r_ld, _dtype_code(d_out), n, d_out.shape[1], int(top_k),
+        None if weights is None else _f32(weights, "weights"),
+        None if slot_rows is None else _i32(slot_rows, "slot_rows"),
+        None if sorted_ids is None else _i32(sorted_ids, "sorted_ids"), op, o_ld,
+        None if d_weights is None else _f32(d_weights, "d_weights"), _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)
+
+
+def mlora_w4_packed_bytes(n_experts: int, k_in: int, n_out: int, group: int, dtype: int,
+                          has_zeros: bool) -> int:
+    """Bytes of the packed form of 4-bit expert weights."""
+    return int(load().mlora_w4_packed_bytes(int(n_experts), int(k_in), int(n_out), int(group),
+                                            int(dtype), int(bool(has_zeros))))
+
+
+def make_w4_route(q, scales, zeros, k_in: int, group: int, stream=None) -> W4Route:
+    """Packed route (mlora_w4_pack) of 4-bit weights: ``q`` [n_experts, n_out,
+    k_in / 2] bytes (k even in the low half), ``scales`` [n_experts, n_out,
+    ceil(k_in / group)] in bf16 or float32 (the dtype of x and out), ``zeros``
+    bytes of the same shape or None (8). The route keeps the packed tensor; the
+    arguments are not needed once the call's work is done."""
+    import torch
+    if q.dim() != 3 or scales.dim() != 3:
+        raise ValueError("q and scales must be 3-D")
+    E, N, half = q.shape
+    if half * 2 != k_in or group < 1:
+        raise ValueError("q must be [n_experts, n_out, k_in / 2]")
+    if tuple(scales.shape) != (E, N, -(-k_in // group)) or (
+            zeros is not None and zeros.shape != scales.shape):
+        raise ValueError("scales and zeros must be [n_experts, n_out, ceil(k_in / group)]")
+    code = _dtype_code(scales)
+    nbytes = mlora_w4_packed_bytes(E, k_in, N, group, code, zeros is not None)
+    if nbytes == 0:
+        raise _err(MLORA_ERR_INVALID)
+    packed = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    route = W4Route()
+    rc = load().mlora_w4_pack(_dev(q, "q", torch.uint8), _dev(scales, "scales"),
+                              None if zeros is None else _dev(zeros, "zeros", torch.uint8),
+                              E, k_in, N, int(group), code, packed.data_ptr(), nbytes,
+                              ctypes.byref(route), _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)
+    route._keep = packed
+    return route
+
+
+def mlora_w4_gather_gemv(route: W4Route, x, out, ids=None, top_k: int = 1,
+                         x_by_row: bool = False, stream=None) -> None:
+    """``out[r]`` = W[ids[r]] x[r // top_k] (or x[r] with ``x_by_row``); rows with
+    an id outside the route's experts get zeros. ``ids`` None: one weight."""
+    code = _dtype_code(x)
+    if code != route.dtype or out.dtype != x.dtype:
+        raise TypeError("x / out dtype differs from the route's")
+    xp, x_rows, x_ld = _rows_2d(x, "x")
+    op, n_rows, o_ld = _rows_2d(out, "out")
+    if x.shape[1] != route.k_in or out.shape[1] != route.n_out:
+        raise ValueError("x / out widths differ from the route's k_in / n_out")
+    if ids is not None and ids.numel() != n_rows:
+        raise ValueError("ids must have one entry per out row")
+    rc = load().mlora_w4_gather_gemv(ctypes.byref(route), xp, x_rows, x_ld, int(bool(x_by_row)),
+                                     op, o_ld, None if ids is None else _i32(ids, "ids"),
+                                     n_rows, int(top_k), _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)

@@ -7,13 +7,16 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmlora.so")
-SOURCES = [os.path.join(CSRC, "mlora_host.cpp"), os.path.join(CSRC, "mlora_fold.hip")]
+SOURCES = [os.path.join(CSRC, name)
+           for name in ("mlora_host.cpp", "mlora_fold.hip", "mlora_moe.hip", "mlora_w4.hip")]
 # measurement probes for bench.py (launch and read-pattern floors), a library of their own
 PROBE_LIB = os.path.join(PKG, "libmlora_probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "mlora_probe.hip")]
@@ -24,7 +27,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # keep hipcc from forming packed fp32 VALU ops (v_pk_*_f32)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -35,9 +37,7 @@ FLAGS = [
 ]
 
 
-def _compile(sources, lib, verbose):
-    tmp = lib + ".tmp"
-    cmd = [HIPCC, *FLAGS, *sources, "-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -47,7 +47,18 @@ def _compile(sources, lib, verbose):
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
-    os.replace(tmp, lib)
+
+
+def _compile(sources, lib, verbose):
+    """Each source to an object, side by side, then one link."""
+    with tempfile.TemporaryDirectory(dir=PKG, prefix="_build") as tmp:
+        objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in sources]
+        with ThreadPoolExecutor(4) as pool:
+            list(pool.map(lambda so: _run([HIPCC, *FLAGS, "-c", so[0], "-o", so[1]], verbose),
+                          zip(sources, objs)))
+        out = os.path.join(tmp, os.path.basename(lib))
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", *objs, "-o", out], verbose)
+        os.replace(out, lib)
 
 
 def build(verbose: bool = False) -> str:

@@ -1,0 +1,143 @@
+// Device and launch helpers shared by the MoE-layer operators around the fold
+// (mlora_moe.hip, mlora_w4.hip).
+#ifndef MLORA_DEVICE_H_
+#define MLORA_DEVICE_H_
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "mlora.h"
+#include "mlora_internal.h"
+
+namespace mlora {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Two fp32 -> two bf16 in one word (low half = a), round to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+// bf16 pair word -> its low / high value as fp32 (exact).
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// A value every lane of the wave holds, moved to a scalar register.
+__device__ __forceinline__ int uniform_i32(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Element types of a row: how many fit 16 bytes, and the exact widening /
+// one round-to-nearest-even narrowing of a 16-byte chunk or one element.
+struct Bf16Row {
+  typedef uint16_t elem;
+  static constexpr int kPer16 = 8;
+  static __device__ __forceinline__ float widen(elem v) {
+    return __uint_as_float((uint32_t)v << 16);
+  }
+  static __device__ __forceinline__ elem narrow(float f) { return (elem)pack_bf16(f, 0.f); }
+  static __device__ __forceinline__ void widen16(u32x4 v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = lo_f(v[i]);
+      f[2 * i + 1] = hi_f(v[i]);
+    }
+  }
+  static __device__ __forceinline__ u32x4 narrow16(const float* f) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+    return v;
+  }
+};
+struct F32Row {
+  typedef float elem;
+  static constexpr int kPer16 = 4;
+  static __device__ __forceinline__ float widen(elem v) { return v; }
+  static __device__ __forceinline__ elem narrow(float f) { return f; }
+  static __device__ __forceinline__ void widen16(u32x4 v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  }
+  static __device__ __forceinline__ u32x4 narrow16(const float* f) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(f[i]);
+    return v;
+  }
+};
+
+// x rotated by N lanes within each row of 16 lanes (one DPP move).
+template <int N>
+__device__ __forceinline__ uint32_t ror16(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + N, 0xf, 0xf, false);
+}
+__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// Reductions over the LPT lanes (16 or 64) that share a row; every lane gets
+// the result. Four rotations inside rows of 16, then, for a whole wave, the
+// four rows' values through scalar registers. The order is fixed.
+template <int LPT>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  v = max(v, ror16<8>(v));
+  v = max(v, ror16<4>(v));
+  v = max(v, ror16<2>(v));
+  v = max(v, ror16<1>(v));
+  if constexpr (LPT == 64)
+    v = max(max(lane_u32(v, 0), lane_u32(v, 16)), max(lane_u32(v, 32), lane_u32(v, 48)));
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  v = min(v, ror16<8>(v));
+  v = min(v, ror16<4>(v));
+  v = min(v, ror16<2>(v));
+  v = min(v, ror16<1>(v));
+  if constexpr (LPT == 64)
+    v = min(min(lane_u32(v, 0), lane_u32(v, 16)), min(lane_u32(v, 32), lane_u32(v, 48)));
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float group_sum(float f) {
+  f += __uint_as_float(ror16<8>(__float_as_uint(f)));
+  f += __uint_as_float(ror16<4>(__float_as_uint(f)));
+  f += __uint_as_float(ror16<2>(__float_as_uint(f)));
+  f += __uint_as_float(ror16<1>(__float_as_uint(f)));
+  if constexpr (LPT == 64) {
+    const uint32_t u = __float_as_uint(f);
+    f = (__uint_as_float(lane_u32(u, 0)) + __uint_as_float(lane_u32(u, 16))) +
+        (__uint_as_float(lane_u32(u, 32)) + __uint_as_float(lane_u32(u, 48)));
+  }
+  return f;
+}
+
+// LDS traffic of one wave is in order; this keeps the compiler from moving
+// accesses across, where lanes of a wave read what other lanes wrote.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+inline int32_t launch_status(const char* who) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(MLORA_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+  clear_error();
+  return MLORA_OK;
+}
+
+inline bool aligned(const void* p, uintptr_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+// Largest token, slot or row count of one call.
+constexpr int64_t kMaxRows = 0x3fffffffll;
+
+}  // namespace mlora
+
+#endif  // MLORA_DEVICE_H_

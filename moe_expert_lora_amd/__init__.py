@@ -382,9 +382,12 @@ def make_route(a_table, b_table, scale_table, n_experts: int, k_in: int, n_out: 
 
 
 def _stream_handle(stream) -> Optional[int]:
+    """The stream's handle; None: the current stream of the current device
+    (its raw handle: building a torch.cuda.Stream takes 2.5 us per call)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev(t, name, dtype=None):
@@ -720,50 +723,64 @@ def mlora_gather_bgmv_multi(route: MultiRoute, x, base_out, indices, row_adapter
 # the MoE layer around the fold
 # ---------------------------------------------------------------------------
 
-def _f32(t, name):
-    import torch
-    return _dev(t, name, torch.float32)
+# A decode step makes these calls back to back, and the wrapper's time is most
+# of a small call's: arguments are taken apart once, in few attribute reads.
+
+def _vec(t, name, dtype) -> int:
+    """Data pointer of a contiguous device tensor of one dtype."""
+    if t.dtype is not dtype or not (t.is_cuda and t.is_contiguous()):
+        return _dev(t, name, dtype)  # raises, naming what is wrong
+    return t.data_ptr()
 
 
-def _i32(t, name):
-    import torch
-    return _dev(t, name, torch.int32)
+def _mat(t, name):
+    """(data pointer, rows, columns, row stride) of a 2-D device tensor with
+    contiguous rows, as _rows_2d."""
+    shape = t.shape
+    if len(shape) == 2 and t.is_cuda and t.is_contiguous():
+        n, m = shape
+        return t.data_ptr(), n, m, m
+    p, n, ld = _rows_2d(t, name)
+    return p, n, shape[1], ld
+
+
+def _call(fn, *args) -> None:
+    rc = fn(*args)
+    if rc != MLORA_OK:
+        raise _err(rc)
 
 
 def mlora_router_topk(logits, indices, weights, renormalize: bool = False, stream=None) -> None:
     """Top-k experts of each row of ``logits`` [n_tokens, n_experts] (bf16 or
     float32, contiguous rows) into ``indices`` (int32) and ``weights``
     (float32), both [n_tokens, top_k]."""
-    p, n, ld = _rows_2d(logits, "logits")
-    if indices.dim() != 2 or indices.shape[0] != n or indices.shape != weights.shape:
+    import torch
+    p, n, experts, ld = _mat(logits, "logits")
+    shape = indices.shape
+    if len(shape) != 2 or shape[0] != n or shape != weights.shape:
         raise ValueError("indices and weights must be [n_tokens, top_k]")
-    rc = load().mlora_router_topk(p, ld, _dtype_code(logits), n, logits.shape[1],
-                                  indices.shape[1], int(bool(renormalize)),
-                                  _i32(indices, "indices"), _f32(weights, "weights"),
-                                  _stream_handle(stream))
-    if rc != MLORA_OK:
-        raise _err(rc)
+    _call(load().mlora_router_topk, p, ld, _dtype_code(logits), n, experts, shape[1],
+          1 if renormalize else 0, _vec(indices, "indices", torch.int32),
+          _vec(weights, "weights", torch.float32), _stream_handle(stream))
 
 
 def mlora_router_topk_backward(logits, indices, d_weights, d_logits, renormalize: bool = False,
                                stream=None) -> None:
     """Gradient of mlora_router_topk's weights into ``d_logits`` (written whole),
     from the forward's logits and indices."""
-    p, n, ld = _rows_2d(logits, "logits")
-    dp, dn, dld = _rows_2d(d_logits, "d_logits")
-    if d_logits.dtype != logits.dtype:
+    import torch
+    p, n, experts, ld = _mat(logits, "logits")
+    dp, dn, d_experts, d_ld = _mat(d_logits, "d_logits")
+    if d_logits.dtype is not logits.dtype:
         raise TypeError("d_logits dtype differs from logits'")
-    if dn != n or d_logits.shape[1] != logits.shape[1]:
+    if dn != n or d_experts != experts:
         raise ValueError("d_logits must have the shape of logits")
-    if indices.dim() != 2 or indices.shape[0] != n or indices.shape != d_weights.shape:
+    shape = indices.shape
+    if len(shape) != 2 or shape[0] != n or shape != d_weights.shape:
         raise ValueError("indices and d_weights must be [n_tokens, top_k]")
-    rc = load().mlora_router_topk_backward(p, ld, _dtype_code(logits), n, logits.shape[1],
-                                           indices.shape[1], int(bool(renormalize)),
-                                           _i32(indices, "indices"),
-                                           _f32(d_weights, "d_weights"), dp, dld,
-                                           _stream_handle(stream))
-    if rc != MLORA_OK:
-        raise _err(rc)
+    _call(load().mlora_router_topk_backward, p, ld, _dtype_code(logits), n, experts, shape[1],
+          1 if renormalize else 0, _vec(indices, "indices", torch.int32),
+          _vec(d_weights, "d_weights", torch.float32), dp, d_ld, _stream_handle(stream))
 
 
 def mlora_moe_sort_workspace_bytes(n_slots: int, n_experts: int) -> int:
@@ -776,6 +793,7 @@ def mlora_moe_sort(ids, n_experts: int, expert_offsets, sorted_ids, slot_rows, w
     """Stable sort of the flat (token, slot) ids by expert: fills
     ``expert_offsets`` [n_experts + 1], ``sorted_ids`` and ``slot_rows``
     (all int32); ids outside [0, n_experts) are dropped (-1)."""
+    import torch
     n = ids.numel()
     if expert_offsets.numel() != n_experts + 1:
         raise ValueError("expert_offsets must have n_experts + 1 entries")
@@ -785,82 +803,78 @@ def mlora_moe_sort(ids, n_experts: int, expert_offsets, sorted_ids, slot_rows, w
     if workspace is not None and workspace.numel():
         ws_ptr = _dev(workspace, "workspace")
         ws_bytes = workspace.numel() * workspace.element_size()
-    rc = load().mlora_moe_sort(_i32(ids, "ids"), n, int(n_experts),
-                               _i32(expert_offsets, "expert_offsets"),
-                               _i32(sorted_ids, "sorted_ids"), _i32(slot_rows, "slot_rows"),
-                               ws_ptr, ws_bytes, _stream_handle(stream))
-    if rc != MLORA_OK:
-        raise _err(rc)
+    i32 = torch.int32
+    _call(load().mlora_moe_sort, _vec(ids, "ids", i32), n, n_experts,
+          _vec(expert_offsets, "expert_offsets", i32), _vec(sorted_ids, "sorted_ids", i32),
+          _vec(slot_rows, "slot_rows", i32), ws_ptr, ws_bytes, _stream_handle(stream))
 
 
 def mlora_moe_dispatch(x, rows, sorted_ids, slot_rows, top_k: int, stream=None) -> None:
     """Copies token rows of ``x`` [n_tokens, dim] to their sorted ``rows``
     [n_tokens * top_k, dim]; rows no slot names get zeros. The maps are
     mlora_moe_sort's. Its gradient: mlora_moe_combine with no weights."""
-    xp, n, x_ld = _rows_2d(x, "x")
-    rp, n_rows, r_ld = _rows_2d(rows, "rows")
-    if rows.dtype != x.dtype:
+    import torch
+    xp, n, dim, x_ld = _mat(x, "x")
+    rp, n_rows, r_dim, r_ld = _mat(rows, "rows")
+    if rows.dtype is not x.dtype:
         raise TypeError("rows dtype differs from x's")
-    if rows.shape[1] != x.shape[1] or n_rows != n * top_k:
+    if r_dim != dim or n_rows != n * top_k:
         raise ValueError("rows must be [n_tokens * top_k, dim]")
     if sorted_ids.numel() != n_rows or slot_rows.numel() != n_rows:
         raise ValueError("sorted_ids and slot_rows must have one entry per row")
-    rc = load().mlora_moe_dispatch(xp, x_ld, _dtype_code(x), n, x.shape[1], int(top_k),
-                                   _i32(sorted_ids, "sorted_ids"), _i32(slot_rows, "slot_rows"),
-                                   rp, r_ld, _stream_handle(stream))
-    if rc != MLORA_OK:
-        raise _err(rc)
+    _call(load().mlora_moe_dispatch, xp, x_ld, _dtype_code(x), n, dim, top_k,
+          _vec(sorted_ids, "sorted_ids", torch.int32), _vec(slot_rows, "slot_rows", torch.int32),
+          rp, r_ld, _stream_handle(stream))
 
 
 def mlora_moe_combine(rows, out, top_k: int, weights=None, slot_rows=None, stream=None) -> None:
     """``out[t]`` = sum over slots of weights[t, j] * rows[slot_rows[t * top_k + j]]
     (``slot_rows`` None: rows in flat (token, slot) order; ``weights`` None: 1)."""
-    rp, n_rows, r_ld = _rows_2d(rows, "rows")
-    op, n, o_ld = _rows_2d(out, "out")
-    if rows.dtype != out.dtype:
+    import torch
+    rp, n_rows, dim, r_ld = _mat(rows, "rows")
+    op, n, o_dim, o_ld = _mat(out, "out")
+    if rows.dtype is not out.dtype:
         raise TypeError("out dtype differs from rows'")
-    if rows.shape[1] != out.shape[1]:
+    if dim != o_dim:
         raise ValueError("rows and out differ in width")
     if (weights is not None and weights.numel() != n * top_k) or (
             slot_rows is not None and slot_rows.numel() != n * top_k):
         raise ValueError("weights and slot_rows must have n_tokens * top_k entries")
-    rc = load().mlora_moe_combine(rp, r_ld, n_rows, _dtype_code(rows), n, rows.shape[1],
-                                  int(top_k),
-                                  None if weights is None else _f32(weights, "weights"),
-                                  None if slot_rows is None else _i32(slot_rows, "slot_rows"),
-                                  op, o_ld, _stream_handle(stream))
-    if rc != MLORA_OK:
-        raise _err(rc)
+    _call(load().mlora_moe_combine, rp, r_ld, n_rows, _dtype_code(rows), n, dim, top_k,
+          None if weights is None else _vec(weights, "weights", torch.float32),
+          None if slot_rows is None else _vec(slot_rows, "slot_rows", torch.int32),
+          op, o_ld, _stream_handle(stream))
 
 
 def mlora_moe_combine_backward(d_out, rows, weights, d_rows, d_weights, top_k: int,
                                slot_rows=None, sorted_ids=None, stream=None) -> None:
     """Gradient of mlora_moe_combine into ``d_rows`` [n_tokens * top_k, dim] and
     ``d_weights`` [n_tokens, top_k] (None: not computed, ``rows`` not read)."""
-    dp, n, d_ld = _rows_2d(d_out, "d_out")
-    op, n_rows, o_ld = _rows_2d(d_rows, "d_rows")
-    if d_rows.dtype != d_out.dtype:
+    import torch
+    dp, n, dim, d_ld = _mat(d_out, "d_out")
+    op, n_rows, o_dim, o_ld = _mat(d_rows, "d_rows")
+    dtype = d_out.dtype
+    if d_rows.dtype is not dtype:
         raise TypeError("d_rows dtype differs from d_out's")
-    if d_rows.shape[1] != d_out.shape[1] or n_rows != n * top_k:
+    if o_dim != dim or n_rows != n * top_k:
         raise ValueError("d_rows must be [n_tokens * top_k, dim]")
     rp, r_ld = None, 0
     if d_weights is not None:
-        rp, r_rows, r_ld = _rows_2d(rows, "rows")
-        if rows.dtype != d_out.dtype:
+        rp, r_rows, r_dim, r_ld = _mat(rows, "rows")
+        if rows.dtype is not dtype:
             raise TypeError("rows dtype differs from d_out's")
-        if rows.shape[1] != d_out.shape[1] or r_rows != n_rows:
+        if r_dim != dim or r_rows != n_rows:
             raise ValueError("rows must have the shape of d_rows")
     for t in (weights, d_weights, slot_rows, sorted_ids):
         if t is not None and t.numel() != n_rows:
             raise ValueError("weights, d_weights and the maps must have one entry per row")
-    rc = load().mlora_moe_combine_backward(
-        dp, d_ld, rp, r_ld, _dtype_code(d_out), n, d_out.shape[1], int(top_k),
-        None if weights is None else _f32(weights, "weights"),
-        None if slot_rows is None else _i32(slot_rows, "slot_rows"),
-        None if sorted_ids is None else _i32(sorted_ids, "sorted_ids"), op, o_ld,
-        None if d_weights is None else _f32(d_weights, "d_weights"), _stream_handle(stream))
-    if rc != MLORA_OK:
-        raise _err(rc)
+    f32, i32 = torch.float32, torch.int32
+    _call(load().mlora_moe_combine_backward, dp, d_ld, rp, r_ld, _dtype_code(d_out), n, dim,
+          top_k, None if weights is None else _vec(weights, "weights", f32),
+          None if slot_rows is None else _vec(slot_rows, "slot_rows", i32),
+          None if sorted_ids is None else _vec(sorted_ids, "sorted_ids", i32), op, o_ld,
+          None if d_weights is None else _vec(d_weights, "d_weights", f32),
+          _stream_handle(stream))
 
 
 def mlora_w4_packed_bytes(n_experts: int, k_in: int, n_out: int, group: int, dtype: int,
@@ -905,17 +919,16 @@ def mlora_w4_gather_gemv(route: W4Route, x, out, ids=None, top_k: int = 1,
                          x_by_row: bool = False, stream=None) -> None:
     """``out[r]`` = W[ids[r]] x[r // top_k] (or x[r] with ``x_by_row``); rows with
     an id outside the route's experts get zeros. ``ids`` None: one weight."""
-    code = _dtype_code(x)
-    if code != route.dtype or out.dtype != x.dtype:
+    import torch
+    if _dtype_code(x) != route.dtype or out.dtype is not x.dtype:
         raise TypeError("x / out dtype differs from the route's")
-    xp, x_rows, x_ld = _rows_2d(x, "x")
-    op, n_rows, o_ld = _rows_2d(out, "out")
-    if x.shape[1] != route.k_in or out.shape[1] != route.n_out:
+    xp, x_rows, k_in, x_ld = _mat(x, "x")
+    op, n_rows, n_out, o_ld = _mat(out, "out")
+    if k_in != route.k_in or n_out != route.n_out:
         raise ValueError("x / out widths differ from the route's k_in / n_out")
     if ids is not None and ids.numel() != n_rows:
         raise ValueError("ids must have one entry per out row")
-    rc = load().mlora_w4_gather_gemv(ctypes.byref(route), xp, x_rows, x_ld, int(bool(x_by_row)),
-                                     op, o_ld, None if ids is None else _i32(ids, "ids"),
-                                     n_rows, int(top_k), _stream_handle(stream))
-    if rc != MLORA_OK:
-        raise _err(rc)
+    _call(load().mlora_w4_gather_gemv, ctypes.byref(route), xp, x_rows, x_ld,
+          1 if x_by_row else 0, op, o_ld,
+          None if ids is None else _vec(ids, "ids", torch.int32), n_rows, top_k,
+          _stream_handle(stream))

@@ -34,9 +34,10 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr int kMaxW4Experts = 1024;
 constexpr uint32_t kMaxBuf = 0xFFFFFF00u;  // largest range one buffer resource describes
-constexpr uint32_t kPast = 0xFFFFFFF0u;    // an offset past every buffer: the load gives 0
+constexpr uint32_t kPast = 0xFFFFFF40u;    // an offset past every buffer: the load gives 0
 constexpr int kScan = 2048;                // rows scanned (and listed) at a time
 constexpr int kMaxWaves = 8;
+constexpr int kNT = 2;                     // non-temporal: weights are read once
 
 __device__ __forceinline__ rsrc_t buf(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
@@ -52,8 +53,9 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 // Packed layout. Weights: per expert and column tile of 16, ksteps = ceil(k /
 // 32) steps of 256 bytes. Four steps make a chunk of 1024 bytes in which lane l
 // of a wave finds its 16 bytes at 16 l: word i is step i, column l % 16, k
-// values 32 i + 8 (l / 16) .. + 7. The steps after the last whole chunk lie
-// one after the other, lane l's word at 4 l. In a word, values 2p and 2p + 1
+// values 32 i + 8 (l / 16) .. + 7. A last chunk of fewer steps keeps as many
+// words per lane; a lane still loads 16 bytes there, and what it reads of the
+// words behind meets x values of 0. In a word, values 2p and 2p + 1
 // of the 8 sit at bits 3 + 4p and 19 + 4p (p = 3 wraps round at bit 31), so
 // that a shift (a rotation for p = 3), a mask and an or leave the two bf16
 // values 16 + v side by side.
@@ -107,8 +109,9 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs a) {
       step = w / 256 * 4 + (w & 3);
       lane = (w & 255) >> 2;
     } else {
-      step = a.ksteps / 4 * 4 + (w - whole) / 64;
-      lane = (w - whole) & 63;
+      const int left = a.ksteps & 3;
+      step = a.ksteps / 4 * 4 + (w - whole) % left;
+      lane = (w - whole) / left;
     }
     const int64_t e = et / a.tiles;
     const int n = (int)(et - e * a.tiles) * 16 + (lane & 15);
@@ -156,7 +159,6 @@ struct W4Args {
   void* out;
   const int32_t* ids;
   int64_t out_ld;
-  int64_t tile_bytes;
   uint32_t x_bytes;
   uint32_t x_ld_bytes;
   uint32_t topk;          // rows per x row (1: a row of its own)
@@ -164,267 +166,574 @@ struct W4Args {
   int32_t E;              // 0: no ids, one weight
   int32_t K, N;
   int32_t tiles, ksteps, blocks, per_block;  // per_block: chunks per scale block
-  int32_t slices;
+  int32_t slices;         // workgroups per expert
+  int32_t pairs, per_slice;  // streaming form: tile pairs, and those of a slice
+  int32_t early;          // request weights before the rows are known
   int32_t out_vec;        // rows of out start on 4 elements
 };
+
+// (w & mask) | base in one operation, mask in a scalar and base in a vector
+// register (the compiler takes two, with both as literals).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t base) {
+  uint32_t r;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(base));
+  return r;
+}
 
 // 8 packed values of one column -> the bf16 values 16 + v.
 __device__ __forceinline__ u32x4 unpack(uint32_t w) {
   constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;
   u32x4 r;
-  r[0] = (w & kMask) | kBase;
-  r[1] = ((w >> 4) & kMask) | kBase;
-  r[2] = ((w >> 8) & kMask) | kBase;
-  r[3] = (__builtin_amdgcn_alignbit(w, w, 12) & kMask) | kBase;
+  r[0] = and_or(w, kMask, kBase);
+  r[1] = and_or(w >> 4, kMask, kBase);
+  r[2] = and_or(w >> 8, kMask, kBase);
+  r[3] = and_or(__builtin_amdgcn_alignbit(w, w, 12), kMask, kBase);
   return r;
 }
 
-// Second MFMA operand of one k step: bf16 as loaded, or an fp32 row's three
-// bf16 parts, smallest first.
+// Second MFMA operand of one k step as loaded: 8 bf16 or 8 fp32 values.
+template <bool F32>
+struct XRaw {
+  u32x4 v[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ XRaw<F32> load_x(rsrc_t rx, uint32_t row_off, int k, int K) {
+  XRaw<F32> f;
+  uint32_t off = row_off + (uint32_t)k * (F32 ? 4u : 2u);
+  off = row_off != kPast && k < K ? off : kPast;
+  f.v[0] = ld16(rx, off);
+  if constexpr (F32) f.v[1] = ld16(rx, off + 16u);  // kPast + 16 is past every buffer's end
+  return f;
+}
+
+// The operand's bf16 parts: the values, or an fp32 value's three parts,
+// smallest first.
 template <bool F32>
 struct XFrag {
   static constexpr int kParts = F32 ? 3 : 1;
   u32x4 p[kParts];
-};
-
-template <bool F32>
-__device__ __forceinline__ XFrag<F32> load_x(rsrc_t rx, uint32_t row_off, int k, int K) {
-  XFrag<F32> f;
-  const bool in = row_off != kPast && k < K;
-  if constexpr (!F32) {
-    f.p[0] = ld16(rx, in ? row_off + (uint32_t)k * 2u : kPast);
-  } else {
-    const uint32_t off = row_off + (uint32_t)k * 4u;
-    const u32x4 a = ld16(rx, in ? off : kPast), b = ld16(rx, in ? off + 16u : kPast);
+  __device__ __forceinline__ void set(const XRaw<F32>& r) {
+    if constexpr (!F32) {
+      p[0] = r.v[0];
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float v0 = __uint_as_float(i < 2 ? a[2 * i] : b[2 * i - 4]);
-      const float v1 = __uint_as_float(i < 2 ? a[2 * i + 1] : b[2 * i - 3]);
-      const uint32_t h = pack_bf16(v0, v1);
-      const float r0 = v0 - lo_f(h), r1 = v1 - hi_f(h);
-      const uint32_t m = pack_bf16(r0, r1);
-      f.p[2][i] = h;
-      f.p[1][i] = m;
-      f.p[0][i] = pack_bf16(r0 - lo_f(m), r1 - hi_f(m));
+      for (int i = 0; i < 4; ++i) {
+        const float v0 = __uint_as_float(r.v[i >> 1][(i & 1) * 2]);
+        const float v1 = __uint_as_float(r.v[i >> 1][(i & 1) * 2 + 1]);
+        const uint32_t h = pack_bf16(v0, v1);
+        const float r0 = v0 - lo_f(h), r1 = v1 - hi_f(h);
+        const uint32_t m = pack_bf16(r0, r1);
+        p[2][i] = h;
+        p[1][i] = m;
+        p[0][i] = pack_bf16(r0 - lo_f(m), r1 - hi_f(m));
+      }
     }
   }
-  return f;
+};
+
+// Buffers of a wave's column tiles et0 .. et0 + n - 1 of the packed form: tiles
+// past them (and everything, for n == 0) lie past their end and read as 0.
+// Built from scalars, so that a load needs no loop over lanes.
+struct WBufs {
+  rsrc_t w, s, z;
+  uint32_t tile_bytes, s_tile, z_tile;  // bytes from one tile to the next
+
+  template <int SG, int ES, bool ZP>
+  __device__ __forceinline__ void set(const W4Args& a, int et0, int n) {
+    et0 = uniform_i32(et0);
+    n = uniform_i32(n);
+    tile_bytes = (uint32_t)a.ksteps * 256u;
+    z_tile = (uint32_t)a.blocks * 16u * SG;
+    s_tile = z_tile * ES;
+    // 16 bytes more: a last lane's load of a short chunk (the scales follow)
+    w = buf(a.w + (int64_t)et0 * tile_bytes, n > 0 ? n * tile_bytes + 16u : 0u);
+    s = buf(a.s + (int64_t)et0 * s_tile, n * s_tile);
+    z = w;
+    if constexpr (ZP) z = buf(a.z + (int64_t)et0 * z_tile, n * z_tile);
+  }
+};
+
+// The weights of one chunk (128 k values) of NT column tiles, as loaded.
+template <bool F32, int SG, bool ZP, int NT>
+struct WChunk {
+  static constexpr int kEs = F32 ? 4 : 2;
+  static constexpr int kWords = SG * kEs;  // 4 scales per group: 2 or 4 words
+  u32x4 w[NT];
+  uint32_t s[NT][kWords];
+  uint32_t z[NT][ZP ? SG : 1];
+
+  __device__ __forceinline__ void load(const W4Args& a, const WBufs& b, int c, int lane) {
+    const uint32_t lg = (uint32_t)lane >> 4, blk = (uint32_t)(c / a.per_block);
+    const uint32_t per_lane = c < (a.ksteps >> 2) ? 16u : (uint32_t)(a.ksteps & 3) * 4u;
+    // offsets wholly in the vector operand: the range check is against it
+    const uint32_t wo = (uint32_t)lane * per_lane + c * 1024u;
+    const uint32_t so = lg * (kWords * 4) + blk * (16u * SG * kEs);
+    const uint32_t zo = lg * (SG * 4) + blk * (16u * SG);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      w[nt] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(b.w, wo + nt * b.tile_bytes, 0, kNT));
+      words<kWords>(s[nt], b.s, so + nt * b.s_tile);
+      if constexpr (ZP) words<SG>(z[nt], b.z, zo + nt * b.z_tile);
+    }
+  }
+  template <int N>
+  static __device__ __forceinline__ void words(uint32_t* d, rsrc_t r, uint32_t off) {
+    if constexpr (N == 1) {
+      d[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+    } else if constexpr (N == 2) {
+      const u32x2 v = __builtin_bit_cast(u32x2,
+                                         __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+      d[0] = v[0];
+      d[1] = v[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const u32x4 v = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + i * 4u, 0, 0));
+        d[i] = v[0];
+        d[i + 1] = v[1];
+        d[i + 2] = v[2];
+        d[i + 3] = v[3];
+      }
+    }
+  }
+};
+
+// acc += the chunk's products, group by group. `x(mb, ks, f)` fills f with the
+// bf16 parts of k step ks of row block mb.
+template <bool F32, int SG, bool ZP, int NT, int MB, typename X>
+__device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x,
+                                          f32x4 (&acc)[NT][MB]) {
+  constexpr int kPer = 4 / SG, kParts = XFrag<F32>::kParts;
+  const uint32_t kc = ZP ? 0xbf80bf80u : 0xc1c0c1c0u;  // bf16 -1, or -(16 + 8)
+  const u32x4 cons = {kc, kc, kc, kc};
+#pragma unroll
+  for (int sg = 0; sg < SG; ++sg) {
+    XFrag<F32> f[MB][kPer];
+    f32x4 dc[MB] = {};
+#pragma unroll
+    for (int ks = 0; ks < kPer; ++ks)
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) x(mb, sg * kPer + ks, f[mb][ks]);
+#pragma unroll
+    for (int ks = 0; ks < kPer; ++ks)
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) dc[mb] = mfma(cons, f[mb][ks].p[p], dc[mb]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 s[MB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) s[mb] = ZP ? f32x4{0.f, 0.f, 0.f, 0.f} : dc[mb];
+#pragma unroll
+      for (int ks = 0; ks < kPer; ++ks) {
+        const u32x4 wf = unpack(wc.w[nt][sg * kPer + ks]);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) s[mb] = mfma(wf, f[mb][ks].p[p], s[mb]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float sc, z = 0.f;
+        if constexpr (F32)
+          sc = __uint_as_float(wc.s[nt][sg * 4 + i]);
+        else
+          sc = (i & 1) ? hi_f(wc.s[nt][sg * 2 + i / 2]) : lo_f(wc.s[nt][sg * 2 + i / 2]);
+        if constexpr (ZP) z = (float)((wc.z[nt][sg] >> (8 * i)) & 0xffu);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const float t = ZP ? fmaf(z, dc[mb][i], s[mb][i]) : s[mb][i];
+          acc[nt][mb][i] = fmaf(sc, t, acc[nt][mb][i]);
+        }
+      }
+    }
+    // group after group: operands of later ones are not fetched into registers
+    // ahead, which the weights in flight need
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
-template <bool F32, int SG, bool ZP, int NT>
-__global__ void __launch_bounds__(64 * kMaxWaves) w4_kernel(W4Args a) {
+template <typename Row>
+__device__ __forceinline__ void store4(typename Row::elem* o, f32x4 v, int left, bool vec) {
+  if (vec && left >= 4) {
+    if constexpr (sizeof(typename Row::elem) == 4)
+      *reinterpret_cast<f32x4*>(o) = v;
+    else
+      *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < left) o[j] = Row::narrow(v[j]);
+  }
+}
+
+// Lists in `list` the rows of rows [seg, seg + len) whose id is e (e == E: the
+// rows without an expert), in row order; returns how many. Each wave scans a
+// run of 64 * rounds ids and lists its hits behind those of the waves before
+// it, so that workgroups which share an expert's rows agree on the list.
+__device__ __forceinline__ int list_rows(const W4Args& a, int e, int seg, int len, int* list,
+                                         int* counts) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
+  const int rounds = (len + 64 * waves - 1) / (64 * waves);  // <= 32
+  const int first = wave * rounds * 64 + lane;
+  uint32_t hits = 0;
+  int n_wave = 0;
+  for (int r0 = 0; r0 < rounds; r0 += 8) {
+    int id[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int i = first + (r0 + r) * 64;
+      id[r] = r0 + r < rounds && i < len ? a.ids[seg + i] : -1;
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const bool in = r0 + r < rounds && first + (r0 + r) * 64 < len;
+      const bool hit = in && ((uint32_t)id[r] < (uint32_t)a.E ? id[r] : a.E) == e;
+      n_wave += __popcll(__ballot(hit));
+      hits |= (hit ? 1u : 0u) << ((r0 + r) & 31);
+    }
+  }
+  __syncthreads();  // the list's last readers are done
+  if (lane == 0) counts[wave] = n_wave;
+  __syncthreads();
+  int at = 0, n = 0;
+  for (int w = 0; w < waves; ++w) {
+    at += w < wave ? counts[w] : 0;
+    n += counts[w];
+  }
+  at = uniform_i32(at);
+  if (n_wave > 0) {
+    for (int r = 0; r < rounds; ++r) {
+      const bool hit = (hits >> r) & 1;
+      const uint64_t m = __ballot(hit);
+      if (hit)
+        list[at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                            __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u))] =
+            seg + first + r * 64;
+      at += __popcll(m);
+    }
+  }
+  __syncthreads();
+  return uniform_i32(n);
+}
+
+// Zeros into columns [n0, n0 + cols) of the listed rows.
+template <typename Row>
+__device__ __forceinline__ void zero_listed(const W4Args& a, const int* list, int n_list, int n0,
+                                            int cols) {
+  typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
+  const int all = (int)(blockDim.x * gridDim.y);
+  for (int i = (int)threadIdx.x + (int)(blockIdx.y * blockDim.x); i < n_list * cols; i += all) {
+    const int n = n0 + i % cols;
+    if (n < a.N) out[(int64_t)list[i / cols] * a.out_ld + n] = 0;
+  }
+}
+
+// Few column tiles: a workgroup owns one tile, its waves split k and add their
+// sums up through LDS in wave order; x goes straight to the operands.
+template <bool F32, int SG, bool ZP, int MB>
+__global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
-  constexpr int kEs = F32 ? 4 : 2;
-  constexpr int kCols = 16 * NT, kStride = kCols + 4;
+  constexpr int kStride = 20, kRows = 16 * MB;
   __shared__ int list[kScan];
   __shared__ int counts[kMaxWaves];
-  extern __shared__ float red[];  // [waves][16][kStride]
+  __shared__ float red[kMaxWaves * kRows * kStride];
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int e = (int)blockIdx.x / a.slices;
-  const int tile0 = ((int)blockIdx.x - e * a.slices) * NT;
-  const int n0 = tile0 * 16;
+  const int e = (int)blockIdx.x / a.tiles, tile = (int)blockIdx.x - e * a.tiles;
+  const int n0 = tile * 16, chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
-  const int64_t et0 = (int64_t)e * a.tiles + tile0;
-  const int chunks = (a.ksteps + 3) >> 2, whole = a.ksteps >> 2;
-  constexpr float kZero = ZP ? -1.f : -24.f;
-  const uint32_t kc = pack_bf16(kZero, kZero);
-  const u32x4 cons = {kc, kc, kc, kc};
+  WBufs wb;
+  wb.set<SG, (F32 ? 4 : 2), ZP>(a, (a.E > 0 ? min(e, a.E - 1) : 0) * a.tiles + tile, 1);
+  WChunk<F32, SG, ZP, 1> wc;
+  // the first chunk's weights are requested before the rows are known where
+  // most experts hold some
+  const bool early = a.early && (a.E == 0 || e < a.E);
+  if (early) wc.load(a, wb, wave, lane);
 
   for (int seg = 0; seg < a.n_rows; seg += kScan) {
     const int len = min(kScan, a.n_rows - seg);
     int n_list = len;
     if (a.E > 0) {
-      if (seg > 0) __syncthreads();
-      // Each wave scans a run of 64 * rounds ids and lists its hits behind
-      // those of the waves before it: in row order, so that workgroups which
-      // share an expert's rows agree on the list.
-      const int rounds = (len + 64 * waves - 1) / (64 * waves);  // <= 32
-      const int first = wave * rounds * 64 + lane;
-      uint32_t hits = 0;
-      int n_wave = 0;
-      for (int r = 0; r < rounds; ++r) {
-        const int i = first + r * 64;
-        const int id = i < len ? a.ids[seg + i] : -1;
-        // workgroups of the place after the last expert write the zeros of
-        // rows without one
-        const bool hit = i < len && ((uint32_t)id < (uint32_t)a.E ? id : a.E) == e;
-        n_wave += __popcll(__ballot(hit));
-        hits |= (hit ? 1u : 0u) << r;
-      }
-      if (lane == 0) counts[wave] = n_wave;
-      __syncthreads();
-      int at = 0;
-      n_list = 0;
-      for (int w = 0; w < waves; ++w) {
-        at += w < wave ? counts[w] : 0;
-        n_list += counts[w];
-      }
-      at = uniform_i32(at);
-      n_list = uniform_i32(n_list);
-      for (int r = 0; r < rounds; ++r) {
-        const bool hit = (hits >> r) & 1;
-        const uint64_t m = __ballot(hit);
-        if (hit)
-          list[at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
-                                              __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u))] =
-              seg + first + r * 64;
-        at += __popcll(m);
-      }
-      __syncthreads();
+      n_list = list_rows(a, e, seg, len, list, counts);
       if (e == a.E) {
-        const int all = (int)(blockDim.x * gridDim.y);
-        for (int i = tid + (int)(blockIdx.y * blockDim.x); i < n_list * kCols; i += all) {
-          const int n = n0 + i % kCols;
-          if (n < a.N) out[(int64_t)list[i / kCols] * a.out_ld + n] = 0;
-        }
+        zero_listed<Row>(a, list, n_list, n0, 16);
         continue;
       }
     }
-    for (int b0 = (int)blockIdx.y * 16; b0 < n_list; b0 += (int)gridDim.y * 16) {
-      const int at = b0 + li;
-      const int row = at < n_list ? (a.E > 0 ? list[at] : seg + at) : -1;
-      const uint32_t row_off = row >= 0 ? (uint32_t)row / a.topk * a.x_ld_bytes : kPast;
-      f32x4 acc[NT] = {};
-      for (int c = wave; c < chunks; c += waves) {
-        u32x4 w[NT];
-        uint32_t sw[NT][SG * kEs];  // 4 scales per group: 2 or 4 words
-        uint32_t zw[NT][SG];
-        const int blk = c / a.per_block;
+    for (int b0 = (int)blockIdx.y * kRows; b0 < n_list; b0 += (int)gridDim.y * kRows) {
+      uint32_t row_off[MB];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // tiles past the last read the last one again and are not stored
-          const int64_t et = et0 + min(nt, a.tiles - 1 - tile0);
-          const uint8_t* p = a.w + et * a.tile_bytes + (int64_t)c * 1024;
-          if (c < whole) {
-            w[nt] = *reinterpret_cast<const u32x4*>(p + lane * 16);
-          } else {
-            const int left = a.ksteps & 3;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[nt][i] = i < left ? *reinterpret_cast<const uint32_t*>(p + i * 256 + lane * 4) : 0;
-          }
-          const int64_t cell = ((et * a.blocks + blk) * 4 + lg) * SG;
-          const uint32_t* ps = reinterpret_cast<const uint32_t*>(a.s + cell * 4 * kEs);
-#pragma unroll
-          for (int i = 0; i < SG * kEs; ++i) sw[nt][i] = ps[i];
-          if constexpr (ZP) {
-            const uint32_t* pz = reinterpret_cast<const uint32_t*>(a.z + cell * 4);
-#pragma unroll
-            for (int i = 0; i < SG; ++i) zw[nt][i] = pz[i];
-          }
-        }
-        XFrag<F32> x[4];
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          x[ks] = load_x<F32>(rx, row_off, c * 128 + ks * 32 + lg * 8, a.K);
-#pragma unroll
-        for (int sg = 0; sg < SG; ++sg) {
-          constexpr int kPer = 4 / SG;
-          f32x4 dc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int ks = sg * kPer; ks < (sg + 1) * kPer; ++ks)
-#pragma unroll
-            for (int p = 0; p < XFrag<F32>::kParts; ++p) dc = mfma(cons, x[ks].p[p], dc);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            f32x4 s = ZP ? f32x4{0.f, 0.f, 0.f, 0.f} : dc;
-#pragma unroll
-            for (int ks = sg * kPer; ks < (sg + 1) * kPer; ++ks) {
-              const u32x4 wf = unpack(w[nt][ks]);
-#pragma unroll
-              for (int p = 0; p < XFrag<F32>::kParts; ++p) s = mfma(wf, x[ks].p[p], s);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float t = s[i];
-              if constexpr (ZP)
-                t = fmaf((float)((zw[nt][sg] >> (8 * i)) & 0xffu), dc[i], t);
-              float sc;
-              if constexpr (F32)
-                sc = __uint_as_float(sw[nt][sg * 4 + i]);
-              else
-                sc = (i & 1) ? hi_f(sw[nt][sg * 2 + i / 2]) : lo_f(sw[nt][sg * 2 + i / 2]);
-              acc[nt][i] = fmaf(sc, t, acc[nt][i]);
-            }
-          }
-        }
+      for (int mb = 0; mb < MB; ++mb) {
+        const int at = b0 + mb * 16 + li;
+        const int row = at < n_list ? (a.E > 0 ? list[at] : seg + at) : -1;
+        row_off[mb] = row >= 0 ? (uint32_t)row / a.topk * a.x_ld_bytes : kPast;
       }
-      // the waves' sums, added in wave order
+      f32x4 acc[1][MB] = {};
+      for (int c = wave; c < chunks; c += waves) {
+        XRaw<F32> x[MB][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<f32x4*>(&red[(wave * 16 + li) * kStride + nt * 16 + lg * 4]) = acc[nt];
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            x[mb][ks] = load_x<F32>(rx, row_off[mb], c * 128 + ks * 32 + lg * 8, a.K);
+        if (!early || c != wave || seg > 0 || b0 != (int)blockIdx.y * kRows)
+          wc.load(a, wb, c, lane);
+        add_chunk<F32, SG, ZP, 1, MB>(
+            wc, [&](int mb, int ks, XFrag<F32>& f) { f.set(x[mb][ks]); }, acc);
+      }
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+        *reinterpret_cast<f32x4*>(&red[(wave * kRows + mb * 16 + li) * kStride + lg * 4]) =
+            acc[0][mb];
       __syncthreads();
-      for (int i = tid; i < 16 * kCols / 4; i += (int)blockDim.x) {
-        const int r = i / (kCols / 4), c4 = i % (kCols / 4) * 4;
+      for (int i = tid; i < kRows * 4; i += (int)blockDim.x) {
+        const int r = i >> 2, c4 = (i & 3) * 4;
         f32x4 sum = *reinterpret_cast<const f32x4*>(&red[r * kStride + c4]);
         for (int w = 1; w < waves; ++w)
-          sum += *reinterpret_cast<const f32x4*>(&red[(w * 16 + r) * kStride + c4]);
-        const int n = n0 + c4;
-        if (b0 + r >= n_list || n >= a.N) continue;
-        const int orow = a.E > 0 ? list[b0 + r] : seg + b0 + r;
-        typename Row::elem* o = out + (int64_t)orow * a.out_ld + n;
-        if (a.out_vec && n + 4 <= a.N) {
-          if constexpr (F32)
-            *reinterpret_cast<f32x4*>(o) = sum;
-          else
-            *reinterpret_cast<u32x2*>(o) =
-                u32x2{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (n + j < a.N) o[j] = Row::narrow(sum[j]);
-        }
+          sum += *reinterpret_cast<const f32x4*>(&red[(w * kRows + r) * kStride + c4]);
+        if (b0 + r >= n_list) continue;
+        const int64_t row = a.E > 0 ? list[b0 + r] : seg + b0 + r;
+        store4<Row>(out + row * a.out_ld + n0 + c4, sum, a.N - n0 - c4, a.out_vec != 0);
       }
       __syncthreads();
     }
+  }
+}
+
+// Many column tiles: x rows go into LDS once per workgroup, as the operands the
+// MFMAs take (k in panels of kPanel chunks where the rows do not fit whole);
+// each wave then streams whole columns: pairs of tiles over all of k, kAhead
+// chunks of weights requested ahead, no barrier between.
+constexpr int kPair = 2;   // tiles per wave and step
+constexpr int kAhead = 3;  // chunks in flight per wave
+constexpr int kLds = 160 * 1024;        // of a CU
+constexpr int kListLds = kScan * 4 + 256;  // the list and the counts
+constexpr int chunk_lds(bool f32, int mb) { return 4 * mb * (f32 ? 3 : 1) * 1024; }
+// Chunks of x rows that fit a workgroup's LDS, in whole turns of the ring.
+constexpr int panel_chunks(bool f32, int mb) {
+  return (kLds - kListLds) / chunk_lds(f32, mb) / kAhead * kAhead;
+}
+constexpr int stream_waves(bool f32) { return f32 ? 8 : 12; }  // most per workgroup
+
+template <bool F32, int SG, bool ZP, int MB>
+__global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Args a) {
+  typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
+  typedef WChunk<F32, SG, ZP, kPair> Chunk;
+  constexpr int kRows = 16 * MB, kParts = XFrag<F32>::kParts;
+  constexpr int kPanel = panel_chunks(F32, MB);
+  __shared__ int list[kScan];
+  __shared__ int counts[stream_waves(F32)];
+  extern __shared__ u32x4 xs[];  // [k step][row block][part][lane]
+  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+  const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
+  const int e = (int)blockIdx.x / a.slices, slice = (int)blockIdx.x - e * a.slices;
+  const int chunks = (a.ksteps + 3) >> 2;
+  typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
+  const rsrc_t rx = buf(a.x, a.x_bytes);
+  // this wave's pairs: every waves-th of the slice's; none in the place after
+  // the last expert
+  const bool none = a.E > 0 && e == a.E;
+  const int pair0 = slice * a.per_slice + wave;
+  const int n_pairs = uniform_i32(
+      none ? 0 : max(0, (min((slice + 1) * a.per_slice, a.pairs) - pair0 + waves - 1) / waves));
+  const int et0 = e * a.tiles;
+  // A pair takes whole turns of the ring: places past its chunks stay empty.
+  const int turns = (chunks + kAhead - 1) / kAhead * kAhead;
+  Chunk ring[kAhead];
+  int lp = 0, lc = 0;  // pair and chunk of the next request
+  auto request = [&](Chunk& w) {
+    const int t0 = (pair0 + lp * waves) * kPair;
+    const bool in = lp < n_pairs && lc < chunks;
+    WBufs wb;
+    wb.set<SG, (F32 ? 4 : 2), ZP>(a, in ? et0 + t0 : 0, in ? min(kPair, a.tiles - t0) : 0);
+    w.load(a, wb, lc, lane);
+    lc = lc + 1 == turns ? 0 : lc + 1;
+    lp += lc == 0;
+  };
+  // The ring's first requests for a block of rows; nothing where none follows.
+  auto restart = [&](bool more) {
+    lp = more ? 0 : n_pairs;
+    lc = 0;
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) request(ring[d]);
+  };
+
+  // The first weights are requested before the rows are known where most
+  // experts hold some (a.early), else behind the scan.
+  int seg = 0, n_list = min(kScan, a.n_rows);
+  if (a.E > 0 && !a.early) n_list = list_rows(a, e, 0, n_list, list, counts);
+  restart(n_list > 0 || kScan < a.n_rows);
+  if (a.E > 0 && a.early) n_list = list_rows(a, e, 0, n_list, list, counts);
+  for (;;) {
+    if (none)
+      zero_listed<Row>(a, list, n_list, slice * a.per_slice * kPair * 16,
+                       a.per_slice * kPair * 16);
+    const int step = (int)gridDim.y * kRows;
+    for (int b0 = (int)blockIdx.y * kRows; b0 < n_list && !none; b0 += step) {
+      uint32_t row_off[MB];
+      int orow[MB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const int at = b0 + mb * 16 + li;
+        orow[mb] = at < n_list ? (a.E > 0 ? list[at] : seg + at) : -1;
+        row_off[mb] = orow[mb] >= 0 ? (uint32_t)orow[mb] / a.topk * a.x_ld_bytes : kPast;
+      }
+      f32x4 acc[kPair][MB];
+      for (int p0 = 0; p0 < chunks; p0 += kPanel) {
+        const int p1 = min(p0 + kPanel, chunks);
+        __syncthreads();
+        const int frags = (p1 - p0) * 4 * MB;
+        constexpr int kBatch = F32 ? 4 : 6;  // loads in flight per wave
+        for (int f0 = wave; f0 < frags; f0 += kBatch * waves) {
+          XRaw<F32> r[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int f = f0 + i * waves;
+            const int mb = f % MB, k = p0 * 128 + f / MB * 32 + lg * 8;
+            r[i] = load_x<F32>(rx, MB == 2 && mb ? row_off[MB - 1] : row_off[0],
+                               f < frags ? k : a.K, a.K);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int f = f0 + i * waves;
+            if (f < frags) {
+              XFrag<F32> q;
+              q.set(r[i]);
+#pragma unroll
+              for (int p = 0; p < kParts; ++p) xs[(f * kParts + p) * 64 + lane] = q.p[p];
+            }
+          }
+        }
+        __syncthreads();
+        // one panel: every pair; several: the wave's one pair's share of them
+        for (int pair = 0; pair < n_pairs; ++pair) {
+          if (p0 == 0) {
+#pragma unroll
+            for (int nt = 0; nt < kPair; ++nt)
+#pragma unroll
+              for (int mb = 0; mb < MB; ++mb) acc[nt][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
+          for (int c0 = p0; c0 < p1; c0 += kAhead) {
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) {
+              if (c0 + d < p1) {
+                const u32x4* px = xs + (c0 + d - p0) * (4 * MB * kParts * 64) + lane;
+                add_chunk<F32, SG, ZP, kPair, MB>(
+                    ring[d],
+                    [&](int mb, int ks, XFrag<F32>& f) {
+#pragma unroll
+                      for (int p = 0; p < kParts; ++p)
+                        f.p[p] = px[((ks * MB + mb) * kParts + p) * 64];
+                    },
+                    acc);
+              }
+              request(ring[d]);
+            }
+          }
+          if (p1 < chunks) continue;
+          const int n = (pair0 + pair * waves) * kPair * 16 + lg * 4;
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
+            if (orow[mb] < 0) continue;
+            typename Row::elem* o = out + (int64_t)orow[mb] * a.out_ld + n;
+#pragma unroll
+            for (int nt = 0; nt < kPair; ++nt)
+              store4<Row>(o + nt * 16, acc[nt][mb], a.N - n - nt * 16, a.out_vec != 0);
+          }
+        }
+      }
+      restart(b0 + step < n_list || seg + kScan < a.n_rows);
+    }
+    seg += kScan;
+    if (seg >= a.n_rows) break;
+    n_list = min(kScan, a.n_rows - seg);
+    if (a.E > 0) n_list = list_rows(a, e, seg, n_list, list, counts);
   }
 }
 
 struct W4Plan {
-  int nt, waves, splits;
+  bool stream;
+  int mb, waves, splits, per_slice, slices;
 };
 
-W4Plan plan_w4(const mlora_w4_route* r, int64_t n_rows, int64_t experts) {
-  W4Plan p;
+W4Plan plan_w4(const mlora_w4_route* r, int64_t n_rows, int64_t experts, bool f32) {
+  W4Plan p{};
   const int64_t tiles = (r->n_out + 15) / 16, chunks = (r->k_in + 127) / 128;
-  // Column tiles per workgroup: 4 while that leaves 512 workgroups or more,
-  // else 1, so that a single weight is spread over as many CUs as it has tiles.
-  p.nt = experts * ((tiles + 3) / 4) >= 512 ? 4 : 1;
-  // Waves: one per chunk up to 8, and no more than it takes for the fewest
-  // chunks per wave.
-  const int64_t per = (chunks + kMaxWaves - 1) / kMaxWaves;
-  p.waves = (int)((chunks + per - 1) / per);
+  const int64_t mean = (n_rows + experts - 1) / experts;  // rows per expert
+  // Row blocks of 16 per pass over the weights: two once an expert holds more
+  // than ten rows on average.
+  p.mb = !f32 && (experts == 1 ? mean > 16 : mean > 10) ? 2 : 1;
+  const int64_t pairs = (tiles + kPair - 1) / kPair;
+  // Streaming pays once there are pairs of tiles for four waves on every CU.
+  p.stream = experts * pairs >= 1024;
+  if (p.stream) {
+    // Workgroups of 8 waves where the x rows leave room for two on a CU, else
+    // of as many as its registers hold; slices of an expert's pairs for one
+    // round of workgroups over the CUs.
+    const int64_t most = panel_chunks(f32, p.mb);
+    const int64_t lds = (chunks < most ? chunks : most) * chunk_lds(f32, p.mb) + kListLds;
+    const int64_t per_cu = lds * 2 <= kLds ? 2 : 1;
+    p.waves = per_cu == 2 ? 8 : stream_waves(f32);
+    if (experts * ((pairs + p.waves - 1) / p.waves) < 256) p.waves = 4;
+    int64_t slices = 256 * per_cu / experts;
+    if (slices > (pairs + p.waves - 1) / p.waves) slices = (pairs + p.waves - 1) / p.waves;
+    if (slices < 1) slices = 1;
+    // k in several panels: one pair per wave, whose sums stay in registers
+    if (chunks > most) slices = (pairs + p.waves - 1) / p.waves;
+    p.per_slice = (int)((pairs + slices - 1) / slices);
+    p.slices = (int)((pairs + p.per_slice - 1) / p.per_slice);
+  } else {
+    const int64_t per = (chunks + kMaxWaves - 1) / kMaxWaves;
+    p.waves = (int)((chunks + per - 1) / per);
+    p.slices = (int)tiles;
+  }
   // Rows of one expert over several workgroups once an expert holds more than
-  // two blocks of 16 on average.
-  const int64_t blocks = (n_rows + experts * 16 - 1) / (experts * 16);
+  // two passes on average.
+  const int64_t blocks = (mean + 16 * p.mb - 1) / (16 * p.mb);
   p.splits = (int)(blocks <= 2 ? 1 : blocks > 64 ? 32 : (blocks + 1) / 2);
   return p;
 }
 
-template <bool F32, int SG, bool ZP>
+template <bool F32, int SG, bool ZP, int MB>
 void launch_w4(const W4Args& a0, const W4Plan& p, int64_t places, hipStream_t s) {
   W4Args a = a0;
-  a.slices = (a.tiles + p.nt - 1) / p.nt;
+  a.slices = p.slices;
+  a.per_slice = p.per_slice;
+  a.pairs = (a.tiles + kPair - 1) / kPair;
   const dim3 grid((unsigned)(places * a.slices), (unsigned)p.splits), block(64 * p.waves);
-  const size_t lds = (size_t)p.waves * 16 * (16 * p.nt + 4) * 4;
-  if (p.nt == 4)
-    hipLaunchKernelGGL((w4_kernel<F32, SG, ZP, 4>), grid, block, lds, s, a);
-  else
-    hipLaunchKernelGGL((w4_kernel<F32, SG, ZP, 1>), grid, block, lds, s, a);
+  if (!p.stream) {
+    hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB>), grid, block, 0, s, a);
+    return;
+  }
+  const int chunks = (a.ksteps + 3) / 4, most = panel_chunks(F32, MB);
+  const size_t lds = (size_t)(chunks < most ? chunks : most) * chunk_lds(F32, MB);
+  hipLaunchKernelGGL((w4_stream_kernel<F32, SG, ZP, MB>), grid, block, lds, s, a);
 }
 
-template <bool F32>
-void dispatch_w4(const W4Args& a, const W4Plan& p, int sg, int64_t places, hipStream_t s) {
+template <int SG, bool ZP>
+void dispatch_w4_sg(const W4Args& a, const W4Plan& p, bool f32, int64_t places, hipStream_t s) {
+  if (f32) return launch_w4<true, SG, ZP, 1>(a, p, places, s);
+  if (p.mb == 2) return launch_w4<false, SG, ZP, 2>(a, p, places, s);
+  launch_w4<false, SG, ZP, 1>(a, p, places, s);
+}
+
+void dispatch_w4(const W4Args& a, const W4Plan& p, bool f32, int sg, int64_t places,
+                 hipStream_t s) {
   if (a.z) {
-    if (sg == 4) return launch_w4<F32, 4, true>(a, p, places, s);
-    if (sg == 2) return launch_w4<F32, 2, true>(a, p, places, s);
-    return launch_w4<F32, 1, true>(a, p, places, s);
+    if (sg == 4) return dispatch_w4_sg<4, true>(a, p, f32, places, s);
+    if (sg == 2) return dispatch_w4_sg<2, true>(a, p, f32, places, s);
+    return dispatch_w4_sg<1, true>(a, p, f32, places, s);
   }
-  if (sg == 4) return launch_w4<F32, 4, false>(a, p, places, s);
-  if (sg == 2) return launch_w4<F32, 2, false>(a, p, places, s);
-  launch_w4<F32, 1, false>(a, p, places, s);
+  if (sg == 4) return dispatch_w4_sg<4, false>(a, p, f32, places, s);
+  if (sg == 2) return dispatch_w4_sg<2, false>(a, p, f32, places, s);
+  dispatch_w4_sg<1, false>(a, p, f32, places, s);
 }
 
 int32_t check_w4(const char* who, int32_t E, int32_t K, int32_t N, int32_t group,
@@ -556,7 +865,6 @@ extern "C" int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void*
   a.out = out;
   a.ids = ids;
   a.out_ld = out_ld;
-  a.tile_bytes = l.tile_bytes;
   a.x_bytes = (uint32_t)(((need - 1) * x_ld + route->k_in) * es);
   a.x_ld_bytes = (uint32_t)(x_ld * es);
   a.topk = x_by_row ? 1u : (uint32_t)top_k;
@@ -570,14 +878,12 @@ extern "C" int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void*
   a.per_block = route->group <= 128 ? 1 : route->group / 128;
   a.out_vec = out_ld % 4 == 0 && aligned(out, 4 * es);
   const int64_t places = ids ? route->n_experts + 1 : 1;
-  const W4Plan p = plan_w4(route, n_rows, route->n_experts);
-  if (places * ((l.tiles + p.nt - 1) / p.nt) > 0x3fffffffll)
+  const bool f32 = route->dtype == MLORA_F32;
+  const W4Plan p = plan_w4(route, n_rows, route->n_experts, f32);
+  a.early = !ids || n_rows >= 2 * (int64_t)route->n_experts;
+  if (places * l.tiles > 0x3fffffffll)
     return fail(MLORA_ERR_INVALID, "%s: weights too large for one launch", who);
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (route->dtype == MLORA_BF16)
-    dispatch_w4<false>(a, p, (int)l.sg, places, s);
-  else
-    dispatch_w4<true>(a, p, (int)l.sg, places, s);
+  dispatch_w4(a, p, f32, (int)l.sg, places, reinterpret_cast<hipStream_t>(stream));
   return launch_status(who);
 }

@@ -168,26 +168,27 @@ struct W4Args {
   int32_t tiles, ksteps, blocks, per_block;  // per_block: chunks per scale block
   int32_t slices;         // workgroups per expert
   int32_t pairs, per_slice;  // streaming form: tile pairs, and those of a slice
-  int32_t early;          // request weights before the rows are known
   int32_t out_vec;        // rows of out start on 4 elements
 };
 
-// (w & mask) | base in one operation, mask in a scalar and base in a vector
-// register (the compiler takes two, with both as literals).
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t base) {
+// The bf16 pair 16, 16 in a vector register. With the base of unpack() there and
+// its mask a literal, and and or are one operation; as two literals they are two.
+// Taken once, at a kernel's start: the statement is opaque to the compiler, which
+// could not keep it clear of an MFMA's registers further down.
+__device__ __forceinline__ uint32_t base_pair() {
   uint32_t r;
-  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(base));
+  asm volatile("v_mov_b32 %0, 0x41804180" : "=v"(r));
   return r;
 }
 
 // 8 packed values of one column -> the bf16 values 16 + v.
-__device__ __forceinline__ u32x4 unpack(uint32_t w) {
-  constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;
+__device__ __forceinline__ u32x4 unpack(uint32_t w, uint32_t base) {
+  constexpr uint32_t kMask = 0x00780078u;
   u32x4 r;
-  r[0] = and_or(w, kMask, kBase);
-  r[1] = and_or(w >> 4, kMask, kBase);
-  r[2] = and_or(w >> 8, kMask, kBase);
-  r[3] = and_or(__builtin_amdgcn_alignbit(w, w, 12), kMask, kBase);
+  r[0] = (w & kMask) | base;
+  r[1] = ((w >> 4) & kMask) | base;
+  r[2] = ((w >> 8) & kMask) | base;
+  r[3] = (__builtin_amdgcn_alignbit(w, w, 12) & kMask) | base;
   return r;
 }
 
@@ -305,7 +306,7 @@ struct WChunk {
 // bf16 parts of k step ks of row block mb.
 template <bool F32, int SG, bool ZP, int NT, int MB, typename X>
 __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x,
-                                          f32x4 (&acc)[NT][MB]) {
+                                          uint32_t base, f32x4 (&acc)[NT][MB]) {
   constexpr int kPer = 4 / SG, kParts = XFrag<F32>::kParts;
   const uint32_t kc = ZP ? 0xbf80bf80u : 0xc1c0c1c0u;  // bf16 -1, or -(16 + 8)
   const u32x4 cons = {kc, kc, kc, kc};
@@ -330,7 +331,7 @@ __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x
       for (int mb = 0; mb < MB; ++mb) s[mb] = ZP ? f32x4{0.f, 0.f, 0.f, 0.f} : dc[mb];
 #pragma unroll
       for (int ks = 0; ks < kPer; ++ks) {
-        const u32x4 wf = unpack(wc.w[nt][sg * kPer + ks]);
+        const u32x4 wf = unpack(wc.w[nt][sg * kPer + ks], base);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -371,18 +372,38 @@ __device__ __forceinline__ void store4(typename Row::elem* o, f32x4 v, int left,
   }
 }
 
-// Lists in `list` the rows of rows [seg, seg + len) whose id is e (e == E: the
-// rows without an expert), in row order; returns how many. Each wave scans a
-// run of 64 * rounds ids and lists its hits behind those of the waves before
-// it, so that workgroups which share an expert's rows agree on the list.
-__device__ __forceinline__ int list_rows(const W4Args& a, int e, int seg, int len, int* list,
-                                         int* counts) {
+// Workgroup barrier that orders LDS only: requested weights stay in flight
+// across it (no kernel here passes global memory between its waves).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The rows of [seg, seg + len) of one workgroup: those whose id is e from the
+// front of `list`, and from its end the rows without an expert that fall to e
+// (by place, spread over the experts; the workgroup writes their zeros), each
+// in row order. Every wave scans a run of 64 * rounds ids and lists its hits
+// behind those of the waves before it, so that workgroups which share an
+// expert's rows agree on the list.
+struct RowList {
+  int live, dead;
+};
+
+__device__ __forceinline__ int lanes_before(uint64_t m) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                        __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+}
+
+__device__ __forceinline__ RowList list_rows(const W4Args& a, int e, int seg, int len, int* list,
+                                             int* counts) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
   const int rounds = (len + 64 * waves - 1) / (64 * waves);  // <= 32
   const int first = wave * rounds * 64 + lane;
-  uint32_t hits = 0;
-  int n_wave = 0;
+  const int shift = 32 - __builtin_clz((unsigned)len);       // len < 2^shift
+  uint32_t hits = 0, drops = 0;
+  int n_hits = 0, n_drops = 0;
   for (int r0 = 0; r0 < rounds; r0 += 8) {
     int id[8];
 #pragma unroll
@@ -392,45 +413,50 @@ __device__ __forceinline__ int list_rows(const W4Args& a, int e, int seg, int le
     }
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const bool in = r0 + r < rounds && first + (r0 + r) * 64 < len;
-      const bool hit = in && ((uint32_t)id[r] < (uint32_t)a.E ? id[r] : a.E) == e;
-      n_wave += __popcll(__ballot(hit));
+      const int i = first + (r0 + r) * 64;
+      const bool in = r0 + r < rounds && i < len;
+      const bool hit = in && id[r] == e;
+      const bool drop = in && (uint32_t)id[r] >= (uint32_t)a.E &&
+                        (int)(((uint32_t)i * (uint32_t)a.E) >> shift) == e;
+      n_hits += __popcll(__ballot(hit));
+      n_drops += __popcll(__ballot(drop));
       hits |= (hit ? 1u : 0u) << ((r0 + r) & 31);
+      drops |= (drop ? 1u : 0u) << ((r0 + r) & 31);
     }
   }
-  __syncthreads();  // the list's last readers are done
-  if (lane == 0) counts[wave] = n_wave;
-  __syncthreads();
-  int at = 0, n = 0;
+  lds_barrier();  // the list's last readers are done
+  if (lane == 0) counts[wave] = n_hits | n_drops << 16;
+  lds_barrier();
+  int at = 0, all = 0;
   for (int w = 0; w < waves; ++w) {
     at += w < wave ? counts[w] : 0;
-    n += counts[w];
+    all += counts[w];
   }
   at = uniform_i32(at);
-  if (n_wave > 0) {
+  all = uniform_i32(all);
+  int at_hit = at & 0xffff, at_drop = at >> 16;
+  if ((n_hits | n_drops) > 0) {
     for (int r = 0; r < rounds; ++r) {
-      const bool hit = (hits >> r) & 1;
-      const uint64_t m = __ballot(hit);
-      if (hit)
-        list[at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
-                                            __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u))] =
-            seg + first + r * 64;
-      at += __popcll(m);
+      const bool hit = (hits >> r) & 1, drop = (drops >> r) & 1;
+      const uint64_t mh = __ballot(hit), md = __ballot(drop);
+      if (hit) list[at_hit + lanes_before(mh)] = seg + first + r * 64;
+      if (drop) list[kScan - 1 - at_drop - lanes_before(md)] = seg + first + r * 64;
+      at_hit += __popcll(mh);
+      at_drop += __popcll(md);
     }
   }
-  __syncthreads();
-  return uniform_i32(n);
+  lds_barrier();
+  return RowList{all & 0xffff, all >> 16};
 }
 
-// Zeros into columns [n0, n0 + cols) of the listed rows.
+// Zeros into columns [n0, n0 + cols) of the rows listed from the end.
 template <typename Row>
-__device__ __forceinline__ void zero_listed(const W4Args& a, const int* list, int n_list, int n0,
-                                            int cols) {
+__device__ __forceinline__ void zero_rows(const W4Args& a, const int* list, int dead, int n0,
+                                          int cols) {
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
-  const int all = (int)(blockDim.x * gridDim.y);
-  for (int i = (int)threadIdx.x + (int)(blockIdx.y * blockDim.x); i < n_list * cols; i += all) {
-    const int n = n0 + i % cols;
-    if (n < a.N) out[(int64_t)list[i / cols] * a.out_ld + n] = 0;
+  for (int i = (int)threadIdx.x; i < dead * cols; i += (int)blockDim.x) {
+    const int r = i / cols, n = n0 + i - r * cols;
+    if (n < a.N) out[(int64_t)list[kScan - 1 - r] * a.out_ld + n] = 0;
   }
 }
 
@@ -443,6 +469,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
   __shared__ int list[kScan];
   __shared__ int counts[kMaxWaves];
   __shared__ float red[kMaxWaves * kRows * kStride];
+  const uint32_t base = base_pair();
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
   const int e = (int)blockIdx.x / a.tiles, tile = (int)blockIdx.x - e * a.tiles;
@@ -450,22 +477,16 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
   WBufs wb;
-  wb.set<SG, (F32 ? 4 : 2), ZP>(a, (a.E > 0 ? min(e, a.E - 1) : 0) * a.tiles + tile, 1);
+  wb.set<SG, (F32 ? 4 : 2), ZP>(a, e * a.tiles + tile, 1);
   WChunk<F32, SG, ZP, 1> wc;
-  // the first chunk's weights are requested before the rows are known where
-  // most experts hold some
-  const bool early = a.early && (a.E == 0 || e < a.E);
-  if (early) wc.load(a, wb, wave, lane);
 
   for (int seg = 0; seg < a.n_rows; seg += kScan) {
     const int len = min(kScan, a.n_rows - seg);
     int n_list = len;
     if (a.E > 0) {
-      n_list = list_rows(a, e, seg, len, list, counts);
-      if (e == a.E) {
-        zero_listed<Row>(a, list, n_list, n0, 16);
-        continue;
-      }
+      const RowList l = list_rows(a, e, seg, len, list, counts);
+      n_list = l.live;
+      if (l.dead > 0 && blockIdx.y == 0) zero_rows<Row>(a, list, l.dead, n0, 16);
     }
     for (int b0 = (int)blockIdx.y * kRows; b0 < n_list; b0 += (int)gridDim.y * kRows) {
       uint32_t row_off[MB];
@@ -483,16 +504,15 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             x[mb][ks] = load_x<F32>(rx, row_off[mb], c * 128 + ks * 32 + lg * 8, a.K);
-        if (!early || c != wave || seg > 0 || b0 != (int)blockIdx.y * kRows)
-          wc.load(a, wb, c, lane);
+        wc.load(a, wb, c, lane);
         add_chunk<F32, SG, ZP, 1, MB>(
-            wc, [&](int mb, int ks, XFrag<F32>& f) { f.set(x[mb][ks]); }, acc);
+            wc, [&](int mb, int ks, XFrag<F32>& f) { f.set(x[mb][ks]); }, base, acc);
       }
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
         *reinterpret_cast<f32x4*>(&red[(wave * kRows + mb * 16 + li) * kStride + lg * 4]) =
             acc[0][mb];
-      __syncthreads();
+      lds_barrier();
       for (int i = tid; i < kRows * 4; i += (int)blockDim.x) {
         const int r = i >> 2, c4 = (i & 3) * 4;
         f32x4 sum = *reinterpret_cast<const f32x4*>(&red[r * kStride + c4]);
@@ -502,7 +522,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
         const int64_t row = a.E > 0 ? list[b0 + r] : seg + b0 + r;
         store4<Row>(out + row * a.out_ld + n0 + c4, sum, a.N - n0 - c4, a.out_vec != 0);
       }
-      __syncthreads();
+      lds_barrier();
     }
   }
 }
@@ -531,23 +551,21 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Arg
   __shared__ int list[kScan];
   __shared__ int counts[stream_waves(F32)];
   extern __shared__ u32x4 xs[];  // [k step][row block][part][lane]
+  const uint32_t base = base_pair();
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
   const int e = (int)blockIdx.x / a.slices, slice = (int)blockIdx.x - e * a.slices;
   const int chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
-  // this wave's pairs: every waves-th of the slice's; none in the place after
-  // the last expert
-  const bool none = a.E > 0 && e == a.E;
+  // this wave's pairs: every waves-th of the slice's
   const int pair0 = slice * a.per_slice + wave;
   const int n_pairs = uniform_i32(
-      none ? 0 : max(0, (min((slice + 1) * a.per_slice, a.pairs) - pair0 + waves - 1) / waves));
+      max(0, (min((slice + 1) * a.per_slice, a.pairs) - pair0 + waves - 1) / waves));
   const int et0 = e * a.tiles;
   // A pair takes whole turns of the ring: places past its chunks stay empty.
   const int turns = (chunks + kAhead - 1) / kAhead * kAhead;
-  Chunk ring[kAhead];
-  int lp = 0, lc = 0;  // pair and chunk of the next request
+  int lp, lc;  // pair and chunk of the next request
   auto request = [&](Chunk& w) {
     const int t0 = (pair0 + lp * waves) * kPair;
     const bool in = lp < n_pairs && lc < chunks;
@@ -557,26 +575,18 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Arg
     lc = lc + 1 == turns ? 0 : lc + 1;
     lp += lc == 0;
   };
-  // The ring's first requests for a block of rows; nothing where none follows.
-  auto restart = [&](bool more) {
-    lp = more ? 0 : n_pairs;
-    lc = 0;
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) request(ring[d]);
-  };
 
-  // The first weights are requested before the rows are known where most
-  // experts hold some (a.early), else behind the scan.
-  int seg = 0, n_list = min(kScan, a.n_rows);
-  if (a.E > 0 && !a.early) n_list = list_rows(a, e, 0, n_list, list, counts);
-  restart(n_list > 0 || kScan < a.n_rows);
-  if (a.E > 0 && a.early) n_list = list_rows(a, e, 0, n_list, list, counts);
-  for (;;) {
-    if (none)
-      zero_listed<Row>(a, list, n_list, slice * a.per_slice * kPair * 16,
+  for (int seg = 0; seg < a.n_rows; seg += kScan) {
+    int n_list = min(kScan, a.n_rows - seg);
+    if (a.E > 0) {
+      const RowList l = list_rows(a, e, seg, n_list, list, counts);
+      n_list = l.live;
+      if (l.dead > 0 && blockIdx.y == 0)
+        zero_rows<Row>(a, list, l.dead, slice * a.per_slice * kPair * 16,
                        a.per_slice * kPair * 16);
+    }
     const int step = (int)gridDim.y * kRows;
-    for (int b0 = (int)blockIdx.y * kRows; b0 < n_list && !none; b0 += step) {
+    for (int b0 = (int)blockIdx.y * kRows; b0 < n_list; b0 += step) {
       uint32_t row_off[MB];
       int orow[MB];
 #pragma unroll
@@ -585,33 +595,52 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Arg
         orow[mb] = at < n_list ? (a.E > 0 ? list[at] : seg + at) : -1;
         row_off[mb] = orow[mb] >= 0 ? (uint32_t)orow[mb] / a.topk * a.x_ld_bytes : kPast;
       }
-      f32x4 acc[kPair][MB];
-      for (int p0 = 0; p0 < chunks; p0 += kPanel) {
-        const int p1 = min(p0 + kPanel, chunks);
-        __syncthreads();
-        const int frags = (p1 - p0) * 4 * MB;
-        constexpr int kBatch = F32 ? 4 : 6;  // loads in flight per wave
-        for (int f0 = wave; f0 < frags; f0 += kBatch * waves) {
-          XRaw<F32> r[kBatch];
+      // x into LDS, k step by k step and row block by row block, the waves in
+      // turn. A wave's first loads are requested ahead of its first weights:
+      // loads return in order, and the weights come from HBM.
+      constexpr int kBatch = F32 ? 4 : 4 * MB;
+      auto load_batch = [&](XRaw<F32>(&r)[kBatch], int p0, int f0, int frags) {
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int f = f0 + i * waves;
-            const int mb = f % MB, k = p0 * 128 + f / MB * 32 + lg * 8;
-            r[i] = load_x<F32>(rx, MB == 2 && mb ? row_off[MB - 1] : row_off[0],
-                               f < frags ? k : a.K, a.K);
-          }
+        for (int i = 0; i < kBatch; ++i) {
+          const int f = f0 + i * waves;
+          const int k = f < frags ? p0 * 128 + f / MB * 32 + lg * 8 : a.K;
+          r[i] = load_x<F32>(rx, MB == 2 && f % MB ? row_off[MB - 1] : row_off[0], k, a.K);
+        }
+      };
+      auto store_batch = [&](const XRaw<F32>(&r)[kBatch], int f0, int frags) {
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int f = f0 + i * waves;
-            if (f < frags) {
-              XFrag<F32> q;
-              q.set(r[i]);
+        for (int i = 0; i < kBatch; ++i) {
+          const int f = f0 + i * waves;
+          if (f < frags) {
+            XFrag<F32> q;
+            q.set(r[i]);
 #pragma unroll
-              for (int p = 0; p < kParts; ++p) xs[(f * kParts + p) * 64 + lane] = q.p[p];
-            }
+            for (int p = 0; p < kParts; ++p) xs[(f * kParts + p) * 64 + lane] = q.p[p];
           }
         }
-        __syncthreads();
+      };
+      f32x4 acc[kPair][MB];
+      Chunk ring[kAhead];
+      {
+        const int frags = min(kPanel, chunks) * 4 * MB;
+        XRaw<F32> r[kBatch];
+        load_batch(r, 0, wave, frags);
+        lp = lc = 0;
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) request(ring[d]);
+        lds_barrier();  // the last block's readers are done
+        store_batch(r, wave, frags);
+      }
+      for (int p0 = 0; p0 < chunks; p0 += kPanel) {
+        const int p1 = min(p0 + kPanel, chunks);
+        const int frags = (p1 - p0) * 4 * MB;
+        if (p0 > 0) lds_barrier();
+        for (int f0 = wave + (p0 > 0 ? 0 : kBatch * waves); f0 < frags; f0 += kBatch * waves) {
+          XRaw<F32> r[kBatch];
+          load_batch(r, p0, f0, frags);
+          store_batch(r, f0, frags);
+        }
+        lds_barrier();
         // one panel: every pair; several: the wave's one pair's share of them
         for (int pair = 0; pair < n_pairs; ++pair) {
           if (p0 == 0) {
@@ -632,7 +661,7 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Arg
                       for (int p = 0; p < kParts; ++p)
                         f.p[p] = px[((ks * MB + mb) * kParts + p) * 64];
                     },
-                    acc);
+                    base, acc);
               }
               request(ring[d]);
             }
@@ -649,12 +678,7 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Arg
           }
         }
       }
-      restart(b0 + step < n_list || seg + kScan < a.n_rows);
     }
-    seg += kScan;
-    if (seg >= a.n_rows) break;
-    n_list = min(kScan, a.n_rows - seg);
-    if (a.E > 0) n_list = list_rows(a, e, seg, n_list, list, counts);
   }
 }
 
@@ -877,10 +901,9 @@ extern "C" int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void*
   a.blocks = (int32_t)l.blocks;
   a.per_block = route->group <= 128 ? 1 : route->group / 128;
   a.out_vec = out_ld % 4 == 0 && aligned(out, 4 * es);
-  const int64_t places = ids ? route->n_experts + 1 : 1;
+  const int64_t places = route->n_experts;
   const bool f32 = route->dtype == MLORA_F32;
   const W4Plan p = plan_w4(route, n_rows, route->n_experts, f32);
-  a.early = !ids || n_rows >= 2 * (int64_t)route->n_experts;
   if (places * l.tiles > 0x3fffffffll)
     return fail(MLORA_ERR_INVALID, "%s: weights too large for one launch", who);
   (void)hipGetLastError();

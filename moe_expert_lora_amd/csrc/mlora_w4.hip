@@ -157,13 +157,10 @@ struct W4Args {
   const uint8_t* z;
   const void* x;
   void* out;
-  const int32_t* ids;
   int64_t out_ld;
   uint32_t x_bytes;
   uint32_t x_ld_bytes;
   uint32_t topk;          // rows per x row (1: a row of its own)
-  int32_t n_rows;
-  int32_t E;              // 0: no ids, one weight
   int32_t K, N;
   int32_t tiles, ksteps, blocks, per_block;  // per_block: chunks per scale block
   int32_t slices;         // workgroups per expert
@@ -260,6 +257,7 @@ template <bool F32, int SG, bool ZP, int NT>
 struct WChunk {
   static constexpr int kEs = F32 ? 4 : 2;
   static constexpr int kWords = SG * kEs;  // 4 scales per group: 2 or 4 words
+  static constexpr int kLoads = NT * (1 + (kWords + 3) / 4 + (ZP ? 1 : 0));
   u32x4 w[NT];
   uint32_t s[NT][kWords];
   uint32_t z[NT][ZP ? SG : 1];
@@ -372,6 +370,22 @@ __device__ __forceinline__ void store4(typename Row::elem* o, f32x4 v, int left,
   }
 }
 
+// 16 bytes of each lane straight into LDS, lane l's at p + l.
+__device__ __forceinline__ void load_to_lds(rsrc_t r, u32x4* p, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      r, (__attribute__((address_space(3))) void*)p, 16, off, 0, 0, 0);
+}
+// Waits until at most N of the wave's loads are outstanding (the last requested
+// ones: loads return in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "the counter has 6 bits");
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  // vmcnt in bits 3:0 and 15:14; expcnt and lgkmcnt left at their maxima
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0f70);
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Workgroup barrier that orders LDS only: requested weights stay in flight
 // across it (no kernel here passes global memory between its waves).
 __device__ __forceinline__ void lds_barrier() {
@@ -395,8 +409,8 @@ __device__ __forceinline__ int lanes_before(uint64_t m) {
                                         __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
 }
 
-__device__ __forceinline__ RowList list_rows(const W4Args& a, int e, int seg, int len, int* list,
-                                             int* counts) {
+__device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, int seg, int len,
+                                             int* list, int* counts) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
   const int rounds = (len + 64 * waves - 1) / (64 * waves);  // <= 32
@@ -404,20 +418,19 @@ __device__ __forceinline__ RowList list_rows(const W4Args& a, int e, int seg, in
   const int shift = 32 - __builtin_clz((unsigned)len);       // len < 2^shift
   uint32_t hits = 0, drops = 0;
   int n_hits = 0, n_drops = 0;
-  for (int r0 = 0; r0 < rounds; r0 += 8) {
-    int id[8];
+  const rsrc_t ri = buf(ids + seg, (uint32_t)len * 4u);  // past the end: 0
+  for (int r0 = 0; r0 < rounds; r0 += 4) {
+    int id[4];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int i = first + (r0 + r) * 64;
-      id[r] = r0 + r < rounds && i < len ? a.ids[seg + i] : -1;
-    }
+    for (int r = 0; r < 4; ++r)
+      id[r] = (int)__builtin_amdgcn_raw_buffer_load_b32(ri, (first + (r0 + r) * 64) * 4, 0, 0);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int r = 0; r < 4; ++r) {
       const int i = first + (r0 + r) * 64;
       const bool in = r0 + r < rounds && i < len;
       const bool hit = in && id[r] == e;
-      const bool drop = in && (uint32_t)id[r] >= (uint32_t)a.E &&
-                        (int)(((uint32_t)i * (uint32_t)a.E) >> shift) == e;
+      const bool drop = in && (uint32_t)id[r] >= (uint32_t)E &&
+                        (int)(((uint32_t)i * (uint32_t)E) >> shift) == e;
       n_hits += __popcll(__ballot(hit));
       n_drops += __popcll(__ballot(drop));
       hits |= (hit ? 1u : 0u) << ((r0 + r) & 31);
@@ -449,21 +462,25 @@ __device__ __forceinline__ RowList list_rows(const W4Args& a, int e, int seg, in
   return RowList{all & 0xffff, all >> 16};
 }
 
-// Zeros into columns [n0, n0 + cols) of the rows listed from the end.
+// Zeros into columns [n0, n0 + cols) of the rows listed from the end, a wave per
+// row.
 template <typename Row>
 __device__ __forceinline__ void zero_rows(const W4Args& a, const int* list, int dead, int n0,
                                           int cols) {
-  typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
-  for (int i = (int)threadIdx.x; i < dead * cols; i += (int)blockDim.x) {
-    const int r = i / cols, n = n0 + i - r * cols;
-    if (n < a.N) out[(int64_t)list[kScan - 1 - r] * a.out_ld + n] = 0;
+  const int lane = threadIdx.x & 63, wave = uniform_i32((int)threadIdx.x >> 6);
+  const int n1 = min(n0 + cols, a.N);
+  for (int r = wave; r < dead; r += (int)(blockDim.x >> 6)) {
+    typename Row::elem* o = static_cast<typename Row::elem*>(a.out) +
+                            (int64_t)uniform_i32(list[kScan - 1 - r]) * a.out_ld;
+    for (int n = n0 + lane * 4; n < n1; n += 256)
+      store4<Row>(o + n, f32x4{0.f, 0.f, 0.f, 0.f}, n1 - n, a.out_vec != 0);
   }
 }
 
 // Few column tiles: a workgroup owns one tile, its waves split k and add their
 // sums up through LDS in wave order; x goes straight to the operands.
 template <bool F32, int SG, bool ZP, int MB>
-__global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
+__global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t* ids, int n_rows, int E, W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
   constexpr int kStride = 20, kRows = 16 * MB;
   __shared__ int list[kScan];
@@ -472,7 +489,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
   const uint32_t base = base_pair();
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int e = (int)blockIdx.x / a.tiles, tile = (int)blockIdx.x - e * a.tiles;
+  const int e = (int)blockIdx.y, tile = (int)blockIdx.x;
   const int n0 = tile * 16, chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
@@ -480,20 +497,20 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
   wb.set<SG, (F32 ? 4 : 2), ZP>(a, e * a.tiles + tile, 1);
   WChunk<F32, SG, ZP, 1> wc;
 
-  for (int seg = 0; seg < a.n_rows; seg += kScan) {
-    const int len = min(kScan, a.n_rows - seg);
+  for (int seg = 0; seg < n_rows; seg += kScan) {
+    const int len = min(kScan, n_rows - seg);
     int n_list = len;
-    if (a.E > 0) {
-      const RowList l = list_rows(a, e, seg, len, list, counts);
+    if (E > 0) {
+      const RowList l = list_rows(ids, E, e, seg, len, list, counts);
       n_list = l.live;
-      if (l.dead > 0 && blockIdx.y == 0) zero_rows<Row>(a, list, l.dead, n0, 16);
+      if (l.dead > 0 && blockIdx.z == 0) zero_rows<Row>(a, list, l.dead, n0, 16);
     }
-    for (int b0 = (int)blockIdx.y * kRows; b0 < n_list; b0 += (int)gridDim.y * kRows) {
+    for (int b0 = (int)blockIdx.z * kRows; b0 < n_list; b0 += (int)gridDim.z * kRows) {
       uint32_t row_off[MB];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         const int at = b0 + mb * 16 + li;
-        const int row = at < n_list ? (a.E > 0 ? list[at] : seg + at) : -1;
+        const int row = at < n_list ? (E > 0 ? list[at] : seg + at) : -1;
         row_off[mb] = row >= 0 ? (uint32_t)row / a.topk * a.x_ld_bytes : kPast;
       }
       f32x4 acc[1][MB] = {};
@@ -519,7 +536,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(W4Args a) {
         for (int w = 1; w < waves; ++w)
           sum += *reinterpret_cast<const f32x4*>(&red[(w * kRows + r) * kStride + c4]);
         if (b0 + r >= n_list) continue;
-        const int64_t row = a.E > 0 ? list[b0 + r] : seg + b0 + r;
+        const int64_t row = E > 0 ? list[b0 + r] : seg + b0 + r;
         store4<Row>(out + row * a.out_ld + n0 + c4, sum, a.N - n0 - c4, a.out_vec != 0);
       }
       lds_barrier();
@@ -543,7 +560,7 @@ constexpr int panel_chunks(bool f32, int mb) {
 constexpr int stream_waves(bool f32) { return f32 ? 8 : 12; }  // most per workgroup
 
 template <bool F32, int SG, bool ZP, int MB>
-__global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Args a) {
+__global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const int32_t* ids, int n_rows, int E, W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
   typedef WChunk<F32, SG, ZP, kPair> Chunk;
   constexpr int kRows = 16 * MB, kParts = XFrag<F32>::kParts;
@@ -554,7 +571,7 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Arg
   const uint32_t base = base_pair();
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int e = (int)blockIdx.x / a.slices, slice = (int)blockIdx.x - e * a.slices;
+  const int e = (int)blockIdx.y, slice = (int)blockIdx.x;
   const int chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
@@ -572,74 +589,96 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Arg
     WBufs wb;
     wb.set<SG, (F32 ? 4 : 2), ZP>(a, in ? et0 + t0 : 0, in ? min(kPair, a.tiles - t0) : 0);
     w.load(a, wb, lc, lane);
+    // requests stay in order, so that a wait for one leaves the later ones out
+    __builtin_amdgcn_sched_barrier(0);
     lc = lc + 1 == turns ? 0 : lc + 1;
     lp += lc == 0;
   };
 
-  for (int seg = 0; seg < a.n_rows; seg += kScan) {
-    int n_list = min(kScan, a.n_rows - seg);
-    if (a.E > 0) {
-      const RowList l = list_rows(a, e, seg, n_list, list, counts);
+  for (int seg = 0; seg < n_rows; seg += kScan) {
+    int n_list = min(kScan, n_rows - seg);
+    if (E > 0) {
+      const RowList l = list_rows(ids, E, e, seg, n_list, list, counts);
       n_list = l.live;
-      if (l.dead > 0 && blockIdx.y == 0)
+      if (l.dead > 0 && blockIdx.z == 0)
         zero_rows<Row>(a, list, l.dead, slice * a.per_slice * kPair * 16,
                        a.per_slice * kPair * 16);
     }
-    const int step = (int)gridDim.y * kRows;
-    for (int b0 = (int)blockIdx.y * kRows; b0 < n_list; b0 += step) {
+    const int step = (int)gridDim.z * kRows;
+    for (int b0 = (int)blockIdx.z * kRows; b0 < n_list; b0 += step) {
       uint32_t row_off[MB];
       int orow[MB];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         const int at = b0 + mb * 16 + li;
-        orow[mb] = at < n_list ? (a.E > 0 ? list[at] : seg + at) : -1;
+        orow[mb] = at < n_list ? (E > 0 ? list[at] : seg + at) : -1;
         row_off[mb] = orow[mb] >= 0 ? (uint32_t)orow[mb] / a.topk * a.x_ld_bytes : kPast;
       }
       // x into LDS, k step by k step and row block by row block, the waves in
-      // turn. A wave's first loads are requested ahead of its first weights:
-      // loads return in order, and the weights come from HBM.
-      constexpr int kBatch = F32 ? 4 : 4 * MB;
-      auto load_batch = [&](XRaw<F32>(&r)[kBatch], int p0, int f0, int frags) {
+      // turn. bf16 operands go there directly, all in flight; fp32 rows pass
+      // through registers on their way into parts.
+      auto stage = [&](int p0, int frags) {
+        if constexpr (!F32) {
+          for (int f = wave; f < frags; f += waves) {
+            const int k = p0 * 128 + f / MB * 32 + lg * 8;
+            const uint32_t row = MB == 2 && f % MB ? row_off[MB - 1] : row_off[0];
+            load_to_lds(rx, xs + f * 64, row != kPast && k < a.K ? row + k * 2u : kPast);
+          }
+        } else {
+          constexpr int kBatch = 4;
+          for (int f0 = wave; f0 < frags; f0 += kBatch * waves) {
+            XRaw<F32> r[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int f = f0 + i * waves;
-          const int k = f < frags ? p0 * 128 + f / MB * 32 + lg * 8 : a.K;
-          r[i] = load_x<F32>(rx, MB == 2 && f % MB ? row_off[MB - 1] : row_off[0], k, a.K);
+            for (int i = 0; i < kBatch; ++i) {
+              const int f = f0 + i * waves;
+              r[i] = load_x<F32>(rx, row_off[0], f < frags ? p0 * 128 + f * 32 + lg * 8 : a.K, a.K);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int f = f0 + i * waves;
+              if (f < frags) {
+                XFrag<F32> q;
+                q.set(r[i]);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) xs[(f * kParts + p) * 64 + lane] = q.p[p];
+              }
+            }
+          }
         }
       };
-      auto store_batch = [&](const XRaw<F32>(&r)[kBatch], int f0, int frags) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int f = f0 + i * waves;
-          if (f < frags) {
-            XFrag<F32> q;
-            q.set(r[i]);
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) xs[(f * kParts + p) * 64 + lane] = q.p[p];
+      // The operands of a last k step past K hold zeros whatever a load past a
+      // buffer's end leaves in LDS.
+      auto stage_end = [&](int p0, int p1, int frags) {
+        if constexpr (!F32) {
+          if (p1 * 128 > a.K) {
+            for (int f = wave; f < frags; f += waves)
+              if (p0 * 128 + f / MB * 32 + lg * 8 >= a.K) xs[f * 64 + lane] = u32x4{0, 0, 0, 0};
           }
         }
       };
       f32x4 acc[kPair][MB];
       Chunk ring[kAhead];
-      {
-        const int frags = min(kPanel, chunks) * 4 * MB;
-        XRaw<F32> r[kBatch];
-        load_batch(r, 0, wave, frags);
-        lp = lc = 0;
+      // x is requested ahead of the first weights: loads return in order, and the
+      // weights come from HBM
+      lds_barrier();  // the last block's readers are done
+      stage(0, min(kPanel, chunks) * 4 * MB);
+      lp = lc = 0;
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) request(ring[d]);
-        lds_barrier();  // the last block's readers are done
-        store_batch(r, wave, frags);
-      }
+      for (int d = 0; d < kAhead; ++d) request(ring[d]);
       for (int p0 = 0; p0 < chunks; p0 += kPanel) {
         const int p1 = min(p0 + kPanel, chunks);
         const int frags = (p1 - p0) * 4 * MB;
-        if (p0 > 0) lds_barrier();
-        for (int f0 = wave + (p0 > 0 ? 0 : kBatch * waves); f0 < frags; f0 += kBatch * waves) {
-          XRaw<F32> r[kBatch];
-          load_batch(r, p0, f0, frags);
-          store_batch(r, f0, frags);
+        if (p0 > 0) {
+          lds_barrier();
+          stage(p0, frags);
         }
+        if constexpr (!F32) {
+          if (p0 > 0)
+            wait_loads<0>();
+          else
+            wait_loads<Chunk::kLoads * kAhead>();
+        }
+        stage_end(p0, p1, frags);
         lds_barrier();
         // one panel: every pair; several: the wave's one pair's share of them
         for (int pair = 0; pair < n_pairs; ++pair) {
@@ -681,6 +720,13 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(W4Arg
     }
   }
 }
+
+// The rows of a call. They lead a kernel's arguments as plain values, which
+// arrive in registers, so that the scan does not wait for the others.
+struct W4Rows {
+  const int32_t* ids;  // null: one weight
+  int32_t n, experts;
+};
 
 struct W4Plan {
   bool stream;
@@ -726,38 +772,40 @@ W4Plan plan_w4(const mlora_w4_route* r, int64_t n_rows, int64_t experts, bool f3
 }
 
 template <bool F32, int SG, bool ZP, int MB>
-void launch_w4(const W4Args& a0, const W4Plan& p, int64_t places, hipStream_t s) {
+void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
   W4Args a = a0;
+  const int32_t* ids = rows.ids;
+  const int n_rows = rows.n, E = rows.ids ? rows.experts : 0;
   a.slices = p.slices;
   a.per_slice = p.per_slice;
   a.pairs = (a.tiles + kPair - 1) / kPair;
-  const dim3 grid((unsigned)(places * a.slices), (unsigned)p.splits), block(64 * p.waves);
+  const dim3 grid((unsigned)a.slices, (unsigned)rows.experts, (unsigned)p.splits), block(64 * p.waves);
   if (!p.stream) {
-    hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB>), grid, block, 0, s, ids, n_rows, E, a);
     return;
   }
   const int chunks = (a.ksteps + 3) / 4, most = panel_chunks(F32, MB);
   const size_t lds = (size_t)(chunks < most ? chunks : most) * chunk_lds(F32, MB);
-  hipLaunchKernelGGL((w4_stream_kernel<F32, SG, ZP, MB>), grid, block, lds, s, a);
+  hipLaunchKernelGGL((w4_stream_kernel<F32, SG, ZP, MB>), grid, block, lds, s, ids, n_rows, E, a);
 }
 
 template <int SG, bool ZP>
-void dispatch_w4_sg(const W4Args& a, const W4Plan& p, bool f32, int64_t places, hipStream_t s) {
-  if (f32) return launch_w4<true, SG, ZP, 1>(a, p, places, s);
-  if (p.mb == 2) return launch_w4<false, SG, ZP, 2>(a, p, places, s);
-  launch_w4<false, SG, ZP, 1>(a, p, places, s);
+void dispatch_w4_sg(const W4Args& a, const W4Plan& p, bool f32, W4Rows rows, hipStream_t s) {
+  if (f32) return launch_w4<true, SG, ZP, 1>(a, p, rows, s);
+  if (p.mb == 2) return launch_w4<false, SG, ZP, 2>(a, p, rows, s);
+  launch_w4<false, SG, ZP, 1>(a, p, rows, s);
 }
 
-void dispatch_w4(const W4Args& a, const W4Plan& p, bool f32, int sg, int64_t places,
+void dispatch_w4(const W4Args& a, const W4Plan& p, bool f32, int sg, W4Rows rows,
                  hipStream_t s) {
   if (a.z) {
-    if (sg == 4) return dispatch_w4_sg<4, true>(a, p, f32, places, s);
-    if (sg == 2) return dispatch_w4_sg<2, true>(a, p, f32, places, s);
-    return dispatch_w4_sg<1, true>(a, p, f32, places, s);
+    if (sg == 4) return dispatch_w4_sg<4, true>(a, p, f32, rows, s);
+    if (sg == 2) return dispatch_w4_sg<2, true>(a, p, f32, rows, s);
+    return dispatch_w4_sg<1, true>(a, p, f32, rows, s);
   }
-  if (sg == 4) return dispatch_w4_sg<4, false>(a, p, f32, places, s);
-  if (sg == 2) return dispatch_w4_sg<2, false>(a, p, f32, places, s);
-  dispatch_w4_sg<1, false>(a, p, f32, places, s);
+  if (sg == 4) return dispatch_w4_sg<4, false>(a, p, f32, rows, s);
+  if (sg == 2) return dispatch_w4_sg<2, false>(a, p, f32, rows, s);
+  dispatch_w4_sg<1, false>(a, p, f32, rows, s);
 }
 
 int32_t check_w4(const char* who, int32_t E, int32_t K, int32_t N, int32_t group,
@@ -887,13 +935,10 @@ extern "C" int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void*
   a.z = static_cast<const uint8_t*>(route->zeros);
   a.x = x;
   a.out = out;
-  a.ids = ids;
   a.out_ld = out_ld;
   a.x_bytes = (uint32_t)(((need - 1) * x_ld + route->k_in) * es);
   a.x_ld_bytes = (uint32_t)(x_ld * es);
   a.topk = x_by_row ? 1u : (uint32_t)top_k;
-  a.n_rows = (int32_t)n_rows;
-  a.E = ids ? route->n_experts : 0;
   a.K = route->k_in;
   a.N = route->n_out;
   a.tiles = (int32_t)l.tiles;
@@ -901,12 +946,10 @@ extern "C" int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void*
   a.blocks = (int32_t)l.blocks;
   a.per_block = route->group <= 128 ? 1 : route->group / 128;
   a.out_vec = out_ld % 4 == 0 && aligned(out, 4 * es);
-  const int64_t places = route->n_experts;
   const bool f32 = route->dtype == MLORA_F32;
   const W4Plan p = plan_w4(route, n_rows, route->n_experts, f32);
-  if (places * l.tiles > 0x3fffffffll)
-    return fail(MLORA_ERR_INVALID, "%s: weights too large for one launch", who);
   (void)hipGetLastError();
-  dispatch_w4(a, p, f32, (int)l.sg, places, reinterpret_cast<hipStream_t>(stream));
+  const W4Rows rows = {ids, (int32_t)n_rows, route->n_experts};
+  dispatch_w4(a, p, f32, (int)l.sg, rows, reinterpret_cast<hipStream_t>(stream));
   return launch_status(who);
 }

@@ -117,6 +117,45 @@ def test_expert_rows(ml, dtype, x_by_row, rows, experts, top_k, k, n, group, zer
             f"{rows}/{experts}")
 
 
+# rows, experts, top_k, k, n, group, zeros: enough column tiles for the form
+# that streams them, with one and two row blocks per pass, k in one panel of
+# LDS and in several, short last chunks, odd widths, rows past one scan
+STREAMED = [(640, 128, 8, 264, 260, 64, True), (640, 128, 8, 136, 289, 128, False),
+            (1600, 100, 4, 72, 340, 32, True), (2600, 128, 1, 320, 257, 32, False),
+            (4500, 90, 2, 1000, 400, 256, True), (300, 20, 1, 2600, 1700, 128, True),
+            (34, 1, 1, 200, 33001, 64, False), (700, 8, 1, 96, 4100, 128, True)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("x_by_row", [False, True])
+@pytest.mark.parametrize("rows,experts,top_k,k,n,group,zeros", STREAMED)
+def test_streamed_expert_rows(ml, dtype, x_by_row, rows, experts, top_k, k, n, group, zeros):
+    w = Weights(ml, experts, k, n, group, zeros, dtype, rows)
+    rng = np.random.default_rng(rows)
+    ids = None
+    if experts > 1:
+        ids = rng.integers(0, experts, size=rows).astype(np.int32)
+        ids[rng.random(rows) < 0.1] = -1
+        ids[rng.random(rows) < 0.03] = experts
+        ids[rows // 2:rows // 2 + 40] = 1       # one expert with more rows than a pass
+    x = _x((rows if x_by_row else -(-rows // top_k), k), dtype, 2)
+    w.check(_run(ml, w, x, rows, ids, top_k, x_by_row), x, ids, top_k, x_by_row,
+            f"{rows}/{experts}")
+
+
+def test_streamed_non_finite_rows_stay_alone(ml):
+    w = Weights(ml, 64, 200, 520, 64, True, "bf16", 17)
+    x = _x((300, 200), "bf16", 5)
+    ids = (np.arange(300) % 64).astype(np.int32)
+    clean = _run(ml, w, x, 300, ids, 1, False)
+    x[4, 10] = float("inf")
+    x[9, 199] = float("nan")
+    got = _run(ml, w, x, 300, ids, 1, False)
+    keep = [r for r in range(300) if r not in (4, 9)]
+    assert torch.equal(got[keep], clean[keep])
+    assert not torch.isfinite(got[4]).any() and torch.isnan(got[9]).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_one_sided_routing(ml, dtype):
     w = Weights(ml, 9, 264, 50, 64, True, dtype, 5)

@@ -614,29 +614,31 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
         orow[mb] = at < n_list ? (E > 0 ? list[at] : seg + at) : -1;
         row_off[mb] = orow[mb] >= 0 ? (uint32_t)orow[mb] / a.topk * a.x_ld_bytes : kPast;
       }
-      // x into LDS, k step by k step and row block by row block, the waves in
-      // turn. bf16 operands go there directly, all in flight; fp32 rows pass
-      // through registers on their way into parts.
-      auto stage = [&](int p0, int frags) {
+      // x into LDS, k step by k step, the waves in turn. bf16 operands go there
+      // directly, all in flight; fp32 rows pass through registers on their way
+      // into parts.
+      auto stage = [&](int p0, int steps) {
         if constexpr (!F32) {
-          for (int f = wave; f < frags; f += waves) {
-            const int k = p0 * 128 + f / MB * 32 + lg * 8;
-            const uint32_t row = MB == 2 && f % MB ? row_off[MB - 1] : row_off[0];
-            load_to_lds(rx, xs + f * 64, row != kPast && k < a.K ? row + k * 2u : kPast);
+          for (int f = wave; f < steps; f += waves) {
+            const int k = p0 * 128 + f * 32 + lg * 8;
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+              load_to_lds(rx, xs + (f * MB + mb) * 64,
+                          row_off[mb] != kPast && k < a.K ? row_off[mb] + k * 2u : kPast);
           }
         } else {
           constexpr int kBatch = 4;
-          for (int f0 = wave; f0 < frags; f0 += kBatch * waves) {
+          for (int f0 = wave; f0 < steps; f0 += kBatch * waves) {
             XRaw<F32> r[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
               const int f = f0 + i * waves;
-              r[i] = load_x<F32>(rx, row_off[0], f < frags ? p0 * 128 + f * 32 + lg * 8 : a.K, a.K);
+              r[i] = load_x<F32>(rx, row_off[0], f < steps ? p0 * 128 + f * 32 + lg * 8 : a.K, a.K);
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
               const int f = f0 + i * waves;
-              if (f < frags) {
+              if (f < steps) {
                 XFrag<F32> q;
                 q.set(r[i]);
 #pragma unroll
@@ -648,11 +650,14 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
       };
       // The operands of a last k step past K hold zeros whatever a load past a
       // buffer's end leaves in LDS.
-      auto stage_end = [&](int p0, int p1, int frags) {
+      auto stage_end = [&](int p0, int p1) {
         if constexpr (!F32) {
           if (p1 * 128 > a.K) {
-            for (int f = wave; f < frags; f += waves)
-              if (p0 * 128 + f / MB * 32 + lg * 8 >= a.K) xs[f * 64 + lane] = u32x4{0, 0, 0, 0};
+            for (int f = wave; f < (p1 - p0) * 4; f += waves) {
+              if (p0 * 128 + f * 32 + lg * 8 < a.K) continue;
+#pragma unroll
+              for (int mb = 0; mb < MB; ++mb) xs[(f * MB + mb) * 64 + lane] = u32x4{0, 0, 0, 0};
+            }
           }
         }
       };
@@ -661,16 +666,15 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
       // x is requested ahead of the first weights: loads return in order, and the
       // weights come from HBM
       lds_barrier();  // the last block's readers are done
-      stage(0, min(kPanel, chunks) * 4 * MB);
+      stage(0, min(kPanel, chunks) * 4);
       lp = lc = 0;
 #pragma unroll
       for (int d = 0; d < kAhead; ++d) request(ring[d]);
       for (int p0 = 0; p0 < chunks; p0 += kPanel) {
         const int p1 = min(p0 + kPanel, chunks);
-        const int frags = (p1 - p0) * 4 * MB;
         if (p0 > 0) {
           lds_barrier();
-          stage(p0, frags);
+          stage(p0, (p1 - p0) * 4);
         }
         if constexpr (!F32) {
           if (p0 > 0)
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
           else
             wait_loads<Chunk::kLoads * kAhead>();
         }
-        stage_end(p0, p1, frags);
+        stage_end(p0, p1);
         lds_barrier();
         // one panel: every pair; several: the wave's one pair's share of them
         for (int pair = 0; pair < n_pairs; ++pair) {

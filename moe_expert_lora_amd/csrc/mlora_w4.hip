@@ -162,9 +162,11 @@ struct W4Args {
   uint32_t x_ld_bytes;
   uint32_t topk;          // rows per x row (1: a row of its own)
   int32_t K, N;
-  int32_t tiles, ksteps, blocks, per_block;  // per_block: chunks per scale block
+  int32_t tiles, ksteps, blocks;
+  uint32_t block_magic;   // ceil(2^31 / chunks per scale block)
   int32_t slices;         // workgroups per expert
   int32_t pairs, per_slice;  // streaming form: tile pairs, and those of a slice
+  uint32_t wave_magic;    // ceil(2^32 / waves)
   int32_t out_vec;        // rows of out start on 4 elements
 };
 
@@ -263,7 +265,7 @@ struct WChunk {
   uint32_t z[NT][ZP ? SG : 1];
 
   __device__ __forceinline__ void load(const W4Args& a, const WBufs& b, int c, int lane) {
-    const uint32_t lg = (uint32_t)lane >> 4, blk = (uint32_t)(c / a.per_block);
+    const uint32_t lg = (uint32_t)lane >> 4, blk = __umulhi(2u * (uint32_t)c, a.block_magic);
     const uint32_t per_lane = c < (a.ksteps >> 2) ? 16u : (uint32_t)(a.ksteps & 3) * 4u;
     // offsets wholly in the vector operand: the range check is against it
     const uint32_t wo = (uint32_t)lane * per_lane + c * 1024u;
@@ -437,7 +439,7 @@ __device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, i
       drops |= (drop ? 1u : 0u) << ((r0 + r) & 31);
     }
   }
-  lds_barrier();  // the list's last readers are done
+  if (seg > 0) lds_barrier();  // the list's last readers are done
   if (lane == 0) counts[wave] = n_hits | n_drops << 16;
   lds_barrier();
   int at = 0, all = 0;
@@ -577,8 +579,8 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
   const rsrc_t rx = buf(a.x, a.x_bytes);
   // this wave's pairs: every waves-th of the slice's
   const int pair0 = slice * a.per_slice + wave;
-  const int n_pairs = uniform_i32(
-      max(0, (min((slice + 1) * a.per_slice, a.pairs) - pair0 + waves - 1) / waves));
+  const int left = max(0, min((slice + 1) * a.per_slice, a.pairs) - pair0) + waves - 1;
+  const int n_pairs = uniform_i32((int)__umulhi((uint32_t)left, a.wave_magic));  // left / waves
   const int et0 = e * a.tiles;
   // A pair takes whole turns of the ring: places past its chunks stay empty.
   const int turns = (chunks + kAhead - 1) / kAhead * kAhead;
@@ -783,6 +785,7 @@ void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
   a.slices = p.slices;
   a.per_slice = p.per_slice;
   a.pairs = (a.tiles + kPair - 1) / kPair;
+  a.wave_magic = (uint32_t)(((1ull << 32) + p.waves - 1) / p.waves);
   const dim3 grid((unsigned)a.slices, (unsigned)rows.experts, (unsigned)p.splits), block(64 * p.waves);
   if (!p.stream) {
     hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB>), grid, block, 0, s, ids, n_rows, E, a);
@@ -948,7 +951,8 @@ extern "C" int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void*
   a.tiles = (int32_t)l.tiles;
   a.ksteps = (int32_t)l.ksteps;
   a.blocks = (int32_t)l.blocks;
-  a.per_block = route->group <= 128 ? 1 : route->group / 128;
+  const uint32_t per_block = route->group <= 128 ? 1u : (uint32_t)route->group / 128u;
+  a.block_magic = ((1u << 31) + per_block - 1) / per_block;
   a.out_vec = out_ld % 4 == 0 && aligned(out, 4 * es);
   const bool f32 = route->dtype == MLORA_F32;
   const W4Plan p = plan_w4(route, n_rows, route->n_experts, f32);

@@ -145,6 +145,12 @@ class W4Route(ctypes.Structure):
 
 
 _lib: Optional[ctypes.CDLL] = None
+# what the device calls take from torch, bound once by load() (device calls
+# load the library before they touch a tensor)
+_torch = None
+_DTYPES: dict = {}   # torch dtype -> MLORA_* code
+_I32 = _F32 = None
+_raw_stream = _device = None
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _i64p = ctypes.POINTER(ctypes.c_int64)
@@ -154,7 +160,7 @@ _f32p = ctypes.POINTER(ctypes.c_float)
 
 def load() -> ctypes.CDLL:
     """Load libmlora.so (once). Raises when it has not been built."""
-    global _lib
+    global _lib, _torch, _I32, _F32, _raw_stream, _device
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -163,7 +169,12 @@ def load() -> ctypes.CDLL:
     # PyTorch ships its own HIP runtime; load it first so that this library
     # binds to the same runtime instance that owns the tensors and streams.
     try:
-        import torch  # noqa: F401
+        import torch
+        _torch = torch
+        _DTYPES.update({torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32})
+        _I32, _F32 = torch.int32, torch.float32
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _device = torch._C._cuda_getDevice
     except ImportError:
         pass
     lib = ctypes.CDLL(LIB_PATH)
@@ -263,8 +274,8 @@ def mlora_pack_expert_tables(expert_ids, a_addrs, b_addrs, scales):
     lib = load()
     n = ctypes.c_int32(0)
     rc = lib.mlora_pack_expert_tables(_ptr(ids, ctypes.c_int32), _ptr(a, ctypes.c_uint64),
-                                      _ptr(b, ctypes.c_uint64), _ptr(s, ctypes.c_float),
-                                      n_entries, None, None, None, 0, ctypes.byref(n))
+                                      _ptr(b, ctypes.c_uint64), _ptr(s, ctypes.c_float), n_entries,
+                                      None, None, None, 0, ctypes.byref(n))
     if rc == MLORA_NONE:
         return None
     if rc != MLORA_ERR_CAPACITY:
@@ -273,10 +284,9 @@ def mlora_pack_expert_tables(expert_ids, a_addrs, b_addrs, scales):
     bt = np.zeros(n.value, dtype=np.uint64)
     st = np.zeros(n.value, dtype=np.float32)
     rc = lib.mlora_pack_expert_tables(_ptr(ids, ctypes.c_int32), _ptr(a, ctypes.c_uint64),
-                                      _ptr(b, ctypes.c_uint64), _ptr(s, ctypes.c_float),
-                                      n_entries, _ptr(at, ctypes.c_uint64),
-                                      _ptr(bt, ctypes.c_uint64), _ptr(st, ctypes.c_float),
-                                      n.value, ctypes.byref(n))
+                                      _ptr(b, ctypes.c_uint64), _ptr(s, ctypes.c_float), n_entries,
+                                      _ptr(at, ctypes.c_uint64), _ptr(bt, ctypes.c_uint64),
+                                      _ptr(st, ctypes.c_float), n.value, ctypes.byref(n))
     if rc != MLORA_OK:
         raise _err(rc)
     return at, bt, st, int(n.value)
@@ -320,8 +330,7 @@ def mlora_build_moe_row_adapter_decode(adapter_slots, padded_n: int, active: int
 def mlora_grouped_down_windows(total_rows: int, cap: int) -> List[Tuple[int, int]]:
     lib = load()
     n = ctypes.c_int64(0)
-    rc = lib.mlora_grouped_down_windows(int(total_rows), int(cap), None, None, 0,
-                                        ctypes.byref(n))
+    rc = lib.mlora_grouped_down_windows(int(total_rows), int(cap), None, None, 0, ctypes.byref(n))
     if rc == MLORA_OK:
         return []
     if rc != MLORA_ERR_CAPACITY:
@@ -357,12 +366,12 @@ def mlora_reload_launch_overrides() -> None:
 # ---------------------------------------------------------------------------
 
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return MLORA_BF16
-    if t.dtype == torch.float32:
-        return MLORA_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    if _lib is None:
+        load()
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def make_route(a_table, b_table, scale_table, n_experts: int, k_in: int, n_out: int,
@@ -386,8 +395,9 @@ def _stream_handle(stream) -> Optional[int]:
     (its raw handle: building a torch.cuda.Stream takes 2.5 us per call)."""
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if _lib is None:
+        load()
+    return _raw_stream(_device())
 
 
 def _dev(t, name, dtype=None):
@@ -728,9 +738,9 @@ def mlora_gather_bgmv_multi(route: MultiRoute, x, base_out, indices, row_adapter
 
 def _vec(t, name, dtype) -> int:
     """Data pointer of a contiguous device tensor of one dtype."""
-    if t.dtype is not dtype or not (t.is_cuda and t.is_contiguous()):
-        return _dev(t, name, dtype)  # raises, naming what is wrong
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, dtype)  # raises, naming what is wrong
 
 
 def _mat(t, name):
@@ -744,31 +754,27 @@ def _mat(t, name):
     return p, n, shape[1], ld
 
 
-def _call(fn, *args) -> None:
-    rc = fn(*args)
-    if rc != MLORA_OK:
-        raise _err(rc)
-
-
 def mlora_router_topk(logits, indices, weights, renormalize: bool = False, stream=None) -> None:
     """Top-k experts of each row of ``logits`` [n_tokens, n_experts] (bf16 or
     float32, contiguous rows) into ``indices`` (int32) and ``weights``
     (float32), both [n_tokens, top_k]."""
-    import torch
+    lib = _lib or load()
     p, n, experts, ld = _mat(logits, "logits")
     shape = indices.shape
     if len(shape) != 2 or shape[0] != n or shape != weights.shape:
         raise ValueError("indices and weights must be [n_tokens, top_k]")
-    _call(load().mlora_router_topk, p, ld, _dtype_code(logits), n, experts, shape[1],
-          1 if renormalize else 0, _vec(indices, "indices", torch.int32),
-          _vec(weights, "weights", torch.float32), _stream_handle(stream))
+    rc = lib.mlora_router_topk(p, ld, _dtype_code(logits), n, experts, shape[1],
+                               1 if renormalize else 0, _vec(indices, "indices", _I32),
+                               _vec(weights, "weights", _F32), _stream_handle(stream))
+    if rc:
+        raise _err(rc)
 
 
 def mlora_router_topk_backward(logits, indices, d_weights, d_logits, renormalize: bool = False,
                                stream=None) -> None:
     """Gradient of mlora_router_topk's weights into ``d_logits`` (written whole),
     from the forward's logits and indices."""
-    import torch
+    lib = _lib or load()
     p, n, experts, ld = _mat(logits, "logits")
     dp, dn, d_experts, d_ld = _mat(d_logits, "d_logits")
     if d_logits.dtype is not logits.dtype:
@@ -778,9 +784,12 @@ def mlora_router_topk_backward(logits, indices, d_weights, d_logits, renormalize
     shape = indices.shape
     if len(shape) != 2 or shape[0] != n or shape != d_weights.shape:
         raise ValueError("indices and d_weights must be [n_tokens, top_k]")
-    _call(load().mlora_router_topk_backward, p, ld, _dtype_code(logits), n, experts, shape[1],
-          1 if renormalize else 0, _vec(indices, "indices", torch.int32),
-          _vec(d_weights, "d_weights", torch.float32), dp, d_ld, _stream_handle(stream))
+    rc = lib.mlora_router_topk_backward(p, ld, _dtype_code(logits), n, experts, shape[1],
+                                        1 if renormalize else 0, _vec(indices, "indices", _I32),
+                                        _vec(d_weights, "d_weights", _F32), dp, d_ld,
+                                        _stream_handle(stream))
+    if rc:
+        raise _err(rc)
 
 
 def mlora_moe_sort_workspace_bytes(n_slots: int, n_experts: int) -> int:
@@ -793,7 +802,7 @@ def mlora_moe_sort(ids, n_experts: int, expert_offsets, sorted_ids, slot_rows, w
     """Stable sort of the flat (token, slot) ids by expert: fills
     ``expert_offsets`` [n_experts + 1], ``sorted_ids`` and ``slot_rows``
     (all int32); ids outside [0, n_experts) are dropped (-1)."""
-    import torch
+    lib = _lib or load()
     n = ids.numel()
     if expert_offsets.numel() != n_experts + 1:
         raise ValueError("expert_offsets must have n_experts + 1 entries")
@@ -803,17 +812,20 @@ def mlora_moe_sort(ids, n_experts: int, expert_offsets, sorted_ids, slot_rows, w
     if workspace is not None and workspace.numel():
         ws_ptr = _dev(workspace, "workspace")
         ws_bytes = workspace.numel() * workspace.element_size()
-    i32 = torch.int32
-    _call(load().mlora_moe_sort, _vec(ids, "ids", i32), n, n_experts,
-          _vec(expert_offsets, "expert_offsets", i32), _vec(sorted_ids, "sorted_ids", i32),
-          _vec(slot_rows, "slot_rows", i32), ws_ptr, ws_bytes, _stream_handle(stream))
+    rc = lib.mlora_moe_sort(_vec(ids, "ids", _I32), n, n_experts,
+                            _vec(expert_offsets, "expert_offsets", _I32),
+                            _vec(sorted_ids, "sorted_ids", _I32),
+                            _vec(slot_rows, "slot_rows", _I32), ws_ptr, ws_bytes,
+                            _stream_handle(stream))
+    if rc:
+        raise _err(rc)
 
 
 def mlora_moe_dispatch(x, rows, sorted_ids, slot_rows, top_k: int, stream=None) -> None:
     """Copies token rows of ``x`` [n_tokens, dim] to their sorted ``rows``
     [n_tokens * top_k, dim]; rows no slot names get zeros. The maps are
     mlora_moe_sort's. Its gradient: mlora_moe_combine with no weights."""
-    import torch
+    lib = _lib or load()
     xp, n, dim, x_ld = _mat(x, "x")
     rp, n_rows, r_dim, r_ld = _mat(rows, "rows")
     if rows.dtype is not x.dtype:
@@ -822,15 +834,18 @@ def mlora_moe_dispatch(x, rows, sorted_ids, slot_rows, top_k: int, stream=None) 
         raise ValueError("rows must be [n_tokens * top_k, dim]")
     if sorted_ids.numel() != n_rows or slot_rows.numel() != n_rows:
         raise ValueError("sorted_ids and slot_rows must have one entry per row")
-    _call(load().mlora_moe_dispatch, xp, x_ld, _dtype_code(x), n, dim, top_k,
-          _vec(sorted_ids, "sorted_ids", torch.int32), _vec(slot_rows, "slot_rows", torch.int32),
-          rp, r_ld, _stream_handle(stream))
+    rc = lib.mlora_moe_dispatch(xp, x_ld, _dtype_code(x), n, dim, top_k,
+                                _vec(sorted_ids, "sorted_ids", _I32),
+                                _vec(slot_rows, "slot_rows", _I32), rp, r_ld,
+                                _stream_handle(stream))
+    if rc:
+        raise _err(rc)
 
 
 def mlora_moe_combine(rows, out, top_k: int, weights=None, slot_rows=None, stream=None) -> None:
     """``out[t]`` = sum over slots of weights[t, j] * rows[slot_rows[t * top_k + j]]
     (``slot_rows`` None: rows in flat (token, slot) order; ``weights`` None: 1)."""
-    import torch
+    lib = _lib or load()
     rp, n_rows, dim, r_ld = _mat(rows, "rows")
     op, n, o_dim, o_ld = _mat(out, "out")
     if rows.dtype is not out.dtype:
@@ -840,17 +855,19 @@ def mlora_moe_combine(rows, out, top_k: int, weights=None, slot_rows=None, strea
     if (weights is not None and weights.numel() != n * top_k) or (
             slot_rows is not None and slot_rows.numel() != n * top_k):
         raise ValueError("weights and slot_rows must have n_tokens * top_k entries")
-    _call(load().mlora_moe_combine, rp, r_ld, n_rows, _dtype_code(rows), n, dim, top_k,
-          None if weights is None else _vec(weights, "weights", torch.float32),
-          None if slot_rows is None else _vec(slot_rows, "slot_rows", torch.int32),
-          op, o_ld, _stream_handle(stream))
+    rc = lib.mlora_moe_combine(rp, r_ld, n_rows, _dtype_code(rows), n, dim, top_k,
+                               None if weights is None else _vec(weights, "weights", _F32),
+                               None if slot_rows is None else _vec(slot_rows, "slot_rows", _I32),
+                               op, o_ld, _stream_handle(stream))
+    if rc:
+        raise _err(rc)
 
 
 def mlora_moe_combine_backward(d_out, rows, weights, d_rows, d_weights, top_k: int,
                                slot_rows=None, sorted_ids=None, stream=None) -> None:
     """Gradient of mlora_moe_combine into ``d_rows`` [n_tokens * top_k, dim] and
     ``d_weights`` [n_tokens, top_k] (None: not computed, ``rows`` not read)."""
-    import torch
+    lib = _lib or load()
     dp, n, dim, d_ld = _mat(d_out, "d_out")
     op, n_rows, o_dim, o_ld = _mat(d_rows, "d_rows")
     dtype = d_out.dtype
@@ -868,13 +885,15 @@ def mlora_moe_combine_backward(d_out, rows, weights, d_rows, d_weights, top_k: i
     for t in (weights, d_weights, slot_rows, sorted_ids):
         if t is not None and t.numel() != n_rows:
             raise ValueError("weights, d_weights and the maps must have one entry per row")
-    f32, i32 = torch.float32, torch.int32
-    _call(load().mlora_moe_combine_backward, dp, d_ld, rp, r_ld, _dtype_code(d_out), n, dim,
-          top_k, None if weights is None else _vec(weights, "weights", f32),
-          None if slot_rows is None else _vec(slot_rows, "slot_rows", i32),
-          None if sorted_ids is None else _vec(sorted_ids, "sorted_ids", i32), op, o_ld,
-          None if d_weights is None else _vec(d_weights, "d_weights", f32),
-          _stream_handle(stream))
+    rc = lib.mlora_moe_combine_backward(dp, d_ld, rp, r_ld, _dtype_code(d_out), n, dim, top_k,
+                                        None if weights is None else _vec(weights, "weights", _F32),
+                                        None if slot_rows is None else _vec(slot_rows, "slot_rows", _I32),
+                                        None if sorted_ids is None else _vec(sorted_ids, "sorted_ids", _I32),
+                                        op, o_ld,
+                                        None if d_weights is None else _vec(d_weights, "d_weights", _F32),
+                                        _stream_handle(stream))
+    if rc:
+        raise _err(rc)
 
 
 def mlora_w4_packed_bytes(n_experts: int, k_in: int, n_out: int, group: int, dtype: int,
@@ -919,7 +938,7 @@ def mlora_w4_gather_gemv(route: W4Route, x, out, ids=None, top_k: int = 1,
                          x_by_row: bool = False, stream=None) -> None:
     """``out[r]`` = W[ids[r]] x[r // top_k] (or x[r] with ``x_by_row``); rows with
     an id outside the route's experts get zeros. ``ids`` None: one weight."""
-    import torch
+    lib = _lib or load()
     if _dtype_code(x) != route.dtype or out.dtype is not x.dtype:
         raise TypeError("x / out dtype differs from the route's")
     xp, x_rows, k_in, x_ld = _mat(x, "x")
@@ -928,7 +947,8 @@ def mlora_w4_gather_gemv(route: W4Route, x, out, ids=None, top_k: int = 1,
         raise ValueError("x / out widths differ from the route's k_in / n_out")
     if ids is not None and ids.numel() != n_rows:
         raise ValueError("ids must have one entry per out row")
-    _call(load().mlora_w4_gather_gemv, ctypes.byref(route), xp, x_rows, x_ld,
-          1 if x_by_row else 0, op, o_ld,
-          None if ids is None else _vec(ids, "ids", torch.int32), n_rows, top_k,
-          _stream_handle(stream))
+    rc = lib.mlora_w4_gather_gemv(ctypes.byref(route), xp, x_rows, x_ld, 1 if x_by_row else 0, op,
+                                  o_ld, None if ids is None else _vec(ids, "ids", _I32), n_rows,
+                                  top_k, _stream_handle(stream))
+    if rc:
+        raise _err(rc)

@@ -743,6 +743,10 @@ def _vec(t, name, dtype) -> int:
     return _dev(t, name, dtype)  # raises, naming what is wrong
 
 
+def _vec_or_null(t, name, dtype) -> Optional[int]:
+    return None if t is None else _vec(t, name, dtype)
+
+
 def _mat(t, name):
     """(data pointer, rows, columns, row stride) of a 2-D device tensor with
     contiguous rows, as _rows_2d."""
@@ -856,8 +860,8 @@ def mlora_moe_combine(rows, out, top_k: int, weights=None, slot_rows=None, strea
             slot_rows is not None and slot_rows.numel() != n * top_k):
         raise ValueError("weights and slot_rows must have n_tokens * top_k entries")
     rc = lib.mlora_moe_combine(rp, r_ld, n_rows, _dtype_code(rows), n, dim, top_k,
-                               None if weights is None else _vec(weights, "weights", _F32),
-                               None if slot_rows is None else _vec(slot_rows, "slot_rows", _I32),
+                               _vec_or_null(weights, "weights", _F32),
+                               _vec_or_null(slot_rows, "slot_rows", _I32),
                                op, o_ld, _stream_handle(stream))
     if rc:
         raise _err(rc)
@@ -886,11 +890,11 @@ def mlora_moe_combine_backward(d_out, rows, weights, d_rows, d_weights, top_k: i
         if t is not None and t.numel() != n_rows:
             raise ValueError("weights, d_weights and the maps must have one entry per row")
     rc = lib.mlora_moe_combine_backward(dp, d_ld, rp, r_ld, _dtype_code(d_out), n, dim, top_k,
-                                        None if weights is None else _vec(weights, "weights", _F32),
-                                        None if slot_rows is None else _vec(slot_rows, "slot_rows", _I32),
-                                        None if sorted_ids is None else _vec(sorted_ids, "sorted_ids", _I32),
+                                        _vec_or_null(weights, "weights", _F32),
+                                        _vec_or_null(slot_rows, "slot_rows", _I32),
+                                        _vec_or_null(sorted_ids, "sorted_ids", _I32),
                                         op, o_ld,
-                                        None if d_weights is None else _vec(d_weights, "d_weights", _F32),
+                                        _vec_or_null(d_weights, "d_weights", _F32),
                                         _stream_handle(stream))
     if rc:
         raise _err(rc)
@@ -948,7 +952,7 @@ def mlora_w4_gather_gemv(route: W4Route, x, out, ids=None, top_k: int = 1,
     if ids is not None and ids.numel() != n_rows:
         raise ValueError("ids must have one entry per out row")
     rc = lib.mlora_w4_gather_gemv(ctypes.byref(route), xp, x_rows, x_ld, 1 if x_by_row else 0, op,
-                                  o_ld, None if ids is None else _vec(ids, "ids", _I32), n_rows,
+                                  o_ld, _vec_or_null(ids, "ids", _I32), n_rows,
                                   top_k, _stream_handle(stream))
     if rc:
         raise _err(rc)

@@ -166,7 +166,11 @@ struct W4Args {
   uint32_t block_magic;   // ceil(2^31 / chunks per scale block)
   int32_t slices;         // workgroups per expert
   int32_t pairs, per_slice;  // streaming form: tile pairs, and those of a slice
-  uint32_t wave_magic;    // ceil(2^32 / waves)
+  int32_t k_waves, pair_waves;  // waves of a workgroup: k_waves to a pair
+  uint32_t wave_magic;    // ceil(2^32 / pair_waves)
+  int32_t turns;          // ring places of a pair, per wave
+  int32_t panel, panel_turns;   // chunks of x in LDS, and their places per wave
+  int32_t by_row;         // a place per row, not per expert
   int32_t out_vec;        // rows of out start on 4 elements
 };
 
@@ -328,7 +332,7 @@ __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x
     for (int nt = 0; nt < NT; ++nt) {
       f32x4 s[MB];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) s[mb] = ZP ? f32x4{0.f, 0.f, 0.f, 0.f} : dc[mb];
+      for (int mb = 0; mb < MB; ++mb) s[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < kPer; ++ks) {
         const u32x4 wf = unpack(wc.w[nt][sg * kPer + ks], base);
@@ -347,15 +351,15 @@ __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x
         if constexpr (ZP) z = (float)((wc.z[nt][sg] >> (8 * i)) & 0xffu);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-          const float t = ZP ? fmaf(z, dc[mb][i], s[mb][i]) : s[mb][i];
+          const float t = ZP ? fmaf(z, dc[mb][i], s[mb][i]) : s[mb][i] + dc[mb][i];
           acc[nt][mb][i] = fmaf(sc, t, acc[nt][mb][i]);
         }
       }
     }
-    // group after group: operands of later ones are not fetched into registers
-    // ahead, which the weights in flight need
-    __builtin_amdgcn_sched_barrier(0);
   }
+  // operands of the next chunk are not fetched into registers ahead, which the
+  // weights in flight need
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 template <typename Row>
@@ -396,12 +400,21 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// The rows of [seg, seg + len) of one workgroup: those whose id is e from the
-// front of `list`, and from its end the rows without an expert that fall to e
-// (by place, spread over the experts; the workgroup writes their zeros), each
-// in row order. Every wave scans a run of 64 * rounds ids and lists its hits
-// behind those of the waves before it, so that workgroups which share an
-// expert's rows agree on the list.
+// A workgroup's place, blockIdx.y, is an expert; in calls of fewer rows than
+// experts (by_row) it is a row, and stands for that row's expert where no
+// earlier row has the same. Returns the expert.
+__device__ __forceinline__ int place_expert(const int32_t* ids, int E, int by_row) {
+  const int y = (int)blockIdx.y;
+  return E > 0 && by_row ? uniform_i32(ids[y]) : y;
+}
+
+// The rows of [seg, seg + len) of one workgroup: those whose id is its expert e
+// from the front of `list` (none if an earlier place has them), and from its
+// end the rows without an expert that fall to this place (the place's own row,
+// or spread over the experts; the workgroup writes their zeros), each in row
+// order. Every wave scans a run of 64 * rounds ids and lists its hits behind
+// those of the waves before it, so that workgroups which share an expert's rows
+// agree on the list.
 struct RowList {
   int live, dead;
 };
@@ -411,12 +424,13 @@ __device__ __forceinline__ int lanes_before(uint64_t m) {
                                         __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
 }
 
-__device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, int seg, int len,
-                                             int* list, int* counts) {
+__device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, int by_row,
+                                             int seg, int len, int* list, int* counts) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
   const int rounds = (len + 64 * waves - 1) / (64 * waves);  // <= 32
   const int first = wave * rounds * 64 + lane;
+  const int y = (int)blockIdx.y;
   const int shift = 32 - __builtin_clz((unsigned)len);       // len < 2^shift
   uint32_t hits = 0, drops = 0;
   int n_hits = 0, n_drops = 0;
@@ -430,9 +444,9 @@ __device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, i
     for (int r = 0; r < 4; ++r) {
       const int i = first + (r0 + r) * 64;
       const bool in = r0 + r < rounds && i < len;
-      const bool hit = in && id[r] == e;
-      const bool drop = in && (uint32_t)id[r] >= (uint32_t)E &&
-                        (int)(((uint32_t)i * (uint32_t)E) >> shift) == e;
+      const bool hit = in && id[r] == e && (uint32_t)e < (uint32_t)E;
+      const int owner = by_row ? i : (int)(((uint32_t)i * (uint32_t)E) >> shift);
+      const bool drop = in && (uint32_t)id[r] >= (uint32_t)E && owner == y;
       n_hits += __popcll(__ballot(hit));
       n_drops += __popcll(__ballot(drop));
       hits |= (hit ? 1u : 0u) << ((r0 + r) & 31);
@@ -461,7 +475,9 @@ __device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, i
     }
   }
   lds_barrier();
-  return RowList{all & 0xffff, all >> 16};
+  int live = all & 0xffff;
+  if (by_row && live > 0 && uniform_i32(list[0]) != y) live = 0;
+  return RowList{live, all >> 16};
 }
 
 // Zeros into columns [n0, n0 + cols) of the rows listed from the end, a wave per
@@ -491,7 +507,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
   const uint32_t base = base_pair();
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int e = (int)blockIdx.y, tile = (int)blockIdx.x;
+  const int e = place_expert(ids, E, a.by_row), tile = (int)blockIdx.x;
   const int n0 = tile * 16, chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
@@ -503,7 +519,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
     const int len = min(kScan, n_rows - seg);
     int n_list = len;
     if (E > 0) {
-      const RowList l = list_rows(ids, E, e, seg, len, list, counts);
+      const RowList l = list_rows(ids, E, e, a.by_row, seg, len, list, counts);
       n_list = l.live;
       if (l.dead > 0 && blockIdx.z == 0) zero_rows<Row>(a, list, l.dead, n0, 16);
     }
@@ -547,7 +563,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
 }
 
 // Many column tiles: x rows go into LDS once per workgroup, as the operands the
-// MFMAs take (k in panels of kPanel chunks where the rows do not fit whole);
+// MFMAs take (k in panels where the rows do not fit whole);
 // each wave then streams whole columns: pairs of tiles over all of k, kAhead
 // chunks of weights requested ahead, no barrier between.
 constexpr int kPair = 2;   // tiles per wave and step
@@ -566,41 +582,43 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
   typedef WChunk<F32, SG, ZP, kPair> Chunk;
   constexpr int kRows = 16 * MB, kParts = XFrag<F32>::kParts;
-  constexpr int kPanel = panel_chunks(F32, MB);
+  const int panel = a.panel;
   __shared__ int list[kScan];
   __shared__ int counts[stream_waves(F32)];
   extern __shared__ u32x4 xs[];  // [k step][row block][part][lane]
   const uint32_t base = base_pair();
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int e = (int)blockIdx.y, slice = (int)blockIdx.x;
+  const int e = place_expert(ids, E, a.by_row), slice = (int)blockIdx.x;
   const int chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
-  // this wave's pairs: every waves-th of the slice's
-  const int pair0 = slice * a.per_slice + wave;
-  const int left = max(0, min((slice + 1) * a.per_slice, a.pairs) - pair0) + waves - 1;
-  const int n_pairs = uniform_i32((int)__umulhi((uint32_t)left, a.wave_magic));  // left / waves
+  // kw waves share a pair, each every kw-th chunk; a wave's pairs: every wn-th
+  // of the slice's
+  const int kw = a.k_waves, n_wn = a.pair_waves, wk = wave % kw, wn = wave / kw;
+  const int pair0 = slice * a.per_slice + wn;
+  const int left = max(0, min((slice + 1) * a.per_slice, a.pairs) - pair0) + n_wn - 1;
+  const int n_pairs = uniform_i32(n_wn == 1 ? left : (int)__umulhi((uint32_t)left, a.wave_magic));
   const int et0 = e * a.tiles;
   // A pair takes whole turns of the ring: places past its chunks stay empty.
-  const int turns = (chunks + kAhead - 1) / kAhead * kAhead;
-  int lp, lc;  // pair and chunk of the next request
+  const int turns = a.turns;
+  int lp, lj;  // pair and turn place of the next request
   auto request = [&](Chunk& w) {
-    const int t0 = (pair0 + lp * waves) * kPair;
+    const int t0 = (pair0 + lp * n_wn) * kPair, lc = wk + lj * kw;
     const bool in = lp < n_pairs && lc < chunks;
     WBufs wb;
     wb.set<SG, (F32 ? 4 : 2), ZP>(a, in ? et0 + t0 : 0, in ? min(kPair, a.tiles - t0) : 0);
     w.load(a, wb, lc, lane);
     // requests stay in order, so that a wait for one leaves the later ones out
     __builtin_amdgcn_sched_barrier(0);
-    lc = lc + 1 == turns ? 0 : lc + 1;
-    lp += lc == 0;
+    lj = lj + 1 == turns ? 0 : lj + 1;
+    lp += lj == 0;
   };
 
   for (int seg = 0; seg < n_rows; seg += kScan) {
     int n_list = min(kScan, n_rows - seg);
     if (E > 0) {
-      const RowList l = list_rows(ids, E, e, seg, n_list, list, counts);
+      const RowList l = list_rows(ids, E, e, a.by_row, seg, n_list, list, counts);
       n_list = l.live;
       if (l.dead > 0 && blockIdx.z == 0)
         zero_rows<Row>(a, list, l.dead, slice * a.per_slice * kPair * 16,
@@ -668,12 +686,12 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
       // x is requested ahead of the first weights: loads return in order, and the
       // weights come from HBM
       lds_barrier();  // the last block's readers are done
-      stage(0, min(kPanel, chunks) * 4);
-      lp = lc = 0;
+      stage(0, min(panel, chunks) * 4);
+      lp = lj = 0;
 #pragma unroll
       for (int d = 0; d < kAhead; ++d) request(ring[d]);
-      for (int p0 = 0; p0 < chunks; p0 += kPanel) {
-        const int p1 = min(p0 + kPanel, chunks);
+      for (int p0 = 0, j0 = 0; p0 < chunks; p0 += panel, j0 += a.panel_turns) {
+        const int p1 = min(p0 + panel, chunks);
         if (p0 > 0) {
           lds_barrier();
           stage(p0, (p1 - p0) * 4);
@@ -686,7 +704,8 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
         }
         stage_end(p0, p1);
         lds_barrier();
-        // one panel: every pair; several: the wave's one pair's share of them
+        // one panel: every pair; several, or several waves a pair: the one pair's
+        // share of them
         for (int pair = 0; pair < n_pairs; ++pair) {
           if (p0 == 0) {
 #pragma unroll
@@ -694,11 +713,12 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
 #pragma unroll
               for (int mb = 0; mb < MB; ++mb) acc[nt][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
           }
-          for (int c0 = p0; c0 < p1; c0 += kAhead) {
+          for (int c0 = wk + j0 * kw; c0 < p1; c0 += kAhead * kw) {
 #pragma unroll
             for (int d = 0; d < kAhead; ++d) {
-              if (c0 + d < p1) {
-                const u32x4* px = xs + (c0 + d - p0) * (4 * MB * kParts * 64) + lane;
+              const int c = c0 + d * kw;
+              if (c < p1) {
+                const u32x4* px = xs + (c - p0) * (4 * MB * kParts * 64) + lane;
                 add_chunk<F32, SG, ZP, kPair, MB>(
                     ring[d],
                     [&](int mb, int ks, XFrag<F32>& f) {
@@ -711,8 +731,8 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
               request(ring[d]);
             }
           }
-          if (p1 < chunks) continue;
-          const int n = (pair0 + pair * waves) * kPair * 16 + lg * 4;
+          if (p1 < chunks || kw > 1) continue;
+          const int n = (pair0 + pair * n_wn) * kPair * 16 + lg * 4;
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb) {
             if (orow[mb] < 0) continue;
@@ -721,6 +741,32 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
             for (int nt = 0; nt < kPair; ++nt)
               store4<Row>(o + nt * 16, acc[nt][mb], a.N - n - nt * 16, a.out_vec != 0);
           }
+        }
+      }
+      if (kw == 1) continue;
+      // the sums of a pair's waves, added in wave order, in the LDS of x
+      lds_barrier();
+      f32x4* red = reinterpret_cast<f32x4*>(xs);  // [wave][tile][row block][lane]
+      if (n_pairs > 0) {
+#pragma unroll
+        for (int nt = 0; nt < kPair; ++nt)
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+            red[((wave * kPair + nt) * MB + mb) * 64 + lane] = acc[nt][mb];
+      }
+      lds_barrier();
+      const int n = pair0 * kPair * 16 + lg * 4;
+#pragma unroll
+      for (int nt = 0; nt < kPair; ++nt) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          if (n_pairs == 0 || (nt * MB + mb) % kw != wk) continue;
+          f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+          for (int w = 0; w < kw; ++w)
+            sum += red[(((wn * kw + w) * kPair + nt) * MB + mb) * 64 + lane];
+          if (orow[mb] >= 0)
+            store4<Row>(out + (int64_t)orow[mb] * a.out_ld + n + nt * 16, sum,
+                        a.N - n - nt * 16, a.out_vec != 0);
         }
       }
     }
@@ -735,45 +781,80 @@ struct W4Rows {
 };
 
 struct W4Plan {
-  bool stream;
-  int mb, waves, splits, per_slice, slices;
+  bool stream, by_row;
+  int places, mb, waves, k_waves, splits, per_slice, slices;
 };
 
-W4Plan plan_w4(const mlora_w4_route* r, int64_t n_rows, int64_t experts, bool f32) {
+W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
+  const bool zp = r->zeros != nullptr;
   W4Plan p{};
+  p.k_waves = 1;
   const int64_t tiles = (r->n_out + 15) / 16, chunks = (r->k_in + 127) / 128;
-  const int64_t mean = (n_rows + experts - 1) / experts;  // rows per expert
+  p.by_row = rows.ids && rows.n < rows.experts;
+  const int64_t places = p.by_row ? rows.n : rows.experts;
+  p.places = (int)places;
+  const int64_t mean = (rows.n + places - 1) / places;  // rows per place
   // Row blocks of 16 per pass over the weights: two once an expert holds more
   // than ten rows on average.
-  p.mb = !f32 && (experts == 1 ? mean > 16 : mean > 10) ? 2 : 1;
+  p.mb = !f32 && (places == 1 ? mean > 16 : mean > 10) ? 2 : 1;
   const int64_t pairs = (tiles + kPair - 1) / kPair;
-  // Streaming pays once there are pairs of tiles for four waves on every CU.
-  p.stream = experts * pairs >= 1024;
+  // Streaming pays from 512 pairs of tiles (9 experts of 2048 x 1024, 16 rows
+  // each: 10.3 us, split 15.6; 4 experts of 4000 x 512, 500 pairs: 7.7, split
+  // 7.0), or from fewer of long k (4 of 4000 x 4000, 500 pairs of 32 chunks: 17,
+  // split 26; 9 of 512 x 4096, 144 pairs: 15, split 16, at 2 rows 9.2 and 8.7).
+  p.stream = places * pairs >= 512 || places * pairs * chunks >= 8192;
   if (p.stream) {
-    // Workgroups of 8 waves where the x rows leave room for two on a CU, else
-    // of as many as its registers hold; slices of an expert's pairs for one
-    // round of workgroups over the CUs.
     const int64_t most = panel_chunks(f32, p.mb);
-    const int64_t lds = (chunks < most ? chunks : most) * chunk_lds(f32, p.mb) + kListLds;
-    const int64_t per_cu = lds * 2 <= kLds ? 2 : 1;
-    p.waves = per_cu == 2 ? 8 : stream_waves(f32);
-    if (experts * ((pairs + p.waves - 1) / p.waves) < 256) p.waves = 4;
-    int64_t slices = 256 * per_cu / experts;
-    if (slices > (pairs + p.waves - 1) / p.waves) slices = (pairs + p.waves - 1) / p.waves;
-    if (slices < 1) slices = 1;
-    // k in several panels: one pair per wave, whose sums stay in registers
-    if (chunks > most) slices = (pairs + p.waves - 1) / p.waves;
-    p.per_slice = (int)((pairs + slices - 1) / slices);
-    p.slices = (int)((pairs + p.per_slice - 1) / p.per_slice);
+    const int64_t reg_waves = f32 ? 8 : sg == 1 && !zp && p.mb == 1 ? 16 : 12;  // of a CU
+    const int64_t most_waves = reg_waves == 16 ? 8 : stream_waves(f32);
+    auto room = [&](int64_t waves, int kw) {  // workgroups the CUs hold at once
+      int64_t lds = (chunks < most ? chunks : most) * chunk_lds(f32, p.mb);
+      const int64_t sums = waves * kPair * p.mb * 1024;
+      if (kw > 1 && lds < sums) lds = sums;
+      const int64_t by_lds = kLds / (lds + kListLds), by_reg = reg_waves / waves;
+      return 256 * (by_lds < by_reg ? by_lds : by_reg);
+    };
+    // All pairs at once, as many waves to a pair as that leaves room for and k
+    // has chunks for (64 experts of 512 x 4096, 2 rows each: 1, 2, 3 waves to a
+    // pair 19.5, 17.0, 23.9 us; 3 do not fit one round of workgroups) ...
+    for (int kw = 4; kw >= 1 && p.waves == 0; --kw) {
+      if (kw > 1 && (chunks < 3 * kw || kAhead * kw > most)) continue;
+      for (int64_t wn = 1; wn * kw <= most_waves; ++wn) {
+        if (wn * kw < 4) continue;
+        const int64_t slices = (pairs + wn - 1) / wn;
+        if (places * slices > room(wn * kw, kw)) continue;
+        p.k_waves = kw;
+        p.waves = (int)(wn * kw);
+        p.slices = (int)slices;
+        p.per_slice = (int)wn;
+        break;
+      }
+    }
+    // ... or several pairs per wave one after the other, in one round of
+    // workgroups (one pair where k takes several panels, whose sums stay in
+    // registers)
+    if (p.waves == 0) {
+      p.waves = (int)most_waves;
+      int64_t slices = room(p.waves, 1) / places;
+      if (slices < 1) slices = 1;
+      if (chunks > most || slices > (pairs + p.waves - 1) / p.waves)
+        slices = (pairs + p.waves - 1) / p.waves;
+      p.per_slice = (int)((pairs + slices - 1) / slices);
+      p.slices = (int)((pairs + p.per_slice - 1) / p.per_slice);
+    }
   } else {
     const int64_t per = (chunks + kMaxWaves - 1) / kMaxWaves;
     p.waves = (int)((chunks + per - 1) / per);
     p.slices = (int)tiles;
   }
-  // Rows of one expert over several workgroups once an expert holds more than
-  // two passes on average.
+  // Rows of one expert over several workgroups: once an expert holds more than
+  // two passes on average, or while there are less than two workgroups a CU (one
+  // weight of 4000 x 4000, 40 rows: 13.6 us in one workgroup per tile, 6.9 in two).
   const int64_t blocks = (mean + 16 * p.mb - 1) / (16 * p.mb);
-  p.splits = (int)(blocks <= 2 ? 1 : blocks > 64 ? 32 : (blocks + 1) / 2);
+  const int64_t wgs = places * p.slices;
+  int64_t splits = blocks <= 2 ? 1 : (blocks + 1) / 2;
+  if (splits < blocks && wgs * splits < 512) splits = blocks < 512 / wgs + 1 ? blocks : 512 / wgs + 1;
+  p.splits = (int)(splits > 32 ? 32 : splits);
   return p;
 }
 
@@ -783,16 +864,24 @@ void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
   const int32_t* ids = rows.ids;
   const int n_rows = rows.n, E = rows.ids ? rows.experts : 0;
   a.slices = p.slices;
+  a.by_row = p.by_row;
   a.per_slice = p.per_slice;
   a.pairs = (a.tiles + kPair - 1) / kPair;
-  a.wave_magic = (uint32_t)(((1ull << 32) + p.waves - 1) / p.waves);
-  const dim3 grid((unsigned)a.slices, (unsigned)rows.experts, (unsigned)p.splits), block(64 * p.waves);
+  a.k_waves = p.k_waves;
+  a.pair_waves = p.waves / p.k_waves;
+  a.wave_magic = (uint32_t)(((1ull << 32) + a.pair_waves - 1) / a.pair_waves);
+  const dim3 grid((unsigned)a.slices, (unsigned)p.places, (unsigned)p.splits), block(64 * p.waves);
   if (!p.stream) {
     hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB>), grid, block, 0, s, ids, n_rows, E, a);
     return;
   }
-  const int chunks = (a.ksteps + 3) / 4, most = panel_chunks(F32, MB);
-  const size_t lds = (size_t)(chunks < most ? chunks : most) * chunk_lds(F32, MB);
+  const int chunks = (a.ksteps + 3) / 4, turn = kAhead * p.k_waves;
+  a.panel = panel_chunks(F32, MB) / turn * turn;
+  a.panel_turns = a.panel / p.k_waves;
+  a.turns = ((chunks + p.k_waves - 1) / p.k_waves + kAhead - 1) / kAhead * kAhead;
+  size_t lds = (size_t)(chunks < a.panel ? chunks : a.panel) * chunk_lds(F32, MB);
+  const size_t sums = (size_t)p.waves * kPair * MB * 1024;
+  if (p.k_waves > 1 && lds < sums) lds = sums;
   hipLaunchKernelGGL((w4_stream_kernel<F32, SG, ZP, MB>), grid, block, lds, s, ids, n_rows, E, a);
 }
 
@@ -955,9 +1044,9 @@ extern "C" int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void*
   a.block_magic = ((1u << 31) + per_block - 1) / per_block;
   a.out_vec = out_ld % 4 == 0 && aligned(out, 4 * es);
   const bool f32 = route->dtype == MLORA_F32;
-  const W4Plan p = plan_w4(route, n_rows, route->n_experts, f32);
   (void)hipGetLastError();
   const W4Rows rows = {ids, (int32_t)n_rows, route->n_experts};
+  const W4Plan p = plan_w4(route, rows, f32, (int)l.sg);
   dispatch_w4(a, p, f32, (int)l.sg, rows, reinterpret_cast<hipStream_t>(stream));
   return launch_status(who);
 }

@@ -143,6 +143,36 @@ def test_streamed_expert_rows(ml, dtype, x_by_row, rows, experts, top_k, k, n, g
             f"{rows}/{experts}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,experts,k,n,group,zeros", [
+    (1, 16, 264, 100, 32, True), (8, 52, 1080, 314, 64, False), (15, 16, 2048, 100, 128, True),
+    (20, 64, 1000, 1000, 32, True), (9, 40, 2104, 1900, 128, False)])
+def test_fewer_rows_than_experts(ml, dtype, rows, experts, k, n, group, zeros):
+    """Places are rows: repeated experts, rows without one, all the same."""
+    w = Weights(ml, experts, k, n, group, zeros, dtype, rows)
+    x = _x((rows, k), dtype, 9)
+    rng = np.random.default_rng(rows)
+    mixed = rng.integers(0, experts, size=rows).astype(np.int32)
+    mixed[rows // 2:] = mixed[0]
+    mixed[rows // 3] = -1
+    mixed[-1] = experts + 3
+    for ids in (mixed, np.full(rows, experts - 1, np.int32), np.full(rows, -1, np.int32),
+                np.arange(rows, dtype=np.int32)):
+        w.check(_run(ml, w, x, rows, ids, 1, True), x, ids, 1, True, f"{rows}/{experts}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,experts,k,n,group,zeros", [
+    (5, 4, 2104, 4000, 64, True),      # four waves to a pair, several panels in float32
+    (90, 4, 2504, 4010, 128, False),   # two row blocks, several panels
+    (40, 16, 704, 1200, 32, True)])
+def test_several_waves_to_a_pair(ml, dtype, rows, experts, k, n, group, zeros):
+    w = Weights(ml, experts, k, n, group, zeros, dtype, rows)
+    x = _x((rows, k), dtype, 10)
+    ids = np.random.default_rng(rows).integers(-1, experts, size=rows).astype(np.int32)
+    w.check(_run(ml, w, x, rows, ids, 1, True), x, ids, 1, True, f"{rows}/{experts}")
+
+
 def test_streamed_non_finite_rows_stay_alone(ml):
     w = Weights(ml, 64, 200, 520, 64, True, "bf16", 17)
     x = _x((300, 200), "bf16", 5)

@@ -298,15 +298,21 @@ int32_t check_router(const char* who, int32_t dtype, int64_t n_tokens, int32_t n
 // and over the keys then turns ranks into places. All sums are integers, so
 // the result does not depend on any order.
 //
-// Up to kSortOne ids run as one workgroup. More take two kernels: counts per
-// block into the workspace, then each block sums the counts before it (and
-// all of them) itself and places its ids.
+// Up to 1024 ids run as one workgroup. Up to kSortOne, each workgroup places
+// 1024 ids and counts every id itself for the places before its own. More take
+// two kernels: counts per block into the workspace, then each block sums the
+// counts before it (and all of them) itself and places its ids.
+//
+// Measured (128 experts, skewed, us a call; a launch alone is 2.3 to 3): 4096
+// ids recounted 4.6, in two kernels 9.0; 32768: 7.9 and 10.1; 49152: 9.7 and
+// 10.2; 65536: 11.6 and 10.5. What bounds the recount is LDS atomics, one per
+// id and workgroup; the two kernels, their two starts.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortR = 4;                       // ids per thread of a tile
 constexpr int kSortTile = kSortThreads * kSortR;
-constexpr int64_t kSortOne = kSortTile;
+constexpr int64_t kSortOne = 40960;             // ids of the one-kernel form
 constexpr int kSortBlocks = 256;                // most blocks of the two-kernel form
 
 struct SortArgs {
@@ -351,6 +357,19 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
     a.counts[(int64_t)blockIdx.x * nk + e] = cnt[e];
 }
 
+// Exclusive prefix over the wave's lanes of v, and its sum over all of them.
+__device__ __forceinline__ int wave_prefix(int v, int* sum) {
+  int run = v;
+  run += __builtin_amdgcn_update_dpp(0, run, 0x111, 0xf, 0xf, false);  // row_shr:1
+  run += __builtin_amdgcn_update_dpp(0, run, 0x112, 0xf, 0xf, false);  // row_shr:2
+  run += __builtin_amdgcn_update_dpp(0, run, 0x114, 0xf, 0xf, false);  // row_shr:4
+  run += __builtin_amdgcn_update_dpp(0, run, 0x118, 0xf, 0xf, false);  // row_shr:8
+  run += __builtin_amdgcn_update_dpp(0, run, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  run += __builtin_amdgcn_update_dpp(0, run, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  *sum = __builtin_amdgcn_readlane(run, 63);
+  return run - v;
+}
+
 // LDS: base[nk] (where the block's next id of a key goes), total[nk] (the
 // call's counts), tile_cnt[nk], then 16-bit counts [kSortWaves][nk] (a tile
 // has 64 R ids a wave and 1024 R in all).
@@ -360,9 +379,18 @@ __global__ void __launch_bounds__(256) sort_empty_kernel(SortArgs a) {
   for (int e = threadIdx.x; e <= a.E; e += 256) a.offsets[e] = 0;
 }
 
-template <int R>
+// How a block learns the counts of the ids before its own, and of all.
+enum SortMode {
+  kSortAlone,    // one block: its tile's counts
+  kSortRecount,  // it counts every id itself (a tile per block)
+  kSortCounted   // sort_count_kernel's counts
+};
+constexpr int kSortCopies = 4;  // of each counter in kSortRecount: fewer lanes on one address
+
+template <int R, SortMode MODE>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
   extern __shared__ int lds[];
+  __shared__ int wave_sum[kSortWaves];
   const int nk = a.E + 1, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int* base = lds;
   int* total = lds + nk;
@@ -370,10 +398,53 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
   uint16_t* waves = reinterpret_cast<uint16_t*>(lds + 3 * nk);
   uint16_t* mine = waves + wave * nk;
   constexpr int kTile = kSortThreads * R;
-  const bool many = a.blocks > 1;
-  for (int e = tid; e < 2 * nk; e += kSortThreads) lds[e] = 0;
-  if (many) {
-    // counts of the blocks before this one, and of all
+  if constexpr (MODE == kSortRecount) {
+    // counters [before this tile, not before][copy][key], over the whole LDS
+    // of the later steps
+    for (int i = tid; i < 2 * kSortCopies * nk; i += kSortThreads) lds[i] = 0;
+    __syncthreads();
+    const int t0 = (int)blockIdx.x * kTile, whole = a.n & ~3;
+    int* mycopy = lds + (lane & (kSortCopies - 1)) * nk;
+    for (int i = tid * 4; i < whole; i += kSortThreads * 4) {
+      const int4 id = *reinterpret_cast<const int4*>(a.ids + i);
+      int* c = mycopy + (i < t0 ? 0 : kSortCopies * nk);  // t0 is a multiple of 4
+      atomicAdd(&c[sort_key(id.x, a.E)], 1);
+      atomicAdd(&c[sort_key(id.y, a.E)], 1);
+      atomicAdd(&c[sort_key(id.z, a.E)], 1);
+      atomicAdd(&c[sort_key(id.w, a.E)], 1);
+    }
+    if (tid < a.n - whole) {
+      const int i = whole + tid;
+      atomicAdd(&mycopy[(i < t0 ? 0 : kSortCopies * nk) + sort_key(a.ids[i], a.E)], 1);
+    }
+    __syncthreads();
+    int before[2], all[2];  // of keys tid and tid + 1024
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = tid + h * kSortThreads;
+      before[h] = all[h] = 0;
+      if (e < nk) {
+#pragma unroll
+        for (int c = 0; c < kSortCopies; ++c) {
+          before[h] += lds[c * nk + e];
+          all[h] += lds[(kSortCopies + c) * nk + e];
+        }
+        all[h] += before[h];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = tid + h * kSortThreads;
+      if (e < nk) {
+        base[e] = before[h];
+        total[e] = all[h];
+      }
+    }
+  } else {
+    for (int e = tid; e < 2 * nk; e += kSortThreads) lds[e] = 0;
+  }
+  if constexpr (MODE == kSortCounted) {
     __syncthreads();
     const int parts = kSortThreads > nk ? kSortThreads / nk : 1;
     for (int i = tid; i < parts * nk; i += kSortThreads) {
@@ -420,29 +491,29 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
         run += c;
       }
       tile_cnt[e] = run;
-      if (!many) total[e] = run;
+      if (MODE == kSortAlone) total[e] = run;
     }
     __syncthreads();
     if (tile == 0) {
-      // exclusive prefix of `total` over the keys: the first wave, 64 at a time
-      if (wave == 0) {
-        int carry = 0;
-        for (int e0 = 0; e0 < nk; e0 += 64) {
-          const int e = e0 + lane;
-          const int c = e < nk ? total[e] : 0;
-          int run = c;
+      // exclusive prefix of `total` over the experts, a thread each (E <= 1024);
+      // the dropped ones' bucket E starts behind them all
+      int sum;
+      int at = wave_prefix(tid < a.E ? total[tid] : 0, &sum);
+      if (lane == 0) wave_sum[wave] = sum;
+      __syncthreads();
+      int live = 0;
 #pragma unroll
-          for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(run, d);
-            run += lane >= d ? up : 0;
-          }
-          if (e < nk) {
-            const int at = carry + run - c;
-            base[e] += at;
-            if (blockIdx.x == 0) a.offsets[e] = at;
-          }
-          carry += __shfl(run, 63);
-        }
+      for (int w = 0; w < kSortWaves; ++w) {
+        at += w < wave ? wave_sum[w] : 0;
+        live += wave_sum[w];
+      }
+      if (tid < a.E) {
+        base[tid] += at;
+        if (blockIdx.x == 0) a.offsets[tid] = at;
+      }
+      if (tid == 0) {
+        base[a.E] += live;
+        if (blockIdx.x == 0) a.offsets[a.E] = live;
       }
       __syncthreads();
     }
@@ -464,9 +535,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
   }
 }
 
-// Blocks of a call (one up to kSortOne ids).
+// Blocks that count ahead in the two-kernel form (0: one kernel).
 int sort_blocks(int64_t n) {
-  if (n <= kSortOne) return 1;
+  if (n <= kSortOne) return 0;
   const int64_t tiles = (n + kSortTile - 1) / kSortTile;
   const int64_t per = (tiles + kSortBlocks - 1) / kSortBlocks;
   return (int)((tiles + per - 1) / per);
@@ -799,7 +870,7 @@ extern "C" int32_t mlora_router_topk_backward(const void* logits, int64_t logits
 extern "C" uint64_t mlora_moe_sort_workspace_bytes(int64_t n_slots, int32_t n_experts) {
   if (n_slots <= 0 || n_slots > kMaxRows || n_experts < 1 || n_experts > kMaxExperts) return 0;
   const int blocks = sort_blocks(n_slots);
-  return blocks == 1 ? 0 : (((uint64_t)blocks * (n_experts + 1) * 4 + 255) & ~255ull);
+  return blocks == 0 ? 0 : (((uint64_t)blocks * (n_experts + 1) * 4 + 255) & ~255ull);
 }
 
 extern "C" int32_t mlora_moe_sort(const int32_t* ids, int64_t n_slots, int32_t n_experts,
@@ -816,6 +887,8 @@ extern "C" int32_t mlora_moe_sort(const int32_t* ids, int64_t n_slots, int32_t n
     return fail(MLORA_ERR_INVALID, "%s: NULL device pointer", who);
   if (!workspace && workspace_bytes != 0)
     return fail(MLORA_ERR_INVALID, "%s: NULL workspace with workspace_bytes > 0", who);
+  if (!aligned(ids, 4))
+    return fail(MLORA_ERR_INVALID, "%s: ids must be 4-byte aligned", who);
   if (!aligned(workspace, 4))
     return fail(MLORA_ERR_INVALID, "%s: workspace must be 4-byte aligned", who);
   const uint64_t need = mlora_moe_sort_workspace_bytes(n_slots, n_experts);
@@ -831,26 +904,30 @@ extern "C" int32_t mlora_moe_sort(const int32_t* ids, int64_t n_slots, int32_t n
   a.n = (int32_t)n_slots;
   a.E = n_experts;
   a.key_bits = 32 - __builtin_clz((unsigned)n_experts + 1);  // keys 0 .. E + 1
-  a.blocks = n_slots > 0 ? sort_blocks(n_slots) : 1;
-  const int64_t tiles = (n_slots + kSortTile - 1) / kSortTile;
-  a.tiles_per_block = (int32_t)((tiles + a.blocks - 1) / a.blocks);
+  a.tiles_per_block = 1;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   const size_t lds = sort_lds_bytes(n_experts);
+  const dim3 threads(kSortThreads);
   if (n_slots == 0) {
     // nothing to place: the offsets alone, all 0
     hipLaunchKernelGGL(sort_empty_kernel, dim3(1), dim3(256), 0, s, a);
-    return launch_status(who);
-  }
-  if (a.blocks > 1) {
-    hipLaunchKernelGGL(sort_count_kernel, dim3(a.blocks), dim3(kSortThreads),
-                       (size_t)(n_experts + 1) * 4, s, a);
-    if (int32_t rc = launch_status(who)) return rc;
-    hipLaunchKernelGGL(sort_place_kernel<kSortR>, dim3(a.blocks), dim3(kSortThreads), lds, s, a);
   } else if (n_slots <= kSortThreads) {
-    hipLaunchKernelGGL(sort_place_kernel<1>, dim3(1), dim3(kSortThreads), lds, s, a);
+    hipLaunchKernelGGL((sort_place_kernel<1, kSortAlone>), dim3(1), threads, lds, s, a);
+  } else if (n_slots <= kSortOne) {
+    const int blocks = (int)((n_slots + kSortThreads - 1) / kSortThreads);
+    const size_t counters = (size_t)2 * kSortCopies * (n_experts + 1) * 4;
+    hipLaunchKernelGGL((sort_place_kernel<1, kSortRecount>), dim3(blocks), threads,
+                       counters > lds ? counters : lds, s, a);
   } else {
-    hipLaunchKernelGGL(sort_place_kernel<kSortR>, dim3(1), dim3(kSortThreads), lds, s, a);
+    a.blocks = sort_blocks(n_slots);
+    const int64_t tiles = (n_slots + kSortTile - 1) / kSortTile;
+    a.tiles_per_block = (int32_t)((tiles + a.blocks - 1) / a.blocks);
+    hipLaunchKernelGGL(sort_count_kernel, dim3(a.blocks), threads, (size_t)(n_experts + 1) * 4, s,
+                       a);
+    if (int32_t rc = launch_status(who)) return rc;
+    hipLaunchKernelGGL((sort_place_kernel<kSortR, kSortCounted>), dim3(a.blocks), threads, lds, s,
+                       a);
   }
   return launch_status(who);
 }

@@ -235,6 +235,7 @@ def _check_sort(ml, host, E):
 @pytest.mark.parametrize("n,experts", [
     (1, 1), (1, 128), (2, 3), (63, 5), (64, 5), (65, 5), (640, 128), (1000, 1024), (1024, 7),
     (1025, 255), (4095, 1), (4096, 127), (4097, 128), (5000, 1023), (8192, 64), (32768, 128),
+    (9001, 1024), (40959, 200), (40960, 3), (40961, 200),
     (70001, 1024), (131064, 255)])
 def test_sort(ml, n, experts):
     rng = np.random.default_rng(n + experts)
@@ -251,6 +252,18 @@ def test_sort_one_sided(ml, n):
         _check_sort(ml, np.full(n, fill, dtype=np.int32), 10)
     _check_sort(ml, np.sort(np.arange(n, dtype=np.int32) % 10), 10)
     _check_sort(ml, (np.arange(n, dtype=np.int32) % 10)[::-1].copy(), 10)
+
+
+def test_sort_ids_from_any_start(ml):
+    """ids that start on 4 bytes only."""
+    rng = np.random.default_rng(22)
+    for n in (700, 5003):
+        ids = rng.integers(-1, 33, size=n + 3).astype(np.int32)
+        dev = torch.from_numpy(ids).to(DEV)
+        for lead in (1, 2, 3):
+            got = _sort(ml, dev[lead:lead + n], 33)
+            for g, w in zip(got, moe.sort_by_expert(ids[lead:lead + n], 33)):
+                assert np.array_equal(_np(g), w)
 
 
 def test_sort_many_tiles_per_block(ml):

@@ -601,28 +601,47 @@ __device__ __forceinline__ U* row_at(const void* base, int64_t row, int64_t ld) 
   return reinterpret_cast<U*>(const_cast<elem*>(static_cast<const elem*>(base)) + row * ld);
 }
 
+// p's entries of slots j0 .. j0 + kSlots - 1 of token t, all requested together
+// (places past the last slot read the last one).
+__device__ __forceinline__ void slot_entries(const int32_t* p, const RowsArgs& a, int t, int j0,
+                                             int (&v)[kSlots]) {
+  p += (int64_t)t * a.k + j0;
+  const int last = a.k - 1 - j0;
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) v[j] = p[min(j, last)];
+}
+
 // Row numbers of slots j0 .. j0 + kSlots - 1 of token t; -1 where there is none.
 __device__ __forceinline__ void slot_numbers(const RowsArgs& a, int t, int j0,
                                              int (&row)[kSlots]) {
+  if (a.slot_rows) {
+    slot_entries(a.slot_rows, a, t, j0, row);
+  } else {
 #pragma unroll
-  for (int j = 0; j < kSlots; ++j) {
-    const int64_t s = (int64_t)t * a.k + j0 + j;
-    int r = -1;
-    if (j0 + j < a.k) r = a.slot_rows ? a.slot_rows[s] : (int)s;
-    row[j] = (uint32_t)r < (uint64_t)a.n_rows ? r : -1;
+    for (int j = 0; j < kSlots; ++j) row[j] = t * a.k + j0 + j;
   }
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j)
+    if (j0 + j >= a.k || (uint32_t)row[j] >= (uint64_t)a.n_rows) row[j] = -1;
 }
 
-// Zeros into the rows t * k + j that no slot names.
-template <typename Row, typename Un, int G>
-__device__ __forceinline__ void zero_rows(const RowsArgs& a, int t, int g) {
-  typedef typename Un::raw raw;
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t r = (int64_t)t * a.k + j;
-    if (a.sorted_ids[r] >= 0) continue;
-    raw* p = row_at<Row, raw>(a.dst, r, a.dst_ld);
-    for (int c = g; c < a.units; c += G) p[c] = Un::zero();
-  }
+// Bit j: row t * k + j0 + j is named by no slot (its zeros fall to this token).
+__device__ __forceinline__ uint32_t unnamed_rows(const RowsArgs& a, int t, int j0) {
+  int id[kSlots];
+  slot_entries(a.sorted_ids, a, t, j0, id);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) bits |= j0 + j < a.k && id[j] < 0 ? 1u << j : 0u;
+  return bits;
+}
+
+// Unit c of the rows that unnamed_rows found.
+template <typename Row, typename Un>
+__device__ __forceinline__ void zero_unit(const RowsArgs& a, int t, int j0, uint32_t bits, int c) {
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j)
+    if ((bits >> j) & 1)
+      row_at<Row, typename Un::raw>(a.dst, (int64_t)t * a.k + j0 + j, a.dst_ld)[c] = Un::zero();
 }
 
 template <typename Row, bool WIDE, int G>
@@ -636,14 +655,15 @@ __global__ void __launch_bounds__(256) dispatch_kernel(RowsArgs a) {
   for (int j0 = 0; j0 < a.k; j0 += kSlots) {
     int row[kSlots];
     slot_numbers(a, t, j0, row);
+    const uint32_t unnamed = unnamed_rows(a, t, j0);
     for (int c = g; c < a.units; c += G) {
       const raw v = x[c];
 #pragma unroll
       for (int j = 0; j < kSlots; ++j)
         if (row[j] >= 0) row_at<Row, raw>(a.dst, row[j], a.dst_ld)[c] = v;
+      if (unnamed) zero_unit<Row, Un>(a, t, j0, unnamed, c);
     }
   }
-  zero_rows<Row, Un, G>(a, t, g);
 }
 
 template <typename Row, bool WIDE, int G>
@@ -660,13 +680,16 @@ __global__ void __launch_bounds__(256) combine_kernel(RowsArgs a) {
       int row[kSlots];
       slot_numbers(a, t, j0, row);
       raw v[kSlots];
+      float ws[kSlots];
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
+      for (int j = 0; j < kSlots; ++j) {
         v[j] = row[j] >= 0 ? row_at<Row, raw>(a.src, row[j], a.src_ld)[c] : Un::zero();
+        ws[j] = a.weights ? a.weights[(int64_t)t * a.k + min(j0 + j, a.k - 1)] : 1.f;
+      }
 #pragma unroll
       for (int j = 0; j < kSlots; ++j) {
         if (row[j] < 0) continue;
-        const float w = a.weights ? a.weights[(int64_t)t * a.k + j0 + j] : 1.f;
+        const float w = ws[j];
         float f[Un::kN];
         Un::widen(v[j], f);
 #pragma unroll
@@ -694,9 +717,10 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(RowsArgs a) {
     int row[kSlots];
     float w[kSlots], dot[kSlots] = {};
     slot_numbers(a, t, j0, row);
+    const uint32_t unnamed = a.sorted_ids ? unnamed_rows(a, t, j0) : 0u;
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
-      w[j] = row[j] >= 0 && a.weights ? a.weights[(int64_t)t * a.k + j0 + j] : 1.f;
+      w[j] = a.weights ? a.weights[(int64_t)t * a.k + min(j0 + j, a.k - 1)] : 1.f;
     for (int c = g; c < units; c += G) {
       float d[Un::kN];
       Un::widen(dout[c], d);
@@ -720,6 +744,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(RowsArgs a) {
           for (int i = 0; i < Un::kN; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
         }
       }
+      if (unnamed) zero_unit<Row, Un>(a, t, j0, unnamed, c);
     }
     if (a.d_weights) {
 #pragma unroll
@@ -744,7 +769,6 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(RowsArgs a) {
       }
     }
   }
-  if (on && a.slot_rows) zero_rows<Row, Un, G>(a, t, g);
 }
 
 enum RowsOp { kDispatch, kCombine, kCombineBackward };

@@ -495,25 +495,25 @@ __device__ __forceinline__ void zero_rows(const W4Args& a, const int* list, int 
   }
 }
 
-// Few column tiles: a workgroup owns one tile, its waves split k and add their
+// Few column tiles: a workgroup owns NT tiles, its waves split k and add their
 // sums up through LDS in wave order; x goes straight to the operands.
-template <bool F32, int SG, bool ZP, int MB>
+template <bool F32, int SG, bool ZP, int MB, int NT>
 __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t* ids, int n_rows, int E, W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
-  constexpr int kStride = 20, kRows = 16 * MB;
+  constexpr int kCols = 16 * NT, kStride = kCols + 4, kRows = 16 * MB;
   __shared__ int list[kScan];
   __shared__ int counts[kMaxWaves];
   __shared__ float red[kMaxWaves * kRows * kStride];
   const uint32_t base = base_pair();
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int e = place_expert(ids, E, a.by_row), tile = (int)blockIdx.x;
+  const int e = place_expert(ids, E, a.by_row), tile = (int)blockIdx.x * NT;
   const int n0 = tile * 16, chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
   WBufs wb;
-  wb.set<SG, (F32 ? 4 : 2), ZP>(a, e * a.tiles + tile, 1);
-  WChunk<F32, SG, ZP, 1> wc;
+  wb.set<SG, (F32 ? 4 : 2), ZP>(a, e * a.tiles + tile, min(NT, a.tiles - tile));
+  WChunk<F32, SG, ZP, NT> wc;
 
   for (int seg = 0; seg < n_rows; seg += kScan) {
     const int len = min(kScan, n_rows - seg);
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
     if (E > 0) {
       const RowList l = list_rows(ids, E, e, a.by_row, seg, len, list, counts);
       n_list = l.live;
-      if (l.dead > 0 && blockIdx.z == 0) zero_rows<Row>(a, list, l.dead, n0, 16);
+      if (l.dead > 0 && blockIdx.z == 0) zero_rows<Row>(a, list, l.dead, n0, kCols);
     }
     for (int b0 = (int)blockIdx.z * kRows; b0 < n_list; b0 += (int)gridDim.z * kRows) {
       uint32_t row_off[MB];
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
         const int row = at < n_list ? (E > 0 ? list[at] : seg + at) : -1;
         row_off[mb] = row >= 0 ? (uint32_t)row / a.topk * a.x_ld_bytes : kPast;
       }
-      f32x4 acc[1][MB] = {};
+      f32x4 acc[NT][MB] = {};
       for (int c = wave; c < chunks; c += waves) {
         XRaw<F32> x[MB][4];
 #pragma unroll
@@ -540,16 +540,18 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
           for (int ks = 0; ks < 4; ++ks)
             x[mb][ks] = load_x<F32>(rx, row_off[mb], c * 128 + ks * 32 + lg * 8, a.K);
         wc.load(a, wb, c, lane);
-        add_chunk<F32, SG, ZP, 1, MB>(
+        add_chunk<F32, SG, ZP, NT, MB>(
             wc, [&](int mb, int ks, XFrag<F32>& f) { f.set(x[mb][ks]); }, base, acc);
       }
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
-        *reinterpret_cast<f32x4*>(&red[(wave * kRows + mb * 16 + li) * kStride + lg * 4]) =
-            acc[0][mb];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          *reinterpret_cast<f32x4*>(
+              &red[(wave * kRows + mb * 16 + li) * kStride + nt * 16 + lg * 4]) = acc[nt][mb];
       lds_barrier();
-      for (int i = tid; i < kRows * 4; i += (int)blockDim.x) {
-        const int r = i >> 2, c4 = (i & 3) * 4;
+      for (int i = tid; i < kRows * (kCols / 4); i += (int)blockDim.x) {
+        const int r = i / (kCols / 4), c4 = i % (kCols / 4) * 4;
         f32x4 sum = *reinterpret_cast<const f32x4*>(&red[r * kStride + c4]);
         for (int w = 1; w < waves; ++w)
           sum += *reinterpret_cast<const f32x4*>(&red[(w * kRows + r) * kStride + c4]);
@@ -782,7 +784,7 @@ struct W4Rows {
 
 struct W4Plan {
   bool stream, by_row;
-  int places, mb, waves, k_waves, splits, per_slice, slices;
+  int places, mb, tiles, waves, k_waves, splits, per_slice, slices;
 };
 
 W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
@@ -797,6 +799,7 @@ W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
   // Row blocks of 16 per pass over the weights: two once an expert holds more
   // than ten rows on average.
   p.mb = !f32 && (places == 1 ? mean > 16 : mean > 10) ? 2 : 1;
+  const int64_t blocks = (mean + 16 * p.mb - 1) / (16 * p.mb);  // passes
   const int64_t pairs = (tiles + kPair - 1) / kPair;
   // Streaming pays from 512 pairs of tiles (9 experts of 2048 x 1024, 16 rows
   // each: 10.3 us, split 15.6; 4 experts of 4000 x 512, 500 pairs: 7.7, split
@@ -845,12 +848,16 @@ W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
   } else {
     const int64_t per = (chunks + kMaxWaves - 1) / kMaxWaves;
     p.waves = (int)((chunks + per - 1) / per);
-    p.slices = (int)tiles;
+    // Two tiles a workgroup where several passes over the rows fill the CUs: x,
+    // which each workgroup reads whole, is then what moves (one weight of 4000 x
+    // 4000, 44 rows: 14.0 us with one tile, 11.2 with two; 24 rows, one pass: 8.7
+    // and 10.2; 2048 x 2048, 44 rows: 6.9 and 7.4).
+    p.tiles = blocks >= 2 && places * tiles * blocks > 320 ? 2 : 1;
+    p.slices = (int)((tiles + p.tiles - 1) / p.tiles);
   }
   // Rows of one expert over several workgroups: once an expert holds more than
   // two passes on average, or while there are less than two workgroups a CU (one
   // weight of 4000 x 4000, 40 rows: 13.6 us in one workgroup per tile, 6.9 in two).
-  const int64_t blocks = (mean + 16 * p.mb - 1) / (16 * p.mb);
   const int64_t wgs = places * p.slices;
   int64_t splits = blocks <= 2 ? 1 : (blocks + 1) / 2;
   if (splits < blocks && wgs * splits < 512) splits = blocks < 512 / wgs + 1 ? blocks : 512 / wgs + 1;
@@ -872,7 +879,12 @@ void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
   a.wave_magic = (uint32_t)(((1ull << 32) + a.pair_waves - 1) / a.pair_waves);
   const dim3 grid((unsigned)a.slices, (unsigned)p.places, (unsigned)p.splits), block(64 * p.waves);
   if (!p.stream) {
-    hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB>), grid, block, 0, s, ids, n_rows, E, a);
+    if (p.tiles == 2)
+      hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 2>), grid, block, 0, s, ids, n_rows, E,
+                         a);
+    else
+      hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 1>), grid, block, 0, s, ids, n_rows, E,
+                         a);
     return;
   }
   const int chunks = (a.ksteps + 3) / 4, turn = kAhead * p.k_waves;

@@ -13,6 +13,9 @@
 // into three bf16 parts (8 + 8 + 8 bits, exact), one MFMA each: the products
 // stay exact and the sums fp32.
 //
+// (In the streaming form fp32 rows bring these sums along in LDS: their MFMAs
+// would be a third of all.)
+//
 // The offset makes |16 + v| sums cancel: their fp32 rounding is about 5 times
 // that of a plain sum of the same length, far below one bf16 rounding and
 // below 1e-6 of an fp32 result. A row of x with an infinity or a NaN gives
@@ -199,6 +202,12 @@ __device__ __forceinline__ u32x4 unpack(uint32_t w, uint32_t base) {
 template <bool F32>
 struct XRaw {
   u32x4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ float sum() const {  // of 8 fp32 values
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += __uint_as_float(v[0][i]) + __uint_as_float(v[F32][i]);
+    return s;
+  }
 };
 
 template <bool F32>
@@ -307,10 +316,13 @@ struct WChunk {
 };
 
 // acc += the chunk's products, group by group. `x(mb, ks, f)` fills f with the
-// bf16 parts of k step ks of row block mb.
-template <bool F32, int SG, bool ZP, int NT, int MB, typename X>
+// bf16 parts of k step ks of row block mb. `sum(mb, ks)`, if given, is minus the
+// sum of that step's x; else MFMAs with a constant first operand take it.
+struct NoSums {};
+template <bool F32, int SG, bool ZP, int NT, int MB, typename X, typename S = NoSums>
 __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x,
-                                          uint32_t base, f32x4 (&acc)[NT][MB]) {
+                                          uint32_t base, f32x4 (&acc)[NT][MB], S sum = S{}) {
+  constexpr bool kSums = !std::is_same<S, NoSums>::value;
   constexpr int kPer = 4 / SG, kParts = XFrag<F32>::kParts;
   const uint32_t kc = ZP ? 0xbf80bf80u : 0xc1c0c1c0u;  // bf16 -1, or -(16 + 8)
   const u32x4 cons = {kc, kc, kc, kc};
@@ -323,11 +335,17 @@ __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) x(mb, sg * kPer + ks, f[mb][ks]);
 #pragma unroll
-    for (int ks = 0; ks < kPer; ++ks)
+    for (int ks = 0; ks < kPer; ++ks) {
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
+      for (int mb = 0; mb < MB; ++mb) {
+        if constexpr (kSums) {
+          dc[mb][0] += sum(mb, sg * kPer + ks);
+        } else {
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) dc[mb] = mfma(cons, f[mb][ks].p[p], dc[mb]);
+          for (int p = 0; p < kParts; ++p) dc[mb] = mfma(cons, f[mb][ks].p[p], dc[mb]);
+        }
+      }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       f32x4 s[MB];
@@ -351,15 +369,19 @@ __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x
         if constexpr (ZP) z = (float)((wc.z[nt][sg] >> (8 * i)) & 0xffu);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-          const float t = ZP ? fmaf(z, dc[mb][i], s[mb][i]) : s[mb][i] + dc[mb][i];
+          float t;
+          if constexpr (kSums)
+            t = fmaf(ZP ? z : 24.f, dc[mb][0], s[mb][i]);
+          else
+            t = ZP ? fmaf(z, dc[mb][i], s[mb][i]) : s[mb][i] + dc[mb][i];
           acc[nt][mb][i] = fmaf(sc, t, acc[nt][mb][i]);
         }
       }
     }
+    // operands of the next chunk (fp32, with three parts: of the next group) are
+    // not fetched into registers ahead, which the weights in flight need
+    if (F32 || sg == SG - 1) __builtin_amdgcn_sched_barrier(0);
   }
-  // operands of the next chunk are not fetched into registers ahead, which the
-  // weights in flight need
-  __builtin_amdgcn_sched_barrier(0);
 }
 
 template <typename Row>
@@ -569,13 +591,15 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
 // each wave then streams whole columns: pairs of tiles over all of k, kAhead
 // chunks of weights requested ahead, no barrier between.
 constexpr int kPair = 2;   // tiles per wave and step
-constexpr int kAhead = 3;  // chunks in flight per wave
+// Chunks in flight per wave (fp32 with groups of 32: what their 16 scales a tile
+// leave of the registers).
+constexpr int ahead(bool f32, int sg) { return f32 && sg == 4 ? 2 : 3; }
 constexpr int kLds = 160 * 1024;        // of a CU
 constexpr int kListLds = kScan * 4 + 256;  // the list and the counts
-constexpr int chunk_lds(bool f32, int mb) { return 4 * mb * (f32 ? 3 : 1) * 1024; }
+constexpr int chunk_lds(bool f32, int mb) { return 4 * mb * (f32 ? 3 * 1024 + 64 : 1024); }
 // Chunks of x rows that fit a workgroup's LDS, in whole turns of the ring.
 constexpr int panel_chunks(bool f32, int mb) {
-  return (kLds - kListLds) / chunk_lds(f32, mb) / kAhead * kAhead;
+  return (kLds - kListLds) / chunk_lds(f32, mb) / 6 * 6;
 }
 constexpr int stream_waves(bool f32) { return f32 ? 8 : 12; }  // most per workgroup
 
@@ -583,11 +607,14 @@ template <bool F32, int SG, bool ZP, int MB>
 __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const int32_t* ids, int n_rows, int E, W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
   typedef WChunk<F32, SG, ZP, kPair> Chunk;
-  constexpr int kRows = 16 * MB, kParts = XFrag<F32>::kParts;
+  constexpr int kRows = 16 * MB, kParts = XFrag<F32>::kParts, kAhead = ahead(F32, SG);
   const int panel = a.panel;
   __shared__ int list[kScan];
   __shared__ int counts[stream_waves(F32)];
   extern __shared__ u32x4 xs[];  // [k step][row block][part][lane]
+  // fp32 rows: minus the sums of x by k step and row, behind the operands
+  float* x_sums = reinterpret_cast<float*>(xs + min(panel, (a.ksteps + 3) >> 2) *
+                                                    (4 * MB * kParts * 64));
   const uint32_t base = base_pair();
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
@@ -665,6 +692,11 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
                 q.set(r[i]);
 #pragma unroll
                 for (int p = 0; p < kParts; ++p) xs[(f * kParts + p) * 64 + lane] = q.p[p];
+                // minus the sum of the step's x of each row
+                float v = -r[i].sum();
+                v += __shfl_xor(v, 16);
+                v += __shfl_xor(v, 32);
+                if (lane < 16) x_sums[f * 16 + lane] = v;
               }
             }
           }
@@ -721,14 +753,17 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
               const int c = c0 + d * kw;
               if (c < p1) {
                 const u32x4* px = xs + (c - p0) * (4 * MB * kParts * 64) + lane;
-                add_chunk<F32, SG, ZP, kPair, MB>(
-                    ring[d],
-                    [&](int mb, int ks, XFrag<F32>& f) {
+                auto operand = [&](int mb, int ks, XFrag<F32>& f) {
 #pragma unroll
-                      for (int p = 0; p < kParts; ++p)
-                        f.p[p] = px[((ks * MB + mb) * kParts + p) * 64];
-                    },
-                    base, acc);
+                  for (int p = 0; p < kParts; ++p) f.p[p] = px[((ks * MB + mb) * kParts + p) * 64];
+                };
+                if constexpr (F32) {
+                  const float* ps = x_sums + (c - p0) * 64 + li;
+                  add_chunk<F32, SG, ZP, kPair, MB>(ring[d], operand, base, acc,
+                                                    [&](int, int ks) { return ps[ks * 16]; });
+                } else {
+                  add_chunk<F32, SG, ZP, kPair, MB>(ring[d], operand, base, acc);
+                }
               }
               request(ring[d]);
             }
@@ -821,7 +856,7 @@ W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
     // has chunks for (64 experts of 512 x 4096, 2 rows each: 1, 2, 3 waves to a
     // pair 19.5, 17.0, 23.9 us; 3 do not fit one round of workgroups) ...
     for (int kw = 4; kw >= 1 && p.waves == 0; --kw) {
-      if (kw > 1 && (chunks < 3 * kw || kAhead * kw > most)) continue;
+      if (kw > 1 && (chunks < 3 * kw || ahead(f32, sg) * kw > most)) continue;
       for (int64_t wn = 1; wn * kw <= most_waves; ++wn) {
         if (wn * kw < 4) continue;
         const int64_t slices = (pairs + wn - 1) / wn;
@@ -857,7 +892,8 @@ W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
   }
   // Rows of one expert over several workgroups: once an expert holds more than
   // two passes on average, or while there are less than two workgroups a CU (one
-  // weight of 4000 x 4000, 40 rows: 13.6 us in one workgroup per tile, 6.9 in two).
+  // weight of 4000 x 4000, 24 rows of fp32: 17.7 us in one workgroup per tile,
+  // 13.4 in two). More, for the experts above the average, gave nothing.
   const int64_t wgs = places * p.slices;
   int64_t splits = blocks <= 2 ? 1 : (blocks + 1) / 2;
   if (splits < blocks && wgs * splits < 512) splits = blocks < 512 / wgs + 1 ? blocks : 512 / wgs + 1;
@@ -887,7 +923,7 @@ void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
                          a);
     return;
   }
-  const int chunks = (a.ksteps + 3) / 4, turn = kAhead * p.k_waves;
+  const int chunks = (a.ksteps + 3) / 4, kAhead = ahead(F32, SG), turn = kAhead * p.k_waves;
   a.panel = panel_chunks(F32, MB) / turn * turn;
   a.panel_turns = a.panel / p.k_waves;
   a.turns = ((chunks + p.k_waves - 1) / p.k_waves + kAhead - 1) / kAhead * kAhead;

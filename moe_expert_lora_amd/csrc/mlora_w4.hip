@@ -322,7 +322,7 @@ struct NoSums {};
 template <bool F32, int SG, bool ZP, int NT, int MB, typename X, typename S = NoSums>
 __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x,
                                           uint32_t base, f32x4 (&acc)[NT][MB], S sum = S{}) {
-  constexpr bool kSums = !std::is_same<S, NoSums>::value;
+  constexpr bool kSums = !std::is_same<S, NoSums>::value, kChain = !ZP && !kSums;
   constexpr int kPer = 4 / SG, kParts = XFrag<F32>::kParts;
   const uint32_t kc = ZP ? 0xbf80bf80u : 0xc1c0c1c0u;  // bf16 -1, or -(16 + 8)
   const u32x4 cons = {kc, kc, kc, kc};
@@ -350,7 +350,7 @@ __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x
     for (int nt = 0; nt < NT; ++nt) {
       f32x4 s[MB];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) s[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int mb = 0; mb < MB; ++mb) s[mb] = kChain ? dc[mb] : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < kPer; ++ks) {
         const u32x4 wf = unpack(wc.w[nt][sg * kPer + ks], base);
@@ -373,7 +373,7 @@ __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x
           if constexpr (kSums)
             t = fmaf(ZP ? z : 24.f, dc[mb][0], s[mb][i]);
           else
-            t = ZP ? fmaf(z, dc[mb][i], s[mb][i]) : s[mb][i] + dc[mb][i];
+            t = ZP ? fmaf(z, dc[mb][i], s[mb][i]) : kChain ? s[mb][i] : s[mb][i] + dc[mb][i];
           acc[nt][mb][i] = fmaf(sc, t, acc[nt][mb][i]);
         }
       }

@@ -4,12 +4,15 @@ Argument marshalling only. Every function has the name of the C entry point it
 calls (include/mlora.h); host functions take and return NumPy arrays, the
 device calls (the folds, and the MoE layer's operators around them) take
 PyTorch tensors (used only for device memory and the current stream) and
-enqueue the library's HIP kernels. There is no fallback path: when
+enqueue the library's HIP kernels. The folds are marshalled here through
+ctypes, the MoE layer's operators by the extension module _native, which reads
+their tensors without Python's attribute calls. There is no fallback path: when
 libmlora.so is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import List, Optional, Tuple
 
@@ -143,13 +146,16 @@ class W4Route(ctypes.Structure):
         ("dtype", ctypes.c_int32),
     ]
 
+    @functools.cached_property
+    def address(self) -> int:
+        """Of the struct (it stays where it is while the object lives)."""
+        return ctypes.addressof(self)
+
 
 _lib: Optional[ctypes.CDLL] = None
-# what the device calls take from torch, bound once by load() (device calls
-# load the library before they touch a tensor)
-_torch = None
+_bound = None        # the extension module _native, once _load_native() has run
+# what the folds take from torch, bound once by load()
 _DTYPES: dict = {}   # torch dtype -> MLORA_* code
-_I32 = _F32 = None
 _raw_stream = _device = None
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
@@ -160,7 +166,7 @@ _f32p = ctypes.POINTER(ctypes.c_float)
 
 def load() -> ctypes.CDLL:
     """Load libmlora.so (once). Raises when it has not been built."""
-    global _lib, _torch, _I32, _F32, _raw_stream, _device
+    global _lib, _raw_stream, _device
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -170,9 +176,7 @@ def load() -> ctypes.CDLL:
     # binds to the same runtime instance that owns the tensors and streams.
     try:
         import torch
-        _torch = torch
         _DTYPES.update({torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32})
-        _I32, _F32 = torch.int32, torch.float32
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _device = torch._C._cuda_getDevice
     except ImportError:
@@ -234,6 +238,20 @@ def load() -> ctypes.CDLL:
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+def _load_native():
+    """Load the extension module (once), after the library and torch. Raises
+    when it has not been built."""
+    global _bound
+    load()
+    try:
+        from . import _native as module
+    except ImportError as e:
+        raise ImportError(f"{e}; build it with `python -m moe_expert_lora_amd.build`") from e
+    module.set_error(MloraError)
+    _bound = module
+    return module
 
 
 def _err(code: int) -> MloraError:
@@ -733,67 +751,22 @@ def mlora_gather_bgmv_multi(route: MultiRoute, x, base_out, indices, row_adapter
 # the MoE layer around the fold
 # ---------------------------------------------------------------------------
 
-# A decode step makes these calls back to back, and the wrapper's time is most
-# of a small call's: arguments are taken apart once, in few attribute reads.
-
-def _vec(t, name, dtype) -> int:
-    """Data pointer of a contiguous device tensor of one dtype."""
-    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    return _dev(t, name, dtype)  # raises, naming what is wrong
-
-
-def _vec_or_null(t, name, dtype) -> Optional[int]:
-    return None if t is None else _vec(t, name, dtype)
-
-
-def _mat(t, name):
-    """(data pointer, rows, columns, row stride) of a 2-D device tensor with
-    contiguous rows, as _rows_2d."""
-    shape = t.shape
-    if len(shape) == 2 and t.is_cuda and t.is_contiguous():
-        n, m = shape
-        return t.data_ptr(), n, m, m
-    p, n, ld = _rows_2d(t, name)
-    return p, n, shape[1], ld
-
+# Arguments are checked in the extension module: TypeError and ValueError for
+# tensors that do not fit each other, MloraError for what the library refuses.
 
 def mlora_router_topk(logits, indices, weights, renormalize: bool = False, stream=None) -> None:
     """Top-k experts of each row of ``logits`` [n_tokens, n_experts] (bf16 or
     float32, contiguous rows) into ``indices`` (int32) and ``weights``
     (float32), both [n_tokens, top_k]."""
-    lib = _lib or load()
-    p, n, experts, ld = _mat(logits, "logits")
-    shape = indices.shape
-    if len(shape) != 2 or shape[0] != n or shape != weights.shape:
-        raise ValueError("indices and weights must be [n_tokens, top_k]")
-    rc = lib.mlora_router_topk(p, ld, _dtype_code(logits), n, experts, shape[1],
-                               1 if renormalize else 0, _vec(indices, "indices", _I32),
-                               _vec(weights, "weights", _F32), _stream_handle(stream))
-    if rc:
-        raise _err(rc)
+    (_bound or _load_native()).router_topk(logits, indices, weights, renormalize, stream)
 
 
 def mlora_router_topk_backward(logits, indices, d_weights, d_logits, renormalize: bool = False,
                                stream=None) -> None:
     """Gradient of mlora_router_topk's weights into ``d_logits`` (written whole),
     from the forward's logits and indices."""
-    lib = _lib or load()
-    p, n, experts, ld = _mat(logits, "logits")
-    dp, dn, d_experts, d_ld = _mat(d_logits, "d_logits")
-    if d_logits.dtype is not logits.dtype:
-        raise TypeError("d_logits dtype differs from logits'")
-    if dn != n or d_experts != experts:
-        raise ValueError("d_logits must have the shape of logits")
-    shape = indices.shape
-    if len(shape) != 2 or shape[0] != n or shape != d_weights.shape:
-        raise ValueError("indices and d_weights must be [n_tokens, top_k]")
-    rc = lib.mlora_router_topk_backward(p, ld, _dtype_code(logits), n, experts, shape[1],
-                                        1 if renormalize else 0, _vec(indices, "indices", _I32),
-                                        _vec(d_weights, "d_weights", _F32), dp, d_ld,
-                                        _stream_handle(stream))
-    if rc:
-        raise _err(rc)
+    (_bound or _load_native()).router_topk_backward(logits, indices, d_weights, d_logits,
+                                                    renormalize, stream)
 
 
 def mlora_moe_sort_workspace_bytes(n_slots: int, n_experts: int) -> int:
@@ -806,98 +779,29 @@ def mlora_moe_sort(ids, n_experts: int, expert_offsets, sorted_ids, slot_rows, w
     """Stable sort of the flat (token, slot) ids by expert: fills
     ``expert_offsets`` [n_experts + 1], ``sorted_ids`` and ``slot_rows``
     (all int32); ids outside [0, n_experts) are dropped (-1)."""
-    lib = _lib or load()
-    n = ids.numel()
-    if expert_offsets.numel() != n_experts + 1:
-        raise ValueError("expert_offsets must have n_experts + 1 entries")
-    if sorted_ids.numel() != n or slot_rows.numel() != n:
-        raise ValueError("sorted_ids and slot_rows must have one entry per id")
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None and workspace.numel():
-        ws_ptr = _dev(workspace, "workspace")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    rc = lib.mlora_moe_sort(_vec(ids, "ids", _I32), n, n_experts,
-                            _vec(expert_offsets, "expert_offsets", _I32),
-                            _vec(sorted_ids, "sorted_ids", _I32),
-                            _vec(slot_rows, "slot_rows", _I32), ws_ptr, ws_bytes,
-                            _stream_handle(stream))
-    if rc:
-        raise _err(rc)
+    (_bound or _load_native()).moe_sort(ids, n_experts, expert_offsets, sorted_ids, slot_rows,
+                                        workspace, stream)
 
 
 def mlora_moe_dispatch(x, rows, sorted_ids, slot_rows, top_k: int, stream=None) -> None:
     """Copies token rows of ``x`` [n_tokens, dim] to their sorted ``rows``
     [n_tokens * top_k, dim]; rows no slot names get zeros. The maps are
     mlora_moe_sort's. Its gradient: mlora_moe_combine with no weights."""
-    lib = _lib or load()
-    xp, n, dim, x_ld = _mat(x, "x")
-    rp, n_rows, r_dim, r_ld = _mat(rows, "rows")
-    if rows.dtype is not x.dtype:
-        raise TypeError("rows dtype differs from x's")
-    if r_dim != dim or n_rows != n * top_k:
-        raise ValueError("rows must be [n_tokens * top_k, dim]")
-    if sorted_ids.numel() != n_rows or slot_rows.numel() != n_rows:
-        raise ValueError("sorted_ids and slot_rows must have one entry per row")
-    rc = lib.mlora_moe_dispatch(xp, x_ld, _dtype_code(x), n, dim, top_k,
-                                _vec(sorted_ids, "sorted_ids", _I32),
-                                _vec(slot_rows, "slot_rows", _I32), rp, r_ld,
-                                _stream_handle(stream))
-    if rc:
-        raise _err(rc)
+    (_bound or _load_native()).moe_dispatch(x, rows, sorted_ids, slot_rows, top_k, stream)
 
 
 def mlora_moe_combine(rows, out, top_k: int, weights=None, slot_rows=None, stream=None) -> None:
     """``out[t]`` = sum over slots of weights[t, j] * rows[slot_rows[t * top_k + j]]
     (``slot_rows`` None: rows in flat (token, slot) order; ``weights`` None: 1)."""
-    lib = _lib or load()
-    rp, n_rows, dim, r_ld = _mat(rows, "rows")
-    op, n, o_dim, o_ld = _mat(out, "out")
-    if rows.dtype is not out.dtype:
-        raise TypeError("out dtype differs from rows'")
-    if dim != o_dim:
-        raise ValueError("rows and out differ in width")
-    if (weights is not None and weights.numel() != n * top_k) or (
-            slot_rows is not None and slot_rows.numel() != n * top_k):
-        raise ValueError("weights and slot_rows must have n_tokens * top_k entries")
-    rc = lib.mlora_moe_combine(rp, r_ld, n_rows, _dtype_code(rows), n, dim, top_k,
-                               _vec_or_null(weights, "weights", _F32),
-                               _vec_or_null(slot_rows, "slot_rows", _I32),
-                               op, o_ld, _stream_handle(stream))
-    if rc:
-        raise _err(rc)
+    (_bound or _load_native()).moe_combine(rows, out, top_k, weights, slot_rows, stream)
 
 
 def mlora_moe_combine_backward(d_out, rows, weights, d_rows, d_weights, top_k: int,
                                slot_rows=None, sorted_ids=None, stream=None) -> None:
     """Gradient of mlora_moe_combine into ``d_rows`` [n_tokens * top_k, dim] and
     ``d_weights`` [n_tokens, top_k] (None: not computed, ``rows`` not read)."""
-    lib = _lib or load()
-    dp, n, dim, d_ld = _mat(d_out, "d_out")
-    op, n_rows, o_dim, o_ld = _mat(d_rows, "d_rows")
-    dtype = d_out.dtype
-    if d_rows.dtype is not dtype:
-        raise TypeError("d_rows dtype differs from d_out's")
-    if o_dim != dim or n_rows != n * top_k:
-        raise ValueError("d_rows must be [n_tokens * top_k, dim]")
-    rp, r_ld = None, 0
-    if d_weights is not None:
-        rp, r_rows, r_dim, r_ld = _mat(rows, "rows")
-        if rows.dtype is not dtype:
-            raise TypeError("rows dtype differs from d_out's")
-        if r_dim != dim or r_rows != n_rows:
-            raise ValueError("rows must have the shape of d_rows")
-    for t in (weights, d_weights, slot_rows, sorted_ids):
-        if t is not None and t.numel() != n_rows:
-            raise ValueError("weights, d_weights and the maps must have one entry per row")
-    rc = lib.mlora_moe_combine_backward(dp, d_ld, rp, r_ld, _dtype_code(d_out), n, dim, top_k,
-                                        _vec_or_null(weights, "weights", _F32),
-                                        _vec_or_null(slot_rows, "slot_rows", _I32),
-                                        _vec_or_null(sorted_ids, "sorted_ids", _I32),
-                                        op, o_ld,
-                                        _vec_or_null(d_weights, "d_weights", _F32),
-                                        _stream_handle(stream))
-    if rc:
-        raise _err(rc)
+    (_bound or _load_native()).moe_combine_backward(d_out, rows, weights, d_rows, d_weights,
+                                                    top_k, slot_rows, sorted_ids, stream)
 
 
 def mlora_w4_packed_bytes(n_experts: int, k_in: int, n_out: int, group: int, dtype: int,
@@ -942,17 +846,5 @@ def mlora_w4_gather_gemv(route: W4Route, x, out, ids=None, top_k: int = 1,
                          x_by_row: bool = False, stream=None) -> None:
     """``out[r]`` = W[ids[r]] x[r // top_k] (or x[r] with ``x_by_row``); rows with
     an id outside the route's experts get zeros. ``ids`` None: one weight."""
-    lib = _lib or load()
-    if _dtype_code(x) != route.dtype or out.dtype is not x.dtype:
-        raise TypeError("x / out dtype differs from the route's")
-    xp, x_rows, k_in, x_ld = _mat(x, "x")
-    op, n_rows, n_out, o_ld = _mat(out, "out")
-    if k_in != route.k_in or n_out != route.n_out:
-        raise ValueError("x / out widths differ from the route's k_in / n_out")
-    if ids is not None and ids.numel() != n_rows:
-        raise ValueError("ids must have one entry per out row")
-    rc = lib.mlora_w4_gather_gemv(ctypes.byref(route), xp, x_rows, x_ld, 1 if x_by_row else 0, op,
-                                  o_ld, _vec_or_null(ids, "ids", _I32), n_rows,
-                                  top_k, _stream_handle(stream))
-    if rc:
-        raise _err(rc)
+    (_bound or _load_native()).w4_gather_gemv(route.address, x, out, ids, top_k, x_by_row,
+                                              stream)

@@ -7,6 +7,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -20,7 +21,11 @@ SOURCES = [os.path.join(CSRC, name)
 # measurement probes for bench.py (launch and read-pattern floors), a library of their own
 PROBE_LIB = os.path.join(PKG, "libmlora_probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "mlora_probe.hip")]
+# the CPython binding of the MoE layer's operators, against libmlora.so and torch
+BINDING = os.path.join(PKG, "_native" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+BINDING_SOURCE = os.path.join(CSRC, "mlora_binding.cpp")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 FLAGS = [
     "--offload-arch=gfx950",
@@ -61,10 +66,27 @@ def _compile(sources, lib, verbose):
         os.replace(out, lib)
 
 
+def _compile_binding(verbose):
+    """Host code only: torch's core headers, Python's and HIP's."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    system = [*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    out = BINDING + ".tmp"
+    _run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+          "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          "-I", INCLUDE, *[a for d in system for a in ("-isystem", d)], BINDING_SOURCE,
+          "-L", lib_dir, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-L", PKG,
+          "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-o", out], verbose)
+    os.replace(out, BINDING)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile moe_expert_lora_amd/libmlora.so (the fold) and libmlora_probe.so
-    (bench.py's measurement probes); returns the fold library's path."""
+    """Compile moe_expert_lora_amd/libmlora.so (the fold and the MoE layer's
+    operators), the CPython binding of the latter, and libmlora_probe.so
+    (bench.py's measurement probes); returns libmlora.so's path."""
     _compile(SOURCES, LIB, verbose)
+    _compile_binding(verbose)
     _compile(PROBE_SOURCES, PROBE_LIB, verbose)
     return LIB
 

@@ -155,6 +155,30 @@ def test_w4_gemv_no_rows_and_null_route(lib):
 
 
 # ---------------------------------------------------------------------------
+# the Python functions
+# ---------------------------------------------------------------------------
+
+def test_python_functions_take_device_tensors():
+    """Host tensors and other objects are refused before anything is called."""
+    torch = pytest.importorskip("torch")
+    x, i = torch.zeros((4, 8)), torch.zeros(4, dtype=torch.int32)
+    route = ml.W4Route(P, P, None, 1, 8, 8, 32, F32)
+    calls = [lambda t: ml.mlora_router_topk(t, i, x),
+             lambda t: ml.mlora_router_topk_backward(t, i, x, x),
+             lambda t: ml.mlora_moe_sort(t, 3, i, i, i),
+             lambda t: ml.mlora_moe_dispatch(t, x, i, i, 1),
+             lambda t: ml.mlora_moe_combine(t, x, 1),
+             lambda t: ml.mlora_moe_combine_backward(t, x, x, x, x, 1),
+             lambda t: ml.mlora_w4_gather_gemv(route, t, x)]
+    for call in calls:
+        with pytest.raises(ValueError, match="must be a device tensor"):
+            call(x)
+        with pytest.raises(TypeError, match="must be a tensor"):
+            call([1.0])
+    assert route.address == ctypes.addressof(route)
+
+
+# ---------------------------------------------------------------------------
 # the fp64 forms themselves
 # ---------------------------------------------------------------------------
 

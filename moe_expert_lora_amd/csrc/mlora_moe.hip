@@ -34,6 +34,19 @@ struct RouterArgs {
   int32_t renorm;
 };
 
+// A kernel's leading plain arguments arrive in registers at its start; what is
+// needed for the first loads is passed there, and the struct, which is read
+// from memory, for the rest.
+__device__ __forceinline__ void set_lead(RouterArgs& a, const void* logits, int64_t ld,
+                                         int32_t n_tokens, int32_t E, int32_t k, int32_t renorm) {
+  a.logits = logits;
+  a.ld = ld;
+  a.n_tokens = n_tokens;
+  a.E = E;
+  a.k = k;
+  a.renorm = renorm;
+}
+
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr float kNegInf = -__builtin_inff();
@@ -78,7 +91,9 @@ __device__ __forceinline__ void load_row(const void* base, int64_t off, int E, i
 }
 
 template <typename Row, int LPT, int VPL, int VEC, bool WIDE>
-__global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
+__global__ void __launch_bounds__(256) router_topk_kernel(const void* logits, int64_t ld, int32_t n_tokens, int32_t E,
+                                                          int32_t k, int32_t renorm, RouterArgs a) {
+  set_lead(a, logits, ld, n_tokens, E, k, renorm);
   constexpr bool kPacked = sizeof(typename Row::elem) == 2;
   const int gl = threadIdx.x & (LPT - 1);
   const int token = (int)((blockIdx.x * blockDim.x + threadIdx.x) / LPT);
@@ -149,7 +164,10 @@ __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
 // dw_e reaches expert e's lane through a row of LDS; a word no dw has marks
 // the experts that were not chosen.
 template <typename Row, int LPT, int VPL, int VEC, bool WIDE>
-__global__ void __launch_bounds__(256) router_backward_kernel(RouterArgs a) {
+__global__ void __launch_bounds__(256) router_backward_kernel(const void* logits, int64_t ld, int32_t n_tokens,
+                                                              int32_t E, int32_t k, int32_t renorm,
+                                                              RouterArgs a) {
+  set_lead(a, logits, ld, n_tokens, E, k, renorm);
   constexpr uint32_t kUnset = 0xffffffffu;
   __shared__ uint32_t lds[256 / LPT][LPT * VPL];
   const int gl = threadIdx.x & (LPT - 1);
@@ -230,9 +248,11 @@ void launch_router(const RouterArgs& a, bool backward, hipStream_t s) {
   const int threads = lanes < 64 * 1024 ? 64 : 256;
   const dim3 grid((unsigned)((lanes + threads - 1) / threads));
   if (backward)
-    hipLaunchKernelGGL((router_backward_kernel<Row, LPT, VPL, VEC, WIDE>), grid, dim3(threads), 0, s, a);
+    hipLaunchKernelGGL((router_backward_kernel<Row, LPT, VPL, VEC, WIDE>), grid, dim3(threads), 0, s,
+                       a.logits, a.ld, a.n_tokens, a.E, a.k, a.renorm, a);
   else
-    hipLaunchKernelGGL((router_topk_kernel<Row, LPT, VPL, VEC, WIDE>), grid, dim3(threads), 0, s, a);
+    hipLaunchKernelGGL((router_topk_kernel<Row, LPT, VPL, VEC, WIDE>), grid, dim3(threads), 0, s,
+                       a.logits, a.ld, a.n_tokens, a.E, a.k, a.renorm, a);
 }
 
 // Lanes per token and values per lane: 16 lanes hold up to 128 experts (four
@@ -396,7 +416,12 @@ enum SortMode {
 constexpr int kSortCopies = 4;  // of each counter in kSortRecount: fewer lanes on one address
 
 template <int R, SortMode MODE>
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t* ids, int32_t n, int32_t E,
+                                                              int32_t key_bits, SortArgs a) {
+  a.ids = ids;
+  a.n = n;
+  a.E = E;
+  a.key_bits = key_bits;
   extern __shared__ int lds[];
   __shared__ int wave_sum[kSortWaves];
   const int nk = a.E + 1, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -666,7 +691,15 @@ __device__ __forceinline__ void zero_unit(const RowsArgs& a, int t, int j0, uint
 }
 
 template <typename Row, bool WIDE, int G>
-__global__ void __launch_bounds__(256) dispatch_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(256) dispatch_kernel(const void* src, int64_t src_ld, const int32_t* slot_rows,
+                                                       const int32_t* sorted_ids, int32_t n_tokens,
+                                                       int32_t k, RowsArgs a) {
+  a.src = src;
+  a.src_ld = src_ld;
+  a.slot_rows = slot_rows;
+  a.sorted_ids = sorted_ids;
+  a.n_tokens = n_tokens;
+  a.k = k;
   typedef Unit<Row, WIDE> Un;
   typedef typename Un::raw raw;
   const int t = uniform_i32((int)(blockIdx.x * (256 / G) + threadIdx.x / G));
@@ -688,7 +721,15 @@ __global__ void __launch_bounds__(256) dispatch_kernel(RowsArgs a) {
 }
 
 template <typename Row, bool WIDE, int G>
-__global__ void __launch_bounds__(256) combine_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(256) combine_kernel(const void* src, int64_t src_ld, const int32_t* slot_rows,
+                                                      const float* weights, int32_t n_tokens,
+                                                      int32_t k, RowsArgs a) {
+  a.src = src;
+  a.src_ld = src_ld;
+  a.slot_rows = slot_rows;
+  a.weights = weights;
+  a.n_tokens = n_tokens;
+  a.k = k;
   typedef Unit<Row, WIDE> Un;
   typedef typename Un::raw raw;
   const int t = uniform_i32((int)(blockIdx.x * (256 / G) + threadIdx.x / G));
@@ -722,7 +763,16 @@ __global__ void __launch_bounds__(256) combine_kernel(RowsArgs a) {
 }
 
 template <typename Row, bool WIDE, int G>
-__global__ void __launch_bounds__(256) combine_backward_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(256) combine_backward_kernel(const void* d_out, const int32_t* slot_rows,
+                                                               const int32_t* sorted_ids,
+                                                               const float* weights, int32_t n_tokens,
+                                                               int32_t k, RowsArgs a) {
+  a.d_out = d_out;
+  a.slot_rows = slot_rows;
+  a.sorted_ids = sorted_ids;
+  a.weights = weights;
+  a.n_tokens = n_tokens;
+  a.k = k;
   typedef Unit<Row, WIDE> Un;
   typedef typename Un::raw raw;
   __shared__ float part[256 / 64][kSlots];
@@ -798,11 +848,14 @@ template <typename Row, bool WIDE, int G>
 void launch_rows(RowsOp op, const RowsArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(((int64_t)a.n_tokens * G + 255) / 256)), block(256);
   if (op == kDispatch)
-    hipLaunchKernelGGL((dispatch_kernel<Row, WIDE, G>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((dispatch_kernel<Row, WIDE, G>), grid, block, 0, s, a.src, a.src_ld,
+                       a.slot_rows, a.sorted_ids, a.n_tokens, a.k, a);
   else if (op == kCombine)
-    hipLaunchKernelGGL((combine_kernel<Row, WIDE, G>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((combine_kernel<Row, WIDE, G>), grid, block, 0, s, a.src, a.src_ld,
+                       a.slot_rows, a.weights, a.n_tokens, a.k, a);
   else
-    hipLaunchKernelGGL((combine_backward_kernel<Row, WIDE, G>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((combine_backward_kernel<Row, WIDE, G>), grid, block, 0, s, a.d_out,
+                       a.slot_rows, a.sorted_ids, a.weights, a.n_tokens, a.k, a);
 }
 
 template <typename Row, bool WIDE>
@@ -958,12 +1011,13 @@ extern "C" int32_t mlora_moe_sort(const int32_t* ids, int64_t n_slots, int32_t n
     // nothing to place: the offsets alone, all 0
     hipLaunchKernelGGL(sort_empty_kernel, dim3(1), dim3(256), 0, s, a);
   } else if (n_slots <= kSortThreads) {
-    hipLaunchKernelGGL((sort_place_kernel<1, kSortAlone>), dim3(1), threads, lds, s, a);
+    hipLaunchKernelGGL((sort_place_kernel<1, kSortAlone>), dim3(1), threads, lds, s, a.ids, a.n,
+                       a.E, a.key_bits, a);
   } else if (n_slots <= kSortOne) {
     const int blocks = (int)((n_slots + kSortThreads - 1) / kSortThreads);
     const size_t counters = (size_t)2 * kSortCopies * (n_experts + 1) * 4;
     hipLaunchKernelGGL((sort_place_kernel<1, kSortRecount>), dim3(blocks), threads,
-                       counters > lds ? counters : lds, s, a);
+                       counters > lds ? counters : lds, s, a.ids, a.n, a.E, a.key_bits, a);
   } else {
     a.blocks = sort_blocks(n_slots);
     const int64_t tiles = (n_slots + kSortTile - 1) / kSortTile;
@@ -972,7 +1026,7 @@ extern "C" int32_t mlora_moe_sort(const int32_t* ids, int64_t n_slots, int32_t n
                        a);
     if (int32_t rc = launch_status(who)) return rc;
     hipLaunchKernelGGL((sort_place_kernel<kSortR, kSortCounted>), dim3(a.blocks), threads, lds, s,
-                       a);
+                       a.ids, a.n, a.E, a.key_bits, a);
   }
   return launch_status(who);
 }

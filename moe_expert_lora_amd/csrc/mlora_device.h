@@ -75,45 +75,49 @@ template <int N>
 __device__ __forceinline__ uint32_t ror16(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + N, 0xf, 0xf, false);
 }
-__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int lane) {
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+// The value of the lane 16 (32) away in the other row (half) of the wave's row
+// pair (halves), beside the lane's own, in an order both lanes agree on.
+__device__ __forceinline__ u32x2 pair_rows(uint32_t v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return u32x2{(uint32_t)r[0], (uint32_t)r[1]};
+}
+__device__ __forceinline__ u32x2 pair_halves(uint32_t v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return u32x2{(uint32_t)r[0], (uint32_t)r[1]};
 }
 
-// Reductions over the LPT lanes (16 or 64) that share a row; every lane gets
-// the result. Four rotations inside rows of 16, then, for a whole wave, the
-// four rows' values through scalar registers. The order is fixed.
+// Reductions over the LPT lanes (16, 32 or 64) that share a row; every lane
+// gets the result. Four rotations inside rows of 16, then the rows in pairs,
+// then the halves. The order is fixed.
+template <int LPT, typename T, typename Op>
+__device__ __forceinline__ T group_reduce(T v, Op op) {
+  auto bits = [](T x) { return __builtin_bit_cast(uint32_t, x); };
+  auto from = [](uint32_t x) { return __builtin_bit_cast(T, x); };
+  v = op(v, from(ror16<8>(bits(v))));
+  v = op(v, from(ror16<4>(bits(v))));
+  v = op(v, from(ror16<2>(bits(v))));
+  v = op(v, from(ror16<1>(bits(v))));
+  if constexpr (LPT >= 32) {
+    const u32x2 r = pair_rows(bits(v));
+    v = op(from(r[0]), from(r[1]));
+  }
+  if constexpr (LPT == 64) {
+    const u32x2 r = pair_halves(bits(v));
+    v = op(from(r[0]), from(r[1]));
+  }
+  return v;
+}
 template <int LPT>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  v = max(v, ror16<8>(v));
-  v = max(v, ror16<4>(v));
-  v = max(v, ror16<2>(v));
-  v = max(v, ror16<1>(v));
-  if constexpr (LPT == 64)
-    v = max(max(lane_u32(v, 0), lane_u32(v, 16)), max(lane_u32(v, 32), lane_u32(v, 48)));
-  return v;
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 template <int LPT>
 __device__ __forceinline__ uint32_t group_min(uint32_t v) {
-  v = min(v, ror16<8>(v));
-  v = min(v, ror16<4>(v));
-  v = min(v, ror16<2>(v));
-  v = min(v, ror16<1>(v));
-  if constexpr (LPT == 64)
-    v = min(min(lane_u32(v, 0), lane_u32(v, 16)), min(lane_u32(v, 32), lane_u32(v, 48)));
-  return v;
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
 }
 template <int LPT>
-__device__ __forceinline__ float group_sum(float f) {
-  f += __uint_as_float(ror16<8>(__float_as_uint(f)));
-  f += __uint_as_float(ror16<4>(__float_as_uint(f)));
-  f += __uint_as_float(ror16<2>(__float_as_uint(f)));
-  f += __uint_as_float(ror16<1>(__float_as_uint(f)));
-  if constexpr (LPT == 64) {
-    const uint32_t u = __float_as_uint(f);
-    f = (__uint_as_float(lane_u32(u, 0)) + __uint_as_float(lane_u32(u, 16))) +
-        (__uint_as_float(lane_u32(u, 32)) + __uint_as_float(lane_u32(u, 48)));
-  }
-  return f;
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<LPT>(v, [](float a, float b) { return a + b; });
 }
 
 // LDS traffic of one wave is in order; this keeps the compiler from moving

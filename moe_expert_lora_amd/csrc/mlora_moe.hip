@@ -256,20 +256,17 @@ void launch_router(const RouterArgs& a, bool backward, hipStream_t s) {
 }
 
 // Lanes per token and values per lane: 16 lanes hold up to 128 experts (four
-// tokens a wave; the reductions stay in rows of 16), a wave holds up to 1024.
-// The choice among 129 to 256 experts takes 16 lanes of 16 values for many
-// tokens, where instructions count (8192 tokens of 256, top 8: bf16 5.3 us a
-// call, a wave each 7.0; fp32 6.5 and 8.2), and a wave for few, where the way
-// through a lane's values does (80 tokens, fp32: 5.0 and 4.3; 4096: the same). With 32 values in
-// 16 lanes, or scalar masks in place of the second reduction, 512 experts took
-// longer than this.
+// tokens a wave; the reductions stay in rows of 16), 32 up to 256, a wave up to
+// 1024; top_k winners need as many lanes. Fewer lanes with more values save
+// instructions where tokens fill the chip and cost latency where they do not.
+// 256 experts, top 8, choice and gradient together, us: 8192 tokens of fp32 in
+// 16, 32, 64 lanes 12.6, 12.1, 13.7; 80 tokens 9.1, 7.2, 7.2. 512 experts in 32
+// lanes 19.6 and 9.6, in 64 20.0 and 7.3.
 template <typename Row, bool WIDE>
 void dispatch_router(const RouterArgs& a, bool backward, hipStream_t s) {
   constexpr int V = Row::kPer16;
   if (a.E <= 128 && a.k <= 16) return launch_router<Row, 16, 8, V, WIDE>(a, backward, s);
-  if (a.E <= 256 && a.k <= 16 && !backward && a.n_tokens >= 6144)
-    return launch_router<Row, 16, 16, V, WIDE>(a, false, s);
-  if (a.E <= 256) return launch_router<Row, 64, 4, 4, WIDE>(a, backward, s);
+  if (a.E <= 256 && a.k <= 32) return launch_router<Row, 32, 8, V, WIDE>(a, backward, s);
   if (a.E <= 512) return launch_router<Row, 64, 8, V, WIDE>(a, backward, s);
   launch_router<Row, 64, 16, V, WIDE>(a, backward, s);
 }

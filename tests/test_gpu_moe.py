@@ -101,7 +101,8 @@ def _check_router(ml, lg, k, renorm, backward=True):
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("tokens,experts,top_k", [
     (1, 1, 1), (1, 2, 2), (3, 7, 3), (5, 8, 8), (80, 128, 8), (67, 100, 6), (9, 64, 1),
-    (33, 128, 16), (33, 128, 17), (10, 129, 8), (10, 250, 4), (17, 256, 8), (6, 257, 2),
+    (33, 128, 16), (33, 128, 17), (10, 129, 8), (10, 250, 4), (17, 256, 8), (9, 200, 32),
+    (9, 200, 33), (11, 256, 64), (6, 257, 2),
     (12, 384, 6), (5, 511, 8), (5, 512, 64), (4, 513, 8), (3, 1000, 8), (3, 1024, 64), (1030, 60, 4),
     (4100, 128, 8), (6144, 256, 8), (6147, 200, 5)])
 def test_router(ml, dtype, renorm, tokens, experts, top_k):

@@ -4,17 +4,14 @@
 //     out[r, n] = sum_k x[src(r), k] * (q[e(r), n, k] - z[e, n, k / group])
 //                                    * s[e, n, k / group]
 //
-// The products run on bf16 MFMA (16x16x32). A 4-bit value v is put into the
-// mantissa of a bf16 as 16 + v (one and/or per pair of values, exact), so a
-// lane's 8 values take 7 VALU operations; the group's offset 16 + z comes off
-// in fp32 afterwards, with the group's sum of x, which one more MFMA per k
-// step (a constant first operand) leaves in every lane. Each group's partial
-// product is scaled in fp32, so weights are never rounded. fp32 rows are split
-// into three bf16 parts (8 + 8 + 8 bits, exact), one MFMA each: the products
-// stay exact and the sums fp32.
-//
-// (In the streaming form fp32 rows bring these sums along in LDS: their MFMAs
-// would be a third of all.)
+// The products run on bf16 MFMA (16x16x32): 16 rows of x by 16 columns of
+// weights. A 4-bit value v is put into the mantissa of a bf16 as 16 + v (one
+// and/or per pair of values, exact), so a lane's 8 values take 7 VALU
+// operations. A group's sums start at -(16 + z) times the group's sum of x, so
+// that the offset is gone at its end; they are then scaled in fp32, so weights
+// are never rounded. A lane's values are of one column: one scale and one zero
+// point for all of them. fp32 rows are split into three bf16 parts (8 + 8 + 8
+// bits, exact), one MFMA each: the products stay exact and the sums fp32.
 //
 // The offset makes |16 + v| sums cancel: their fp32 rounding is about 5 times
 // that of a plain sum of the same length, far below one bf16 rounding and
@@ -34,12 +31,14 @@ namespace mlora {
 namespace {
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxW4Experts = 1024;
 constexpr uint32_t kMaxBuf = 0xFFFFFF00u;  // largest range one buffer resource describes
 constexpr uint32_t kPast = 0xFFFFFF40u;    // an offset past every buffer: the load gives 0
 constexpr int kScan = 2048;                // rows scanned (and listed) at a time
-constexpr int kMaxWaves = 8;
+constexpr int kSplitWaves = 8;             // most per workgroup, split form
+constexpr int kMaxWaves = 12;              // of both
 constexpr int kNT = 2;                     // non-temporal: weights are read once
 
 __device__ __forceinline__ rsrc_t buf(const void* p, uint32_t bytes) {
@@ -53,34 +52,33 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Packed layout. Weights: per expert and column tile of 16, ksteps = ceil(k /
-// 32) steps of 256 bytes. Four steps make a chunk of 1024 bytes in which lane l
-// of a wave finds its 16 bytes at 16 l: word i is step i, column l % 16, k
-// values 32 i + 8 (l / 16) .. + 7. A last chunk of fewer steps keeps as many
-// words per lane; a lane still loads 16 bytes there, and what it reads of the
-// words behind meets x values of 0. In a word, values 2p and 2p + 1
-// of the 8 sit at bits 3 + 4p and 19 + 4p (p = 3 wraps round at bit 31), so
-// that a shift (a rotation for p = 3), a mask and an or leave the two bf16
-// values 16 + v side by side.
-// Scales and zero points: per expert, tile and scale block (the groups of one
-// chunk, or the chunks of one group), lane group l / 16 finds SG groups of 4
-// columns each; a zero point is kept as the byte 16 + z.
+// Packed layout. Weights: per expert and pair of column tiles of 16, ksteps =
+// ceil(k / 32) steps of 2 x 256 bytes. Four steps make a chunk of 2 x 1024 bytes,
+// one tile behind the other, in which lane l of a wave finds its 16 bytes at
+// 16 l: word i is step i, column l % 16, k values 32 i + 8 (l / 16) .. + 7. A last
+// chunk of fewer steps keeps as many words per lane; a lane still loads 16 bytes
+// there, and what it reads of the words behind meets x values of 0. In a word,
+// values 2p and 2p + 1 of the 8 sit at bits 3 + 4p and 19 + 4p (p = 3 wraps round
+// at bit 31), so that a shift (a rotation for p = 3), a mask and an or leave the
+// two bf16 values 16 + v side by side.
+// Scales and zero points: per expert, pair and scale block (the groups of one
+// chunk, or the chunks of one group), column l % 16 finds SG groups of the two
+// tiles' values; a zero point is kept as the byte 16 + z.
 struct W4Layout {
-  int64_t tiles, ksteps, blocks, sg, tile_bytes;
+  int64_t pairs, ksteps, blocks, sg;
   int64_t w_bytes, s_bytes, z_bytes, s_off, z_off, total;
 };
 
 W4Layout w4_layout(int64_t E, int64_t K, int64_t N, int64_t group, int es, bool zeros) {
   W4Layout l;
-  l.tiles = (N + 15) / 16;
+  l.pairs = (N + 31) / 32;
   l.ksteps = (K + 31) / 32;
   l.sg = group < 128 ? 128 / group : 1;
   const int64_t span = group < 128 ? 128 : group;
   l.blocks = (K + span - 1) / span;
-  l.tile_bytes = l.ksteps * 256;
-  l.w_bytes = E * l.tiles * l.tile_bytes;
-  l.s_bytes = E * l.tiles * l.blocks * 16 * l.sg * es;
-  l.z_bytes = zeros ? E * l.tiles * l.blocks * 16 * l.sg : 0;
+  l.w_bytes = E * l.pairs * l.ksteps * 512;
+  l.s_bytes = E * l.pairs * l.blocks * 32 * l.sg * es;
+  l.z_bytes = zeros ? E * l.pairs * l.blocks * 32 * l.sg : 0;
   l.s_off = (l.w_bytes + 255) & ~255ll;
   l.z_off = (l.s_off + l.s_bytes + 255) & ~255ll;
   l.total = (l.z_off + l.z_bytes + 255) & ~255ll;
@@ -95,7 +93,7 @@ struct W4PackArgs {
   void* s;
   uint8_t* z;
   int64_t words, cells;
-  int32_t K, N, group, groups, tiles, ksteps, blocks, sg;
+  int32_t K, N, group, groups, pairs, ksteps, blocks, sg;
 };
 
 // One thread per packed word, then one per scale cell.
@@ -103,21 +101,23 @@ template <typename Row>
 __global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs a) {
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at < a.words) {
-    const int64_t per_tile = (int64_t)a.ksteps * 64;
-    const int64_t et = at / per_tile;
-    const int w = (int)(at - et * per_tile);
-    const int whole = a.ksteps / 4 * 256;  // words of the tile in whole chunks
-    int step, lane;
+    const int64_t per_pair = (int64_t)a.ksteps * 128;
+    const int64_t ep = at / per_pair;
+    const int w = (int)(at - ep * per_pair);
+    const int whole = a.ksteps / 4 * 512;  // words of the pair in whole chunks
+    int step, lane, tile;
     if (w < whole) {
-      step = w / 256 * 4 + (w & 3);
+      step = w / 512 * 4 + (w & 3);
+      tile = (w >> 8) & 1;
       lane = (w & 255) >> 2;
     } else {
-      const int left = a.ksteps & 3;
-      step = a.ksteps / 4 * 4 + (w - whole) % left;
-      lane = (w - whole) / left;
+      const int left = a.ksteps & 3, r = w - whole;
+      tile = r / (left * 64);
+      step = a.ksteps / 4 * 4 + r % left;
+      lane = r / left & 63;
     }
-    const int64_t e = et / a.tiles;
-    const int n = (int)(et - e * a.tiles) * 16 + (lane & 15);
+    const int64_t e = ep / a.pairs;
+    const int n = (int)(ep - e * a.pairs) * 32 + tile * 16 + (lane & 15);
     const int k = step * 32 + (lane >> 4) * 8;
     uint32_t out = 0;
     if (n < a.N && k < a.K) {
@@ -135,17 +135,17 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs a) {
   }
   const int64_t c = at - a.words;
   if (c >= a.cells) return;
-  // cell: [expert][tile][block][lane group][sg][4 columns]
-  const int col = (int)(c & 3);
-  int64_t rest = c >> 2;
+  // cell: [expert][pair][block][16 columns][sg][2 tiles]
+  const int tile = (int)(c & 1);
+  int64_t rest = c >> 1;
   const int sg = (int)(rest % a.sg);
   rest /= a.sg;
-  const int lg = (int)(rest & 3);
-  rest >>= 2;
+  const int col = (int)(rest & 15);
+  rest >>= 4;
   const int blk = (int)(rest % a.blocks);
   rest /= a.blocks;
-  const int64_t e = rest / a.tiles;
-  const int n = (int)(rest - e * a.tiles) * 16 + lg * 4 + col;
+  const int64_t e = rest / a.pairs;
+  const int n = (int)(rest - e * a.pairs) * 32 + tile * 16 + col;
   const int g = blk * a.sg + sg;
   typedef typename Row::elem elem;
   const bool in = n < a.N && g < a.groups;
@@ -164,18 +164,45 @@ struct W4Args {
   uint32_t x_bytes;
   uint32_t x_ld_bytes;
   uint32_t topk;          // rows per x row (1: a row of its own)
+  uint32_t topk_magic;    // floor((2^32 - 1) / topk)
   int32_t K, N;
-  int32_t tiles, ksteps, blocks;
+  int32_t ksteps, blocks;
   uint32_t block_magic;   // ceil(2^31 / chunks per scale block)
   int32_t slices;         // workgroups per expert
-  int32_t pairs, per_slice;  // streaming form: tile pairs, and those of a slice
-  int32_t k_waves, pair_waves;  // waves of a workgroup: k_waves to a pair
+  int32_t pairs, per_slice;  // tile pairs; streaming form: those of a slice
+  int32_t pair_waves;     // pairs a workgroup's waves hold at a time
   uint32_t wave_magic;    // ceil(2^32 / pair_waves)
   int32_t turns;          // ring places of a pair, per wave
   int32_t panel, panel_turns;   // chunks of x in LDS, and their places per wave
-  int32_t by_row;         // a place per row, not per expert
   int32_t out_vec;        // rows of out start on 4 elements
 };
+
+// What a kernel's start needs. These lead its arguments as plain values, which
+// arrive in registers; the struct lies in memory, three cold lines away.
+struct W4Lead {
+  const int32_t* ids;  // null: one weight
+  int n_rows, E;       // E 0: one weight
+  int waves, k_waves;  // waves of a workgroup; those that share a pair
+  int by_row;          // a place per row, not per expert
+};
+
+// Has the lines of the struct requested together, at the kernel's start.
+__device__ __forceinline__ void fetch_args(const W4Args& a) {
+  asm volatile("" ::"s"(a.w), "s"(a.x), "s"(a.K), "s"(a.panel), "s"(a.out_vec));
+}
+
+// The value as one the compiler cannot trace: what is computed from it stays
+// where it is written, not in registers kept from the kernel's start.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The x row of a row.
+__device__ __forceinline__ uint32_t x_row(const W4Args& a, uint32_t row) {
+  const uint32_t q = __umulhi(row, a.topk_magic);  // or one less
+  return row - q * a.topk >= a.topk ? q + 1 : q;
+}
 
 // The bf16 pair 16, 16 in a vector register. With the base of unpack() there and
 // its mask a literal, and and or are one operation; as two literals they are two.
@@ -202,12 +229,6 @@ __device__ __forceinline__ u32x4 unpack(uint32_t w, uint32_t base) {
 template <bool F32>
 struct XRaw {
   u32x4 v[F32 ? 2 : 1];
-  __device__ __forceinline__ float sum() const {  // of 8 fp32 values
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s += __uint_as_float(v[0][i]) + __uint_as_float(v[F32][i]);
-    return s;
-  }
 };
 
 template <bool F32>
@@ -245,52 +266,52 @@ struct XFrag {
   }
 };
 
-// Buffers of a wave's column tiles et0 .. et0 + n - 1 of the packed form: tiles
-// past them (and everything, for n == 0) lie past their end and read as 0.
-// Built from scalars, so that a load needs no loop over lanes.
-struct WBufs {
+// Where a chunk of one pair of tiles lies. Built from scalars, so that a load
+// needs no loop over lanes; a chunk that is not there reads as 0.
+struct ChunkAt {
   rsrc_t w, s, z;
-  uint32_t tile_bytes, s_tile, z_tile;  // bytes from one tile to the next
+  bool whole;
 
   template <int SG, int ES, bool ZP>
-  __device__ __forceinline__ void set(const W4Args& a, int et0, int n) {
-    et0 = uniform_i32(et0);
-    n = uniform_i32(n);
-    tile_bytes = (uint32_t)a.ksteps * 256u;
-    z_tile = (uint32_t)a.blocks * 16u * SG;
-    s_tile = z_tile * ES;
-    // 16 bytes more: a last lane's load of a short chunk (the scales follow)
-    w = buf(a.w + (int64_t)et0 * tile_bytes, n > 0 ? n * tile_bytes + 16u : 0u);
-    s = buf(a.s + (int64_t)et0 * s_tile, n * s_tile);
-    z = w;
-    if constexpr (ZP) z = buf(a.z + (int64_t)et0 * z_tile, n * z_tile);
+  __device__ __forceinline__ void set(const W4Args& a, const uint8_t* pw, const uint8_t* ps,
+                                      const uint8_t* pz, int c, bool in) {
+    constexpr uint32_t kCell = 32u * SG;
+    whole = c < (a.ksteps >> 2);
+    const uint32_t blk = SG > 1 ? (uint32_t)c : __umulhi(2u * (uint32_t)c, a.block_magic);
+    w = buf(pw, in ? 2048u : 0u);
+    s = buf(ps + (uint64_t)blk * (kCell * ES), in ? kCell * ES : 0u);
+    z = s;
+    if constexpr (ZP) z = buf(pz + (uint64_t)blk * kCell, in ? kCell : 0u);
   }
 };
 
-// The weights of one chunk (128 k values) of NT column tiles, as loaded.
+// The weights of one chunk (128 k values) of NT column tiles of a pair, as
+// loaded, and both tiles' scales and zero points.
 template <bool F32, int SG, bool ZP, int NT>
 struct WChunk {
   static constexpr int kEs = F32 ? 4 : 2;
-  static constexpr int kWords = SG * kEs;  // 4 scales per group: 2 or 4 words
-  static constexpr int kLoads = NT * (1 + (kWords + 3) / 4 + (ZP ? 1 : 0));
+  static constexpr int kWords = SG * kEs / 2;
+  static constexpr int kLoads = NT + (kWords + 3) / 4 + (ZP ? 1 : 0);
   u32x4 w[NT];
-  uint32_t s[NT][kWords];
-  uint32_t z[NT][ZP ? SG : 1];
+  uint32_t s[kWords];
+  uint32_t z[ZP ? (SG + 1) / 2 : 1];
 
-  __device__ __forceinline__ void load(const W4Args& a, const WBufs& b, int c, int lane) {
-    const uint32_t lg = (uint32_t)lane >> 4, blk = __umulhi(2u * (uint32_t)c, a.block_magic);
-    const uint32_t per_lane = c < (a.ksteps >> 2) ? 16u : (uint32_t)(a.ksteps & 3) * 4u;
+  // t0: the pair's first tile to load (0 for both)
+  __device__ __forceinline__ void load(const W4Args& a, const ChunkAt& at, int t0, int lane) {
+    const uint32_t left = (uint32_t)(a.ksteps & 3);
     // offsets wholly in the vector operand: the range check is against it
-    const uint32_t wo = (uint32_t)lane * per_lane + c * 1024u;
-    const uint32_t so = lg * (kWords * 4) + blk * (16u * SG * kEs);
-    const uint32_t zo = lg * (SG * 4) + blk * (16u * SG);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      w[nt] = __builtin_bit_cast(
-          u32x4, __builtin_amdgcn_raw_buffer_load_b128(b.w, wo + nt * b.tile_bytes, 0, kNT));
-      words<kWords>(s[nt], b.s, so + nt * b.s_tile);
-      if constexpr (ZP) words<SG>(z[nt], b.z, zo + nt * b.z_tile);
+      const uint32_t o = at.whole ? (uint32_t)lane * 16u + (t0 + nt) * 1024u
+                                  : (uint32_t)lane * 4u * left + (t0 + nt) * 256u * left;
+      w[nt] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(at.w, o, 0, kNT));
     }
+    const uint32_t col = (uint32_t)lane & 15u;
+    words<kWords>(s, at.s, col * (kWords * 4u));
+    if constexpr (ZP && SG == 1)
+      z[0] = __builtin_amdgcn_raw_buffer_load_b16(at.z, col * 2u, 0, 0);
+    else if constexpr (ZP)
+      words<SG / 2>(z, at.z, col * (SG * 2u));
   }
   template <int N>
   static __device__ __forceinline__ void words(uint32_t* d, rsrc_t r, uint32_t off) {
@@ -313,74 +334,81 @@ struct WChunk {
       }
     }
   }
+  // of group sg and tile t of the pair
+  __device__ __forceinline__ float scale(int sg, int t) const {
+    if constexpr (F32)
+      return __uint_as_float(t ? s[sg * 2 + 1] : s[sg * 2]);
+    else
+      return t ? hi_f(s[sg]) : lo_f(s[sg]);
+  }
+  __device__ __forceinline__ float zero(int sg, int t) const {
+    return (float)((z[sg / 2] >> (16 * (sg & 1) + 8 * t)) & 0xffu);
+  }
 };
 
+// Minus the sum of x that a group's sums start from, times 24 where every zero
+// point is 8.
+constexpr uint32_t minus_ones(bool zp) { return zp ? 0xbf80bf80u : 0xc1c0c1c0u; }
+
 // acc += the chunk's products, group by group. `x(mb, ks, f)` fills f with the
-// bf16 parts of k step ks of row block mb. `sum(mb, ks)`, if given, is minus the
-// sum of that step's x; else MFMAs with a constant first operand take it.
+// bf16 parts of k step ks of row block mb. `sum(mb, sg)`, if given, is minus the
+// sum of that group's x; else MFMAs with a constant operand take it.
 struct NoSums {};
 template <bool F32, int SG, bool ZP, int NT, int MB, typename X, typename S = NoSums>
-__device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, X x,
+__device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, int t0, X x,
                                           uint32_t base, f32x4 (&acc)[NT][MB], S sum = S{}) {
-  constexpr bool kSums = !std::is_same<S, NoSums>::value, kChain = !ZP && !kSums;
+  constexpr bool kSums = !std::is_same<S, NoSums>::value;
   constexpr int kPer = 4 / SG, kParts = XFrag<F32>::kParts;
-  const uint32_t kc = ZP ? 0xbf80bf80u : 0xc1c0c1c0u;  // bf16 -1, or -(16 + 8)
+  constexpr uint32_t kc = minus_ones(ZP);
   const u32x4 cons = {kc, kc, kc, kc};
 #pragma unroll
   for (int sg = 0; sg < SG; ++sg) {
     XFrag<F32> f[MB][kPer];
     f32x4 dc[MB] = {};
 #pragma unroll
-    for (int ks = 0; ks < kPer; ++ks)
+    for (int mb = 0; mb < MB; ++mb) {
+      if constexpr (kSums) dc[mb] = sum(mb, sg);
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) x(mb, sg * kPer + ks, f[mb][ks]);
+      for (int ks = 0; ks < kPer; ++ks) x(mb, sg * kPer + ks, f[mb][ks]);
+    }
+    if constexpr (!kSums) {
 #pragma unroll
-    for (int ks = 0; ks < kPer; ++ks) {
+      for (int ks = 0; ks < kPer; ++ks)
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        if constexpr (kSums) {
-          dc[mb][0] += sum(mb, sg * kPer + ks);
-        } else {
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-          for (int p = 0; p < kParts; ++p) dc[mb] = mfma(cons, f[mb][ks].p[p], dc[mb]);
-        }
-      }
+          for (int p = 0; p < kParts; ++p) dc[mb] = mfma(f[mb][ks].p[p], cons, dc[mb]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      f32x4 s[MB];
+      f32x4 t[MB];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) s[mb] = kChain ? dc[mb] : f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int mb = 0; mb < MB; ++mb) {
+        t[mb] = dc[mb];
+        if constexpr (ZP) {
+          const float z = wc.zero(sg, t0 + nt);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[mb][i] *= z;
+        }
+      }
 #pragma unroll
       for (int ks = 0; ks < kPer; ++ks) {
         const u32x4 wf = unpack(wc.w[nt][sg * kPer + ks], base);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-          for (int p = 0; p < kParts; ++p) s[mb] = mfma(wf, f[mb][ks].p[p], s[mb]);
+          for (int p = 0; p < kParts; ++p) t[mb] = mfma(f[mb][ks].p[p], wf, t[mb]);
       }
+      const float sc = wc.scale(sg, t0 + nt);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float sc, z = 0.f;
-        if constexpr (F32)
-          sc = __uint_as_float(wc.s[nt][sg * 4 + i]);
-        else
-          sc = (i & 1) ? hi_f(wc.s[nt][sg * 2 + i / 2]) : lo_f(wc.s[nt][sg * 2 + i / 2]);
-        if constexpr (ZP) z = (float)((wc.z[nt][sg] >> (8 * i)) & 0xffu);
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          float t;
-          if constexpr (kSums)
-            t = fmaf(ZP ? z : 24.f, dc[mb][0], s[mb][i]);
-          else
-            t = ZP ? fmaf(z, dc[mb][i], s[mb][i]) : kChain ? s[mb][i] : s[mb][i] + dc[mb][i];
-          acc[nt][mb][i] = fmaf(sc, t, acc[nt][mb][i]);
-        }
-      }
+        for (int i = 0; i < 4; ++i) acc[nt][mb][i] = fmaf(sc, t[mb][i], acc[nt][mb][i]);
     }
-    // operands of the next chunk (fp32, with three parts: of the next group) are
-    // not fetched into registers ahead, which the weights in flight need
-    if (F32 || sg == SG - 1) __builtin_amdgcn_sched_barrier(0);
+    // operands of the next chunk (fp32, with three parts, and small groups: of the
+    // next group) are not fetched into registers ahead, which the weights in flight
+    // need
+    if (F32 || SG == 4 || sg == SG - 1) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -424,11 +452,32 @@ __device__ __forceinline__ void lds_barrier() {
 
 // A workgroup's place, blockIdx.y, is an expert; in calls of fewer rows than
 // experts (by_row) it is a row, and stands for that row's expert where no
-// earlier row has the same. Returns the expert.
-__device__ __forceinline__ int place_expert(const int32_t* ids, int E, int by_row) {
+// earlier row has the same. Returns the expert, -1 for none.
+__device__ __forceinline__ int place_expert(const W4Lead& l) {
   const int y = (int)blockIdx.y;
-  return E > 0 && by_row ? uniform_i32(ids[y]) : y;
+  const int e = l.E > 0 && l.by_row ? uniform_i32(l.ids[y]) : y;
+  return l.E > 0 && (uint32_t)e >= (uint32_t)l.E ? -1 : e;
 }
+
+// A segment's ids, in runs of 64 * rounds per wave, four rounds at a time. The
+// first four are requested ahead of a workgroup's weights.
+struct IdRun {
+  rsrc_t r;
+  int rounds, first;
+  int id[4];
+
+  __device__ __forceinline__ void set(const W4Lead& l, int seg, int len, int wave, int lane) {
+    rounds = (len + 64 * l.waves - 1) / (64 * l.waves);  // <= 32
+    first = wave * rounds * 64 + lane;
+    r = buf(l.ids + seg, l.E > 0 ? (uint32_t)len * 4u : 0u);  // past the end: 0
+    load(0);
+  }
+  __device__ __forceinline__ void load(int r0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      id[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(r, (first + (r0 + i) * 64) * 4, 0, 0);
+  }
+};
 
 // The rows of [seg, seg + len) of one workgroup: those whose id is its expert e
 // from the front of `list` (none if an earlier place has them), and from its
@@ -446,28 +495,23 @@ __device__ __forceinline__ int lanes_before(uint64_t m) {
                                         __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
 }
 
-__device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, int by_row,
-                                             int seg, int len, int* list, int* counts) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int rounds = (len + 64 * waves - 1) / (64 * waves);  // <= 32
-  const int first = wave * rounds * 64 + lane;
+__device__ __forceinline__ RowList list_rows(const W4Lead& l, IdRun& run, int e, int seg, int len,
+                                             int wave, int* list, int* counts) {
+  const int lane = here(threadIdx.x & 63);
+  const int E = l.E, rounds = run.rounds, first = run.first;
+  const int(&id)[4] = run.id;
   const int y = (int)blockIdx.y;
   const int shift = 32 - __builtin_clz((unsigned)len);       // len < 2^shift
   uint32_t hits = 0, drops = 0;
   int n_hits = 0, n_drops = 0;
-  const rsrc_t ri = buf(ids + seg, (uint32_t)len * 4u);  // past the end: 0
   for (int r0 = 0; r0 < rounds; r0 += 4) {
-    int id[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      id[r] = (int)__builtin_amdgcn_raw_buffer_load_b32(ri, (first + (r0 + r) * 64) * 4, 0, 0);
+    if (r0 > 0) run.load(r0);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = first + (r0 + r) * 64;
       const bool in = r0 + r < rounds && i < len;
-      const bool hit = in && id[r] == e && (uint32_t)e < (uint32_t)E;
-      const int owner = by_row ? i : (int)(((uint32_t)i * (uint32_t)E) >> shift);
+      const bool hit = in && id[r] == e && e >= 0;
+      const int owner = l.by_row ? i : (int)(((uint32_t)i * (uint32_t)E) >> shift);
       const bool drop = in && (uint32_t)id[r] >= (uint32_t)E && owner == y;
       n_hits += __popcll(__ballot(hit));
       n_drops += __popcll(__ballot(drop));
@@ -479,9 +523,15 @@ __device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, i
   if (lane == 0) counts[wave] = n_hits | n_drops << 16;
   lds_barrier();
   int at = 0, all = 0;
-  for (int w = 0; w < waves; ++w) {
-    at += w < wave ? counts[w] : 0;
-    all += counts[w];
+  static_assert(kMaxWaves % 4 == 0, "counts are read four at a time");
+#pragma unroll
+  for (int w = 0; w < kMaxWaves; w += 4) {
+    const i32x4 c = *reinterpret_cast<const i32x4*>(counts + w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      at += w + i < wave ? c[i] : 0;
+      all += w + i < l.waves ? c[i] : 0;
+    }
   }
   at = uniform_i32(at);
   all = uniform_i32(all);
@@ -498,7 +548,7 @@ __device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, i
   }
   lds_barrier();
   int live = all & 0xffff;
-  if (by_row && live > 0 && uniform_i32(list[0]) != y) live = 0;
+  if (l.by_row && live > 0 && uniform_i32(list[0]) != y) live = 0;
   return RowList{live, all >> 16};
 }
 
@@ -506,10 +556,10 @@ __device__ __forceinline__ RowList list_rows(const int32_t* ids, int E, int e, i
 // row.
 template <typename Row>
 __device__ __forceinline__ void zero_rows(const W4Args& a, const int* list, int dead, int n0,
-                                          int cols) {
-  const int lane = threadIdx.x & 63, wave = uniform_i32((int)threadIdx.x >> 6);
+                                          int cols, int wave, int waves) {
+  const int lane = here(threadIdx.x & 63);
   const int n1 = min(n0 + cols, a.N);
-  for (int r = wave; r < dead; r += (int)(blockDim.x >> 6)) {
+  for (int r = wave; r < dead; r += waves) {
     typename Row::elem* o = static_cast<typename Row::elem*>(a.out) +
                             (int64_t)uniform_i32(list[kScan - 1 - r]) * a.out_ld;
     for (int n = n0 + lane * 4; n < n1; n += 256)
@@ -520,30 +570,48 @@ __device__ __forceinline__ void zero_rows(const W4Args& a, const int* list, int 
 // Few column tiles: a workgroup owns NT tiles, its waves split k and add their
 // sums up through LDS in wave order; x goes straight to the operands.
 template <bool F32, int SG, bool ZP, int MB, int NT>
-__global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t* ids, int n_rows, int E, W4Args a) {
+__global__ void __launch_bounds__(64 * kSplitWaves)
+w4_split_kernel(const int32_t* ids, int n_rows, int E, int waves, int k_waves, int by_row, W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
   constexpr int kCols = 16 * NT, kStride = kCols + 4, kRows = 16 * MB;
   __shared__ int list[kScan];
-  __shared__ int counts[kMaxWaves];
-  __shared__ float red[kMaxWaves * kRows * kStride];
-  const uint32_t base = base_pair();
+  __shared__ __attribute__((aligned(16))) int counts[kMaxWaves];
+  __shared__ float red[kSplitWaves * kRows * kStride];
+  const W4Lead lead = {ids, n_rows, E, waves, k_waves, by_row};
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
-  const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int e = place_expert(ids, E, a.by_row), tile = (int)blockIdx.x * NT;
+  const int wave = uniform_i32(tid >> 6);
+  IdRun run;
+  run.set(lead, 0, min(kScan, n_rows), wave, lane);
+  fetch_args(a);
+  const uint32_t base = base_pair();
+  const int e = place_expert(lead), tile = (int)blockIdx.x * NT;
   const int n0 = tile * 16, chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
-  WBufs wb;
-  wb.set<SG, (F32 ? 4 : 2), ZP>(a, e * a.tiles + tile, min(NT, a.tiles - tile));
+  constexpr int kCell = 32 * SG;
+  const int64_t ep = (int64_t)max(e, 0) * a.pairs + (tile >> 1);
+  const uint8_t* pw = a.w + ep * a.ksteps * 512;
+  const uint8_t* ps = a.s + ep * a.blocks * (kCell * (F32 ? 4 : 2));
+  const uint8_t* pz = a.z + (ZP ? ep * a.blocks * kCell : 0);
+  const int t0 = NT == 1 ? tile & 1 : 0;
   WChunk<F32, SG, ZP, NT> wc;
+  auto request = [&](int c) {
+    ChunkAt at;
+    at.set<SG, (F32 ? 4 : 2), ZP>(a, pw + (int64_t)c * 2048, ps, pz, c, c < chunks);
+    wc.load(a, at, t0, lane);
+  };
+  request(wave);  // the first chunk's weights, ahead of the rows they meet
+  bool primed = true;
 
   for (int seg = 0; seg < n_rows; seg += kScan) {
     const int len = min(kScan, n_rows - seg);
     int n_list = len;
     if (E > 0) {
-      const RowList l = list_rows(ids, E, e, a.by_row, seg, len, list, counts);
+      if (seg > 0) run.set(lead, seg, len, wave, lane);
+      const RowList l = list_rows(lead, run, e, seg, len, wave, list, counts);
       n_list = l.live;
-      if (l.dead > 0 && blockIdx.z == 0) zero_rows<Row>(a, list, l.dead, n0, kCols);
+      if (l.dead > 0 && blockIdx.z == 0)
+        zero_rows<Row>(a, list, l.dead, n0, kCols, wave, waves);
     }
     for (int b0 = (int)blockIdx.z * kRows; b0 < n_list; b0 += (int)gridDim.z * kRows) {
       uint32_t row_off[MB];
@@ -551,8 +619,10 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
       for (int mb = 0; mb < MB; ++mb) {
         const int at = b0 + mb * 16 + li;
         const int row = at < n_list ? (E > 0 ? list[at] : seg + at) : -1;
-        row_off[mb] = row >= 0 ? (uint32_t)row / a.topk * a.x_ld_bytes : kPast;
+        row_off[mb] = row >= 0 ? x_row(a, (uint32_t)row) * a.x_ld_bytes : kPast;
       }
+      if (!primed) request(wave);
+      primed = false;
       f32x4 acc[NT][MB] = {};
       for (int c = wave; c < chunks; c += waves) {
         XRaw<F32> x[MB][4];
@@ -561,18 +631,19 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             x[mb][ks] = load_x<F32>(rx, row_off[mb], c * 128 + ks * 32 + lg * 8, a.K);
-        wc.load(a, wb, c, lane);
         add_chunk<F32, SG, ZP, NT, MB>(
-            wc, [&](int mb, int ks, XFrag<F32>& f) { f.set(x[mb][ks]); }, base, acc);
+            wc, t0, [&](int mb, int ks, XFrag<F32>& f) { f.set(x[mb][ks]); }, base, acc);
+        if (c + waves < chunks) request(c + waves);
       }
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          *reinterpret_cast<f32x4*>(
-              &red[(wave * kRows + mb * 16 + li) * kStride + nt * 16 + lg * 4]) = acc[nt][mb];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            red[(wave * kRows + mb * 16 + lg * 4 + i) * kStride + nt * 16 + li] = acc[nt][mb][i];
       lds_barrier();
-      for (int i = tid; i < kRows * (kCols / 4); i += (int)blockDim.x) {
+      for (int i = tid; i < kRows * (kCols / 4); i += 64 * waves) {
         const int r = i / (kCols / 4), c4 = i % (kCols / 4) * 4;
         f32x4 sum = *reinterpret_cast<const f32x4*>(&red[r * kStride + c4]);
         for (int w = 1; w < waves; ++w)
@@ -591,82 +662,141 @@ __global__ void __launch_bounds__(64 * kMaxWaves) w4_split_kernel(const int32_t*
 // each wave then streams whole columns: pairs of tiles over all of k, kAhead
 // chunks of weights requested ahead, no barrier between.
 constexpr int kPair = 2;   // tiles per wave and step
-// Chunks in flight per wave (fp32 with groups of 32: what their 16 scales a tile
-// leave of the registers).
-constexpr int ahead(bool f32, int sg) { return f32 && sg == 4 ? 2 : 3; }
+// Chunks in flight per wave: a CU's cache has lines for 32 KB of loads on their
+// way, which 12 waves' chunks of two tiles fill; further ones wait at the cache,
+// and hold registers (3 instead of 2: 128 experts of 2048 x 768, 2048 rows 30.2 ->
+// 30.9 us, with groups of 32 34.5 -> 35.7; 4: 31.1 and 43.7).
+constexpr int kAhead = 2;
 constexpr int kLds = 160 * 1024;        // of a CU
 constexpr int kListLds = kScan * 4 + 256;  // the list and the counts
-constexpr int chunk_lds(bool f32, int mb) { return 4 * mb * (f32 ? 3 * 1024 + 64 : 1024); }
-// Chunks of x rows that fit a workgroup's LDS, in whole turns of the ring.
-constexpr int panel_chunks(bool f32, int mb) {
-  return (kLds - kListLds) / chunk_lds(f32, mb) / 6 * 6;
+// A chunk of x rows: the operands and the groups' sums.
+constexpr int chunk_lds(bool f32, int mb, int sg) {
+  return mb * (4 * (f32 ? 3 : 1) * 1024 + sg * 64);
 }
-constexpr int stream_waves(bool f32) { return f32 ? 8 : 12; }  // most per workgroup
+// Chunks of x rows that fit a workgroup's LDS.
+constexpr int panel_chunks(bool f32, int mb, int sg) {
+  return (kLds - kListLds) / chunk_lds(f32, mb, sg);
+}
+
+// Waves a SIMD holds: what the registers are kept to.
+constexpr int simd_waves(bool f32, int mb) { return f32 || mb > 1 ? 3 : 4; }
 
 template <bool F32, int SG, bool ZP, int MB>
-__global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const int32_t* ids, int n_rows, int E, W4Args a) {
+__global__ void __launch_bounds__(64 * kMaxWaves, simd_waves(F32, MB))
+w4_stream_kernel(const int32_t* ids, int n_rows, int E, int waves, int k_waves, int by_row, W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
   typedef WChunk<F32, SG, ZP, kPair> Chunk;
-  constexpr int kRows = 16 * MB, kParts = XFrag<F32>::kParts, kAhead = ahead(F32, SG);
-  const int panel = a.panel;
+  constexpr int kRows = 16 * MB, kParts = XFrag<F32>::kParts;
   __shared__ int list[kScan];
-  __shared__ int counts[stream_waves(F32)];
+  __shared__ __attribute__((aligned(16))) int counts[kMaxWaves];
   extern __shared__ u32x4 xs[];  // [k step][row block][part][lane]
-  // fp32 rows: minus the sums of x by k step and row, behind the operands
-  float* x_sums = reinterpret_cast<float*>(xs + min(panel, (a.ksteps + 3) >> 2) *
-                                                    (4 * MB * kParts * 64));
-  const uint32_t base = base_pair();
+  const W4Lead lead = {ids, n_rows, E, waves, k_waves, by_row};
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
-  const int waves = (int)(blockDim.x >> 6), wave = uniform_i32(tid >> 6);
-  const int e = place_expert(ids, E, a.by_row), slice = (int)blockIdx.x;
+  const int wave = uniform_i32(tid >> 6);
+  IdRun run;
+  run.set(lead, 0, min(kScan, n_rows), wave, lane);
+  fetch_args(a);
+  const int panel = a.panel;
+  // behind the operands, minus the sums of x: [group][row block][row]
+  f32x4* x_sums = reinterpret_cast<f32x4*>(xs + panel * (4 * MB * kParts * 64));
+  const uint32_t base = base_pair();
+  const int e = place_expert(lead), slice = (int)blockIdx.x;
   const int chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
   const rsrc_t rx = buf(a.x, a.x_bytes);
   // kw waves share a pair, each every kw-th chunk; a wave's pairs: every wn-th
   // of the slice's
-  const int kw = a.k_waves, n_wn = a.pair_waves, wk = wave % kw, wn = wave / kw;
+  const int kw = k_waves, n_wn = a.pair_waves;
+  const int wn = kw == 1 ? wave : kw == 2 ? wave >> 1 : kw == 4 ? wave >> 2 : wave * 11 >> 5;
+  const int wk = wave - wn * kw;  // kw <= 4, and wave * 11 / 32 = wave / 3 up to 15
   const int pair0 = slice * a.per_slice + wn;
   const int left = max(0, min((slice + 1) * a.per_slice, a.pairs) - pair0) + n_wn - 1;
-  const int n_pairs = uniform_i32(n_wn == 1 ? left : (int)__umulhi((uint32_t)left, a.wave_magic));
-  const int et0 = e * a.tiles;
+  const int all_pairs = n_wn == 1 ? left : (int)__umulhi((uint32_t)left, a.wave_magic);
+  const int n_pairs = uniform_i32(e < 0 ? 0 : all_pairs);
   // A pair takes whole turns of the ring: places past its chunks stay empty.
   const int turns = a.turns;
-  int lp, lj;  // pair and turn place of the next request
+  constexpr int kEs = F32 ? 4 : 2, kCell = 32 * SG;
+  const int64_t ep = (int64_t)max(e, 0) * a.pairs + pair0;
+  const int64_t w_pair = (int64_t)a.ksteps * 512, s_pair = (int64_t)a.blocks * kCell;
+  const uint8_t* const pw0 = a.w + ep * w_pair;
+  const uint8_t* const ps0 = a.s + ep * s_pair * kEs;
+  const uint8_t* const pz0 = a.z + (ZP ? ep * s_pair : 0);
+  int lp, lj, lc;  // pair, turn place and chunk of the next request
+  const uint8_t *pw, *ps, *pz;
+  auto first_request = [&] {
+    lp = lj = 0;
+    lc = wk;
+    pw = pw0;
+    ps = ps0;
+    pz = pz0;
+  };
   auto request = [&](Chunk& w) {
-    const int t0 = (pair0 + lp * n_wn) * kPair, lc = wk + lj * kw;
-    const bool in = lp < n_pairs && lc < chunks;
-    WBufs wb;
-    wb.set<SG, (F32 ? 4 : 2), ZP>(a, in ? et0 + t0 : 0, in ? min(kPair, a.tiles - t0) : 0);
-    w.load(a, wb, lc, lane);
+    ChunkAt at;
+    at.set<SG, kEs, ZP>(a, pw + (int64_t)lc * 2048, ps, pz, lc, lp < n_pairs && lc < chunks);
+    w.load(a, at, 0, lane);
     // requests stay in order, so that a wait for one leaves the later ones out
     __builtin_amdgcn_sched_barrier(0);
-    lj = lj + 1 == turns ? 0 : lj + 1;
-    lp += lj == 0;
+    lc += kw;
+    if (++lj == turns) {
+      lj = 0;
+      lc = wk;
+      ++lp;
+      pw += n_wn * w_pair;
+      ps += n_wn * s_pair * kEs;
+      pz += ZP ? n_wn * s_pair : 0;
+    }
   };
+
+  // One row block: the first weights are requested ahead of the rows they meet, the
+  // ring's last place once x has been requested, so that weights arrive while x
+  // does (128 experts of 2048 x 768, 640 rows: 23.2 us, all of them after x 26.2).
+  // Two row blocks have twice the x, which would wait behind them (2048 rows: 30.2
+  // and 28.2 us); fp32 rows pass through registers, which would.
+  constexpr int kEarly = F32 || MB > 1 ? 0 : kAhead - 1;
+  Chunk ring[kAhead];
+  auto first_requests = [&] {
+    first_request();
+#pragma unroll
+    for (int d = 0; d < kEarly; ++d) request(ring[d]);
+  };
+  first_requests();
+  bool primed = true;
 
   for (int seg = 0; seg < n_rows; seg += kScan) {
     int n_list = min(kScan, n_rows - seg);
     if (E > 0) {
-      const RowList l = list_rows(ids, E, e, a.by_row, seg, n_list, list, counts);
+      if (seg > 0) run.set(lead, seg, n_list, wave, lane);
+      const RowList l = list_rows(lead, run, e, seg, n_list, wave, list, counts);
       n_list = l.live;
       if (l.dead > 0 && blockIdx.z == 0)
         zero_rows<Row>(a, list, l.dead, slice * a.per_slice * kPair * 16,
-                       a.per_slice * kPair * 16);
+                       a.per_slice * kPair * 16, wave, waves);
     }
     const int step = (int)gridDim.z * kRows;
     for (int b0 = (int)blockIdx.z * kRows; b0 < n_list; b0 += step) {
       uint32_t row_off[MB];
-      int orow[MB];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
-        const int at = b0 + mb * 16 + li;
-        orow[mb] = at < n_list ? (E > 0 ? list[at] : seg + at) : -1;
-        row_off[mb] = orow[mb] >= 0 ? (uint32_t)orow[mb] / a.topk * a.x_ld_bytes : kPast;
+        const int at = b0 + mb * 16 + here(li);
+        const int row = at < n_list ? (E > 0 ? list[at] : seg + at) : -1;
+        row_off[mb] = row >= 0 ? x_row(a, (uint32_t)row) * a.x_ld_bytes : kPast;
       }
+      // the sums of a pair's tile and row block into the rows of out
+      auto store = [&](int pair, int nt, int mb, f32x4 v) {
+        const int l = here(tid & 63), n = pair * (kPair * 16) + nt * 16 + (l & 15);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = b0 + mb * 16 + (l >> 4) * 4 + i;
+          if (at >= n_list || n >= a.N) continue;
+          const int row = E > 0 ? list[at] : seg + at;
+          out[(int64_t)row * a.out_ld + n] = Row::narrow(v[i]);
+        }
+      };
       // x into LDS, k step by k step, the waves in turn. bf16 operands go there
       // directly, all in flight; fp32 rows pass through registers on their way
       // into parts.
       auto stage = [&](int p0, int steps) {
+        const int lane = here(tid & 63), lg = lane >> 4;
         if constexpr (!F32) {
           for (int f = wave; f < steps; f += waves) {
             const int k = p0 * 128 + f * 32 + lg * 8;
@@ -692,11 +822,6 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
                 q.set(r[i]);
 #pragma unroll
                 for (int p = 0; p < kParts; ++p) xs[(f * kParts + p) * 64 + lane] = q.p[p];
-                // minus the sum of the step's x of each row
-                float v = -r[i].sum();
-                v += __shfl_xor(v, 16);
-                v += __shfl_xor(v, 32);
-                if (lane < 16) x_sums[f * 16 + lane] = v;
               }
             }
           }
@@ -705,6 +830,7 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
       // The operands of a last k step past K hold zeros whatever a load past a
       // buffer's end leaves in LDS.
       auto stage_end = [&](int p0, int p1) {
+        const int lane = here(tid & 63), lg = lane >> 4;
         if constexpr (!F32) {
           if (p1 * 128 > a.K) {
             for (int f = wave; f < (p1 - p0) * 4; f += waves) {
@@ -715,15 +841,33 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
           }
         }
       };
+      // The groups' sums of x, the waves in turn.
+      auto sum_groups = [&](int groups) {
+        constexpr int kPer = 4 / SG;
+        constexpr uint32_t kc = minus_ones(ZP);
+        const u32x4 cons = {kc, kc, kc, kc};
+        const int lane = here(tid & 63), li = lane & 15, lg = lane >> 4;
+#pragma unroll 1
+        for (int g = wave; g < groups; g += waves) {
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < kPer; ++ks)
+#pragma unroll
+              for (int p = 0; p < kParts; ++p)
+                d = mfma(xs[(((g * kPer + ks) * MB + mb) * kParts + p) * 64 + lane], cons, d);
+            if (li == 0) x_sums[(g * MB + mb) * 4 + lg] = d;
+          }
+        }
+      };
       f32x4 acc[kPair][MB];
-      Chunk ring[kAhead];
-      // x is requested ahead of the first weights: loads return in order, and the
-      // weights come from HBM
+      if (!primed) first_requests();
+      primed = false;
       lds_barrier();  // the last block's readers are done
       stage(0, min(panel, chunks) * 4);
-      lp = lj = 0;
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) request(ring[d]);
+      for (int d = kEarly; d < kAhead; ++d) request(ring[d]);
       for (int p0 = 0, j0 = 0; p0 < chunks; p0 += panel, j0 += a.panel_turns) {
         const int p1 = min(p0 + panel, chunks);
         if (p0 > 0) {
@@ -734,9 +878,11 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
           if (p0 > 0)
             wait_loads<0>();
           else
-            wait_loads<Chunk::kLoads * kAhead>();
+            wait_loads<Chunk::kLoads *(kAhead - kEarly)>();
         }
         stage_end(p0, p1);
+        lds_barrier();
+        sum_groups((p1 - p0) * SG);
         lds_barrier();
         // one panel: every pair; several, or several waves a pair: the one pair's
         // share of them
@@ -757,42 +903,33 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
 #pragma unroll
                   for (int p = 0; p < kParts; ++p) f.p[p] = px[((ks * MB + mb) * kParts + p) * 64];
                 };
-                if constexpr (F32) {
-                  const float* ps = x_sums + (c - p0) * 64 + li;
-                  add_chunk<F32, SG, ZP, kPair, MB>(ring[d], operand, base, acc,
-                                                    [&](int, int ks) { return ps[ks * 16]; });
-                } else {
-                  add_chunk<F32, SG, ZP, kPair, MB>(ring[d], operand, base, acc);
-                }
+                const f32x4* px_sums = x_sums + (c - p0) * (SG * MB * 4) + lg;
+                add_chunk<F32, SG, ZP, kPair, MB>(
+                    ring[d], 0, operand, base, acc,
+                    [&](int mb, int sg) { return px_sums[(sg * MB + mb) * 4]; });
               }
               request(ring[d]);
             }
           }
           if (p1 < chunks || kw > 1) continue;
-          const int n = (pair0 + pair * n_wn) * kPair * 16 + lg * 4;
 #pragma unroll
-          for (int mb = 0; mb < MB; ++mb) {
-            if (orow[mb] < 0) continue;
-            typename Row::elem* o = out + (int64_t)orow[mb] * a.out_ld + n;
+          for (int nt = 0; nt < kPair; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < kPair; ++nt)
-              store4<Row>(o + nt * 16, acc[nt][mb], a.N - n - nt * 16, a.out_vec != 0);
-          }
+            for (int mb = 0; mb < MB; ++mb) store(pair0 + pair * n_wn, nt, mb, acc[nt][mb]);
         }
       }
       if (kw == 1) continue;
       // the sums of a pair's waves, added in wave order, in the LDS of x
       lds_barrier();
-      f32x4* red = reinterpret_cast<f32x4*>(xs);  // [wave][tile][row block][lane]
+      f32x4* red = reinterpret_cast<f32x4*>(xs) + here(lane);  // [wave][tile][row block][lane]
       if (n_pairs > 0) {
 #pragma unroll
         for (int nt = 0; nt < kPair; ++nt)
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
-            red[((wave * kPair + nt) * MB + mb) * 64 + lane] = acc[nt][mb];
+            red[((wave * kPair + nt) * MB + mb) * 64] = acc[nt][mb];
       }
       lds_barrier();
-      const int n = pair0 * kPair * 16 + lg * 4;
 #pragma unroll
       for (int nt = 0; nt < kPair; ++nt) {
 #pragma unroll
@@ -800,10 +937,8 @@ __global__ void __launch_bounds__(64 * stream_waves(F32)) w4_stream_kernel(const
           if (n_pairs == 0 || (nt * MB + mb) % kw != wk) continue;
           f32x4 sum = {0.f, 0.f, 0.f, 0.f};
           for (int w = 0; w < kw; ++w)
-            sum += red[(((wn * kw + w) * kPair + nt) * MB + mb) * 64 + lane];
-          if (orow[mb] >= 0)
-            store4<Row>(out + (int64_t)orow[mb] * a.out_ld + n + nt * 16, sum,
-                        a.N - n - nt * 16, a.out_vec != 0);
+            sum += red[(((wn * kw + w) * kPair + nt) * MB + mb) * 64];
+          store(pair0, nt, mb, sum);
         }
       }
     }
@@ -823,7 +958,6 @@ struct W4Plan {
 };
 
 W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
-  const bool zp = r->zeros != nullptr;
   W4Plan p{};
   p.k_waves = 1;
   const int64_t tiles = (r->n_out + 15) / 16, chunks = (r->k_in + 127) / 128;
@@ -842,21 +976,25 @@ W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
   // split 26; 9 of 512 x 4096, 144 pairs: 15, split 16, at 2 rows 9.2 and 8.7).
   p.stream = places * pairs >= 512 || places * pairs * chunks >= 8192;
   if (p.stream) {
-    const int64_t most = panel_chunks(f32, p.mb);
-    const int64_t reg_waves = f32 ? 8 : sg == 1 && !zp && p.mb == 1 ? 16 : 12;  // of a CU
-    const int64_t most_waves = reg_waves == 16 ? 8 : stream_waves(f32);
+    const int64_t most = panel_chunks(f32, p.mb, sg);
+    const int64_t x_lds = (chunks < most ? chunks : most) * chunk_lds(f32, p.mb, sg);
+    // Two workgroups a CU, where x leaves room for them, cover each other's starts
+    // (128 experts of 768 x 2048, 640 rows: 21.5 us in eights, 22.6 in twelves); one
+    // alone has twelve waves (20 of 4000 x 4000, 60 rows: 34.5 us, in eights 40).
+    const int64_t per_simd = simd_waves(f32, p.mb);
+    const int64_t most_waves = per_simd == 4 && 2 * (x_lds + kListLds) <= kLds ? 8 : kMaxWaves;
     auto room = [&](int64_t waves, int kw) {  // workgroups the CUs hold at once
-      int64_t lds = (chunks < most ? chunks : most) * chunk_lds(f32, p.mb);
+      int64_t lds = x_lds;
       const int64_t sums = waves * kPair * p.mb * 1024;
       if (kw > 1 && lds < sums) lds = sums;
-      const int64_t by_lds = kLds / (lds + kListLds), by_reg = reg_waves / waves;
+      const int64_t by_lds = kLds / (lds + kListLds), by_reg = per_simd / ((waves + 3) / 4);
       return 256 * (by_lds < by_reg ? by_lds : by_reg);
     };
     // All pairs at once, as many waves to a pair as that leaves room for and k
     // has chunks for (64 experts of 512 x 4096, 2 rows each: 1, 2, 3 waves to a
     // pair 19.5, 17.0, 23.9 us; 3 do not fit one round of workgroups) ...
     for (int kw = 4; kw >= 1 && p.waves == 0; --kw) {
-      if (kw > 1 && (chunks < 3 * kw || ahead(f32, sg) * kw > most)) continue;
+      if (kw > 1 && (chunks < 3 * kw || kAhead * kw > most)) continue;
       for (int64_t wn = 1; wn * kw <= most_waves; ++wn) {
         if (wn * kw < 4) continue;
         const int64_t slices = (pairs + wn - 1) / wn;
@@ -881,7 +1019,7 @@ W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
       p.slices = (int)((pairs + p.per_slice - 1) / p.per_slice);
     }
   } else {
-    const int64_t per = (chunks + kMaxWaves - 1) / kMaxWaves;
+    const int64_t per = (chunks + kSplitWaves - 1) / kSplitWaves;
     p.waves = (int)((chunks + per - 1) / per);
     // Two tiles a workgroup where several passes over the rows fill the CUs: x,
     // which each workgroup reads whole, is then what moves (one weight of 4000 x
@@ -907,30 +1045,29 @@ void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
   const int32_t* ids = rows.ids;
   const int n_rows = rows.n, E = rows.ids ? rows.experts : 0;
   a.slices = p.slices;
-  a.by_row = p.by_row;
   a.per_slice = p.per_slice;
-  a.pairs = (a.tiles + kPair - 1) / kPair;
-  a.k_waves = p.k_waves;
   a.pair_waves = p.waves / p.k_waves;
   a.wave_magic = (uint32_t)(((1ull << 32) + a.pair_waves - 1) / a.pair_waves);
   const dim3 grid((unsigned)a.slices, (unsigned)p.places, (unsigned)p.splits), block(64 * p.waves);
   if (!p.stream) {
     if (p.tiles == 2)
       hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 2>), grid, block, 0, s, ids, n_rows, E,
-                         a);
+                         p.waves, 1, (int)p.by_row, a);
     else
       hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 1>), grid, block, 0, s, ids, n_rows, E,
-                         a);
+                         p.waves, 1, (int)p.by_row, a);
     return;
   }
-  const int chunks = (a.ksteps + 3) / 4, kAhead = ahead(F32, SG), turn = kAhead * p.k_waves;
-  a.panel = panel_chunks(F32, MB) / turn * turn;
+  const int chunks = (a.ksteps + 3) / 4, turn = kAhead * p.k_waves;
+  a.panel = panel_chunks(F32, MB, SG) / turn * turn;
+  if (chunks <= panel_chunks(F32, MB, SG)) a.panel = chunks;
   a.panel_turns = a.panel / p.k_waves;
   a.turns = ((chunks + p.k_waves - 1) / p.k_waves + kAhead - 1) / kAhead * kAhead;
-  size_t lds = (size_t)(chunks < a.panel ? chunks : a.panel) * chunk_lds(F32, MB);
+  size_t lds = (size_t)a.panel * chunk_lds(F32, MB, SG);
   const size_t sums = (size_t)p.waves * kPair * MB * 1024;
   if (p.k_waves > 1 && lds < sums) lds = sums;
-  hipLaunchKernelGGL((w4_stream_kernel<F32, SG, ZP, MB>), grid, block, lds, s, ids, n_rows, E, a);
+  hipLaunchKernelGGL((w4_stream_kernel<F32, SG, ZP, MB>), grid, block, lds, s, ids, n_rows, E,
+                     p.waves, p.k_waves, (int)p.by_row, a);
 }
 
 template <int SG, bool ZP>
@@ -1006,12 +1143,12 @@ extern "C" int32_t mlora_w4_pack(const uint8_t* q, const void* scales, const uin
   a.s = base + l.s_off;
   a.z = zeros ? base + l.z_off : nullptr;
   a.words = l.w_bytes / 4;
-  a.cells = (int64_t)n_experts * l.tiles * l.blocks * 16 * l.sg;
+  a.cells = (int64_t)n_experts * l.pairs * l.blocks * 32 * l.sg;
   a.K = k_in;
   a.N = n_out;
   a.group = group;
   a.groups = (k_in + group - 1) / group;
-  a.tiles = (int32_t)l.tiles;
+  a.pairs = (int32_t)l.pairs;
   a.ksteps = (int32_t)l.ksteps;
   a.blocks = (int32_t)l.blocks;
   a.sg = (int32_t)l.sg;
@@ -1083,9 +1220,10 @@ extern "C" int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void*
   a.x_bytes = (uint32_t)(((need - 1) * x_ld + route->k_in) * es);
   a.x_ld_bytes = (uint32_t)(x_ld * es);
   a.topk = x_by_row ? 1u : (uint32_t)top_k;
+  a.topk_magic = 0xffffffffu / a.topk;
   a.K = route->k_in;
   a.N = route->n_out;
-  a.tiles = (int32_t)l.tiles;
+  a.pairs = (int32_t)l.pairs;
   a.ksteps = (int32_t)l.ksteps;
   a.blocks = (int32_t)l.blocks;
   const uint32_t per_block = route->group <= 128 ? 1u : (uint32_t)route->group / 128u;

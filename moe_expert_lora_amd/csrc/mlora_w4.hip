@@ -1050,12 +1050,16 @@ void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
   a.wave_magic = (uint32_t)(((1ull << 32) + a.pair_waves - 1) / a.pair_waves);
   const dim3 grid((unsigned)a.slices, (unsigned)p.places, (unsigned)p.splits), block(64 * p.waves);
   if (!p.stream) {
-    if (p.tiles == 2)
-      hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 2>), grid, block, 0, s, ids, n_rows, E,
-                         p.waves, 1, (int)p.by_row, a);
-    else
-      hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 1>), grid, block, 0, s, ids, n_rows, E,
-                         p.waves, 1, (int)p.by_row, a);
+    // two tiles: calls of several passes, which have two row blocks or fp32 rows
+    if constexpr (F32 || MB > 1) {
+      if (p.tiles == 2) {
+        hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 2>), grid, block, 0, s, ids, n_rows,
+                           E, p.waves, 1, (int)p.by_row, a);
+        return;
+      }
+    }
+    hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 1>), grid, block, 0, s, ids, n_rows, E,
+                       p.waves, 1, (int)p.by_row, a);
     return;
   }
   const int chunks = (a.ksteps + 3) / 4, turn = kAhead * p.k_waves;

@@ -113,8 +113,8 @@ def test_w4_refuses_weights(lib, bad):
 
 
 def test_w4_packed_bytes(lib):
-    # 7 column tiles of 16, 8 k steps of 256 bytes; 4 groups of 16 columns
-    w, s, z = 4 * 7 * 8 * 256, 4 * 7 * 4 * 16 * 2, 4 * 7 * 4 * 16
+    # 4 pairs of column tiles of 16, 8 k steps of 512 bytes; 4 groups of 32 columns
+    w, s, z = 4 * 4 * 8 * 512, 4 * 4 * 4 * 32 * 2, 4 * 4 * 4 * 32
     up = lambda v: -(-v // 256) * 256  # noqa: E731
     assert ml.mlora_w4_packed_bytes(4, 256, 100, 64, BF16, False) == up(w) + up(s)
     assert ml.mlora_w4_packed_bytes(4, 256, 100, 64, BF16, True) == up(w) + up(s) + up(z)

@@ -704,11 +704,14 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const void* src, int64_t 
   if (t >= a.n_tokens) return;
   const raw* x = row_at<Row, raw>(a.src, t, a.src_ld);
   for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+    // x is requested ahead of the row numbers, a unit ahead of its stores
+    raw next = x[min(g, a.units - 1)];
     int row[kSlots];
     slot_numbers(a, t, j0, row);
     const uint32_t unnamed = unnamed_rows(a, t, j0);
     for (int c = g; c < a.units; c += G) {
-      const raw v = x[c];
+      const raw v = next;
+      if (c + G < a.units) next = x[c + G];
 #pragma unroll
       for (int j = 0; j < kSlots; ++j)
         if (row[j] >= 0) store_once(&row_at<Row, raw>(a.dst, row[j], a.dst_ld)[c], v);

@@ -755,12 +755,10 @@ w4_stream_kernel(const int32_t* ids, int n_rows, int E, int waves, int k_waves, 
     }
   };
 
-  // One row block: the first weights are requested ahead of the rows they meet, the
-  // ring's last place once x has been requested, so that weights arrive while x
-  // does (128 experts of 2048 x 768, 640 rows: 23.2 us, all of them after x 26.2).
-  // Two row blocks have twice the x, which would wait behind them (2048 rows: 30.2
-  // and 28.2 us); fp32 rows pass through registers, which would.
-  constexpr int kEarly = F32 || MB > 1 ? 0 : kAhead - 1;
+  // The first weights are requested ahead of the rows they meet, the others once x
+  // has been, so that weights arrive while x does (128 experts of 2048 x 768, 640
+  // rows: 23.4 us, all of them after x 24.2).
+  constexpr int kEarly = 1;
   Chunk ring[kAhead];
   auto first_requests = [&] {
     first_request();
@@ -978,10 +976,10 @@ W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
   p.mb = !f32 && (places == 1 ? mean > 16 : mean > 10) ? 2 : 1;
   const int64_t blocks = (mean + 16 * p.mb - 1) / (16 * p.mb);  // passes
   const int64_t pairs = (tiles + kPair - 1) / kPair;
-  // Streaming pays from 512 pairs of tiles (9 experts of 2048 x 1024, 16 rows
-  // each: 10.3 us, split 15.6; 4 experts of 4000 x 512, 500 pairs: 7.7, split
-  // 7.0), or from fewer of long k (4 of 4000 x 4000, 500 pairs of 32 chunks: 17,
-  // split 26; 9 of 512 x 4096, 144 pairs: 15, split 16, at 2 rows 9.2 and 8.7).
+  // Streaming pays from 512 pairs of tiles (16 experts of 1024 x 1024, 64 rows, 512
+  // pairs: 9.2 us, split 10.2; 60 of 512 x 200, 420 pairs: 8.2, split 6.0), or from
+  // fewer of long k (4 of 4000 x 4000, 500 pairs of 32 chunks, 64 rows: 19.8, split
+  // 26.3; 60 of 2048 x 200, 420 of 16 chunks: 10.5, split 10.4).
   p.stream = places * pairs >= 512 || places * pairs * chunks >= 8192;
   if (p.stream) {
     const int64_t most = panel_chunks(f32, p.mb, sg);
@@ -998,11 +996,13 @@ W4Plan plan_w4(const mlora_w4_route* r, W4Rows rows, bool f32, int sg) {
       const int64_t by_lds = kLds / (lds + kListLds), by_reg = per_simd / ((waves + 3) / 4);
       return 256 * (by_lds < by_reg ? by_lds : by_reg);
     };
-    // All pairs at once, as many waves to a pair as that leaves room for and k
-    // has chunks for (64 experts of 512 x 4096, 2 rows each: 1, 2, 3 waves to a
-    // pair 19.5, 17.0, 23.9 us; 3 do not fit one round of workgroups) ...
+    // All pairs at once, as many waves to a pair as k has chunks for, until a CU has
+    // eight: their requests fill its cache's lines (64 experts of 4096 x 512, 128
+    // rows, 1024 pairs: 1, 2, 3 waves to a pair 19.8, 16.4, 17.7 us; 4 of 4000 x
+    // 4000, 8 rows, 500 pairs: 20.1, 14.5, 13.6, with four 12.3) ...
     for (int kw = 4; kw >= 1 && p.waves == 0; --kw) {
       if (kw > 1 && (chunks < 3 * kw || kAhead * kw > most)) continue;
+      if (kw > 1 && places * pairs * (kw - 1) >= 256 * 8) continue;
       for (int64_t wn = 1; wn * kw <= most_waves; ++wn) {
         if (wn * kw < 4) continue;
         const int64_t slices = (pairs + wn - 1) / wn;

@@ -176,7 +176,6 @@ struct W4Args {
   int32_t K, N;
   int32_t ksteps, blocks;
   uint32_t block_magic;   // ceil(2^31 / chunks per scale block)
-  int32_t slices;         // workgroups per expert
   int32_t pairs, per_slice;  // tile pairs; streaming form: those of a slice
   int32_t pair_waves;     // pairs a workgroup's waves hold at a time
   uint32_t wave_magic;    // ceil(2^32 / pair_waves)
@@ -190,7 +189,7 @@ struct W4Args {
 struct W4Lead {
   const int32_t* ids;  // null: one weight
   int n_rows, E;       // E 0: one weight
-  int waves, k_waves;  // waves of a workgroup; those that share a pair
+  int waves;           // of a workgroup
   int by_row;          // a place per row, not per expert
 };
 
@@ -233,7 +232,7 @@ __device__ __forceinline__ u32x4 unpack(uint32_t w, uint32_t base) {
   return r;
 }
 
-// Second MFMA operand of one k step as loaded: 8 bf16 or 8 fp32 values.
+// x operand of one k step as loaded: 8 bf16 or 8 fp32 values.
 template <bool F32>
 struct XRaw {
   u32x4 v[F32 ? 2 : 1];
@@ -579,13 +578,13 @@ __device__ __forceinline__ void zero_rows(const W4Args& a, const int* list, int 
 // sums up through LDS in wave order; x goes straight to the operands.
 template <bool F32, int SG, bool ZP, int MB, int NT>
 __global__ void __launch_bounds__(64 * kSplitWaves)
-w4_split_kernel(const int32_t* ids, int n_rows, int E, int waves, int k_waves, int by_row, W4Args a) {
+w4_split_kernel(const int32_t* ids, int n_rows, int E, int waves, int by_row, W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
   constexpr int kCols = 16 * NT, kStride = kCols + 4, kRows = 16 * MB;
   __shared__ int list[kScan];
   __shared__ __attribute__((aligned(16))) int counts[kMaxWaves];
   __shared__ float red[kSplitWaves * kRows * kStride];
-  const W4Lead lead = {ids, n_rows, E, waves, k_waves, by_row};
+  const W4Lead lead = {ids, n_rows, E, waves, by_row};
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int wave = uniform_i32(tid >> 6);
   IdRun run;
@@ -691,14 +690,15 @@ constexpr int simd_waves(bool f32, int mb) { return f32 || mb > 1 ? 3 : 4; }
 
 template <bool F32, int SG, bool ZP, int MB>
 __global__ void __launch_bounds__(64 * kMaxWaves, simd_waves(F32, MB))
-w4_stream_kernel(const int32_t* ids, int n_rows, int E, int waves, int k_waves, int by_row, W4Args a) {
+w4_stream_kernel(const int32_t* ids, int n_rows, int E, int waves, int by_row, int k_waves,
+                 W4Args a) {
   typedef typename std::conditional<F32, F32Row, Bf16Row>::type Row;
   typedef WChunk<F32, SG, ZP, kPair> Chunk;
   constexpr int kRows = 16 * MB, kParts = XFrag<F32>::kParts;
   __shared__ int list[kScan];
   __shared__ __attribute__((aligned(16))) int counts[kMaxWaves];
   extern __shared__ u32x4 xs[];  // [k step][row block][part][lane]
-  const W4Lead lead = {ids, n_rows, E, waves, k_waves, by_row};
+  const W4Lead lead = {ids, n_rows, E, waves, by_row};
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int wave = uniform_i32(tid >> 6);
   IdRun run;
@@ -1052,22 +1052,21 @@ void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
   W4Args a = a0;
   const int32_t* ids = rows.ids;
   const int n_rows = rows.n, E = rows.ids ? rows.experts : 0;
-  a.slices = p.slices;
   a.per_slice = p.per_slice;
   a.pair_waves = p.waves / p.k_waves;
   a.wave_magic = (uint32_t)(((1ull << 32) + a.pair_waves - 1) / a.pair_waves);
-  const dim3 grid((unsigned)a.slices, (unsigned)p.places, (unsigned)p.splits), block(64 * p.waves);
+  const dim3 grid((unsigned)p.slices, (unsigned)p.places, (unsigned)p.splits), block(64 * p.waves);
   if (!p.stream) {
     // two tiles: calls of several passes, which have two row blocks or fp32 rows
     if constexpr (F32 || MB > 1) {
       if (p.tiles == 2) {
         hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 2>), grid, block, 0, s, ids, n_rows,
-                           E, p.waves, 1, (int)p.by_row, a);
+                           E, p.waves, (int)p.by_row, a);
         return;
       }
     }
     hipLaunchKernelGGL((w4_split_kernel<F32, SG, ZP, MB, 1>), grid, block, 0, s, ids, n_rows, E,
-                       p.waves, 1, (int)p.by_row, a);
+                       p.waves, (int)p.by_row, a);
     return;
   }
   const int chunks = (a.ksteps + 3) / 4, turn = kAhead * p.k_waves;
@@ -1079,7 +1078,7 @@ void launch_w4(const W4Args& a0, const W4Plan& p, W4Rows rows, hipStream_t s) {
   const size_t sums = (size_t)p.waves * kPair * MB * 1024;
   if (p.k_waves > 1 && lds < sums) lds = sums;
   hipLaunchKernelGGL((w4_stream_kernel<F32, SG, ZP, MB>), grid, block, lds, s, ids, n_rows, E,
-                     p.waves, p.k_waves, (int)p.by_row, a);
+                     p.waves, (int)p.by_row, p.k_waves, a);
 }
 
 template <int SG, bool ZP>

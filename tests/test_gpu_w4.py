@@ -165,7 +165,9 @@ def test_fewer_rows_than_experts(ml, dtype, rows, experts, k, n, group, zeros):
 @pytest.mark.parametrize("rows,experts,k,n,group,zeros", [
     (5, 4, 2104, 4000, 64, True),      # four waves to a pair, several panels in float32
     (90, 4, 2504, 4010, 128, False),   # two row blocks, several panels
-    (40, 16, 704, 1200, 32, True)])
+    (40, 16, 704, 1200, 32, True),
+    (60, 16, 1200, 1030, 64, True),    # three waves to a pair
+    (70, 32, 1000, 1000, 128, False)])  # two, the last tile alone in its pair
 def test_several_waves_to_a_pair(ml, dtype, rows, experts, k, n, group, zeros):
     w = Weights(ml, experts, k, n, group, zeros, dtype, rows)
     x = _x((rows, k), dtype, 10)

@@ -567,8 +567,10 @@ int32_t mlora_w4_pack(const uint8_t* q, const void* scales, const uint8_t* zeros
  * (n_experts == 1) for every row. x_by_row as in mlora_projection: row r reads
  * x[r / top_k] or x[r]. x rows start on 16 bytes (x_ld a multiple of 8) and
  * span at most 4 GiB. Weights enter exactly, sums are fp32, one rounding. A
- * row of x that is not finite, or above 2^122 in magnitude, gives its own
- * output row no defined finite values; other rows do not change. */
+ * row of x with a value that is not finite, or above 2^117 in magnitude (15 times
+ * 128 of which fill fp32's range), gives its own output row no defined finite
+ * values; other rows do not change. Values of x enter to within 2^-126: subnormal
+ * parts may count as zeros (fp32 values of 2^-103 and more enter exactly). */
 int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void* x, int64_t x_rows,
                              int64_t x_ld, int32_t x_by_row, void* out, int64_t out_ld,
                              const int32_t* ids, int64_t n_rows, int32_t top_k, void* stream);

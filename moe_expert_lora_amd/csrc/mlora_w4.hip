@@ -13,8 +13,10 @@
 // group's sum of x, so that v - z is what they hold at its end; they are then
 // scaled in fp32, so weights are never rounded. A lane's values are of one
 // column: one scale and one zero point for all of them. fp32 rows are split into
-// three bf16 parts (8 + 8 + 8 bits, exact while the last is a normal number, from
-// |x| = 2^-110), one MFMA each: the products stay exact and the sums fp32.
+// three bf16 parts (8 + 8 + 8 bits, exact while the last is no subnormal number,
+// from |x| = 2^-103), one MFMA each: the products stay exact and the sums fp32.
+// Up to |x| = 2^117 no sum overflows: one of a group of at most 128 values stays
+// below (7.5 + 7.5) sum |x|.
 //
 // The offset is small (0.5 without zero points), so that the sums, like a plain
 // fp32 one's, pass through little that cancels: relative L2 errors of fp32 rows of

@@ -103,3 +103,58 @@ def test_every_weight_is_exact(ml, zeros, group):
     want = moe.w4_weights(q, s, z, k, group)[0].T
     got = out.double().cpu().numpy()
     assert (np.abs(got - want) <= U * np.abs(want)).all()
+
+
+def _one_row_each(ml, dtype, zeros, group, special):
+    """Rows of ordinary values with ``special`` in row 3, and the same without it."""
+    k, n, rows = 264, 520, 40
+    route, q, s, z = _weights(ml, 2, k, n, group, zeros, dtype, 9)
+    x = torch.randn((rows, k), generator=torch.Generator(device=DEV).manual_seed(6),
+                    device=DEV).to(dtype)
+    ids = (torch.arange(rows, device=DEV) % 2).to(torch.int32)
+    clean, got = (torch.empty((rows, n), dtype=dtype, device=DEV) for _ in range(2))
+    ml.mlora_w4_gather_gemv(route, x, clean, ids)
+    x[3] = special.to(DEV)
+    ml.mlora_w4_gather_gemv(route, x, got, ids)
+    keep = [r for r in range(rows) if r != 3]
+    assert torch.equal(got[keep], clean[keep])
+    w = moe.w4_weights(q, s, z, k, group)[1]
+    scale = s[1][:, np.arange(k) // group]
+    return w, scale, x[3].double().cpu().numpy(), got[3].double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("signs", ["same", "mixed"])
+def test_largest_values(ml, dtype, zeros, group, signs):
+    """A whole row of 2^117, the largest that the header names: finite and right
+    (scales below 2^-4 keep the sums over groups in range). Its neighbours stay
+    as they are. A group's 128 sums and its start are each off by half a step of
+    at most 15 sum |x|; the scaled sum over groups by one of its own size."""
+    big = torch.full((264,), 2.0 ** 117)
+    if signs == "mixed":
+        big[::3] = -big[::3]
+    w, scale, x, got = _one_row_each(ml, dtype, zeros, group, big.to(dtype))
+    ref = w @ x
+    tol = (3 * 129 + 264) * U * 15 * (np.abs(scale) @ np.abs(x))
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    assert np.isfinite(got).all()
+    assert (np.abs(got - ref) <= tol + half * (np.abs(ref) + tol)).all()
+
+
+@pytest.mark.parametrize("dtype,size", [(torch.float32, 2.0 ** -104), (torch.float32, 2.0 ** -112),
+                                        (torch.float32, 2.0 ** -124), (torch.float32, 2.0 ** -130),
+                                        (torch.bfloat16, 2.0 ** -120),
+                                        (torch.bfloat16, 2.0 ** -130)])
+def test_smallest_values(ml, dtype, size):
+    """Values enter to within 2^-126; a sum that is subnormal may be 0, at each of
+    the additions (three parts, a start, one for the groups)."""
+    g = torch.Generator().manual_seed(8)
+    row = (torch.randn(264, generator=g, dtype=torch.float64) * size).to(dtype)
+    w, scale, x, got = _one_row_each(ml, dtype, True, 64, row)
+    ref = w @ x
+    mag = 15 * (scale @ np.abs(x))
+    tol = 2.0 ** -126 * (np.abs(w).sum(1) + 5 * scale.sum(1) + 1) + 1056 * U * mag
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    assert (np.abs(got - ref) <= tol + half * np.abs(ref)).all()

@@ -22,7 +22,7 @@
 // fp32 one's, pass through little that cancels: relative L2 errors of fp32 rows of
 // 264 and 768 values, means 0 and 3, are 0.9 to 3.3 u (u = 2^-24), a plain fp32
 // sum's 0.8 to 1.6. (With bf16 values 16 + v, made by an and/or a pair, 5.7 to 39 u
-// in the same time: 128 experts of 768 x 2048, 640 rows 21.7 us, now 21.8.)
+// in the same time: 128 experts of 768 x 2048, 640 rows 21.7 us, as now.)
 // A row of x with an infinity or a NaN gives no finite outputs, in that row alone.
 //
 // Two forms, each of which reads an expert's weights once per 16 or 32 of its
@@ -220,21 +220,27 @@ __device__ __forceinline__ uint32_t x_row(const W4Args& a, uint32_t row) {
   return row - q * a.topk >= a.topk ? q + 1 : q;
 }
 
-// The lowest magnitude bits of unpack()'s bytes in a vector register: beside the
-// mask in a scalar one, and and or are one operation. Taken once, at a kernel's
-// start: the statement is opaque to the compiler, which could not keep it clear of
-// an MFMA's registers further down.
-__device__ __forceinline__ uint32_t low_bits() {
-  uint32_t r;
-  asm volatile("v_mov_b32 %0, 0x01010101" : "=v"(r));
-  return r;
+// The bits of unpack()'s bytes that a word holds, and the lowest of the magnitude,
+// which it does not. The mask in a scalar register and the other in a vector one
+// make an and and an or one operation. Taken once, at a kernel's start: the
+// statements are opaque to the compiler, which would move a mask it knows across
+// the reversal, and could not keep the vector one clear of an MFMA's registers
+// further down.
+struct Codes {
+  uint32_t mask, low;
+};
+__device__ __forceinline__ Codes codes() {
+  Codes c;
+  asm volatile("s_mov_b32 %0, 0x8e8e8e8e" : "=s"(c.mask));
+  asm volatile("v_mov_b32 %0, 0x01010101" : "=v"(c.low));
+  return c;
 }
 
 // 8 packed values of one column -> the bf16 values v - 7.5.
-__device__ __forceinline__ u32x4 unpack(uint32_t w, uint32_t low) {
-  constexpr uint32_t kMask = 0x8e8e8e8eu;
+__device__ __forceinline__ u32x4 unpack(uint32_t w, Codes c) {
   constexpr float kScale = 256.f;  // of (2 v - 15) / 512
-  const int a = (int)((w & kMask) | low), b = (int)((__builtin_bitreverse32(w) & kMask) | low);
+  const int a = (int)((w & c.mask) | c.low);
+  const int b = (int)((__builtin_bitreverse32(w) & c.mask) | c.low);
   auto pair = [](auto v) { return __builtin_bit_cast(uint32_t, v); };
   u32x4 r;
   r[0] = pair(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, kScale, false));
@@ -375,7 +381,7 @@ constexpr uint32_t minus_ones(bool zp) { return zp ? 0xbf80bf80u : 0xbf00bf00u; 
 struct NoSums {};
 template <bool F32, int SG, bool ZP, int NT, int MB, typename X, typename S = NoSums>
 __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, int t0, X x,
-                                          uint32_t low, f32x4 (&acc)[NT][MB], S sum = S{}) {
+                                          Codes cd, f32x4 (&acc)[NT][MB], S sum = S{}) {
   constexpr bool kSums = !std::is_same<S, NoSums>::value;
   constexpr int kPer = 4 / SG, kParts = XFrag<F32>::kParts;
   constexpr uint32_t kc = minus_ones(ZP);
@@ -412,7 +418,7 @@ __device__ __forceinline__ void add_chunk(const WChunk<F32, SG, ZP, NT>& wc, int
       }
 #pragma unroll
       for (int ks = 0; ks < kPer; ++ks) {
-        const u32x4 wf = unpack(wc.w[nt][sg * kPer + ks], low);
+        const u32x4 wf = unpack(wc.w[nt][sg * kPer + ks], cd);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -602,7 +608,7 @@ w4_split_kernel(const int32_t* ids, int n_rows, int E, int waves, int by_row, W4
   IdRun run;
   run.set(lead, 0, min(kScan, n_rows), wave, lane);
   fetch_args(a);
-  const uint32_t low = low_bits();
+  const Codes cd = codes();
   const int e = place_expert(lead), tile = (int)blockIdx.x * NT;
   const int n0 = tile * 16, chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
@@ -650,8 +656,12 @@ w4_split_kernel(const int32_t* ids, int n_rows, int E, int waves, int by_row, W4
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             x[mb][ks] = load_x<F32>(rx, row_off[mb], c * 128 + ks * 32 + lg * 8, a.K);
+        // bf16: all of them requested ahead of the first product's wait, which the
+        // compiler else puts between them; fp32 rows, whose conversions it spreads
+        // over the loads, take 8.0 us without and 8.3 with (5 of 1000 x 1365, 37 rows)
+        if constexpr (!F32) __builtin_amdgcn_sched_barrier(0);
         add_chunk<F32, SG, ZP, NT, MB>(
-            wc, t0, [&](int mb, int ks, XFrag<F32>& f) { f.set(x[mb][ks]); }, low, acc);
+            wc, t0, [&](int mb, int ks, XFrag<F32>& f) { f.set(x[mb][ks]); }, cd, acc);
         if (c + waves < chunks) request(c + waves);
       }
 #pragma unroll
@@ -719,7 +729,7 @@ w4_stream_kernel(const int32_t* ids, int n_rows, int E, int waves, int by_row, i
   const int panel = a.panel;
   // behind the operands, minus the sums of x: [group][row block][row]
   f32x4* x_sums = reinterpret_cast<f32x4*>(xs + panel * (4 * MB * kParts * 64));
-  const uint32_t low = low_bits();
+  const Codes cd = codes();
   const int e = place_expert(lead), slice = (int)blockIdx.x;
   const int chunks = (a.ksteps + 3) >> 2;
   typename Row::elem* out = static_cast<typename Row::elem*>(a.out);
@@ -923,7 +933,7 @@ w4_stream_kernel(const int32_t* ids, int n_rows, int E, int waves, int by_row, i
                 };
                 const f32x4* px_sums = x_sums + (c - p0) * (SG * MB * 4) + lg;
                 add_chunk<F32, SG, ZP, kPair, MB>(
-                    ring[d], 0, operand, low, acc,
+                    ring[d], 0, operand, cd, acc,
                     [&](int mb, int sg) { return px_sums[(sg * MB + mb) * 4]; });
               }
               request(ring[d]);

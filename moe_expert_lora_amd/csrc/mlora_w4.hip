@@ -1180,7 +1180,7 @@ extern "C" int32_t mlora_w4_pack(const uint8_t* q, const void* scales, const uin
   a.K = k_in;
   a.N = n_out;
   a.group = group;
-  a.groups = (k_in + group - 1) / group;
+  a.groups = (int32_t)(((int64_t)k_in + group - 1) / group);  // group may be near 2^31
   a.pairs = (int32_t)l.pairs;
   a.ksteps = (int32_t)l.ksteps;
   a.blocks = (int32_t)l.blocks;

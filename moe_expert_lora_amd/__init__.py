@@ -11,6 +11,7 @@ libmlora.so is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -816,7 +817,11 @@ def make_w4_route(q, scales, zeros, k_in: int, group: int, stream=None) -> W4Rou
     k_in / 2] bytes (k even in the low half), ``scales`` [n_experts, n_out,
     ceil(k_in / group)] in bf16 or float32 (the dtype of x and out), ``zeros``
     bytes of the same shape or None (8). The route keeps the packed tensor; the
-    arguments are not needed once the call's work is done."""
+    arguments are not needed once the call's work is done.
+
+    The packed tensor is written by and belongs to ``stream`` (None: the current
+    one). Work on another stream has to wait for it, and ``stream`` for that work
+    before the route is dropped."""
     import torch
     if q.dim() != 3 or scales.dim() != 3:
         raise ValueError("q and scales must be 3-D")
@@ -830,7 +835,9 @@ def make_w4_route(q, scales, zeros, k_in: int, group: int, stream=None) -> W4Rou
     nbytes = mlora_w4_packed_bytes(E, k_in, N, group, code, zeros is not None)
     if nbytes == 0:
         raise _err(MLORA_ERR_INVALID)
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    # of the stream that writes it: a block of another stream's may still be in use there
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        packed = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     route = W4Route()
     rc = load().mlora_w4_pack(_dev(q, "q", torch.uint8), _dev(scales, "scales"),
                               None if zeros is None else _dev(zeros, "zeros", torch.uint8),

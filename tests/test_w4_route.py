@@ -1,0 +1,83 @@
+"""make_w4_route without a GPU: where the packed memory comes from and which
+tensors it takes, with the library's call and the tensors stood in for."""
+from __future__ import annotations
+
+import contextlib
+import types
+
+import pytest
+
+import moe_expert_lora_amd as ml
+
+torch = pytest.importorskip("torch")
+
+
+class Tensor:
+    """What make_w4_route asks of a device tensor."""
+
+    is_cuda = True
+
+    def __init__(self, shape, dtype, index=0):
+        self.shape, self.dtype = shape, dtype
+        self.device = torch.device("cuda", index)
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The pack calls and allocations made, and the stream current at each allocation."""
+    seen = types.SimpleNamespace(packs=[], allocations=[], current="current")
+    real = ml.load()
+
+    def pack(*args):
+        seen.packs.append(args[-1])
+        return ml.MLORA_OK
+
+    @contextlib.contextmanager
+    def on_stream(stream):
+        old, seen.current = seen.current, stream
+        yield
+        seen.current = old
+
+    def empty(n, dtype, device):
+        seen.allocations.append((n, device, seen.current))
+        return Tensor((n,), dtype, device.index)
+
+    lib = types.SimpleNamespace(mlora_w4_pack=pack,
+                                mlora_w4_packed_bytes=real.mlora_w4_packed_bytes)
+    monkeypatch.setattr(ml, "load", lambda: lib)
+    monkeypatch.setattr(ml, "_stream_handle", lambda s: "handle of current" if s is None else s)
+    monkeypatch.setattr(ml, "_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "stream", on_stream)
+    monkeypatch.setattr(torch, "empty", empty)
+    return seen
+
+
+def _args(q=0, scales=0, zeros=0):
+    """Tensors of 2 x 48 x 64 in groups of 32, each on the device of that index."""
+    return (Tensor((2, 48, 32), torch.uint8, q), Tensor((2, 48, 2), torch.bfloat16, scales),
+            None if zeros is None else Tensor((2, 48, 2), torch.uint8, zeros), 64, 32)
+
+
+def test_packed_memory_is_of_the_stream_that_writes_it(calls):
+    """A block of the current stream's could still be in use there while `side`
+    writes it, and would go back there while `side` still reads it."""
+    route = ml.make_w4_route(*_args(), stream="side")
+    nbytes = ml.mlora_w4_packed_bytes(2, 64, 48, 32, ml.MLORA_BF16, True)
+    assert calls.allocations == [(nbytes, torch.device("cuda", 0), "side")]
+    assert calls.packs == ["side"] and calls.current == "current"
+    assert route._keep.shape == (nbytes,)
+
+
+def test_packed_memory_of_the_current_stream(calls):
+    ml.make_w4_route(*_args(zeros=None))
+    assert [a[2] for a in calls.allocations] == ["current"]
+    assert calls.packs == ["handle of current"]

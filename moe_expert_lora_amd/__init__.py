@@ -832,6 +832,10 @@ def make_w4_route(q, scales, zeros, k_in: int, group: int, stream=None) -> W4Rou
             zeros is not None and zeros.shape != scales.shape):
         raise ValueError("scales and zeros must be [n_experts, n_out, ceil(k_in / group)]")
     code = _dtype_code(scales)
+    for name, t in (("q", q), ("scales", scales), ("zeros", zeros)):
+        # the call runs on the current device's stream, as those of _native
+        if t is not None and t.is_cuda and t.device.index != _device():
+            raise ValueError(f"{name} must be on the current device")
     nbytes = mlora_w4_packed_bytes(E, k_in, N, group, code, zeros is not None)
     if nbytes == 0:
         raise _err(MLORA_ERR_INVALID)

@@ -81,3 +81,12 @@ def test_packed_memory_of_the_current_stream(calls):
     ml.make_w4_route(*_args(zeros=None))
     assert [a[2] for a in calls.allocations] == ["current"]
     assert calls.packs == ["handle of current"]
+
+
+@pytest.mark.parametrize("where,name", [((1, 1, 1), "q"), ((1, 0, 0), "q"), ((0, 1, 0), "scales"),
+                                        ((0, 0, 1), "zeros"), ((0, 1, None), "scales")])
+def test_tensors_of_another_device_are_refused(calls, where, name):
+    """The pack runs on the current device (0 here)."""
+    with pytest.raises(ValueError, match=f"{name} must be on the current device"):
+        ml.make_w4_route(*_args(*where))
+    assert not calls.packs and not calls.allocations

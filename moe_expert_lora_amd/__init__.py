@@ -178,8 +178,11 @@ def load() -> ctypes.CDLL:
     try:
         import torch
         _DTYPES.update({torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32})
-        _raw_stream = torch._C._cuda_getCurrentRawStream
-        _device = torch._C._cuda_getDevice
+        # torch's own short forms of these calls (no objects made); a torch without
+        # them (a build for the CPU, another version) still serves the host functions
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     except ImportError:
         pass
     lib = ctypes.CDLL(LIB_PATH)

@@ -66,6 +66,15 @@ def _compile(sources, lib, verbose):
         os.replace(out, lib)
 
 
+def has_torch() -> bool:
+    """Whether a PyTorch for ROCm is there to build the binding against."""
+    try:
+        import torch
+    except ImportError:
+        return False
+    return torch.version.hip is not None
+
+
 def _compile_binding(verbose):
     """Host code only: torch's core headers, Python's and HIP's."""
     import torch
@@ -83,11 +92,16 @@ def _compile_binding(verbose):
 
 def build(verbose: bool = False) -> str:
     """Compile moe_expert_lora_amd/libmlora.so (the fold and the MoE layer's
-    operators), the CPython binding of the latter, and libmlora_probe.so
-    (bench.py's measurement probes); returns libmlora.so's path."""
+    operators), libmlora_probe.so (bench.py's measurement probes) and, where there
+    is a PyTorch for ROCm, the CPython binding of the MoE layer's operators (the C
+    interface and the host functions do without); returns libmlora.so's path."""
     _compile(SOURCES, LIB, verbose)
-    _compile_binding(verbose)
     _compile(PROBE_SOURCES, PROBE_LIB, verbose)
+    if has_torch():
+        _compile_binding(verbose)
+    else:
+        print("no PyTorch for ROCm: " + os.path.basename(BINDING) + " is not built",
+              file=sys.stderr)
     return LIB
 
 

@@ -128,6 +128,17 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
+// A grid of any number of workgroups. HIP takes fewer than 2^32 threads along one
+// dimension: from kGridRow workgroups (of up to 256 threads) on, further rows lie
+// along y, the last of them with workgroups past the end.
+constexpr int kGridRow = 1 << 23;
+inline dim3 flat_grid(int64_t workgroups) {
+  if (workgroups <= kGridRow) return dim3((unsigned)workgroups);
+  return dim3(kGridRow, (unsigned)((workgroups + kGridRow - 1) / kGridRow));
+}
+// The workgroup's number in it.
+__device__ __forceinline__ int flat_group() { return (int)(blockIdx.y * kGridRow + blockIdx.x); }
+
 inline int32_t launch_status(const char* who) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(MLORA_ERR_HIP, "%s: %s", who, hipGetErrorString(e));

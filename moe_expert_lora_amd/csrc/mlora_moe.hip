@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(256) router_topk_kernel(const void* logits, in
   set_lead(a, logits, ld, n_tokens, E, k, renorm);
   constexpr bool kPacked = sizeof(typename Row::elem) == 2;
   const int gl = threadIdx.x & (LPT - 1);
-  const int token = (int)((blockIdx.x * blockDim.x + threadIdx.x) / LPT);
+  const int token = flat_group() * (int)(blockDim.x / LPT) + (int)(threadIdx.x / LPT);
   const bool on = token < a.n_tokens;  // lanes past the end stay for the reductions
   float v[VPL];
   load_row<Row, LPT, VPL, VEC, WIDE>(a.logits, (int64_t)(on ? token : 0) * a.ld, a.E, gl, v);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(256) router_backward_kernel(const void* logits
   constexpr uint32_t kUnset = 0xffffffffu;
   __shared__ uint32_t lds[256 / LPT][LPT * VPL];
   const int gl = threadIdx.x & (LPT - 1);
-  const int token = (int)((blockIdx.x * blockDim.x + threadIdx.x) / LPT);
+  const int token = flat_group() * (int)(blockDim.x / LPT) + (int)(threadIdx.x / LPT);
   const bool on = token < a.n_tokens;
   const int64_t t = on ? token : 0;
   uint32_t* s = lds[threadIdx.x / LPT];
@@ -246,7 +246,7 @@ void launch_router(const RouterArgs& a, bool backward, hipStream_t s) {
   // over the CUs; large ones four waves.
   const int64_t lanes = (int64_t)a.n_tokens * LPT;
   const int threads = lanes < 64 * 1024 ? 64 : 256;
-  const dim3 grid((unsigned)((lanes + threads - 1) / threads));
+  const dim3 grid = flat_grid((lanes + threads - 1) / threads);
   if (backward)
     hipLaunchKernelGGL((router_backward_kernel<Row, LPT, VPL, VEC, WIDE>), grid, dim3(threads), 0, s,
                        a.logits, a.ld, a.n_tokens, a.E, a.k, a.renorm, a);
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const void* src, int64_t 
   a.k = k;
   typedef Unit<Row, WIDE> Un;
   typedef typename Un::raw raw;
-  const int t = uniform_i32((int)(blockIdx.x * (256 / G) + threadIdx.x / G));
+  const int t = uniform_i32(flat_group() * (256 / G) + (int)(threadIdx.x / G));
   const int g = threadIdx.x & (G - 1);
   if (t >= a.n_tokens) return;
   const raw* x = row_at<Row, raw>(a.src, t, a.src_ld);
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* src, int64_t s
   a.k = k;
   typedef Unit<Row, WIDE> Un;
   typedef typename Un::raw raw;
-  const int t = uniform_i32((int)(blockIdx.x * (256 / G) + threadIdx.x / G));
+  const int t = uniform_i32(flat_group() * (256 / G) + (int)(threadIdx.x / G));
   const int g = threadIdx.x & (G - 1);
   if (t >= a.n_tokens) return;
   raw* out = row_at<Row, raw>(a.dst, t, a.dst_ld);
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const void* d_out
   __shared__ float part[256 / 64][kSlots];
   // every thread of a workgroup reaches the barriers: a token past the end
   // has no slots and no columns
-  const int tok = uniform_i32((int)(blockIdx.x * (256 / G) + threadIdx.x / G));
+  const int tok = uniform_i32(flat_group() * (256 / G) + (int)(threadIdx.x / G));
   const int g = threadIdx.x & (G - 1);
   const bool on = tok < a.n_tokens;
   const int t = on ? tok : 0;
@@ -846,7 +846,7 @@ enum RowsOp { kDispatch, kCombine, kCombineBackward };
 
 template <typename Row, bool WIDE, int G>
 void launch_rows(RowsOp op, const RowsArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.n_tokens * G + 255) / 256)), block(256);
+  const dim3 grid = flat_grid(((int64_t)a.n_tokens * G + 255) / 256), block(256);
   if (op == kDispatch)
     hipLaunchKernelGGL((dispatch_kernel<Row, WIDE, G>), grid, block, 0, s, a.src, a.src_ld,
                        a.slot_rows, a.sorted_ids, a.n_tokens, a.k, a);

@@ -115,7 +115,7 @@ struct W4PackArgs {
 // One thread per packed word, then one per scale cell.
 template <typename Row>
 __global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs a) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t at = (int64_t)flat_group() * 256 + threadIdx.x;
   if (at < a.words) {
     const int64_t per_pair = (int64_t)a.ksteps * 128;
     const int64_t ep = at / per_pair;
@@ -1185,14 +1185,14 @@ extern "C" int32_t mlora_w4_pack(const uint8_t* q, const void* scales, const uin
   a.ksteps = (int32_t)l.ksteps;
   a.blocks = (int32_t)l.blocks;
   a.sg = (int32_t)l.sg;
-  const int64_t grid = (a.words + a.cells + 255) / 256;
-  if (grid > 0x7fffffffll) return fail(MLORA_ERR_INVALID, "%s: weights too large", who);
+  const int64_t groups = (a.words + a.cells + 255) / 256;
+  if (groups > kMaxRows) return fail(MLORA_ERR_INVALID, "%s: weights too large", who);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (dtype == MLORA_BF16)
-    hipLaunchKernelGGL(w4_pack_kernel<Bf16Row>, dim3((unsigned)grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(w4_pack_kernel<Bf16Row>, flat_grid(groups), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL(w4_pack_kernel<F32Row>, dim3((unsigned)grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(w4_pack_kernel<F32Row>, flat_grid(groups), dim3(256), 0, s, a);
   if (int32_t rc = launch_status(who)) return rc;
   route->weights = a.w;
   route->scales = a.s;

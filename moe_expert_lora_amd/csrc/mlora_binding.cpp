@@ -104,6 +104,11 @@ int32_t integer32(PyObject* o) {
   if (v != (int32_t)v) throw Refused(PyExc_ValueError, "integer argument out of range");
   return (int32_t)v;
 }
+// A size of a tensor that the library takes in 32 bits.
+int32_t size32(int64_t v, const char* name) {
+  if (v != (int32_t)v) throw Refused(PyExc_ValueError, std::string(name) + " is too wide");
+  return (int32_t)v;
+}
 bool truth(PyObject* o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) throw Refused(nullptr, "");
@@ -160,8 +165,8 @@ PyObject* router_topk(PyObject*, Args a, Py_ssize_t n) {
     require(it.dim() == 2 && it.size(0) == lg.rows && it.sizes() == tensor(a[2], "weights").sizes(),
             "indices and weights must be [n_tokens, top_k]");
     const Vec idx(a[1], "indices", at::kInt), w(a[2], "weights", at::kFloat);
-    return mlora_router_topk(lg.p, lg.ld, lg.dtype, lg.rows, (int32_t)lg.cols,
-                             (int32_t)it.size(1), truth(a[3]), (int32_t*)idx.p, (float*)w.p,
+    return mlora_router_topk(lg.p, lg.ld, lg.dtype, lg.rows, size32(lg.cols, "logits"),
+                             size32(it.size(1), "indices"), truth(a[3]), (int32_t*)idx.p, (float*)w.p,
                              stream_of(a[4]));
   });
 }
@@ -177,8 +182,9 @@ PyObject* router_topk_backward(PyObject*, Args a, Py_ssize_t n) {
                 it.sizes() == tensor(a[2], "d_weights").sizes(),
             "indices and d_weights must be [n_tokens, top_k]");
     const Vec idx(a[1], "indices", at::kInt), dw(a[2], "d_weights", at::kFloat);
-    return mlora_router_topk_backward(lg.p, lg.ld, lg.dtype, lg.rows, (int32_t)lg.cols,
-                                      (int32_t)it.size(1), truth(a[4]), (const int32_t*)idx.p,
+    return mlora_router_topk_backward(lg.p, lg.ld, lg.dtype, lg.rows,
+                                      size32(lg.cols, "logits"), size32(it.size(1), "indices"),
+                                      truth(a[4]), (const int32_t*)idx.p,
                                       (const float*)dw.p, dl.p, dl.ld, stream_of(a[5]));
   });
 }

@@ -116,3 +116,25 @@ def test_packed_words(ml):
         ref, mag = w @ x[r].double(), w.abs() @ x[r].double().abs()
         tol = 10 * 8192 ** 0.5 * U * mag
         assert bool(((out[r].double() - ref).abs() <= tol + 2.0 ** -8 * (ref.abs() + tol)).all())
+
+
+def test_rows_wider_than_32_bits(ml):
+    """2^32 + 8 experts are refused, not taken as 8."""
+    wide = torch.empty((1, (1 << 32) + 8), dtype=torch.bfloat16, device=DEV)
+    idx = torch.full((1, 4), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((1, 4), 9.0, device=DEV)
+    with pytest.raises(ValueError, match="logits is too wide"):
+        ml.mlora_router_topk(wide, idx, w)
+    with pytest.raises(ValueError, match="logits is too wide"):
+        ml.mlora_router_topk_backward(wide, idx, w, wide)
+    torch.cuda.synchronize()
+    assert bool((idx == -7).all()) and bool((w == 9).all())
+
+
+def test_more_choices_than_32_bits(ml):
+    """2^32 + 4 choices are refused, not taken as 4."""
+    lg = torch.zeros((1, 16), device=DEV)
+    idx = torch.empty((1, (1 << 32) + 4), dtype=torch.int32, device=DEV)
+    w = torch.empty((1, (1 << 32) + 4), device=DEV)
+    with pytest.raises(ValueError, match="indices is too wide"):
+        ml.mlora_router_topk(lg, idx, w)

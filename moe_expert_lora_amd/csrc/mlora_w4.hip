@@ -894,6 +894,8 @@ w4_stream_kernel(const int32_t* ids, int n_rows, int E, int waves, int by_row, i
       primed = false;
       lds_barrier();  // the last block's readers are done
       stage(0, min(panel, chunks) * 4);
+      // x's loads stay ahead of these requests, which the wait below counts
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int d = kEarly; d < kAhead; ++d) request(ring[d]);
       for (int p0 = 0, j0 = 0; p0 < chunks; p0 += panel, j0 += a.panel_turns) {

@@ -773,9 +773,17 @@ def mlora_router_topk_backward(logits, indices, d_weights, d_logits, renormalize
                                                     renormalize, stream)
 
 
+def _i32(value: int, name: str) -> int:
+    """The value, which ctypes would cut to its low 32 bits without a word."""
+    value = int(value)
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{name}={value} is out of range")
+    return value
+
+
 def mlora_moe_sort_workspace_bytes(n_slots: int, n_experts: int) -> int:
     """Workspace bytes of mlora_moe_sort (0 for small calls)."""
-    return int(load().mlora_moe_sort_workspace_bytes(int(n_slots), int(n_experts)))
+    return int(load().mlora_moe_sort_workspace_bytes(int(n_slots), _i32(n_experts, "n_experts")))
 
 
 def mlora_moe_sort(ids, n_experts: int, expert_offsets, sorted_ids, slot_rows, workspace=None,
@@ -811,8 +819,9 @@ def mlora_moe_combine_backward(d_out, rows, weights, d_rows, d_weights, top_k: i
 def mlora_w4_packed_bytes(n_experts: int, k_in: int, n_out: int, group: int, dtype: int,
                           has_zeros: bool) -> int:
     """Bytes of the packed form of 4-bit expert weights."""
-    return int(load().mlora_w4_packed_bytes(int(n_experts), int(k_in), int(n_out), int(group),
-                                            int(dtype), int(bool(has_zeros))))
+    return int(load().mlora_w4_packed_bytes(
+        _i32(n_experts, "n_experts"), _i32(k_in, "k_in"), _i32(n_out, "n_out"),
+        _i32(group, "group"), int(dtype), int(bool(has_zeros))))
 
 
 def make_w4_route(q, scales, zeros, k_in: int, group: int, stream=None) -> W4Route:

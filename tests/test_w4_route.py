@@ -90,3 +90,24 @@ def test_tensors_of_another_device_are_refused(calls, where, name):
     with pytest.raises(ValueError, match=f"{name} must be on the current device"):
         ml.make_w4_route(*_args(*where))
     assert not calls.packs and not calls.allocations
+
+
+@pytest.mark.parametrize("k_in,group,q,scales", [
+    (264, (1 << 32) + 64, (1, 48, 132), (1, 48, 1)),    # as 64: five scales a row, one is there
+    ((1 << 32) + 64, 1 << 20, (1, 1, (1 << 31) + 32), (1, 1, (1 << 12) + 1)),
+    (64, 64, (1, (1 << 32) + 8, 32), (1, (1 << 32) + 8, 1)),
+    (64, 64, ((1 << 32) + 1, 8, 32), ((1 << 32) + 1, 8, 1))])
+def test_sizes_past_32_bits_are_refused(calls, k_in, group, q, scales):
+    """Not taken by their low halves."""
+    with pytest.raises(ValueError, match="out of range"):
+        ml.make_w4_route(Tensor(q, torch.uint8), Tensor(scales, torch.bfloat16), None, k_in, group)
+    assert not calls.packs and not calls.allocations
+
+
+def test_size_queries_past_32_bits():
+    for args in ((1, 64, 64, (1 << 32) + 64), (1, (1 << 32) + 64, 64, 64),
+                 (1, 64, (1 << 32) + 64, 64), ((1 << 32) + 1, 64, 64, 64)):
+        with pytest.raises(ValueError, match="out of range"):
+            ml.mlora_w4_packed_bytes(*args, ml.MLORA_BF16, False)
+    with pytest.raises(ValueError, match="out of range"):
+        ml.mlora_moe_sort_workspace_bytes(100000, (1 << 32) + 4)

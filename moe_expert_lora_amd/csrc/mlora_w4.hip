@@ -21,8 +21,9 @@
 // The offset is small (0.5 without zero points), so that the sums, like a plain
 // fp32 one's, pass through little that cancels: relative L2 errors of fp32 rows of
 // 264 and 768 values, means 0 and 3, are 0.9 to 3.3 u (u = 2^-24), a plain fp32
-// sum's 0.8 to 1.6. (With bf16 values 16 + v, made by an and/or a pair, 5.7 to 39 u
-// in the same time: 128 experts of 768 x 2048, 640 rows 21.7 us, as now.)
+// sum's 0.8 to 1.6. (With bf16 values 16 + v, made by an and/or a pair, they were 5.7
+// to 39 u, in about the same time: 128 experts of 768 x 2048, 640 rows 21.7 us, as
+// now, of 2048 x 768, 2048 rows 30.7, now 31.0.)
 // A row of x with an infinity or a NaN gives no finite outputs, in that row alone.
 //
 // Two forms, each of which reads an expert's weights once per 16 or 32 of its
@@ -32,9 +33,11 @@
 // operands. The streaming form stages x rows in LDS once per workgroup and gives
 // each wave whole pairs of tiles.
 //
-// What bounds them, at 128 experts of 2048 x 768, groups of 128: one row each on
-// average 16 us, 5 rows 22.5, 16 rows 27.5; the main loop reads weights at 6.3
-// TB/s, as fast as a CU's cache takes misses on (32 KB on their way, 1.4 us each).
+// What bounds them, at 128 experts of 2048 x 768, groups of 128, bf16 rows: one row
+// each on average 21 us a call, 5 rows 24.7, 16 rows 30 (fp32 rows, three products
+// and three reads of x from LDS for one: 24.8, 32.3, 56.5); the main loop reads
+// weights at 6.3 TB/s, as fast as a CU's cache takes misses on (32 KB on their way,
+// 1.4 us each).
 // Ahead of it lie 8 to 10 us in which the ids, then x arrive, one round trip after
 // the other, and only the first weights beside them. Single weights of a few MB:
 // those round trips and the launch (2048 x 2048, one row: 4.3 us).

@@ -575,6 +575,155 @@ int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void* x, int64_t
                              int64_t x_ld, int32_t x_by_row, void* out, int64_t out_ld,
                              const int32_t* ids, int64_t n_rows, int32_t top_k, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* 8-bit base products, a whole MoE layer for a few tokens, and the norms    */
+/* around a block.                                                           */
+/* ------------------------------------------------------------------------ */
+/*
+ * Conventions as for the operators above (streams, strides, errors, no floating-
+ * point atomics). 8-bit values are OCP E4M3 codes (largest value 448, 0x7f and
+ * 0xff NaN, no infinity). Weights have one fp32 scale for each block of 128 x 128,
+ * rows one for each group of 128 values. Blocks and groups start at 0; the last
+ * ones may be short. Any width from 1 to 2^20, 1024 experts.
+ */
+
+/* Device pointers of 8-bit expert weights as mlora_fp8_pack lays them out (the
+ * struct itself lives in host memory). */
+typedef struct mlora_fp8_route {
+  const void* weights;
+  const void* scales;
+  int32_t n_experts;
+  int32_t k_in;
+  int32_t n_out;
+} mlora_fp8_route;
+
+/* Bytes of the packed form; 0 for arguments mlora_fp8_pack refuses. */
+uint64_t mlora_fp8_packed_bytes(int32_t n_experts, int32_t k_in, int32_t n_out);
+
+/* Lays 8-bit weights out for mlora_fp8_gemm and mlora_moe_layer, once per weight.
+ *   w       [n_experts, n_out, k_in] codes
+ *   scales  [n_experts, ceil(n_out / 128), ceil(k_in / 128)] fp32
+ *   packed  mlora_fp8_packed_bytes bytes, 256-byte aligned, kept while the route
+ *           is used; w and scales are not needed afterwards
+ * transpose: w is [n_experts, k_in, n_out] and scales follow it: the route of the
+ * transposed weight, with which mlora_fp8_gemm takes the gradient of its rows
+ * (the forward's n_out is k_in here). Fills *route. */
+int32_t mlora_fp8_pack(const uint8_t* w, const float* scales, int32_t n_experts, int32_t k_in,
+                       int32_t n_out, int32_t transpose, void* packed, uint64_t packed_bytes,
+                       mlora_fp8_route* route, void* stream);
+
+/* Bytes of a quantised row of k values: k rounded up to a multiple of 128 (0 for
+ * a k outside [1, 2^20]). */
+int32_t mlora_fp8_row_width(int32_t k);
+
+/* Quantises rows: x, or silu(x) * up (in fp32) where up is given. Of each group
+ * of 128 values, m = the largest magnitude or 448 * 2^-126, whichever is larger:
+ * scale = m / 448, code = 448 x / m to the nearest E4M3 value, ties to even. A
+ * group with an infinity or NaN gets a NaN scale and codes of 0 (its product rows
+ * are NaN; other rows do not change).
+ *   x, up     [n_rows, k] dtype
+ *   q         [n_rows, mlora_fp8_row_width(k)] codes, zeros past k; 16-byte
+ *             aligned, q_ld (bytes) a multiple of 16
+ *   q_scales  [ceil(k / 128), n_rows] fp32: a group's scales of all rows lie
+ *             together */
+int32_t mlora_fp8_quant(const void* x, int64_t x_ld, const void* up, int64_t up_ld, int32_t dtype,
+                        int64_t n_rows, int32_t k, uint8_t* q, int64_t q_ld, float* q_scales,
+                        void* stream);
+
+/* out[r, n] = sum over blocks b of q_scales[b, s] scales[e, n / 128, b] times the
+ * sum of the block's products of codes, in fp32, rounded once. As in
+ * mlora_grouped_down, sorted row r belongs to the expert e whose span of
+ * expert_offsets holds it and reads the token row s = sorted_ids[r] / top_k of q;
+ * sorted_ids == NULL: s = r (rows of an earlier product). expert_offsets == NULL:
+ * one weight (n_experts == 1) for every row. Rows in no span, or whose s is
+ * outside q, are left as they were. Offsets must be non-decreasing (other
+ * contents stay in bounds but give unspecified rows).
+ *   q         [q_rows, mlora_fp8_row_width(k_in)] codes and
+ *   q_scales  [ceil(k_in / 128), q_rows], as mlora_fp8_quant writes them
+ *   out       [n_rows, n_out] out_dtype */
+int32_t mlora_fp8_gemm(const mlora_fp8_route* route, const uint8_t* q, int64_t q_rows,
+                       int64_t q_ld, const float* q_scales, void* out, int64_t out_ld,
+                       int32_t out_dtype, int64_t n_rows, const int32_t* expert_offsets,
+                       const int32_t* sorted_ids, int32_t top_k, void* stream);
+
+/* Bytes of workspace mlora_moe_layer needs; 0 for no tokens and for arguments it
+ * refuses. */
+uint64_t mlora_moe_layer_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t top_k,
+                                         int32_t dim, int32_t hidden);
+
+/* A MoE layer for up to 16 tokens without adapters, in two kernels: the choice of
+ * mlora_router_topk from the logits (to which a router's adapter is folded before),
+ *   out[t] = sum over j of p[t, j] down_e (silu(gate_e x[t]) * (up_e x[t])),
+ * e the j-th chosen expert and p its weight. gate and up are routes of
+ * [hidden, dim], down of [dim, hidden]. Weights enter exactly, x is not
+ * quantised; the activated row, times p, enters the last product to within 2^-16
+ * (fp32: 2^-24) of each value; sums are fp32, one rounding. Values of x up to
+ * 2^117 in magnitude; a token with others, or with a NaN among its weights, gives
+ * its own row no defined finite values, and other rows do not change.
+ *   x, out      [n_tokens, dim] dtype
+ *   logits      [n_tokens, n_experts] dtype
+ *   indices, weights  [n_tokens, top_k]: the choice, as mlora_router_topk writes
+ *               it; either may be NULL
+ *   workspace   mlora_moe_layer_workspace_bytes bytes, 256-byte aligned; needs no
+ *               initialisation, dead afterwards; calls that share it must be
+ *               ordered */
+int32_t mlora_moe_layer(const mlora_fp8_route* gate, const mlora_fp8_route* up,
+                        const mlora_fp8_route* down, const void* x, int64_t x_ld, int32_t dtype,
+                        int64_t n_tokens, const void* logits, int64_t logits_ld, int32_t top_k,
+                        int32_t renormalize, void* out, int64_t out_ld, int32_t* indices,
+                        float* weights, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* What the norms around a block read (host struct of device pointers). */
+typedef struct mlora_norm_block {
+  const void* residual;   /* [n_tokens, dim] dtype                             */
+  int64_t residual_ld;
+  const void* y;          /* the block's output, the same shape; NULL: none    */
+  int64_t y_ld;
+  const void* x_weight;   /* [dim] w_dtype, of the norm behind; NULL: all 1    */
+  const void* y_weight;   /* [dim] w_dtype, of the norm of y; NULL: no norm    */
+  const void* gate;       /* dtype                                             */
+  int64_t gate_ld;
+  int32_t gate_form;      /* 0: none, 1: [dim], 2: one per token (gate_ld      */
+                          /* apart), 3: [n_tokens, dim]                        */
+  int32_t dtype;
+  int32_t w_dtype;
+  int32_t dim;            /* 1 .. 16384                                        */
+  int64_t n_tokens;
+  float residual_scale;
+  float y_scale;
+  float weight_offset;    /* added to the given weights (1: they are stored    */
+                          /* less one)                                         */
+  float eps;              /* >= 0                                              */
+} mlora_norm_block;
+
+/* n = y / rms(y) * (y_weight + offset) (y itself without a y_weight),
+ * r = residual_scale * residual + y_scale * gate * n,
+ * x = r / rms(r) * (x_weight + offset), rms(v) = sqrt(mean(v^2) + eps), in fp32,
+ * each output rounded once (x from the unrounded r). r, x [n_tokens, dim] dtype;
+ * either may be NULL, and either may be the memory of residual or of y (with its
+ * stride). */
+int32_t mlora_block_norm(const mlora_norm_block* block, void* r, int64_t r_ld, void* x,
+                         int64_t x_ld, void* stream);
+
+/* Bytes of workspace for d_x_weight, d_y_weight and a gate per channel; 0 for
+ * arguments that are refused and for no tokens. */
+uint64_t mlora_block_norm_backward_workspace_bytes(int64_t n_tokens, int32_t dim);
+
+/* Gradients of mlora_block_norm for d_r and d_x (dtype; NULL: zeros, not both),
+ * from the forward's inputs. Outputs that are NULL are not computed:
+ *   d_residual, d_y        [n_tokens, dim] dtype; may be the memory of d_r or d_x
+ *   d_x_weight, d_y_weight [dim] fp32, sums over the tokens (zeros for none)
+ *   d_gate                 form 1: [dim] fp32, 2: one fp32 per token (d_gate_ld
+ *                          apart), 3: [n_tokens, dim] dtype
+ * The workspace (256-byte aligned) is needed for d_x_weight, d_y_weight and
+ * d_gate of form 1; it needs no initialisation and is dead afterwards. */
+int32_t mlora_block_norm_backward(const mlora_norm_block* block, const void* d_r, int64_t d_r_ld,
+                                  const void* d_x, int64_t d_x_ld, void* d_residual,
+                                  int64_t d_residual_ld, void* d_y, int64_t d_y_ld,
+                                  float* d_x_weight, float* d_y_weight, void* d_gate,
+                                  int64_t d_gate_ld, void* workspace, uint64_t workspace_bytes,
+                                  void* stream);
+
 /* Reads the MLORA_* launch-shape overrides from the environment again (they
  * are otherwise read once, at the first fold call). For measurement tools and
  * tests that change the environment within one process. Not safe while

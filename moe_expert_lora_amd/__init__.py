@@ -72,6 +72,16 @@ EXPORTS = (
     "mlora_w4_packed_bytes",
     "mlora_w4_pack",
     "mlora_w4_gather_gemv",
+    "mlora_fp8_packed_bytes",
+    "mlora_fp8_pack",
+    "mlora_fp8_row_width",
+    "mlora_fp8_quant",
+    "mlora_fp8_gemm",
+    "mlora_moe_layer_workspace_bytes",
+    "mlora_moe_layer",
+    "mlora_block_norm",
+    "mlora_block_norm_backward_workspace_bytes",
+    "mlora_block_norm_backward",
 )
 
 
@@ -151,6 +161,47 @@ class W4Route(ctypes.Structure):
     def address(self) -> int:
         """Of the struct (it stays where it is while the object lives)."""
         return ctypes.addressof(self)
+
+
+class Fp8Route(ctypes.Structure):
+    """``mlora_fp8_route``: packed 8-bit expert weights of one projection."""
+
+    _fields_ = [
+        ("weights", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("n_experts", ctypes.c_int32),
+        ("k_in", ctypes.c_int32),
+        ("n_out", ctypes.c_int32),
+    ]
+
+    @functools.cached_property
+    def address(self) -> int:
+        """Of the struct (it stays where it is while the object lives)."""
+        return ctypes.addressof(self)
+
+
+class NormBlock(ctypes.Structure):
+    """``mlora_norm_block``: what the norms around a block read."""
+
+    _fields_ = [
+        ("residual", ctypes.c_void_p),
+        ("residual_ld", ctypes.c_int64),
+        ("y", ctypes.c_void_p),
+        ("y_ld", ctypes.c_int64),
+        ("x_weight", ctypes.c_void_p),
+        ("y_weight", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("gate_ld", ctypes.c_int64),
+        ("gate_form", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("w_dtype", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int64),
+        ("residual_scale", ctypes.c_float),
+        ("y_scale", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -235,6 +286,20 @@ def load() -> ctypes.CDLL:
                                 ctypes.POINTER(W4Route), vp]),
         "mlora_w4_gather_gemv": (i32, [ctypes.POINTER(W4Route), vp, i64, i64, i32, vp, i64, vp,
                                        i64, i32, vp]),
+        "mlora_fp8_packed_bytes": (ctypes.c_uint64, [i32] * 3),
+        "mlora_fp8_pack": (i32, [vp, vp, i32, i32, i32, i32, vp, ctypes.c_uint64,
+                                 ctypes.POINTER(Fp8Route), vp]),
+        "mlora_fp8_row_width": (i32, [i32]),
+        "mlora_fp8_quant": (i32, [vp, i64, vp, i64, i32, i64, i32, vp, i64, vp, vp]),
+        "mlora_fp8_gemm": (i32, [ctypes.POINTER(Fp8Route), vp, i64, i64, vp, vp, i64, i32, i64,
+                                 vp, vp, i32, vp]),
+        "mlora_moe_layer_workspace_bytes": (ctypes.c_uint64, [i64, i32, i32, i32, i32]),
+        "mlora_moe_layer": (i32, [ctypes.POINTER(Fp8Route)] * 3 + [
+            vp, i64, i32, i64, vp, i64, i32, i32, vp, i64, vp, vp, vp, ctypes.c_uint64, vp]),
+        "mlora_block_norm": (i32, [ctypes.POINTER(NormBlock), vp, i64, vp, i64, vp]),
+        "mlora_block_norm_backward_workspace_bytes": (ctypes.c_uint64, [i64, i32]),
+        "mlora_block_norm_backward": (i32, [ctypes.POINTER(NormBlock)] + [vp, i64] * 4 + [
+            vp, vp, vp, i64, vp, ctypes.c_uint64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -871,3 +936,125 @@ def mlora_w4_gather_gemv(route: W4Route, x, out, ids=None, top_k: int = 1,
     an id outside the route's experts get zeros. ``ids`` None: one weight."""
     (_bound or _load_native()).w4_gather_gemv(route.address, x, out, ids, top_k, x_by_row,
                                               stream)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit products, the layer of a few tokens, the norms around a block
+# ---------------------------------------------------------------------------
+
+def mlora_fp8_packed_bytes(n_experts: int, k_in: int, n_out: int) -> int:
+    """Bytes of the packed form of 8-bit expert weights."""
+    return int(load().mlora_fp8_packed_bytes(_i32(n_experts, "n_experts"), _i32(k_in, "k_in"),
+                                             _i32(n_out, "n_out")))
+
+
+def mlora_fp8_row_width(k: int) -> int:
+    """Bytes of a quantised row of ``k`` values: the width of ``q``."""
+    return int(load().mlora_fp8_row_width(_i32(k, "k")))
+
+
+def make_fp8_route(w, scales, transpose: bool = False, stream=None) -> Fp8Route:
+    """Packed route (mlora_fp8_pack) of 8-bit weights: ``w`` [n_experts, n_out,
+    k_in] as float8_e4m3fn (or its bytes), ``scales`` float32 [n_experts,
+    ceil(n_out / 128), ceil(k_in / 128)]. ``transpose``: of the transposed weights
+    ([n_experts, n_out, k_in] holds the route's k_in before its n_out), for the
+    gradient of the rows. The route keeps the packed tensor; the arguments are not
+    needed once the call's work is done.
+
+    The packed tensor is written by and belongs to ``stream`` (None: the current
+    one). Work on another stream has to wait for it, and ``stream`` for that work
+    before the route is dropped."""
+    import torch
+    if w.dim() != 3 or scales.dim() != 3:
+        raise ValueError("w and scales must be 3-D")
+    if w.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError("w must be float8_e4m3fn (or its bytes)")
+    E, rows, cols = w.shape
+    if tuple(scales.shape) != (E, -(-rows // 128), -(-cols // 128)):
+        raise ValueError("scales must have one entry for each block of 128 x 128")
+    n, k = (cols, rows) if transpose else (rows, cols)
+    nbytes = mlora_fp8_packed_bytes(E, k, n)
+    if nbytes == 0:
+        raise _err(MLORA_ERR_INVALID)
+    for name, t in (("w", w), ("scales", scales)):
+        # the call runs on the current device's stream, as those of _native
+        if t.is_cuda and t.device.index != _device():
+            raise ValueError(f"{name} must be on the current device")
+    wp, sp = _dev(w, "w"), _dev(scales, "scales", torch.float32)
+    # of the stream that writes it: a block of another stream's may still be in use there
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        packed = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
+    route = Fp8Route()
+    rc = load().mlora_fp8_pack(wp, sp, E, k, n, int(bool(transpose)), packed.data_ptr(), nbytes,
+                               ctypes.byref(route), _stream_handle(stream))
+    if rc != MLORA_OK:
+        raise _err(rc)
+    route._keep = packed
+    return route
+
+
+def mlora_fp8_quant(x, q, q_scales, up=None, stream=None) -> None:
+    """Quantises rows of ``x`` [n_rows, k] (bf16 or float32), or of silu(x) * up,
+    into ``q`` [n_rows, mlora_fp8_row_width(k)] (float8_e4m3fn or uint8) and
+    ``q_scales`` [ceil(k / 128), n_rows] float32."""
+    (_bound or _load_native()).fp8_quant(x, q, q_scales, up, stream)
+
+
+def mlora_fp8_gemm(route: Fp8Route, q, q_scales, out, expert_offsets=None, sorted_ids=None,
+                   top_k: int = 1, stream=None) -> None:
+    """``out[r]`` = W_e q[sorted_ids[r] // top_k] (``sorted_ids`` None: q[r]) for the
+    rows of each expert's span of ``expert_offsets`` (None: one weight for all);
+    rows in no span are left as they were."""
+    (_bound or _load_native()).fp8_gemm(route.address, q, q_scales, out, expert_offsets,
+                                        sorted_ids, top_k, stream)
+
+
+def mlora_moe_layer_workspace_bytes(n_tokens: int, n_experts: int, top_k: int, dim: int,
+                                    hidden: int) -> int:
+    """Workspace bytes of mlora_moe_layer."""
+    return int(load().mlora_moe_layer_workspace_bytes(
+        int(n_tokens), _i32(n_experts, "n_experts"), _i32(top_k, "top_k"), _i32(dim, "dim"),
+        _i32(hidden, "hidden")))
+
+
+def mlora_moe_layer(gate: Fp8Route, up: Fp8Route, down: Fp8Route, x, logits, out, top_k: int,
+                    workspace, renormalize: bool = False, indices=None, weights=None,
+                    stream=None) -> None:
+    """A MoE layer of up to 16 tokens without adapters: the choice of
+    mlora_router_topk from ``logits`` (written to ``indices`` and ``weights`` where
+    given), gate, up, silu, down and the weighted sum into ``out``."""
+    (_bound or _load_native()).moe_layer(gate.address, up.address, down.address, x, logits, out,
+                                         top_k, workspace, renormalize, indices, weights, stream)
+
+
+def mlora_block_norm(residual, r=None, x=None, y=None, x_weight=None, y_weight=None, gate=None,
+                     residual_scale: float = 1.0, y_scale: float = 1.0,
+                     weight_offset: float = 0.0, eps: float = 1e-6, stream=None) -> None:
+    """``r`` = residual_scale * residual + y_scale * gate * norm(y) and ``x`` =
+    norm(r), RMS norms with weights (+ ``weight_offset``) ``y_weight`` (None: y as
+    it is) and ``x_weight`` (None: 1). ``gate``: [dim], [n_tokens, 1] or [n_tokens,
+    dim] in the rows' dtype. Either output may be None, or be ``residual`` or
+    ``y`` itself."""
+    (_bound or _load_native()).block_norm(residual, r, x, y, x_weight, y_weight, gate,
+                                          residual_scale, y_scale, weight_offset, eps, stream)
+
+
+def mlora_block_norm_backward_workspace_bytes(n_tokens: int, dim: int) -> int:
+    """Workspace bytes of mlora_block_norm_backward."""
+    return int(load().mlora_block_norm_backward_workspace_bytes(int(n_tokens), _i32(dim, "dim")))
+
+
+def mlora_block_norm_backward(residual, d_r=None, d_x=None, d_residual=None, d_y=None,
+                              d_x_weight=None, d_y_weight=None, d_gate=None, y=None,
+                              x_weight=None, y_weight=None, gate=None,
+                              residual_scale: float = 1.0, y_scale: float = 1.0,
+                              weight_offset: float = 0.0, eps: float = 1e-6, workspace=None,
+                              stream=None) -> None:
+    """Gradients of mlora_block_norm for ``d_r`` and ``d_x`` (None: zeros) into the
+    outputs that are given: ``d_residual`` and ``d_y`` (the rows' dtype, may be
+    ``d_r`` or ``d_x``), ``d_x_weight`` and ``d_y_weight`` (float32), ``d_gate`` of
+    the gate's shape (float32; [n_tokens, dim]: the rows' dtype). The workspace is
+    needed for sums over the tokens."""
+    (_bound or _load_native()).block_norm_backward(
+        residual, d_r, d_x, d_residual, d_y, d_x_weight, d_y_weight, d_gate, y, x_weight, y_weight,
+        gate, residual_scale, y_scale, weight_offset, eps, workspace, stream)

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmlora.so")
 SOURCES = [os.path.join(CSRC, name)
-           for name in ("mlora_host.cpp", "mlora_fold.hip", "mlora_moe.hip", "mlora_w4.hip")]
+           for name in ("mlora_host.cpp", "mlora_fold.hip", "mlora_moe.hip", "mlora_w4.hip",
+                       "mlora_fp8.hip", "mlora_layer.hip", "mlora_norm.hip")]
 # measurement probes for bench.py (launch and read-pattern floors), a library of their own
 PROBE_LIB = os.path.join(PKG, "libmlora_probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "mlora_probe.hip")]

@@ -157,6 +157,21 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F body) {
 
 typedef PyObject* const* Args;
 
+// A workspace's memory and size; None: nothing.
+struct Space {
+  void* p = nullptr;
+  uint64_t bytes = 0;
+  explicit Space(PyObject* o) {
+    if (o == Py_None) return;
+    const at::Tensor& t = tensor(o, "workspace");
+    bytes = (uint64_t)t.numel() * t.element_size();
+    if (!bytes) return;
+    on_device(t, "workspace");
+    require(t.is_contiguous(), "workspace must be contiguous");
+    p = t.data_ptr();
+  }
+};
+
 // logits, indices, weights, renormalize, stream
 PyObject* router_topk(PyObject*, Args a, Py_ssize_t n) {
   return guarded(n, 5, [&] {
@@ -198,19 +213,9 @@ PyObject* moe_sort(PyObject*, Args a, Py_ssize_t n) {
     require(off.n == (int64_t)experts + 1, "expert_offsets must have n_experts + 1 entries");
     require(order.n == ids.n && rows.n == ids.n,
             "sorted_ids and slot_rows must have one entry per id");
-    void* ws = nullptr;
-    uint64_t bytes = 0;
-    if (a[5] != Py_None) {
-      const at::Tensor& t = tensor(a[5], "workspace");
-      bytes = (uint64_t)t.numel() * t.element_size();
-      if (bytes) {
-        on_device(t, "workspace");
-        require(t.is_contiguous(), "workspace must be contiguous");
-        ws = t.data_ptr();
-      }
-    }
+    const Space ws(a[5]);
     return mlora_moe_sort((const int32_t*)ids.p, ids.n, experts, (int32_t*)off.p,
-                          (int32_t*)order.p, (int32_t*)rows.p, ws, bytes, stream_of(a[6]));
+                          (int32_t*)order.p, (int32_t*)rows.p, ws.p, ws.bytes, stream_of(a[6]));
   });
 }
 
@@ -297,6 +302,231 @@ PyObject* w4_gather_gemv(PyObject*, Args a, Py_ssize_t n) {
   });
 }
 
+// Bytes of E4M3 codes, 2-D with contiguous rows.
+struct Codes {
+  uint8_t* p;
+  int64_t rows, cols, ld;
+  Codes(PyObject* o, const char* name) {
+    const at::Tensor& t = tensor(o, name);
+    on_device(t, name);
+    if (t.scalar_type() != at::kFloat8_e4m3fn && t.scalar_type() != at::kByte)
+      throw Refused(PyExc_TypeError, std::string(name) + " must be float8_e4m3fn (or its bytes)");
+    if (t.dim() != 2) throw Refused(PyExc_ValueError, std::string(name) + " must be 2-D");
+    rows = t.size(0);
+    cols = t.size(1);
+    if (rows > 0 && cols > 1 && t.stride(1) != 1)
+      throw Refused(PyExc_ValueError, std::string(name) + " must have contiguous rows");
+    ld = rows > 1 ? t.stride(0) : cols;
+    p = static_cast<uint8_t*>(t.data_ptr());
+  }
+};
+
+// A group's scales of every row: [groups, rows].
+float* group_scales(PyObject* o, int64_t width, int64_t rows) {
+  const at::Tensor& t = tensor(o, "q_scales");
+  const Vec v(o, "q_scales", at::kFloat);
+  require(t.dim() == 2 && t.size(0) == width / 128 && t.size(1) == rows,
+          "q_scales must be [ceil(k / 128), rows of q]");
+  return static_cast<float*>(v.p);
+}
+
+float real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused(nullptr, "");
+  return (float)v;
+}
+
+const mlora_fp8_route* fp8_route(PyObject* o) {
+  const void* p = PyLong_AsVoidPtr(o);
+  if (PyErr_Occurred()) throw Refused(nullptr, "");
+  return static_cast<const mlora_fp8_route*>(p);
+}
+
+// x, q, q_scales, up, stream
+PyObject* fp8_quant(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 5, [&] {
+    const Mat x(a[0], "x");
+    const Codes q(a[1], "q");
+    const int32_t k = size32(x.cols, "x");
+    require(q.rows == x.rows && q.cols == mlora_fp8_row_width(k),
+            "q must be [n_rows, mlora_fp8_row_width(k)]");
+    float* scales = group_scales(a[2], q.cols, x.rows);
+    const void* up = nullptr;
+    int64_t up_ld = 0;
+    if (a[3] != Py_None) {
+      const Mat u(a[3], "up");
+      same_type(x, u, "up dtype differs from x's");
+      require(u.rows == x.rows && u.cols == x.cols, "up must have the shape of x");
+      up = u.p;
+      up_ld = u.ld;
+    }
+    return mlora_fp8_quant(x.p, x.ld, up, up_ld, x.dtype, x.rows, k, q.p, q.ld, scales,
+                           stream_of(a[4]));
+  });
+}
+
+// route's address, q, q_scales, out, expert_offsets, sorted_ids, top_k, stream
+PyObject* fp8_gemm(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 8, [&] {
+    const mlora_fp8_route* route = fp8_route(a[0]);
+    const Codes q(a[1], "q");
+    const Mat out(a[3], "out");
+    require(q.cols == mlora_fp8_row_width(route->k_in) && out.cols == route->n_out,
+            "q / out widths differ from the route's k_in / n_out");
+    const float* scales = group_scales(a[2], q.cols, q.rows);
+    const Vec off(a[4], "expert_offsets", at::kInt, true), ids(a[5], "sorted_ids", at::kInt, true);
+    require(a[4] == Py_None || off.n == (int64_t)route->n_experts + 1,
+            "expert_offsets must have n_experts + 1 entries");
+    require(a[5] == Py_None || ids.n == out.rows, "sorted_ids must have one entry per out row");
+    // a tensor without entries still says that rows go by it
+    static const int32_t kNothing = 0;
+    const int32_t* ip = a[5] == Py_None ? nullptr : ids.p ? (const int32_t*)ids.p : &kNothing;
+    return mlora_fp8_gemm(route, q.p, q.rows, q.ld, scales, out.p, out.ld, out.dtype, out.rows,
+                          (const int32_t*)off.p, ip, integer32(a[6]), stream_of(a[7]));
+  });
+}
+
+// gate, up, down (addresses), x, logits, out, top_k, workspace, renormalize, indices, weights,
+// stream
+PyObject* moe_layer(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 12, [&] {
+    const mlora_fp8_route *gate = fp8_route(a[0]), *up = fp8_route(a[1]), *down = fp8_route(a[2]);
+    const Mat x(a[3], "x"), lg(a[4], "logits"), out(a[5], "out");
+    same_type(x, lg, "logits dtype differs from x's");
+    same_type(x, out, "out dtype differs from x's");
+    require(x.cols == gate->k_in && lg.cols == gate->n_experts && lg.rows == x.rows,
+            "x must be [n_tokens, dim] and logits [n_tokens, n_experts]");
+    require(out.rows == x.rows && out.cols == x.cols, "out must have the shape of x");
+    const int32_t k = integer32(a[6]);
+    const Space ws(a[7]);
+    const Vec idx(a[9], "indices", at::kInt, true), w(a[10], "weights", at::kFloat, true);
+    require((a[9] == Py_None || idx.n == x.rows * k) && (a[10] == Py_None || w.n == x.rows * k),
+            "indices and weights must be [n_tokens, top_k]");
+    return mlora_moe_layer(gate, up, down, x.p, x.ld, x.dtype, x.rows, lg.p, lg.ld, k, truth(a[8]),
+                           out.p, out.ld, (int32_t*)idx.p, (float*)w.p, ws.p, ws.bytes,
+                           stream_of(a[11]));
+  });
+}
+
+// An optional matrix of the residual's type and shape.
+struct LikeRows {
+  void* p = nullptr;
+  int64_t ld = 0;
+  LikeRows(PyObject* o, const char* name, const Mat& like) : ld(like.cols) {
+    if (o == Py_None) return;
+    const Mat m(o, name);
+    same_type(m, like, (std::string(name) + " dtype differs from residual's").c_str());
+    require(m.rows == like.rows && m.cols == like.cols,
+            (std::string(name) + " must have the shape of residual").c_str());
+    p = m.p;
+    ld = m.ld;
+  }
+};
+
+const void* norm_weight(PyObject* o, const char* name, int64_t dim, int32_t* code) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  const int32_t c = code_of(t, name);
+  if (*code >= 0 && c != *code)
+    throw Refused(PyExc_TypeError, "x_weight and y_weight differ in dtype");
+  *code = c;
+  const Vec v(o, name, t.scalar_type());
+  require(v.n == dim, (std::string(name) + " must have dim entries").c_str());
+  return v.p;
+}
+
+enum { kNoGate, kChannelGate, kTokenGate, kFullGate };
+
+// y, x_weight, y_weight, gate, residual_scale, y_scale, weight_offset, eps from a[at] on
+mlora_norm_block norm_block(const Mat& res, Args a) {
+  mlora_norm_block b{};
+  b.residual = res.p;
+  b.residual_ld = res.ld;
+  b.dtype = res.dtype;
+  b.dim = size32(res.cols, "residual");
+  b.n_tokens = res.rows;
+  const LikeRows y(a[0], "y", res);
+  b.y = y.p;
+  b.y_ld = y.ld;
+  // rows without entries have no memory; the block still has a y then
+  static const char kNothing = 0;
+  if (a[0] != Py_None && !b.y) b.y = &kNothing;
+  int32_t code = -1;
+  b.x_weight = norm_weight(a[1], "x_weight", res.cols, &code);
+  b.y_weight = norm_weight(a[2], "y_weight", res.cols, &code);
+  b.w_dtype = code < 0 ? MLORA_F32 : code;
+  if (a[3] != Py_None) {
+    const at::Tensor& t = tensor(a[3], "gate");
+    on_device(t, "gate");
+    if (code_of(t, "gate") != res.dtype)
+      throw Refused(PyExc_TypeError, "gate dtype differs from residual's");
+    if (t.dim() == 1) {
+      require(t.size(0) == res.cols && t.is_contiguous(), "a gate per channel must be [dim]");
+      b.gate_form = kChannelGate;
+    } else {
+      require(t.dim() == 2 && t.size(0) == res.rows && (t.size(1) == 1 || t.size(1) == res.cols),
+              "gate must be [dim], [n_tokens, 1] or [n_tokens, dim]");
+      b.gate_form = t.size(1) == 1 ? kTokenGate : kFullGate;
+      require(t.size(1) == 1 || res.rows == 0 || t.stride(1) == 1, "gate must have contiguous rows");
+      b.gate_ld = res.rows > 1 ? t.stride(0) : t.size(1);
+    }
+    b.gate = t.data_ptr();
+  }
+  b.residual_scale = real(a[4]);
+  b.y_scale = real(a[5]);
+  b.weight_offset = real(a[6]);
+  b.eps = real(a[7]);
+  return b;
+}
+
+// residual, r, x, y, x_weight, y_weight, gate, residual_scale, y_scale, weight_offset, eps, stream
+PyObject* block_norm(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 12, [&] {
+    const Mat res(a[0], "residual");
+    const mlora_norm_block b = norm_block(res, a + 3);
+    const LikeRows r(a[1], "r", res), x(a[2], "x", res);
+    return mlora_block_norm(&b, r.p, r.ld, x.p, x.ld, stream_of(a[11]));
+  });
+}
+
+// A [dim] vector of sums, or None.
+float* sums_of(PyObject* o, const char* name, int64_t dim) {
+  const Vec v(o, name, at::kFloat, true);
+  require(o == Py_None || v.n == dim, (std::string(name) + " must have dim entries").c_str());
+  return static_cast<float*>(v.p);
+}
+
+// residual, d_r, d_x, d_residual, d_y, d_x_weight, d_y_weight, d_gate, y, x_weight, y_weight, gate,
+// residual_scale, y_scale, weight_offset, eps, workspace, stream
+PyObject* block_norm_backward(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 18, [&] {
+    const Mat res(a[0], "residual");
+    const mlora_norm_block b = norm_block(res, a + 8);
+    const LikeRows dr(a[1], "d_r", res), dx(a[2], "d_x", res), dres(a[3], "d_residual", res),
+        dy(a[4], "d_y", res);
+    float *dwx = sums_of(a[5], "d_x_weight", res.cols), *dwy = sums_of(a[6], "d_y_weight", res.cols);
+    void* dg = nullptr;
+    int64_t dg_ld = 0;
+    if (a[7] != Py_None) {
+      require(b.gate_form != kNoGate, "d_gate without a gate");
+      if (b.gate_form == kFullGate) {
+        const LikeRows g(a[7], "d_gate", res);
+        dg = g.p;
+        dg_ld = g.ld;
+      } else {
+        const Vec g(a[7], "d_gate", at::kFloat);
+        require(tensor(a[7], "d_gate").sizes() == tensor(a[11], "gate").sizes(),
+                "d_gate must have the gate's shape");
+        dg = g.p;
+        dg_ld = 1;
+      }
+    }
+    const Space ws(a[16]);
+    return mlora_block_norm_backward(&b, dr.p, dr.ld, dx.p, dx.ld, dres.p, dres.ld, dy.p, dy.ld,
+                                     dwx, dwy, dg, dg_ld, ws.p, ws.bytes, stream_of(a[17]));
+  });
+}
+
 // The class of the exceptions that failing calls raise.
 PyObject* set_error(PyObject*, PyObject* type) {
   Py_INCREF(type);
@@ -314,6 +544,11 @@ PyMethodDef kMethods[] = {MLORA_FAST(router_topk),
                           MLORA_FAST(moe_combine),
                           MLORA_FAST(moe_combine_backward),
                           MLORA_FAST(w4_gather_gemv),
+                          MLORA_FAST(fp8_quant),
+                          MLORA_FAST(fp8_gemm),
+                          MLORA_FAST(moe_layer),
+                          MLORA_FAST(block_norm),
+                          MLORA_FAST(block_norm_backward),
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods,

@@ -1,5 +1,5 @@
 // Device and launch helpers shared by the MoE-layer operators around the fold
-// (mlora_moe.hip, mlora_w4.hip).
+// (mlora_moe.hip, mlora_w4.hip, mlora_fp8.hip, mlora_layer.hip, mlora_norm.hip).
 #ifndef MLORA_DEVICE_H_
 #define MLORA_DEVICE_H_
 
@@ -118,6 +118,19 @@ __device__ __forceinline__ uint32_t group_min(uint32_t v) {
 template <int LPT>
 __device__ __forceinline__ float group_sum(float v) {
   return group_reduce<LPT>(v, [](float a, float b) { return a + b; });
+}
+
+// Exclusive prefix over the wave's lanes of v, and its sum over all of them.
+__device__ __forceinline__ int wave_prefix(int v, int* sum) {
+  int run = v;
+  run += __builtin_amdgcn_update_dpp(0, run, 0x111, 0xf, 0xf, false);  // row_shr:1
+  run += __builtin_amdgcn_update_dpp(0, run, 0x112, 0xf, 0xf, false);  // row_shr:2
+  run += __builtin_amdgcn_update_dpp(0, run, 0x114, 0xf, 0xf, false);  // row_shr:4
+  run += __builtin_amdgcn_update_dpp(0, run, 0x118, 0xf, 0xf, false);  // row_shr:8
+  run += __builtin_amdgcn_update_dpp(0, run, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  run += __builtin_amdgcn_update_dpp(0, run, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  *sum = __builtin_amdgcn_readlane(run, 63);
+  return run - v;
 }
 
 // LDS traffic of one wave is in order; this keeps the compiler from moving

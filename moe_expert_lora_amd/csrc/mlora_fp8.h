@@ -1,0 +1,94 @@
+// The layout of packed 8-bit weights and the matrix instruction that reads it,
+// shared by mlora_fp8.hip and mlora_layer.hip.
+#ifndef MLORA_FP8_H_
+#define MLORA_FP8_H_
+
+#include <algorithm>
+
+#include "mlora_device.h"
+
+namespace mlora {
+
+// Packed: for each expert, tile of 16 out rows n and block of 128 k, in this
+// order, kFp8Tile bytes; rows and columns past the weight's own are zeros, and
+// the tiles fill whole blocks of 128 rows. A tile's byte (half h, lane l, j) is
+// the code of row n = l % 16 and k = 32 (l / 16) + 16 h + j: the operand of
+// lane l, so that a wave's 16-byte loads are 1 KB in one piece. The scales
+// follow, [n_experts][blocks of n][blocks of k].
+constexpr int kFp8Tile = 2048;
+constexpr int kFp8MaxExperts = 1024;
+constexpr int kFp8MaxDim = 1 << 20;
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+struct Fp8Frag {
+  u32x4 h[2];
+};
+
+__device__ __forceinline__ Fp8Frag load_frag(const uint8_t* p, int half) {
+  return Fp8Frag{{*reinterpret_cast<const u32x4*>(p), *reinterpret_cast<const u32x4*>(p + half)}};
+}
+
+__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// 8 codes -> 8 bf16 values.
+__device__ __forceinline__ u32x4 widen_codes(uint32_t lo, uint32_t hi) {
+  u32x4 v;
+  v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false));
+  v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true));
+  v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false));
+  v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true));
+  return v;
+}
+
+// 16 x 16 sums of 128 products of E4M3 codes; result i of lane l is row
+// 4 (l / 16) + i of the first operand by row l % 16 of the second. Either the
+// 8-bit instruction (block scales of 2^0): it aligns the products of 8 neighbouring
+// k to their largest and cuts them off below 2^-13 of its power of two, then adds in
+// fp32, so it is off by 1.5e-5 relative over random codes and by 7 * 2^-13 of the
+// sum of the products' magnitudes at most (measured), a fraction of a bf16 rounding.
+// Or, for fp32 results, bf16 values made of the codes (exact), at half the rate:
+// 9e-9 relative.
+__device__ __forceinline__ f32x4 mfma_fp8(const Fp8Frag& a, const Fp8Frag& b) {
+  const i32x8 av = __builtin_bit_cast(i32x8, a), bv = __builtin_bit_cast(i32x8, b);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
+                                                          0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+}
+
+__device__ __forceinline__ f32x4 mfma_fp8_as_bf16(const Fp8Frag& a, const Fp8Frag& b) {
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    s = mfma_bf16(widen_codes(a.h[j / 2][2 * (j % 2)], a.h[j / 2][2 * (j % 2) + 1]),
+                  widen_codes(b.h[j / 2][2 * (j % 2)], b.h[j / 2][2 * (j % 2) + 1]), s);
+  return s;
+}
+
+// 8 values of a row from column k on; zeros past K.
+template <typename Row, bool WIDE>
+__device__ __forceinline__ void load8(const void* base, int64_t off, int k, int K, float* f) {
+  const typename Row::elem* p = static_cast<const typename Row::elem*>(base) + off;
+  if constexpr (WIDE) {  // K is a multiple of 8, rows start on 16 bytes
+    u32x4 v[8 / Row::kPer16];
+#pragma unroll
+    for (int i = 0; i < 8 / Row::kPer16; ++i) {
+      v[i] = u32x4{0, 0, 0, 0};
+      if (k < K) v[i] = *reinterpret_cast<const u32x4*>(p + k + i * Row::kPer16);
+    }
+#pragma unroll
+    for (int i = 0; i < 8 / Row::kPer16; ++i) Row::widen16(v[i], f + i * Row::kPer16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = k + i < K ? Row::widen(p[k + i]) : 0.f;
+  }
+}
+
+// MLORA_OK, or why the route is refused.
+int32_t check_fp8_route(const char* who, const char* name, const mlora_fp8_route* r);
+
+}  // namespace mlora
+
+#endif  // MLORA_FP8_H_

@@ -1,0 +1,405 @@
+// A whole MoE layer for a few tokens in two kernels, for gfx950 (MI355X): the
+// router's choice, gate and up with their activation; down and the weighted sum.
+#include "mlora_fp8.h"
+#include "mlora_router.h"
+
+namespace mlora {
+namespace {
+
+// out[t] = sum over j of p[t, j] down_e (silu(gate_e x[t]) * (up_e x[t])), e the
+// j-th expert of token t. The weights of the chosen experts are read once, as
+// E4M3 codes that become bf16 values (exactly) in front of bf16 MFMAs of 16
+// weight rows by 16 tokens; every token of the call is a column of them, and the
+// ones that did not choose the expert are left out of the result. x stays as it
+// is: a bf16 value is one operand, an fp32 value three (24 bits). The activated
+// rows, times p, pass from kernel to kernel as two (three) bf16 parts, 2^-16
+// (2^-24) of the value. A block's sums enter the fp32 sums times its scale.
+//
+// Kernel one: each workgroup chooses every token's experts itself (the logits
+// are a few KB), lists the experts that are chosen, and takes tiles of 16 hidden
+// columns of them in turn; its waves share the blocks of k. Kernel two: a
+// workgroup owns 16 out columns and its waves share the experts' blocks, so that
+// the sum over the experts needs no atomics. Which wave takes a block goes by the
+// expert and the block alone: a token's sums have the same order, and its row the
+// same bits, whatever the other tokens choose.
+
+constexpr int kTokens = 16;
+constexpr int kWaves = 8;
+constexpr int kNone = 255;
+
+struct LayerArgs {
+  const void* logits;
+  int64_t logits_ld;
+  const void* x;
+  int64_t x_ld;
+  const uint8_t *gate, *up, *down;
+  const float *gate_s, *up_s, *down_s;
+  void* out;
+  int64_t out_ld;
+  int32_t* indices;  // may be null
+  float* weights;    // may be null
+  int32_t* head;     // workspace: count, experts [max_active], slots [max_active][16]
+  uint16_t* act;     // workspace: [T * k][parts][hidden, whole blocks]
+  int32_t T, E, k, renorm, dim, hidden, DB, HB, max_active;
+};
+
+template <typename Row>
+constexpr int parts_of_x() { return sizeof(typename Row::elem) == 2 ? 1 : 3; }
+template <typename Row>
+constexpr int parts_of_act() { return sizeof(typename Row::elem) == 2 ? 2 : 3; }
+
+// f as P bf16 values whose sum it is, the largest first.
+template <int P>
+__device__ __forceinline__ void split8(const float* f, u32x4 (&out)[P]) {
+  float left[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) left[i] = f[i];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    out[p] = Bf16Row::narrow16(left);
+    if (p + 1 < P) {
+      float part[8];
+      Bf16Row::widen16(out[p], part);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) left[i] -= part[i];
+    }
+  }
+}
+
+// A block's sums: the tile's 128 products a result, for one or more parts of x.
+// Lane group g = lane / 16 holds k = 32 g + 8 j .. + 7 of both operands in step j.
+template <int P>
+__device__ __forceinline__ f32x4 block_sum(const Fp8Frag& w, const u32x4 (&x)[4][P]) {
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const u32x4 wf = widen_codes(w.h[j / 2][2 * (j % 2)], w.h[j / 2][2 * (j % 2) + 1]);
+#pragma unroll
+    for (int p = P - 1; p >= 0; --p) s = mfma_bf16(wf, x[j][p], s);
+  }
+  return s;
+}
+
+// Dynamic LDS of kernel one, in words from the start.
+struct Lds {
+  int ids, wts, place, list, slots, part, total;
+};
+__host__ __device__ inline Lds lds_of(int n, int E, int max_active) {
+  Lds l{};
+  l.ids = 4;  // word 0: the number of chosen experts
+  l.wts = l.ids + n;
+  l.place = l.wts + n;
+  l.list = l.place + E;
+  l.slots = l.list + max_active;
+  l.part = (l.slots + max_active * (kTokens / 4) + 3) & ~3;
+  l.total = l.part + kWaves * 2 * 256;
+  return l;
+}
+
+// Every token's choice into LDS, by all waves.
+template <typename Row, int LPT, int VPL>
+__device__ __forceinline__ void choose_all(const LayerArgs& a, int* ids, float* wts, bool publish) {
+  const int gl = threadIdx.x & (LPT - 1);
+  constexpr int kPer = kWaves * 64 / LPT;
+  for (int t0 = 0; t0 < a.T; t0 += kPer) {
+    const int t = t0 + (int)(threadIdx.x / LPT);
+    float v[VPL];
+    load_row<Row, LPT, VPL, Row::kPer16, false>(a.logits, (int64_t)(t < a.T ? t : 0) * a.logits_ld,
+                                                a.E, gl, v);
+    int e;
+    const float w = choose_experts<Row, LPT, VPL, Row::kPer16>(v, a.E, a.k, a.renorm, gl, &e);
+    if (t < a.T && gl < a.k) {
+      ids[t * a.k + gl] = e;
+      wts[t * a.k + gl] = w;
+      if (publish && a.indices) a.indices[t * a.k + gl] = e;
+      if (publish && a.weights) a.weights[t * a.k + gl] = w;
+    }
+  }
+}
+
+template <typename Row, bool WIDE>
+__global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a) {
+  extern __shared__ int lds[];
+  constexpr int P = parts_of_x<Row>(), PA = parts_of_act<Row>();
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i32(tid >> 6);
+  const int n = a.T * a.k;
+  const Lds l = lds_of(n, a.E, a.max_active);
+  int *ids = lds + l.ids, *place = lds + l.place, *list = lds + l.list;
+  float *wts = reinterpret_cast<float*>(lds + l.wts), *part = reinterpret_cast<float*>(lds + l.part);
+  uint8_t* slots = reinterpret_cast<uint8_t*>(lds + l.slots);
+  const bool first = blockIdx.x == 0;
+
+  if (a.E <= 128 && a.k <= 16)
+    choose_all<Row, 16, 8>(a, ids, wts, first);
+  else if (a.E <= 256 && a.k <= 32)
+    choose_all<Row, 32, 8>(a, ids, wts, first);
+  else
+    choose_all<Row, 64, 16>(a, ids, wts, first);
+  for (int e = tid; e < a.E; e += 64 * kWaves) place[e] = 0;
+  for (int i = tid; i < a.max_active * (kTokens / 4); i += 64 * kWaves)
+    lds[l.slots + i] = -1;  // four times kNone
+  __syncthreads();
+  for (int i = tid; i < n; i += 64 * kWaves) place[ids[i]] = 1;
+  __syncthreads();
+  if (wave == 0) {
+    int count = 0;
+    for (int base = 0; base < a.E; base += 64) {
+      const int e = base + lane;
+      const int on = e < a.E ? place[e] : 0;
+      int sum;
+      const int at = count + wave_prefix(on, &sum);
+      if (on) {
+        place[e] = at;
+        list[at] = e;
+      }
+      count += sum;
+    }
+    if (lane == 0) lds[0] = count;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += 64 * kWaves) {
+    const int t = i / a.k;
+    slots[place[ids[i]] * kTokens + t] = (uint8_t)(i - t * a.k);
+  }
+  __syncthreads();
+  const int active = lds[0];
+  if (first) {
+    if (tid == 0) a.head[0] = active;
+    for (int i = tid; i < active; i += 64 * kWaves) a.head[1 + i] = list[i];
+    for (int i = tid; i < active * (kTokens / 4); i += 64 * kWaves)
+      a.head[1 + a.max_active + i] = lds[l.slots + i];
+  }
+
+  const int tiles = a.HB * 8;
+  const int t_col = lane & 15, g = lane >> 4;
+  const int64_t x_off = (int64_t)min(t_col, a.T - 1) * a.x_ld;
+  const int k0 = a.DB * wave / kWaves, k1 = a.DB * (wave + 1) / kWaves;
+  for (int item = blockIdx.x; item < active * tiles; item += gridDim.x) {
+    const int at = item / tiles, nt = item - at * tiles;
+    const int e = uniform_i32(list[at]);
+    const int64_t tile = ((int64_t)e * tiles + nt) * a.DB;
+    const uint8_t* gw = a.gate + tile * kFp8Tile + lane * 16;
+    const uint8_t* uw = a.up + tile * kFp8Tile + lane * 16;
+    const int64_t sc = ((int64_t)e * a.HB + nt / 8) * a.DB;
+    f32x4 gs = {0.f, 0.f, 0.f, 0.f}, us = gs;
+    for (int kb = k0; kb < k1; ++kb) {
+      const Fp8Frag gf = load_frag(gw + (int64_t)kb * kFp8Tile, 1024);
+      const Fp8Frag uf = load_frag(uw + (int64_t)kb * kFp8Tile, 1024);
+      u32x4 xf[4][P];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[8];
+        load8<Row, WIDE>(a.x, x_off, kb * 128 + g * 32 + j * 8, a.dim, v);
+        split8<P>(v, xf[j]);
+      }
+      const f32x4 gp = block_sum<P>(gf, xf), up = block_sum<P>(uf, xf);
+      const float sg = a.gate_s[sc + kb], su = a.up_s[sc + kb];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        gs[i] = fmaf(gp[i], sg, gs[i]);
+        us[i] = fmaf(up[i], su, us[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      part[(wave * 2 + 0) * 256 + i * 64 + lane] = gs[i];
+      part[(wave * 2 + 1) * 256 + i * 64 + lane] = us[i];
+    }
+    __syncthreads();
+    if (tid < 256) {
+      const int t = tid >> 4, c = tid & 15;  // token and column of the tile
+      const int src = (c & 3) * 64 + (c >> 2) * 16 + t;
+      float gate = 0.f, up = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        gate += part[(w * 2 + 0) * 256 + src];
+        up += part[(w * 2 + 1) * 256 + src];
+      }
+      const int j = slots[at * kTokens + t];
+      if (j != kNone) {
+        const int slot = t * a.k + j;
+        float v = gate / (1.f + expf(-gate)) * up * wts[slot];
+        uint16_t* dst = a.act + (int64_t)slot * PA * (a.HB * 128) + nt * 16 + c;
+#pragma unroll
+        for (int p = 0; p < PA; ++p) {
+          const uint16_t b = Bf16Row::narrow(v);
+          dst[(int64_t)p * (a.HB * 128)] = b;
+          v -= Bf16Row::widen(b);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename Row>
+__global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, bool wide) {
+  __shared__ f32x4 part[kWaves][64];
+  constexpr int PA = parts_of_act<Row>();
+  const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
+  const int nt = blockIdx.x, t = lane & 15, g = lane >> 4;
+  const int active = a.head[0];
+  const int* list = a.head + 1;
+  const uint8_t* slots = reinterpret_cast<const uint8_t*>(a.head + 1 + a.max_active);
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int at = 0; at < active; ++at) {
+    const int e = uniform_i32(list[at]);
+    const int j = slots[at * kTokens + t];
+    const uint8_t* w = a.down + ((int64_t)e * a.DB * 8 + nt) * a.HB * kFp8Tile + lane * 16;
+    const float* ws = a.down_s + ((int64_t)e * a.DB + nt / 8) * a.HB;
+    const uint16_t* act = a.act + (int64_t)(j == kNone ? 0 : t * a.k + j) * PA * (a.HB * 128) + g * 32;
+    for (int b = (int)((uint32_t)(wave - e * a.HB) % kWaves); b < a.HB; b += kWaves) {
+      const Fp8Frag wf = load_frag(w + (int64_t)b * kFp8Tile, 1024);
+      u32x4 xf[4][PA];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+          xf[i][p] = *reinterpret_cast<const u32x4*>(act + (int64_t)p * (a.HB * 128) + b * 128 + i * 8);
+      const f32x4 s = block_sum<PA>(wf, xf);
+      const float sc = ws[b];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = j == kNone ? acc[i] : fmaf(s[i], sc, acc[i]);
+    }
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (wave > 0 || t >= a.T) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) acc += part[w][lane];
+  const int n = nt * 16 + g * 4;
+  typename Row::elem* p = static_cast<typename Row::elem*>(a.out) + (int64_t)t * a.out_ld + n;
+  if (wide && n + 4 <= a.dim) {
+    if constexpr (sizeof(typename Row::elem) == 2)
+      *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])};
+    else
+      *reinterpret_cast<f32x4*>(p) = acc;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.dim) p[i] = Row::narrow(acc[i]);
+  }
+}
+
+struct LayerSpace {
+  int64_t act, total;  // bytes
+};
+LayerSpace space_of(int64_t T, int64_t E, int64_t k, int64_t hidden) {
+  const int64_t active = std::min(E, T * k), width = (hidden + 127) / 128 * 128;
+  LayerSpace s{};
+  s.act = ((1 + active + active * (kTokens / 4)) * 4 + 255) / 256 * 256;
+  s.total = s.act + T * k * 3 * width * 2;
+  return s;
+}
+
+int32_t check_layer(const char* who, int64_t n_tokens, int32_t n_experts, int32_t top_k,
+                    int32_t dim, int32_t hidden) {
+  if (n_tokens < 0 || n_tokens > kTokens)
+    return fail(MLORA_ERR_INVALID, "%s: n_tokens=%lld outside [0, %d]", who, (long long)n_tokens,
+                kTokens);
+  if (n_experts < 1 || n_experts > kMaxExperts)
+    return fail(MLORA_ERR_INVALID, "%s: n_experts=%d outside [1, %d]", who, n_experts, kMaxExperts);
+  if (top_k < 1 || top_k > n_experts || top_k > kMaxTopK)
+    return fail(MLORA_ERR_INVALID, "%s: top_k=%d outside [1, min(n_experts=%d, %d)]", who, top_k,
+                n_experts, kMaxTopK);
+  if (dim < 1 || dim > kFp8MaxDim || hidden < 1 || hidden > kFp8MaxDim)
+    return fail(MLORA_ERR_INVALID, "%s: dim=%d, hidden=%d outside [1, %d]", who, dim, hidden,
+                kFp8MaxDim);
+  return MLORA_OK;
+}
+
+template <typename Row>
+int32_t launch_layer(const char* who, const LayerArgs& a, bool x_wide, bool out_wide,
+                     hipStream_t s) {
+  const Lds l = lds_of(a.T * a.k, a.E, a.max_active);
+  const int64_t items = (int64_t)a.max_active * a.HB * 8;
+  const int grid = (int)std::min<int64_t>(items, 1024);
+  if (x_wide)
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, true>), dim3(grid), dim3(64 * kWaves),
+                       l.total * 4, s, a);
+  else
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, false>), dim3(grid), dim3(64 * kWaves),
+                       l.total * 4, s, a);
+  if (int32_t rc = launch_status(who)) return rc;
+  hipLaunchKernelGGL((layer_down_kernel<Row>), dim3((a.dim + 15) / 16), dim3(64 * kWaves), 0, s, a,
+                     out_wide);
+  return launch_status(who);
+}
+
+}  // namespace
+}  // namespace mlora
+
+using namespace mlora;
+
+extern "C" uint64_t mlora_moe_layer_workspace_bytes(int64_t n_tokens, int32_t n_experts,
+                                                    int32_t top_k, int32_t dim, int32_t hidden) {
+  if (check_layer("mlora_moe_layer_workspace_bytes", n_tokens, n_experts, top_k, dim, hidden))
+    return 0;
+  return n_tokens == 0 ? 0 : (uint64_t)space_of(n_tokens, n_experts, top_k, hidden).total;
+}
+
+extern "C" int32_t mlora_moe_layer(const mlora_fp8_route* gate, const mlora_fp8_route* up,
+                                   const mlora_fp8_route* down, const void* x, int64_t x_ld,
+                                   int32_t dtype, int64_t n_tokens, const void* logits,
+                                   int64_t logits_ld, int32_t top_k, int32_t renormalize,
+                                   void* out, int64_t out_ld, int32_t* indices, float* weights,
+                                   void* workspace, uint64_t workspace_bytes, void* stream) {
+  const char* who = "mlora_moe_layer";
+  if (int32_t rc = check_fp8_route(who, "gate", gate)) return rc;
+  if (int32_t rc = check_fp8_route(who, "up", up)) return rc;
+  if (int32_t rc = check_fp8_route(who, "down", down)) return rc;
+  if (gate->n_experts != up->n_experts || gate->n_experts != down->n_experts ||
+      gate->k_in != up->k_in || gate->n_out != up->n_out || down->k_in != gate->n_out ||
+      down->n_out != gate->k_in)
+    return fail(MLORA_ERR_INVALID, "%s: the routes' sizes do not fit each other", who);
+  if (dtype != MLORA_BF16 && dtype != MLORA_F32)
+    return fail(MLORA_ERR_INVALID, "%s: dtype %d is neither bf16 nor f32", who, dtype);
+  const int32_t E = gate->n_experts, dim = gate->k_in, hidden = gate->n_out;
+  if (int32_t rc = check_layer(who, n_tokens, E, top_k, dim, hidden)) return rc;
+  if (x_ld < dim || out_ld < dim || logits_ld < E)
+    return fail(MLORA_ERR_INVALID, "%s: row stride below the row's width", who);
+  if (n_tokens == 0) {
+    clear_error();
+    return MLORA_OK;
+  }
+  if (!x || !logits || !out) return fail(MLORA_ERR_INVALID, "%s: NULL pointer", who);
+  const LayerSpace sp = space_of(n_tokens, E, top_k, hidden);
+  if (!workspace || workspace_bytes < (uint64_t)sp.total)
+    return fail(MLORA_ERR_CAPACITY, "%s: workspace of %llu bytes, %lld needed", who,
+                (unsigned long long)(workspace ? workspace_bytes : 0), (long long)sp.total);
+  if (!aligned(workspace, 256))
+    return fail(MLORA_ERR_INVALID, "%s: workspace must be 256-byte aligned", who);
+  LayerArgs a{};
+  a.logits = logits;
+  a.logits_ld = logits_ld;
+  a.x = x;
+  a.x_ld = x_ld;
+  a.gate = static_cast<const uint8_t*>(gate->weights);
+  a.up = static_cast<const uint8_t*>(up->weights);
+  a.down = static_cast<const uint8_t*>(down->weights);
+  a.gate_s = static_cast<const float*>(gate->scales);
+  a.up_s = static_cast<const float*>(up->scales);
+  a.down_s = static_cast<const float*>(down->scales);
+  a.out = out;
+  a.out_ld = out_ld;
+  a.indices = indices;
+  a.weights = weights;
+  a.head = static_cast<int32_t*>(workspace);
+  a.act = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + sp.act);
+  a.T = (int32_t)n_tokens;
+  a.E = E;
+  a.k = top_k;
+  a.renorm = renormalize;
+  a.dim = dim;
+  a.hidden = hidden;
+  a.DB = (dim + 127) / 128;
+  a.HB = (hidden + 127) / 128;
+  a.max_active = std::min(E, a.T * top_k);
+  const int per = dtype == MLORA_BF16 ? 8 : 4;
+  const bool x_wide = dim % 8 == 0 && x_ld % per == 0 && aligned(x, 16);
+  const bool out_wide = out_ld % 4 == 0 && aligned(out, dtype == MLORA_BF16 ? 8 : 16);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  return dtype == MLORA_BF16 ? launch_layer<Bf16Row>(who, a, x_wide, out_wide, s)
+                             : launch_layer<F32Row>(who, a, x_wide, out_wide, s);
+}

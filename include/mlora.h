@@ -612,8 +612,10 @@ int32_t mlora_fp8_pack(const uint8_t* w, const float* scales, int32_t n_experts,
                        int32_t n_out, int32_t transpose, void* packed, uint64_t packed_bytes,
                        mlora_fp8_route* route, void* stream);
 
-/* Bytes of a quantised row of k values: k rounded up to a multiple of 128 (0 for
- * a k outside [1, 2^20]). */
+/* Bytes of a quantised row of k values, the width of q: ceil(k / 128) blocks of
+ * 128, plus one more where that number is even (its bytes are neither written nor
+ * read: rows a multiple of 512 bytes apart would share the L2's channels badly).
+ * 0 for a k outside [1, 2^20]. */
 int32_t mlora_fp8_row_width(int32_t k);
 
 /* Quantises rows: x, or silu(x) * up (in fp32) where up is given. Of each group
@@ -622,8 +624,8 @@ int32_t mlora_fp8_row_width(int32_t k);
  * group with an infinity or NaN gets a NaN scale and codes of 0 (its product rows
  * are NaN; other rows do not change).
  *   x, up     [n_rows, k] dtype
- *   q         [n_rows, mlora_fp8_row_width(k)] codes, zeros past k; 16-byte
- *             aligned, q_ld (bytes) a multiple of 16
+ *   q         [n_rows, mlora_fp8_row_width(k)] codes, zeros from k to the end of
+ *             its block; 16-byte aligned, q_ld (bytes) a multiple of 16
  *   q_scales  [ceil(k / 128), n_rows] fp32: a group's scales of all rows lie
  *             together */
 int32_t mlora_fp8_quant(const void* x, int64_t x_ld, const void* up, int64_t up_ld, int32_t dtype,

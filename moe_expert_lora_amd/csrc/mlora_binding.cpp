@@ -322,10 +322,10 @@ struct Codes {
 };
 
 // A group's scales of every row: [groups, rows].
-float* group_scales(PyObject* o, int64_t width, int64_t rows) {
+float* group_scales(PyObject* o, int64_t k, int64_t rows) {
   const at::Tensor& t = tensor(o, "q_scales");
   const Vec v(o, "q_scales", at::kFloat);
-  require(t.dim() == 2 && t.size(0) == width / 128 && t.size(1) == rows,
+  require(t.dim() == 2 && t.size(0) == (k + 127) / 128 && t.size(1) == rows,
           "q_scales must be [ceil(k / 128), rows of q]");
   return static_cast<float*>(v.p);
 }
@@ -350,7 +350,7 @@ PyObject* fp8_quant(PyObject*, Args a, Py_ssize_t n) {
     const int32_t k = size32(x.cols, "x");
     require(q.rows == x.rows && q.cols == mlora_fp8_row_width(k),
             "q must be [n_rows, mlora_fp8_row_width(k)]");
-    float* scales = group_scales(a[2], q.cols, x.rows);
+    float* scales = group_scales(a[2], k, x.rows);
     const void* up = nullptr;
     int64_t up_ld = 0;
     if (a[3] != Py_None) {
@@ -373,7 +373,7 @@ PyObject* fp8_gemm(PyObject*, Args a, Py_ssize_t n) {
     const Mat out(a[3], "out");
     require(q.cols == mlora_fp8_row_width(route->k_in) && out.cols == route->n_out,
             "q / out widths differ from the route's k_in / n_out");
-    const float* scales = group_scales(a[2], q.cols, q.rows);
+    const float* scales = group_scales(a[2], route->k_in, q.rows);
     const Vec off(a[4], "expert_offsets", at::kInt, true), ids(a[5], "sorted_ids", at::kInt, true);
     require(a[4] == Py_None || off.n == (int64_t)route->n_experts + 1,
             "expert_offsets must have n_experts + 1 entries");

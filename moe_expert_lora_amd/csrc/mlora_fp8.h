@@ -9,15 +9,32 @@
 
 namespace mlora {
 
-// Packed: for each expert, tile of 16 out rows n and block of 128 k, in this
-// order, kFp8Tile bytes; rows and columns past the weight's own are zeros, and
-// the tiles fill whole blocks of 128 rows. A tile's byte (half h, lane l, j) is
-// the code of row n = l % 16 and k = 32 (l / 16) + 16 h + j: the operand of
-// lane l, so that a wave's 16-byte loads are 1 KB in one piece. The scales
-// follow, [n_experts][blocks of n][blocks of k].
+// Packed: for each expert, block of 128 out rows n, block of 128 k and tile of 16 of
+// the block's rows, in this order, kFp8Tile bytes; rows and columns past the weight's
+// own are zeros. A tile's byte (half h, lane l, j) is the code of the tile's row
+// l % 16 and k = 32 (l / 16) + 16 h + j: the operand of lane l, so that a wave's
+// 16-byte loads are 1 KB in one piece. A block of 128 x 128 is 16 KB in one piece, so
+// that the blocks of a column strip come from all of an L2's 16 channels (256 bytes
+// each), not from the same few. A pair of tiles shares 32 rows: row r of tile t is
+// n = 32 (t / 2) + 8 (r / 4) + 4 (t % 2) + r % 4, so that the four results a lane has
+// of each of the two are 8 neighbours, one 16-byte store of bf16. The scales follow,
+// [n_experts][blocks of n][blocks of k].
 constexpr int kFp8Tile = 2048;
 constexpr int kFp8MaxExperts = 1024;
 constexpr int kFp8MaxDim = 1 << 20;
+
+// Tile of the columns 16 nt .. + 15 and block kb of the expert's first one.
+__device__ __forceinline__ int64_t fp8_tile(int nt, int kb, int KB) {
+  return ((int64_t)(nt / 8) * KB + kb) * 8 + nt % 8;
+}
+
+// The out column of a lane group's (lane / 16) first result of tile nt; the other three
+// follow.
+__device__ __forceinline__ int fp8_column(int nt, int g) {
+  return (nt >> 1) * 32 + g * 8 + (nt & 1) * 4;
+}
+// Tiles that hold columns of N: whole pairs.
+inline int32_t fp8_tiles(int32_t N) { return (N + 31) / 32 * 2; }
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 

@@ -2,6 +2,7 @@
 // block of 128 x 128), for gfx950 (MI355X): the weights' layout, the rows'
 // quantiser, and the product over rows sorted by expert.
 #include "mlora_fp8.h"
+#include <type_traits>
 
 namespace mlora {
 namespace {
@@ -29,11 +30,14 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(Fp8PackArgs a) {
   if (i < a.chunks) {
     const int lane = (int)(i & 63), half = (int)(i >> 6) & 1;
     int64_t t = i >> 7;
+    const int part = (int)(t & 7);
+    t >>= 3;
     const int kb = (int)(t % a.KB);
     t /= a.KB;
-    const int nt = (int)(t % (a.NB * 8));
-    const int64_t e = t / (a.NB * 8);
-    const int n = nt * 16 + (lane & 15), k = kb * 128 + (lane >> 4) * 32 + half * 16;
+    const int nb = (int)(t % a.NB);
+    const int64_t e = t / a.NB;
+    const int r = lane & 15;
+    const int n = fp8_column(nb * 8 + part, r >> 2) + (r & 3), k = kb * 128 + (lane >> 4) * 32 + half * 16;
     const uint8_t* src = a.w + e * a.N * a.K;
     u32x4 v = {0, 0, 0, 0};
     if (n < a.N && k < a.K) {
@@ -173,6 +177,7 @@ struct GemmArgs {
   const float* ws;
   const uint8_t* q;
   int64_t q_ld;
+  uint32_t q_bytes;           // of q, for its buffer
   const float* qs;            // [KB][q_rows]
   const int32_t* offsets;     // null: one span of every row
   const int32_t* sorted_ids;  // null: row r reads q row r
@@ -182,41 +187,59 @@ struct GemmArgs {
   int32_t n_groups, ks;
 };
 
-// The rows of one tile: up to `size` of expert e from `row` on, below `end`.
+// One tile: rows row .. end - 1 (as many as the tile takes of them) of expert e, and
+// the tile's number among the columns. e < 0: there are fewer tiles.
 struct Span {
-  int e, row, end;
+  int e, row, end, n;
 };
 
-// Tile number `tile` among the spans' tiles of `size` rows, found by the wave
-// together: 64 spans at a time, their tiles' prefix in the lanes. e < 0: there
-// are fewer tiles. Offsets past the rows count as the last row.
+// Workgroup `group`'s tile among the spans' tiles of `size` rows by n_groups column
+// tiles, found by the wave together: 64 spans at a time, their tiles' prefix in the
+// lanes. The tiles of an XCD (every eighth workgroup) are neighbours, an eighth of
+// those that there are, so that they share rows and weights in its L2 and no XCD gets
+// more of them. Offsets past the rows count as the last row.
 __device__ __forceinline__ Span find_tile(const int32_t* offsets, int E, int n_rows, int size,
-                                          int tile) {
-  if (!offsets) {
-    const int row = tile * size;
-    return Span{row < n_rows ? 0 : -1, row, n_rows};
-  }
+                                          int n_groups, int group) {
   const int lane = threadIdx.x & 63;
-  for (int base = 0; base < E; base += 64) {
-    const int e = base + lane;
-    int lo = 0, hi = 0;
+  auto span = [&](int e, int* lo, int* hi) {
+    *lo = *hi = 0;
     if (e < E) {
-      lo = min(max(offsets[e], 0), n_rows);
-      hi = min(max(offsets[e + 1], lo), n_rows);
+      *lo = min(max(offsets[e], 0), n_rows);
+      *hi = min(max(offsets[e + 1], *lo), n_rows);
     }
-    const int tiles = (hi - lo + size - 1) / size;
+    return (*hi - *lo + size - 1) / size;
+  };
+  int total = 0, lo, hi;
+  if (!offsets) {
+    total = (n_rows + size - 1) / size;
+  } else {
+    for (int base = 0; base < E; base += 64) {
+      int sum;
+      wave_prefix(span(base + lane, &lo, &hi), &sum);
+      total += sum;
+    }
+  }
+  const int per = (int)(((int64_t)total * n_groups + 7) / 8);
+  const int64_t at = (int64_t)(group % 8) * per + group / 8;
+  if (group / 8 >= per || at >= (int64_t)total * n_groups) return Span{-1, 0, 0, 0};
+  int tile = (int)(at / n_groups);
+  const int n = (int)(at % n_groups);
+  if (!offsets) return Span{0, tile * size, n_rows, n};
+  for (int base = 0; base < E; base += 64) {
+    const int tiles = span(base + lane, &lo, &hi);
     int sum;
     const int before = wave_prefix(tiles, &sum);
     if (tile < sum) {
       const uint64_t here = __ballot(tile >= before && tile < before + tiles);
+      if (!here) break;  // sums past 32 bits, of offsets that are none
       const int l = __builtin_ctzll(here);
       const int row = __builtin_amdgcn_readlane(lo, l) +
                       (tile - __builtin_amdgcn_readlane(before, l)) * size;
-      return Span{base + l, row, __builtin_amdgcn_readlane(hi, l)};
+      return Span{base + l, row, __builtin_amdgcn_readlane(hi, l), n};
     }
     tile -= sum;
   }
-  return Span{-1, 0, 0};
+  return Span{-1, 0, 0, 0};
 }
 
 // The q row that sorted row r reads; -1: none.
@@ -228,17 +251,24 @@ __device__ __forceinline__ int source_row(const GemmArgs& a, int r, int end) {
   return id >= 0 && t < a.q_rows ? t : -1;
 }
 
-template <typename Row>
-__device__ __forceinline__ void store4(const GemmArgs& a, int64_t row, int n, f32x4 v, bool wide) {
+// A lane's results from column n on, 4 or (a pair of tiles) 8 of them.
+template <typename Row, int C>
+__device__ __forceinline__ void store_columns(const GemmArgs& a, int64_t row, int n, const float* v,
+                                              bool wide) {
   typename Row::elem* p = static_cast<typename Row::elem*>(a.out) + row * a.out_ld + n;
-  if (wide && n + 4 <= a.N) {
-    if constexpr (sizeof(typename Row::elem) == 2)
+  if (wide && n + C <= a.N) {
+    if constexpr (sizeof(typename Row::elem) == 4) {
+#pragma unroll
+      for (int i = 0; i < C; i += 4)
+        *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else if constexpr (C == 8) {
+      *reinterpret_cast<u32x4*>(p) = Row::narrow16(v);
+    } else {
       *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-    else
-      *reinterpret_cast<f32x4*>(p) = v;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C; ++i)
       if (n + i < a.N) p[i] = Row::narrow(v[i]);
   }
 }
@@ -252,35 +282,36 @@ __device__ __forceinline__ f32x4 block_products(const Fp8Frag& w, const Fp8Frag&
     return mfma_fp8_as_bf16(w, q);
 }
 
-// A wave makes 16 columns of 16 rows, operands straight from memory; ks waves
-// of a workgroup share a tile's blocks and add their sums up in order.
+// A wave makes 16 columns of 16 rows, operands straight from memory: for calls too
+// small to fill the chip with larger tiles. ks waves of a workgroup share a tile's
+// blocks and add their sums up in order.
 template <typename Row>
 __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a, bool wide) {
   __shared__ f32x4 part[8][64];
   const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
   const int nw = (int)(blockDim.x >> 6) / a.ks;
-  const int group = flat_group();
-  const Span sp = find_tile(a.offsets, a.E, a.n_rows, 16, group / a.n_groups);
+  const Span sp = find_tile(a.offsets, a.E, a.n_rows, 16, a.n_groups, flat_group());
   if (sp.e < 0) return;  // the whole workgroup
   const int kp = wave / nw;
-  const int nt = (group % a.n_groups) * nw + wave - kp * nw;
+  const int nt = sp.n * nw + wave - kp * nw;
   const bool on = nt < a.NT;
   const int row = sp.row + (lane & 15);
   const int src = source_row(a, row, sp.end);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   if (on) {
-    const uint8_t* w = a.w + (((int64_t)sp.e * a.NB * 8 + nt) * a.KB) * kFp8Tile + lane * 16;
+    const uint8_t* w =
+        a.w + ((int64_t)sp.e * a.NB * 8 * a.KB + fp8_tile(nt, 0, a.KB)) * kFp8Tile + lane * 16;
     const float* ws = a.ws + ((int64_t)sp.e * a.NB + nt / 8) * a.KB;
     const uint8_t* q = a.q + (int64_t)max(src, 0) * a.q_ld + (lane >> 4) * 32;
     const float* qs = a.qs + max(src, 0);
     const int k0 = a.KB * kp / a.ks, k1 = a.KB * (kp + 1) / a.ks;
     for (int kb = k0; kb < k1; ++kb) {
-      const Fp8Frag wf = load_frag(w + (int64_t)kb * kFp8Tile, 1024);
+      const Fp8Frag wf = load_frag(w + (int64_t)kb * (8 * kFp8Tile), 1024);
       const Fp8Frag qf = load_frag(q + kb * 128, 16);
       const float s = ws[kb] * qs[(int64_t)kb * a.q_rows];
       const f32x4 p = block_products<Row>(wf, qf);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
+      for (int v = 0; v < 4; ++v) acc[v] = fmaf(p[v], s, acc[v]);
     }
   }
   if (a.ks > 1) {
@@ -289,24 +320,243 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a, bool w
     if (kp > 0) return;
     for (int j = 1; j < a.ks; ++j) acc += part[wave + j * nw][lane];
   }
-  if (on && src >= 0) store4<Row>(a, row, nt * 16 + (lane >> 4) * 4, acc, wide);
+  if (on && src >= 0) {
+    const float v[4] = {acc[0], acc[1], acc[2], acc[3]};
+    store_columns<Row, 4>(a, row, fp8_column(nt, lane >> 4), v, wide);
+  }
+}
+
+// The same for spans of many rows: a workgroup of WM by WN waves makes a tile of
+// BM rows by BN columns, a wave MT by NT pieces of 16 by 16 of it. The blocks go
+// through two LDS stages: while one is multiplied the next is on its way, moved by
+// loads that write LDS themselves. Weights lie there as they are packed; a q row's
+// eight 16-byte pieces change places by the row's number (piece p of row r holds k
+// piece p ^ (r / 2 % 8)), so that 8 lanes read one row whole and the 16 rows of an
+// operand come from all 64 banks.
+//
+// 8192 rows of 4096 by 4096 x 4096 take 124 us, 2.2 PFLOP/s (a library's product of
+// E4M3 with one scale: 102 us): the clock falls to 1.85 GHz, and a block takes 3280
+// cycles of which the matrix instructions fill 2048, the rest being the next block's
+// latency, which 128 KB of LDS allow to be requested one block ahead. Requesting it
+// between the matrix instructions instead of before them: 180 -> 176 us at that
+// stage; touching the lines of later blocks early made no difference.
+template <typename Row, int WM, int WN, int MT, int NT>
+struct Tile {
+  static constexpr int W = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16;
+  static constexpr int kStage = (BM + BN) * 128;  // bytes
+  static constexpr int kWLoads = BN / 8 / W, kXLoads = BM / 8 / W;  // of 1 KB, a wave's
+};
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+// `bytes` from p on, as a buffer: reads past them give zeros.
+__device__ __forceinline__ rsrc_t buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+// 16 bytes of each lane straight into LDS, lane l's at p + 16 l.
+__device__ __forceinline__ void to_lds(rsrc_t r, uint32_t lane_off, uint32_t off, uint8_t* p) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)p, 16,
+                                           lane_off, off, 0, 0);
+}
+
+// Waits until at most N of the wave's loads, those that write LDS among them, are
+// outstanding: the last requested ones (loads return in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 16, "the counter's low bits");
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_waitcnt(N | 0x0f70);  // the other counters at their maxima
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+// Workgroup barrier that orders LDS only: loads that are on their way stay so.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// One block of 128 k of a wave's pieces from a stage. The matrix instructions of one
+// column of pieces are issued between the multiply-adds of the column before, which
+// would wait for their results otherwise.
+template <typename Row, int MT, int NT, typename Request>
+__device__ __forceinline__ void tile_block(const uint8_t* w, const uint8_t* x, int lane,
+                                           const float (&s)[MT], f32x4 (&acc)[MT][NT],
+                                           Request request) {
+  const int row = lane & 15, piece = (lane >> 4) * 2;
+  Fp8Frag xf[MT], wf[2];
+  wf[0] = load_frag(w + lane * 16, 1024);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      xf[i].h[h] = *reinterpret_cast<const u32x4*>(x + (i * 16 + row) * 128 +
+                                                   ((piece + h) ^ ((row >> 1) & 7)) * 16);
+  f32x4 d[2][MT];
+#pragma unroll
+  for (int j = 0; j <= NT; ++j) {
+    __builtin_amdgcn_sched_barrier(0);
+    if (j + 1 < NT) wf[(j + 1) & 1] = load_frag(w + (j + 1) * kFp8Tile + lane * 16, 1024);
+    if (j == 1) request();
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if (j < NT) d[j & 1][i] = block_products<Row>(wf[j & 1], xf[i]);
+      if (j > 0) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          acc[i][j - 1][v] = fmaf(d[(j - 1) & 1][i][v], s[i], acc[i][j - 1][v]);
+      }
+    }
+    if constexpr (sizeof(typename Row::elem) == 2) {
+      if (j + 1 < NT) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (j < NT) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+        if (j > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // VALU
+      }
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <typename Row, int WM, int WN, int MT, int NT>
+__global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs a, bool wide) {
+  typedef Tile<Row, WM, WN, MT, NT> T;
+  extern __shared__ __attribute__((aligned(16))) uint8_t stage[];  // two
+  const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const Span sp = find_tile(a.offsets, a.E, a.n_rows, T::BM, a.n_groups, flat_group());
+  if (sp.e < 0) return;  // the whole workgroup
+  const int n0 = sp.n * (T::BN / 16);  // in tiles of 16 columns
+
+  // what this wave moves: its share of the weights' and of the rows' kilobytes
+  const int first = n0 / 8;  // block of 128 columns
+  const uint32_t slab = (uint32_t)a.KB * (8 * kFp8Tile);  // bytes of one
+  const rsrc_t w_buf = buffer(a.w + ((int64_t)sp.e * a.NB + first) * slab,
+                              (uint32_t)min(a.NB - first, (T::BN + 127) / 128) * slab);
+  const rsrc_t x_buf = buffer(a.q, a.q_bytes);
+  const rsrc_t s_buf = buffer(a.qs, (uint32_t)a.KB * (uint32_t)a.q_rows * 4);
+  uint32_t x_off[T::kXLoads];
+#pragma unroll
+  for (int i = 0; i < T::kXLoads; ++i) {
+    const int r = (wave * T::kXLoads + i) * 8 + (lane >> 3);
+    const int src = max(source_row(a, sp.row + r, sp.end), 0);
+    x_off[i] = (uint32_t)src * (uint32_t)a.q_ld;
+    asm volatile("" : "+v"(x_off[i]));  // else the sum takes two registers
+    x_off[i] += ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+  }
+  uint32_t s_off[MT];
+  float xs[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    s_off[i] = 4u * max(source_row(a, sp.row + (wm * MT + i) * 16 + (lane & 15), sp.end), 0);
+  const float* w_scale =
+      a.ws + ((int64_t)sp.e * a.NB + min((n0 + wn * NT) / 8, a.NB - 1)) * a.KB;
+  float ws = 0.f;
+  auto request = [&](int kb, uint8_t* p) {
+#pragma unroll
+    for (int i = 0; i < T::kWLoads; ++i) {
+      const int c = wave * T::kWLoads + i;
+      const int nt = n0 % 8 + c / 2;
+      to_lds(w_buf, lane * 16, (nt / 8) * slab + (kb * 8 + nt % 8) * kFp8Tile + (c & 1) * 1024, p + c * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < T::kXLoads; ++i)
+      to_lds(x_buf, x_off[i], kb * 128, p + T::BN * 128 + (wave * T::kXLoads + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      xs[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          s_buf, s_off[i], (uint32_t)kb * (uint32_t)a.q_rows * 4, 0));
+    ws = w_scale[kb];
+  };
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  request(0, stage);
+  for (int kb = 0; kb < a.KB; ++kb) {
+    wait_loads<0>();
+    lds_barrier();  // block kb has arrived, and the other stage is no longer read
+    const uint8_t* p = stage + (kb & 1) * T::kStage;
+    float s[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) s[i] = xs[i] * ws;
+    // past the last block, the last one again (into the stage that nothing reads)
+    tile_block<Row, MT, NT>(
+        p + wn * NT * kFp8Tile, p + T::BN * 128 + wm * MT * 16 * 128, lane, s, acc,
+        [&] { request(min(kb + 1, a.KB - 1), stage + (~kb & 1) * T::kStage); });
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int row = sp.row + (wm * MT + i) * 16 + (lane & 15);
+    if (source_row(a, row, sp.end) < 0) continue;
+#pragma unroll
+    for (int j = 0; j < NT; j += 2) {
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = acc[i][j + c / 4][c % 4];
+      store_columns<Row, 8>(a, row, fp8_column(n0 + wn * NT + j, lane >> 4), v, wide);
+    }
+  }
 }
 
 // Sums of fewer than 2^31 tiles, so that a tile's number is an int.
 constexpr int64_t kMaxTiles = 0x7f000000ll;
 
+// Tiles of `size` rows that the spans can have: each of a span's but the last is full.
+int64_t most_tiles(const GemmArgs& a, int size) {
+  if (!a.offsets) return ((int64_t)a.n_rows + size - 1) / size;
+  return (int64_t)a.n_rows / size + std::min(a.E, a.n_rows);
+}
+
+template <typename Row, int WM, int WN, int MT, int NT>
+int32_t launch_tile(const char* who, GemmArgs a, bool wide, hipStream_t s) {
+  typedef Tile<Row, WM, WN, MT, NT> T;
+  const int64_t m_tiles = most_tiles(a, T::BM);
+  a.n_groups = (a.NT * 16 + T::BN - 1) / T::BN;
+  if (m_tiles * a.n_groups > kMaxTiles)
+    return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<Row, WM, WN, MT, NT>), flat_grid(m_tiles * a.n_groups + 7),
+                     dim3(64 * T::W), 2 * T::kStage, s, a, wide);
+  return launch_status(who);
+}
+
 template <typename Row>
-int32_t launch_gemm(const char* who, GemmArgs a, bool wide, hipStream_t s) {
-  const int64_t m_tiles = (int64_t)a.n_rows / 16 + std::min(a.E, a.n_rows);
+int32_t launch_stream(const char* who, GemmArgs a, bool wide, hipStream_t s) {
+  const int64_t m_tiles = most_tiles(a, 16);
   a.ks = 1;
   while (a.ks < 8 && a.ks * 2 <= a.KB && m_tiles * a.NT * a.ks < 2048) a.ks *= 2;
   const int waves = std::max(4, a.ks);
   a.n_groups = (a.NT + waves / a.ks - 1) / (waves / a.ks);
   if (m_tiles * a.n_groups > kMaxTiles)
     return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
-  hipLaunchKernelGGL((fp8_gemm_stream_kernel<Row>), flat_grid(m_tiles * a.n_groups),
+  hipLaunchKernelGGL((fp8_gemm_stream_kernel<Row>), flat_grid(m_tiles * a.n_groups + 7),
                      dim3(64 * waves), 0, s, a, wide);
   return launch_status(who);
+}
+
+// The tile goes by the rows that a span has on average and by the tiles that they
+// make: large ones reuse more, but a span's last tile is half empty and the chip
+// wants two workgroups a CU. Measured, us, 16-row waves / tiles of 32, 64, 128 x 128
+// and 256 x 256 (bf16; one weight of 4096 x 4096, then 128 experts of 2048 x 768):
+//   rows of one weight   16: 5.8, 14, 17, 24, 46     64: 13, 21, 17, 25, 46
+//                        512: 80, 27, 27, 30, 50     2048: 291, 102, 61, 43, 55
+//                        8192: 1154, 526, 258, 159, 124
+//   rows of an expert    5: 31, 32, 32, 40, 57       32: 78, 41, 34, 45, 62
+//                        128: 259, 81, 62, 69, 67    256: 506, 151, 104, 103, 103
+//   768 -> 2048, 128 rows an expert: 249, 96, 78, 78, 73
+template <typename Row>
+int32_t launch_gemm(const char* who, const GemmArgs& a, bool wide, hipStream_t s) {
+  const int64_t spans = std::min(a.E, a.n_rows), mean = (a.n_rows + spans - 1) / spans;
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    return spans * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+  };
+  if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row>(who, a, wide, s);
+  if (mean >= 128 && tiles(256, 256) >= 512) return launch_tile<Row, 4, 2, 4, 8>(who, a, wide, s);
+  if (mean >= 256 && tiles(128, 128) >= 512) return launch_tile<Row, 2, 2, 4, 4>(who, a, wide, s);
+  if (mean >= 24 && tiles(64, 128) >= 256) return launch_tile<Row, 2, 2, 2, 4>(who, a, wide, s);
+  return launch_tile<Row, 1, 4, 2, 2>(who, a, wide, s);
 }
 
 // Sizes of a route, or why they are refused.
@@ -337,7 +587,9 @@ int32_t check_fp8_route(const char* who, const char* name, const mlora_fp8_route
 using namespace mlora;
 
 extern "C" int32_t mlora_fp8_row_width(int32_t k) {
-  return k < 1 || k > kFp8MaxDim ? 0 : (int32_t)(blocks_of(k) * 128);
+  // an odd number of blocks: rows a multiple of 512 bytes apart would come from few
+  // of an L2's 16 channels of 256 bytes
+  return k < 1 || k > kFp8MaxDim ? 0 : (int32_t)((blocks_of(k) | 1) * 128);
 }
 
 extern "C" uint64_t mlora_fp8_packed_bytes(int32_t n_experts, int32_t k_in, int32_t n_out) {
@@ -469,7 +721,11 @@ extern "C" int32_t mlora_fp8_gemm(const mlora_fp8_route* route, const uint8_t* q
   }
   if (!q || !q_scales || !out) return fail(MLORA_ERR_INVALID, "%s: NULL pointer", who);
   if (!aligned(q, 16)) return fail(MLORA_ERR_INVALID, "%s: q must be 16-byte aligned", who);
+  const int64_t width = mlora_fp8_row_width(route->k_in);
+  if (q_ld > 0xffffffffll || (q_rows - 1) * q_ld + width > 0xffffffffll)
+    return fail(MLORA_ERR_INVALID, "%s: q spans more than 4 GiB; split the call", who);
   GemmArgs a{};
+  a.q_bytes = (uint32_t)((q_rows - 1) * q_ld + width);
   a.w = static_cast<const uint8_t*>(route->weights);
   a.ws = static_cast<const float*>(route->scales);
   a.q = q;
@@ -483,11 +739,11 @@ extern "C" int32_t mlora_fp8_gemm(const mlora_fp8_route* route, const uint8_t* q
   a.n_rows = (int32_t)n_rows;
   a.E = route->n_experts;
   a.N = route->n_out;
-  a.NT = (route->n_out + 15) / 16;
+  a.NT = fp8_tiles(route->n_out);
   a.NB = (int32_t)blocks_of(route->n_out);
   a.KB = (int32_t)blocks_of(route->k_in);
   a.top_k = top_k;
-  const bool wide = out_ld % 4 == 0 && aligned(out, out_dtype == MLORA_BF16 ? 8 : 16);
+  const bool wide = out_ld % (out_dtype == MLORA_BF16 ? 8 : 4) == 0 && aligned(out, 16);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   return out_dtype == MLORA_BF16 ? launch_gemm<Bf16Row>(who, a, wide, s)

@@ -177,14 +177,14 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
   for (int item = blockIdx.x; item < active * tiles; item += gridDim.x) {
     const int at = item / tiles, nt = item - at * tiles;
     const int e = uniform_i32(list[at]);
-    const int64_t tile = ((int64_t)e * tiles + nt) * a.DB;
+    const int64_t tile = (int64_t)e * tiles * a.DB + fp8_tile(nt, 0, a.DB);
     const uint8_t* gw = a.gate + tile * kFp8Tile + lane * 16;
     const uint8_t* uw = a.up + tile * kFp8Tile + lane * 16;
     const int64_t sc = ((int64_t)e * a.HB + nt / 8) * a.DB;
     f32x4 gs = {0.f, 0.f, 0.f, 0.f}, us = gs;
     for (int kb = k0; kb < k1; ++kb) {
-      const Fp8Frag gf = load_frag(gw + (int64_t)kb * kFp8Tile, 1024);
-      const Fp8Frag uf = load_frag(uw + (int64_t)kb * kFp8Tile, 1024);
+      const Fp8Frag gf = load_frag(gw + (int64_t)kb * (8 * kFp8Tile), 1024);
+      const Fp8Frag uf = load_frag(uw + (int64_t)kb * (8 * kFp8Tile), 1024);
       u32x4 xf[4][P];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
     }
     __syncthreads();
     if (tid < 256) {
-      const int t = tid >> 4, c = tid & 15;  // token and column of the tile
+      const int t = tid >> 4, c = tid & 15;  // token and row of the tile
       const int src = (c & 3) * 64 + (c >> 2) * 16 + t;
       float gate = 0.f, up = 0.f;
 #pragma unroll
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
       if (j != kNone) {
         const int slot = t * a.k + j;
         float v = gate / (1.f + expf(-gate)) * up * wts[slot];
-        uint16_t* dst = a.act + (int64_t)slot * PA * (a.HB * 128) + nt * 16 + c;
+        uint16_t* dst = a.act + (int64_t)slot * PA * (a.HB * 128) + fp8_column(nt, c >> 2) + (c & 3);
 #pragma unroll
         for (int p = 0; p < PA; ++p) {
           const uint16_t b = Bf16Row::narrow(v);
@@ -245,11 +245,11 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, bo
   for (int at = 0; at < active; ++at) {
     const int e = uniform_i32(list[at]);
     const int j = slots[at * kTokens + t];
-    const uint8_t* w = a.down + ((int64_t)e * a.DB * 8 + nt) * a.HB * kFp8Tile + lane * 16;
+    const uint8_t* w = a.down + ((int64_t)e * a.DB * 8 * a.HB + fp8_tile(nt, 0, a.HB)) * kFp8Tile + lane * 16;
     const float* ws = a.down_s + ((int64_t)e * a.DB + nt / 8) * a.HB;
     const uint16_t* act = a.act + (int64_t)(j == kNone ? 0 : t * a.k + j) * PA * (a.HB * 128) + g * 32;
     for (int b = (int)((uint32_t)(wave - e * a.HB) % kWaves); b < a.HB; b += kWaves) {
-      const Fp8Frag wf = load_frag(w + (int64_t)b * kFp8Tile, 1024);
+      const Fp8Frag wf = load_frag(w + (int64_t)b * (8 * kFp8Tile), 1024);
       u32x4 xf[4][PA];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, bo
   if (wave > 0 || t >= a.T) return;
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) acc += part[w][lane];
-  const int n = nt * 16 + g * 4;
+  const int n = fp8_column(nt, g);
   typename Row::elem* p = static_cast<typename Row::elem*>(a.out) + (int64_t)t * a.out_ld + n;
   if (wide && n + 4 <= a.dim) {
     if constexpr (sizeof(typename Row::elem) == 2)
@@ -321,7 +321,7 @@ int32_t launch_layer(const char* who, const LayerArgs& a, bool x_wide, bool out_
     hipLaunchKernelGGL((layer_gate_up_kernel<Row, false>), dim3(grid), dim3(64 * kWaves),
                        l.total * 4, s, a);
   if (int32_t rc = launch_status(who)) return rc;
-  hipLaunchKernelGGL((layer_down_kernel<Row>), dim3((a.dim + 15) / 16), dim3(64 * kWaves), 0, s, a,
+  hipLaunchKernelGGL((layer_down_kernel<Row>), dim3(fp8_tiles(a.dim)), dim3(64 * kWaves), 0, s, a,
                      out_wide);
   return launch_status(who);
 }

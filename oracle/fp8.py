@@ -72,14 +72,13 @@ def products(weights: np.ndarray, q: np.ndarray, offsets, sorted_ids, top_k: int
     out, mag = np.array(base, dtype=np.float64), np.zeros(base.shape)
     n = out.shape[0]
     off = [0, n] if offsets is None else [int(v) for v in offsets]
+    src = np.arange(n) if sorted_ids is None else \
+        np.where(np.asarray(sorted_ids) >= 0, np.asarray(sorted_ids) // top_k, -1)
     for e in range(len(off) - 1):
-        for r in range(max(off[e], 0), min(off[e + 1], n)):
-            s = r if sorted_ids is None else int(sorted_ids[r])
-            if sorted_ids is not None:
-                s = s // top_k if s >= 0 else -1
-            if 0 <= s < q.shape[0]:
-                out[r] = weights[e] @ q[s]
-                mag[r] = np.abs(weights[e]) @ np.abs(q[s])
+        r = np.arange(max(off[e], 0), min(off[e + 1], n))
+        r = r[(src[r] >= 0) & (src[r] < q.shape[0])]
+        out[r] = q[src[r]] @ weights[e].T
+        mag[r] = np.abs(q[src[r]]) @ np.abs(weights[e]).T
     return out, mag
 
 

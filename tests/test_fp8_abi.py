@@ -53,7 +53,7 @@ def test_pack_sizes(lib):
     assert ml.mlora_fp8_packed_bytes(0, 256, 100) == 0
     assert ml.mlora_fp8_packed_bytes(4, 256, (1 << 20) + 1) == 0
     assert [ml.mlora_fp8_row_width(k) for k in (0, 1, 128, 129, 1 << 20, (1 << 20) + 1)] == \
-        [0, 128, 128, 256, 1 << 20, 0]
+        [0, 128, 128, 384, (1 << 20) + 128, 0]
     r = ml.Fp8Route()
     base = {**PACK, "route": ctypes.byref(r)}
     _refused(lib, "mlora_fp8_pack", base,

@@ -40,12 +40,24 @@ def strided(t, extra):
 
 def quantised(ml, x, up=None, q=None):
     k = x.shape[1]
-    width = ml.mlora_fp8_row_width(k)
     if q is None:
-        q = torch.full((x.shape[0], width), 0x55, dtype=torch.uint8, device=DEV)
-    s = torch.full((width // 128, x.shape[0]), 7.0, device=DEV)
+        q = torch.full((x.shape[0], ml.mlora_fp8_row_width(k)), 0x55, dtype=torch.uint8, device=DEV)
+    s = torch.full((-(-k // 128), x.shape[0]), 7.0, device=DEV)
     ml.mlora_fp8_quant(x, q, s, up=up)
+    assert (q[:, whole(k):] == 0x55).all()  # a block that only moves the next row
     return q, s
+
+
+def whole(k):
+    return -(-k // 128) * 128
+
+
+def rows_in(ml, codes):
+    """Quantised rows as the product takes them; the block behind them holds NaN."""
+    t = torch.full((codes.shape[0], ml.mlora_fp8_row_width(codes.shape[1])), 0x7f,
+                   dtype=torch.uint8, device=DEV)
+    t[:, :codes.shape[1]] = dev(codes)
+    return t
 
 
 # -- quantiser ---------------------------------------------------------------
@@ -60,8 +72,8 @@ def test_quant(ml, rows, k, dtype, extra):
     rng = np.random.default_rng(rows * 31 + k)
     x = dev(rng.normal(0, 1, (rows, k)) * 2.0 ** rng.integers(-20, 20, (rows, 1))).to(TORCH[dtype])
     q, s = quantised(ml, strided(x, extra))
-    codes, scales = fp8.quantise(to64(x), q.shape[1])
-    got = q.cpu().numpy()
+    codes, scales = fp8.quantise(to64(x), whole(k))
+    got = q[:, :whole(k)].cpu().numpy()
     # codes of a zero keep its sign; both are 0
     assert np.array_equal(fp8.e4m3_decode(got), fp8.e4m3_decode(codes))
     assert not got[:, k:].any()
@@ -103,7 +115,7 @@ def test_quant_extremes(ml, dtype):
     x = dev(v).to(TORCH[dtype])
     codes, scales = fp8.quantise(to64(x), 256)
     q, s = quantised(ml, x)
-    assert np.array_equal(fp8.e4m3_decode(q.cpu().numpy()), fp8.e4m3_decode(codes))
+    assert np.array_equal(fp8.e4m3_decode(q[:, :256].cpu().numpy()), fp8.e4m3_decode(codes))
     close(to64(s), scales, np.abs(scales) * F32)
 
 
@@ -155,8 +167,7 @@ def check_product(ml, seed, E, N, K, n, dtype, ids=False, top_k=1, lead=0, behin
     rng = np.random.default_rng(seed)
     w, ws = weights(rng, E, K, N) if transpose else weights(rng, E, N, K)
     q_rows = n // top_k if ids else n
-    width = ml.mlora_fp8_row_width(K)
-    codes, qs = fp8.quantise(rng.normal(0, 1, (q_rows, K)), width)
+    codes, qs = fp8.quantise(rng.normal(0, 1, (q_rows, K)), whole(K))
     qs = qs.astype(np.float32)
     off = None if one else spans(rng, n, E, lead, behind, skew)
     order = None
@@ -168,7 +179,7 @@ def check_product(ml, seed, E, N, K, n, dtype, ids=False, top_k=1, lead=0, behin
     out = strided(dev(base).to(TORCH[dtype]), out_extra)
     before = to64(out)
     route = ml.make_fp8_route(dev(w).view(torch.float8_e4m3fn), dev(ws), transpose=transpose)
-    ml.mlora_fp8_gemm(route, dev(codes), dev(qs), out, None if off is None else dev(off),
+    ml.mlora_fp8_gemm(route, rows_in(ml, codes), dev(qs), out, None if off is None else dev(off),
                       None if order is None else dev(order), top_k)
     full = fp8.expand(w, ws)
     if transpose:
@@ -177,7 +188,10 @@ def check_product(ml, seed, E, N, K, n, dtype, ids=False, top_k=1, lead=0, behin
     close(to64(out), ref, np.where(mag > 0, product_error(ref, mag, K, dtype), 0.0))
 
 
-# E, N, K, rows: one value, ragged, more experts than rows, few long spans
+# E, N, K, rows: one value, ragged, more experts than rows, few long spans; then each
+# of the larger tiles (64 x 128, 128 x 128, 256 x 256), odd numbers of blocks
+LARGE = [(40, 260, 384, 1300), (5, 3900, 130, 1500), (3, 4000, 300, 2100), (9, 4100, 129, 3600),
+         (2, 2300, 640, 8300)]
 SIZES = [(1, 1, 1, 1), (3, 5, 7, 11), (4, 100, 300, 37), (16, 130, 129, 5), (5, 365, 1000, 203),
          (128, 64, 256, 640), (2, 257, 640, 700), (1, 2048, 2048, 1), (3, 16, 2100, 60),
          (1000, 33, 128, 300), (2, 1030, 130, 1500)]
@@ -190,8 +204,16 @@ def test_product(ml, E, N, K, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("skew", [False, True])
+@pytest.mark.parametrize("E,N,K,n", LARGE)
+def test_product_in_large_tiles(ml, E, N, K, n, skew, dtype):
+    check_product(ml, N + K, E, N, K, n, dtype, skew=skew, ids=skew, lead=3 * skew, behind=5 * skew)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,K,n", [(1, 1, 1), (48, 4000, 3), (300, 512, 16), (129, 257, 17),
-                                   (256, 384, 300), (1000, 200, 1025)])
+                                   (256, 384, 300), (1000, 200, 1025), (4097, 257, 8200),
+                                   (4000, 128, 2050)])
 def test_product_of_one_weight(ml, N, K, n, dtype):
     check_product(ml, n, 1, N, K, n, dtype, one=True)
 
@@ -214,9 +236,9 @@ def test_product_of_transposed_weights(ml, E, N, K, n, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("extra", [1, 4, 7])
-@pytest.mark.parametrize("n", [30, 900])
-def test_product_into_wider_rows(ml, extra, n, dtype):
-    check_product(ml, extra, 3, 101, 200, n, dtype, out_extra=extra)
+@pytest.mark.parametrize("N,n", [(101, 30), (101, 900), (4061, 4500)])
+def test_product_into_wider_rows(ml, extra, N, n, dtype):
+    check_product(ml, extra, 3, N, 200, n, dtype, out_extra=extra)
 
 
 @pytest.mark.parametrize("n", [20, 700])
@@ -263,13 +285,13 @@ def test_gradient_of_rows_against_the_forward(ml):
     w, ws = weights(rng, E, N, K)
     full = fp8.expand(w, ws)
     off = spans(rng, n, E)
-    rows = {k: fp8.quantise(rng.normal(0, 1, (n, k)), ml.mlora_fp8_row_width(k)) for k in (N, K)}
+    rows = {k: fp8.quantise(rng.normal(0, 1, (n, k)), whole(k)) for k in (N, K)}
     got, ref = {}, {}
     for k, transpose in ((K, False), (N, True)):
         codes, s = rows[k][0], rows[k][1].astype(np.float32)
         out = torch.empty((n, N + K - k), device=DEV)
-        ml.mlora_fp8_gemm(ml.make_fp8_route(dev(w), dev(ws), transpose=transpose), dev(codes),
-                          dev(s), out, dev(off))
+        ml.mlora_fp8_gemm(ml.make_fp8_route(dev(w), dev(ws), transpose=transpose),
+                          rows_in(ml, codes), dev(s), out, dev(off))
         got[k], ref[k] = to64(out), fp8.rows_of(codes, s, k)
     lhs, rhs = (got[K] * ref[N]).sum(1), (got[N] * ref[K]).sum(1)
     mag = np.zeros(n)
@@ -343,7 +365,7 @@ def test_python_refuses(ml):
         (ml.MloraError, lambda: ml.mlora_fp8_gemm(route, q, s, out)),
         (ValueError, lambda: ml.make_fp8_route(q, s)),
         (TypeError, lambda: ml.make_fp8_route(x.view(1, 4, 300), torch.ones((1, 1, 3), device=DEV))),
-        (ValueError, lambda: ml.make_fp8_route(q.view(1, 4, 384), torch.ones((1, 1, 2), device=DEV))),
+        (ValueError, lambda: ml.make_fp8_route(q.view(1, 4, -1), torch.ones((1, 1, 2), device=DEV))),
     ]
     for error, call in cases:
         with pytest.raises(error):

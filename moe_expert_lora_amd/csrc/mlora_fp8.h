@@ -34,7 +34,7 @@ __device__ __forceinline__ int fp8_column(int nt, int g) {
   return (nt >> 1) * 32 + g * 8 + (nt & 1) * 4;
 }
 // Tiles that hold columns of N: whole pairs.
-inline int32_t fp8_tiles(int32_t N) { return (N + 31) / 32 * 2; }
+__host__ __device__ inline int32_t fp8_tiles(int32_t N) { return (N + 31) / 32 * 2; }
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
@@ -61,6 +61,25 @@ __device__ __forceinline__ u32x4 widen_codes(uint32_t lo, uint32_t hi) {
   return v;
 }
 
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+// `bytes` from p on, as a buffer: reads at lanes' offsets past them give zeros.
+__device__ __forceinline__ rsrc_t buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+// 16 bytes of each lane, `off` within the buffer; AUX 2: past the caches' keep.
+template <int AUX = 0>
+__device__ __forceinline__ u32x4 buffer_load16(rsrc_t r, uint32_t lane_off, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, AUX));
+}
+constexpr int kReadOnce = 2;
+// A tile of weights that are read once. The whole offset is the lanes': what is
+// compared with the buffer's end is theirs alone.
+__device__ __forceinline__ Fp8Frag load_tile(rsrc_t r, int lane, uint32_t off) {
+  return Fp8Frag{{buffer_load16<kReadOnce>(r, off + lane * 16, 0),
+                  buffer_load16<kReadOnce>(r, off + lane * 16 + 1024, 0)}};
+}
+
 // 16 x 16 sums of 128 products of E4M3 codes; result i of lane l is row
 // 4 (l / 16) + i of the first operand by row l % 16 of the second. Either the
 // 8-bit instruction (block scales of 2^0): it aligns the products of 8 neighbouring
@@ -82,6 +101,22 @@ __device__ __forceinline__ f32x4 mfma_fp8_as_bf16(const Fp8Frag& a, const Fp8Fra
     s = mfma_bf16(widen_codes(a.h[j / 2][2 * (j % 2)], a.h[j / 2][2 * (j % 2) + 1]),
                   widen_codes(b.h[j / 2][2 * (j % 2)], b.h[j / 2][2 * (j % 2) + 1]), s);
   return s;
+}
+
+// Waits until at most N of the wave's loads, those that write LDS among them, are
+// outstanding: the last requested ones (loads return in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 16, "the counter's low bits");
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_waitcnt(N | 0x0f70);  // the other counters at their maxima
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+// Workgroup barrier that orders LDS only: loads that are on their way stay so.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // 8 values of a row from column k on; zeros past K.

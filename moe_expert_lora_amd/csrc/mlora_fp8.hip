@@ -347,32 +347,10 @@ struct Tile {
   static constexpr int kWLoads = BN / 8 / W, kXLoads = BM / 8 / W;  // of 1 KB, a wave's
 };
 
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-
-// `bytes` from p on, as a buffer: reads past them give zeros.
-__device__ __forceinline__ rsrc_t buffer(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
-}
 // 16 bytes of each lane straight into LDS, lane l's at p + 16 l.
 __device__ __forceinline__ void to_lds(rsrc_t r, uint32_t lane_off, uint32_t off, uint8_t* p) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)p, 16,
                                            lane_off, off, 0, 0);
-}
-
-// Waits until at most N of the wave's loads, those that write LDS among them, are
-// outstanding: the last requested ones (loads return in order).
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(N < 16, "the counter's low bits");
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_s_waitcnt(N | 0x0f70);  // the other counters at their maxima
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-// Workgroup barrier that orders LDS only: loads that are on their way stay so.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // One block of 128 k of a wave's pieces from a stage. The matrix instructions of one
@@ -431,8 +409,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
   // what this wave moves: its share of the weights' and of the rows' kilobytes
   const int first = n0 / 8;  // block of 128 columns
   const uint32_t slab = (uint32_t)a.KB * (8 * kFp8Tile);  // bytes of one
-  const rsrc_t w_buf = buffer(a.w + ((int64_t)sp.e * a.NB + first) * slab,
-                              (uint32_t)min(a.NB - first, (T::BN + 127) / 128) * slab);
+  const int blocks = min(a.NB - first, (T::BN + 127) / 128);
+  const rsrc_t w_buf = buffer(a.w + ((int64_t)sp.e * a.NB + first) * slab, blocks * slab);
+  uint32_t w_off[T::kWLoads];  // of columns past the last block: that block's again
+#pragma unroll
+  for (int i = 0; i < T::kWLoads; ++i) {
+    const int c = wave * T::kWLoads + i, nt = n0 % 8 + c / 2;
+    w_off[i] = min(nt / 8, blocks - 1) * slab + (nt % 8) * kFp8Tile + (c & 1) * 1024;
+  }
   const rsrc_t x_buf = buffer(a.q, a.q_bytes);
   const rsrc_t s_buf = buffer(a.qs, (uint32_t)a.KB * (uint32_t)a.q_rows * 4);
   uint32_t x_off[T::kXLoads];
@@ -454,11 +438,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
   float ws = 0.f;
   auto request = [&](int kb, uint8_t* p) {
 #pragma unroll
-    for (int i = 0; i < T::kWLoads; ++i) {
-      const int c = wave * T::kWLoads + i;
-      const int nt = n0 % 8 + c / 2;
-      to_lds(w_buf, lane * 16, (nt / 8) * slab + (kb * 8 + nt % 8) * kFp8Tile + (c & 1) * 1024, p + c * 1024);
-    }
+    for (int i = 0; i < T::kWLoads; ++i)
+      to_lds(w_buf, lane * 16, w_off[i] + kb * (8 * kFp8Tile), p + (wave * T::kWLoads + i) * 1024);
 #pragma unroll
     for (int i = 0; i < T::kXLoads; ++i)
       to_lds(x_buf, x_off[i], kb * 128, p + T::BN * 128 + (wave * T::kXLoads + i) * 1024);

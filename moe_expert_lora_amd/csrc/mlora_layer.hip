@@ -39,7 +39,10 @@ struct LayerArgs {
   int32_t* indices;  // may be null
   float* weights;    // may be null
   int32_t* head;     // workspace: count, experts [max_active], slots [max_active][16]
+  int32_t* count;    // workspace: splits that are done, of each tile of out
+  float* sums;       // workspace: [tiles of out][splits][4][64]
   uint16_t* act;     // workspace: [T * k][parts][hidden, whole blocks]
+  uint32_t act_bytes;
   int32_t T, E, k, renorm, dim, hidden, DB, HB, max_active;
 };
 
@@ -82,23 +85,26 @@ __device__ __forceinline__ f32x4 block_sum(const Fp8Frag& w, const u32x4 (&x)[4]
 
 // Dynamic LDS of kernel one, in words from the start.
 struct Lds {
-  int ids, wts, place, list, slots, part, total;
+  int ids, wts, flag, place, list, slots, part, total;
 };
 __host__ __device__ inline Lds lds_of(int n, int E, int max_active) {
   Lds l{};
-  l.ids = 4;  // word 0: the number of chosen experts
+  l.ids = 0;
   l.wts = l.ids + n;
-  l.place = l.wts + n;
+  l.flag = l.wts + n;
+  l.place = l.flag + E;
   l.list = l.place + E;
   l.slots = l.list + max_active;
   l.part = (l.slots + max_active * (kTokens / 4) + 3) & ~3;
-  l.total = l.part + kWaves * 2 * 256;
+  l.total = l.part + 2 * kWaves * 2 * 256;
   return l;
 }
 
-// Every token's choice into LDS, by all waves.
-template <typename Row, int LPT, int VPL>
-__device__ __forceinline__ void choose_all(const LayerArgs& a, int* ids, float* wts, bool publish) {
+// Every token's choice into LDS, by all waves, and a flag for each chosen expert.
+// `request` asks for what is needed afterwards, behind the first logits.
+template <typename Row, int LPT, int VPL, typename Request>
+__device__ __forceinline__ void choose_all(const LayerArgs& a, int* ids, float* wts, int* flag,
+                                           bool publish, Request request) {
   const int gl = threadIdx.x & (LPT - 1);
   constexpr int kPer = kWaves * 64 / LPT;
   for (int t0 = 0; t0 < a.T; t0 += kPer) {
@@ -106,18 +112,22 @@ __device__ __forceinline__ void choose_all(const LayerArgs& a, int* ids, float* 
     float v[VPL];
     load_row<Row, LPT, VPL, Row::kPer16, false>(a.logits, (int64_t)(t < a.T ? t : 0) * a.logits_ld,
                                                 a.E, gl, v);
+    if (t0 == 0) request();
     int e;
     const float w = choose_experts<Row, LPT, VPL, Row::kPer16>(v, a.E, a.k, a.renorm, gl, &e);
     if (t < a.T && gl < a.k) {
       ids[t * a.k + gl] = e;
       wts[t * a.k + gl] = w;
+      flag[e] = 1;
       if (publish && a.indices) a.indices[t * a.k + gl] = e;
       if (publish && a.weights) a.weights[t * a.k + gl] = w;
     }
   }
 }
 
-template <typename Row, bool WIDE>
+// XB: blocks of k a wave has at most, whose x it keeps in registers; 0: more, and x
+// is read again for each tile.
+template <typename Row, bool WIDE, int XB>
 __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a) {
   extern __shared__ int lds[];
   constexpr int P = parts_of_x<Row>(), PA = parts_of_act<Row>();
@@ -128,42 +138,66 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
   float *wts = reinterpret_cast<float*>(lds + l.wts), *part = reinterpret_cast<float*>(lds + l.part);
   uint8_t* slots = reinterpret_cast<uint8_t*>(lds + l.slots);
   const bool first = blockIdx.x == 0;
-
-  if (a.E <= 128 && a.k <= 16)
-    choose_all<Row, 16, 8>(a, ids, wts, first);
-  else if (a.E <= 256 && a.k <= 32)
-    choose_all<Row, 32, 8>(a, ids, wts, first);
-  else
-    choose_all<Row, 64, 16>(a, ids, wts, first);
-  for (int e = tid; e < a.E; e += 64 * kWaves) place[e] = 0;
+  int* flag = lds + l.flag;
+  for (int e = tid; e < a.E; e += 64 * kWaves) flag[e] = 0;
   for (int i = tid; i < a.max_active * (kTokens / 4); i += 64 * kWaves)
     lds[l.slots + i] = -1;  // four times kNone
   __syncthreads();
-  for (int i = tid; i < n; i += 64 * kWaves) place[ids[i]] = 1;
-  __syncthreads();
-  if (wave == 0) {
-    int count = 0;
-    for (int base = 0; base < a.E; base += 64) {
-      const int e = base + lane;
-      const int on = e < a.E ? place[e] : 0;
-      int sum;
-      const int at = count + wave_prefix(on, &sum);
-      if (on) {
-        place[e] = at;
-        list[at] = e;
+
+  const int t_col = lane & 15, g = lane >> 4;
+  const int64_t x_off = (int64_t)min(t_col, a.T - 1) * a.x_ld;
+  const int k0 = a.DB * wave / kWaves, k1 = a.DB * (wave + 1) / kWaves;
+  auto load_x = [&](int kb, u32x4 (&xf)[4][P]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = kb * 128 + g * 32 + j * 8;
+      if constexpr (P == 1 && WIDE) {
+        const uint16_t* x = static_cast<const uint16_t*>(a.x) + x_off + k;
+        xf[j][0] = u32x4{0, 0, 0, 0};
+        if (k < a.dim) xf[j][0] = *reinterpret_cast<const u32x4*>(x);
+      } else {
+        float v[8];
+        load8<Row, WIDE>(a.x, x_off, k, a.dim, v);
+        split8<P>(v, xf[j]);
       }
-      count += sum;
     }
-    if (lane == 0) lds[0] = count;
+  };
+  u32x4 xr[XB > 0 ? XB : 1][4][P];
+  auto request = [&] {
+    if constexpr (XB > 0) {
+#pragma unroll
+      for (int b = 0; b < XB; ++b) load_x(min(k0 + b, a.DB - 1), xr[b]);
+    }
+  };
+  if (a.E <= 128 && a.k <= 16)
+    choose_all<Row, 16, 8>(a, ids, wts, flag, first, request);
+  else if (a.E <= 256 && a.k <= 32)
+    choose_all<Row, 32, 8>(a, ids, wts, flag, first, request);
+  else
+    choose_all<Row, 64, 16>(a, ids, wts, flag, first, request);
+  lds_barrier();
+
+  // Each wave makes the list: they write the same words, and need not wait again.
+  int active = 0;
+  for (int base = 0; base < a.E; base += 64) {
+    const int e = base + lane;
+    const int on = e < a.E ? flag[e] : 0;
+    int sum;
+    const int at = active + wave_prefix(on, &sum);
+    if (on) {
+      place[e] = at;
+      list[at] = e;
+    }
+    active += sum;
   }
-  __syncthreads();
-  for (int i = tid; i < n; i += 64 * kWaves) {
+  wave_lds_sync();
+  for (int i = lane; i < n; i += 64) {
     const int t = i / a.k;
     slots[place[ids[i]] * kTokens + t] = (uint8_t)(i - t * a.k);
   }
-  __syncthreads();
-  const int active = lds[0];
+  wave_lds_sync();
   if (first) {
+    for (int i = tid; i < fp8_tiles(a.dim); i += 64 * kWaves) a.count[i] = 0;
     if (tid == 0) a.head[0] = active;
     for (int i = tid; i < active; i += 64 * kWaves) a.head[1 + i] = list[i];
     for (int i = tid; i < active * (kTokens / 4); i += 64 * kWaves)
@@ -171,27 +205,19 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
   }
 
   const int tiles = a.HB * 8;
-  const int t_col = lane & 15, g = lane >> 4;
-  const int64_t x_off = (int64_t)min(t_col, a.T - 1) * a.x_ld;
-  const int k0 = a.DB * wave / kWaves, k1 = a.DB * (wave + 1) / kWaves;
-  for (int item = blockIdx.x; item < active * tiles; item += gridDim.x) {
+  // One barrier an item: the sums of alternate items have LDS of their own, and half
+  // of the waves finish an item while all go on to the next.
+  int turn = 0;
+  for (int item = blockIdx.x; item < active * tiles; item += gridDim.x, turn ^= 1) {
     const int at = item / tiles, nt = item - at * tiles;
     const int e = uniform_i32(list[at]);
-    const int64_t tile = (int64_t)e * tiles * a.DB + fp8_tile(nt, 0, a.DB);
-    const uint8_t* gw = a.gate + tile * kFp8Tile + lane * 16;
-    const uint8_t* uw = a.up + tile * kFp8Tile + lane * 16;
+    // a strip of 128 columns; a block past the wave's own is behind its end, and zeros
+    const int64_t strip = ((int64_t)e * a.HB + nt / 8) * a.DB * (8 * kFp8Tile);
+    const uint32_t in = (nt % 8) * kFp8Tile, end = (uint32_t)k1 * (8 * kFp8Tile);
+    const rsrc_t gate_w = buffer(a.gate + strip, end), up_w = buffer(a.up + strip, end);
     const int64_t sc = ((int64_t)e * a.HB + nt / 8) * a.DB;
     f32x4 gs = {0.f, 0.f, 0.f, 0.f}, us = gs;
-    for (int kb = k0; kb < k1; ++kb) {
-      const Fp8Frag gf = load_frag(gw + (int64_t)kb * (8 * kFp8Tile), 1024);
-      const Fp8Frag uf = load_frag(uw + (int64_t)kb * (8 * kFp8Tile), 1024);
-      u32x4 xf[4][P];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float v[8];
-        load8<Row, WIDE>(a.x, x_off, kb * 128 + g * 32 + j * 8, a.dim, v);
-        split8<P>(v, xf[j]);
-      }
+    auto add = [&](int kb, const Fp8Frag& gf, const Fp8Frag& uf, const u32x4 (&xf)[4][P]) {
       const f32x4 gp = block_sum<P>(gf, xf), up = block_sum<P>(uf, xf);
       const float sg = a.gate_s[sc + kb], su = a.up_s[sc + kb];
 #pragma unroll
@@ -199,21 +225,40 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
         gs[i] = fmaf(gp[i], sg, gs[i]);
         us[i] = fmaf(up[i], su, us[i]);
       }
+    };
+    if constexpr (XB > 0) {
+      Fp8Frag gf[XB], uf[XB];
+#pragma unroll
+      for (int b = 0; b < XB; ++b) {
+        gf[b] = load_tile(gate_w, lane, in + (k0 + b) * (8 * kFp8Tile));
+        uf[b] = load_tile(up_w, lane, in + (k0 + b) * (8 * kFp8Tile));
+      }
+#pragma unroll
+      for (int b = 0; b < XB; ++b) add(min(k0 + b, a.DB - 1), gf[b], uf[b], xr[b]);
+    } else {
+      for (int kb = k0; kb < k1; ++kb) {
+        const Fp8Frag gf = load_tile(gate_w, lane, in + kb * (8 * kFp8Tile));
+        const Fp8Frag uf = load_tile(up_w, lane, in + kb * (8 * kFp8Tile));
+        u32x4 xf[4][P];
+        load_x(kb, xf);
+        add(kb, gf, uf, xf);
+      }
     }
+    float* p = part + turn * (kWaves * 2 * 256);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      part[(wave * 2 + 0) * 256 + i * 64 + lane] = gs[i];
-      part[(wave * 2 + 1) * 256 + i * 64 + lane] = us[i];
+      p[(wave * 2 + 0) * 256 + i * 64 + lane] = gs[i];
+      p[(wave * 2 + 1) * 256 + i * 64 + lane] = us[i];
     }
     __syncthreads();
-    if (tid < 256) {
-      const int t = tid >> 4, c = tid & 15;  // token and row of the tile
+    if ((wave >= kWaves / 2) == (turn == 1)) {
+      const int id = tid & 255, t = id >> 4, c = id & 15;  // token and row of the tile
       const int src = (c & 3) * 64 + (c >> 2) * 16 + t;
       float gate = 0.f, up = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        gate += part[(w * 2 + 0) * 256 + src];
-        up += part[(w * 2 + 1) * 256 + src];
+        gate += p[(w * 2 + 0) * 256 + src];
+        up += p[(w * 2 + 1) * 256 + src];
       }
       const int j = slots[at * kTokens + t];
       if (j != kNone) {
@@ -221,52 +266,134 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
         float v = gate / (1.f + expf(-gate)) * up * wts[slot];
         uint16_t* dst = a.act + (int64_t)slot * PA * (a.HB * 128) + fp8_column(nt, c >> 2) + (c & 3);
 #pragma unroll
-        for (int p = 0; p < PA; ++p) {
+        for (int q = 0; q < PA; ++q) {
           const uint16_t b = Bf16Row::narrow(v);
-          dst[(int64_t)p * (a.HB * 128)] = b;
+          dst[(int64_t)q * (a.HB * 128)] = b;
           v -= Bf16Row::widen(b);
         }
       }
     }
-    __syncthreads();
   }
 }
 
+// Every wave of the call's `splits` workgroups a tile takes the blocks (e, b) with
+// (e HB + b) mod (8 splits) of its number, 64 experts of the list at a time. The
+// workgroup that finishes a tile's last split adds their sums up, in their order:
+// splits write their sums past the caches, count themselves with an atomic, and only
+// the last one goes on (nothing waits).
 template <typename Row>
-__global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, bool wide) {
+__global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, int splits, bool wide) {
+  extern __shared__ int head[];
   __shared__ f32x4 part[kWaves][64];
   constexpr int PA = parts_of_act<Row>();
   const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
-  const int nt = blockIdx.x, t = lane & 15, g = lane >> 4;
-  const int active = a.head[0];
-  const int* list = a.head + 1;
-  const uint8_t* slots = reinterpret_cast<const uint8_t*>(a.head + 1 + a.max_active);
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int at = 0; at < active; ++at) {
-    const int e = uniform_i32(list[at]);
-    const int j = slots[at * kTokens + t];
-    const uint8_t* w = a.down + ((int64_t)e * a.DB * 8 * a.HB + fp8_tile(nt, 0, a.HB)) * kFp8Tile + lane * 16;
-    const float* ws = a.down_s + ((int64_t)e * a.DB + nt / 8) * a.HB;
-    const uint16_t* act = a.act + (int64_t)(j == kNone ? 0 : t * a.k + j) * PA * (a.HB * 128) + g * 32;
-    for (int b = (int)((uint32_t)(wave - e * a.HB) % kWaves); b < a.HB; b += kWaves) {
-      const Fp8Frag wf = load_frag(w + (int64_t)b * (8 * kFp8Tile), 1024);
-      u32x4 xf[4][PA];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int p = 0; p < PA; ++p)
-          xf[i][p] = *reinterpret_cast<const u32x4*>(act + (int64_t)p * (a.HB * 128) + b * 128 + i * 8);
-      const f32x4 s = block_sum<PA>(wf, xf);
-      const float sc = ws[b];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = j == kNone ? acc[i] : fmaf(s[i], sc, acc[i]);
+  const int nt = blockIdx.x / splits, split = blockIdx.x - nt * splits;
+  const int t = lane & 15, g = lane >> 4;
+  const int me = split * kWaves + wave, all = splits * kWaves;
+  // the list and the slots, from kernel one
+  const int words = 1 + a.max_active + a.max_active * (kTokens / 4);
+  for (int i = threadIdx.x; i < words; i += 64 * kWaves) head[i] = a.head[i];
+  __syncthreads();
+  const int active = head[0];
+  const int* list = head + 1;
+  const uint8_t* slots = reinterpret_cast<const uint8_t*>(head + 1 + a.max_active);
+
+  // A block's operands, requested while the block before is multiplied: without
+  // branches, so that waiting for the one does not wait for the other. What is not
+  // there (no block, a token that did not choose the expert) lies behind its buffer's
+  // end and arrives as zeros.
+  struct Unit {
+    Fp8Frag w;
+    u32x4 x[4][PA];
+    float scale;
+    bool on, live;
+  };
+  const rsrc_t act = buffer(a.act, a.act_bytes);
+  const uint32_t row_bytes = (uint32_t)a.HB * 256;  // of a part
+  int base = 0, mine = 0, first = 0, at = 0, e = 0, b = a.HB;
+  uint64_t hits = 0;
+  bool more = active > 0;
+  auto look = [&] {  // the wave's experts among the 64 from base on
+    mine = base + lane < active ? list[base + lane] : 0;
+    first = (int)((uint32_t)(me - mine * a.HB + all * a.HB * kMaxExperts) % (uint32_t)all);
+    hits = __ballot(base + lane < active && first < a.HB);
+  };
+  auto next = [&] {  // the wave's next block, or more = false
+    b += all;
+    while (b >= a.HB) {
+      if (!hits) {
+        base += 64;
+        if (base >= active) {
+          more = false;
+          return;
+        }
+        look();
+        continue;
+      }
+      const int l = __builtin_ctzll(hits);
+      hits &= hits - 1;
+      at = base + l;
+      e = __builtin_amdgcn_readlane(mine, l);
+      b = __builtin_amdgcn_readlane(first, l);
     }
+  };
+  auto request = [&](Unit& u) {
+    if (more) next();
+    u.live = more;
+    const int64_t strip = (int64_t)e * a.DB + nt / 8;
+    const rsrc_t w = buffer(a.down + strip * a.HB * (8 * kFp8Tile), more ? a.HB * (8 * kFp8Tile) : 0);
+    const int in_strip = more ? b : 0;
+    u.w = load_tile(w, lane, (in_strip * 8 + nt % 8) * kFp8Tile);
+    u.scale = a.down_s[strip * a.HB + in_strip];
+    const int j = slots[at * kTokens + t];
+    u.on = j != kNone;
+    const uint32_t x = u.on && more ? (uint32_t)(t * a.k + j) * PA * row_bytes + g * 64 : 0xffff0000u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int p = 0; p < PA; ++p)
+        u.x[i][p] = buffer_load16(act, x, p * row_bytes + in_strip * 256 + i * 16);
+  };
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto add = [&](const Unit& u) {
+    const f32x4 s = block_sum<PA>(u.w, u.x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = u.on ? fmaf(s[i], u.scale, acc[i]) : acc[i];
+  };
+  if (more) look();
+  Unit u0, u1;
+  request(u0);
+  while (u0.live) {
+    request(u1);
+    add(u0);
+    if (!u1.live) break;
+    request(u0);
+    add(u1);
   }
   part[wave][lane] = acc;
   __syncthreads();
-  if (wave > 0 || t >= a.T) return;
+  if (wave > 0) return;
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) acc += part[w][lane];
+  if (splits > 1) {
+    float* sums = a.sums + (int64_t)nt * splits * 256;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __hip_atomic_store(&sums[split * 256 + i * 64 + lane], acc[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0: the sums are where every XCD sees them
+    int done = 0;
+    if (lane == 0)
+      done = __hip_atomic_fetch_add(&a.count[nt], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (uniform_i32(done) != splits - 1) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[i] += __hip_atomic_load(&sums[s * 256 + i * 64 + lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (t >= a.T) return;
   const int n = fp8_column(nt, g);
   typename Row::elem* p = static_cast<typename Row::elem*>(a.out) + (int64_t)t * a.out_ld + n;
   if (wide && n + 4 <= a.dim) {
@@ -281,13 +408,28 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, bo
   }
 }
 
+// Splits of the down product's blocks, so that there is a workgroup a CU, as long as
+// its waves have two blocks each. 128 tiles in 1, 2, 4 splits, the layer, us: one token
+// 20.7, 19.4, 20.3; sixteen 104, 82, 83; 448 tiles (dim 7168): 109, 110, 121.
+int splits_of(int64_t T, int64_t E, int64_t k, int64_t dim, int64_t hidden) {
+  const int64_t tiles = fp8_tiles((int32_t)dim);
+  const int64_t blocks = std::min(E, T * k) * ((hidden + 127) / 128);
+  int s = 1;
+  while (s < 8 && tiles * s < 256 && blocks >= 2 * s * kWaves) s *= 2;
+  return s;
+}
+
 struct LayerSpace {
-  int64_t act, total;  // bytes
+  int64_t count, sums, act, total;  // bytes
 };
-LayerSpace space_of(int64_t T, int64_t E, int64_t k, int64_t hidden) {
+LayerSpace space_of(int64_t T, int64_t E, int64_t k, int64_t dim, int64_t hidden) {
   const int64_t active = std::min(E, T * k), width = (hidden + 127) / 128 * 128;
+  const int64_t tiles = fp8_tiles((int32_t)dim);
+  auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   LayerSpace s{};
-  s.act = ((1 + active + active * (kTokens / 4)) * 4 + 255) / 256 * 256;
+  s.count = up((1 + active + active * (kTokens / 4)) * 4);
+  s.sums = s.count + up(tiles * 4);
+  s.act = s.sums + tiles * 8 * 1024;
   s.total = s.act + T * k * 3 * width * 2;
   return s;
 }
@@ -305,24 +447,44 @@ int32_t check_layer(const char* who, int64_t n_tokens, int32_t n_experts, int32_
   if (dim < 1 || dim > kFp8MaxDim || hidden < 1 || hidden > kFp8MaxDim)
     return fail(MLORA_ERR_INVALID, "%s: dim=%d, hidden=%d outside [1, %d]", who, dim, hidden,
                 kFp8MaxDim);
+  // the activated rows are read with 32-bit offsets
+  if (n_tokens * top_k * 6 * (((int64_t)hidden + 127) / 128 * 128) >= 0xff000000ll)
+    return fail(MLORA_ERR_INVALID, "%s: hidden=%d is too wide for %lld rows", who, hidden,
+                (long long)(n_tokens * top_k));
   return MLORA_OK;
+}
+
+template <typename Row, bool WIDE>
+void launch_gate_up(const LayerArgs& a, hipStream_t s) {
+  const Lds l = lds_of(a.T * a.k, a.E, a.max_active);
+  const int64_t items = (int64_t)a.max_active * a.HB * 8;
+  // Two workgroups a CU are there at once (16 of their waves hold their registers);
+  // more would choose the experts again. Sixteen tokens, 256, 512, 768, 1024: the layer
+  // 85, 82, 93, 95 us.
+  const dim3 grid((unsigned)std::min<int64_t>(items, 512)), block(64 * kWaves);
+  const int blocks = (a.DB + kWaves - 1) / kWaves;  // a wave's
+  constexpr bool kBf16 = sizeof(typename Row::elem) == 2;
+  if (blocks <= 1)
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, WIDE, 1>), grid, block, l.total * 4, s, a);
+  else if (blocks <= 2)
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, WIDE, 2>), grid, block, l.total * 4, s, a);
+  else if (kBf16 && blocks <= 4)
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, WIDE, kBf16 ? 4 : 0>), grid, block, l.total * 4, s, a);
+  else
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, WIDE, 0>), grid, block, l.total * 4, s, a);
 }
 
 template <typename Row>
 int32_t launch_layer(const char* who, const LayerArgs& a, bool x_wide, bool out_wide,
                      hipStream_t s) {
-  const Lds l = lds_of(a.T * a.k, a.E, a.max_active);
-  const int64_t items = (int64_t)a.max_active * a.HB * 8;
-  const int grid = (int)std::min<int64_t>(items, 1024);
   if (x_wide)
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, true>), dim3(grid), dim3(64 * kWaves),
-                       l.total * 4, s, a);
+    launch_gate_up<Row, true>(a, s);
   else
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, false>), dim3(grid), dim3(64 * kWaves),
-                       l.total * 4, s, a);
+    launch_gate_up<Row, false>(a, s);
   if (int32_t rc = launch_status(who)) return rc;
-  hipLaunchKernelGGL((layer_down_kernel<Row>), dim3(fp8_tiles(a.dim)), dim3(64 * kWaves), 0, s, a,
-                     out_wide);
+  const int splits = splits_of(a.T, a.E, a.k, a.dim, a.hidden);
+  hipLaunchKernelGGL((layer_down_kernel<Row>), dim3(fp8_tiles(a.dim) * splits), dim3(64 * kWaves),
+                     (1 + a.max_active + a.max_active * (kTokens / 4)) * 4, s, a, splits, out_wide);
   return launch_status(who);
 }
 
@@ -335,7 +497,7 @@ extern "C" uint64_t mlora_moe_layer_workspace_bytes(int64_t n_tokens, int32_t n_
                                                     int32_t top_k, int32_t dim, int32_t hidden) {
   if (check_layer("mlora_moe_layer_workspace_bytes", n_tokens, n_experts, top_k, dim, hidden))
     return 0;
-  return n_tokens == 0 ? 0 : (uint64_t)space_of(n_tokens, n_experts, top_k, hidden).total;
+  return n_tokens == 0 ? 0 : (uint64_t)space_of(n_tokens, n_experts, top_k, dim, hidden).total;
 }
 
 extern "C" int32_t mlora_moe_layer(const mlora_fp8_route* gate, const mlora_fp8_route* up,
@@ -363,7 +525,7 @@ extern "C" int32_t mlora_moe_layer(const mlora_fp8_route* gate, const mlora_fp8_
     return MLORA_OK;
   }
   if (!x || !logits || !out) return fail(MLORA_ERR_INVALID, "%s: NULL pointer", who);
-  const LayerSpace sp = space_of(n_tokens, E, top_k, hidden);
+  const LayerSpace sp = space_of(n_tokens, E, top_k, dim, hidden);
   if (!workspace || workspace_bytes < (uint64_t)sp.total)
     return fail(MLORA_ERR_CAPACITY, "%s: workspace of %llu bytes, %lld needed", who,
                 (unsigned long long)(workspace ? workspace_bytes : 0), (long long)sp.total);
@@ -385,7 +547,10 @@ extern "C" int32_t mlora_moe_layer(const mlora_fp8_route* gate, const mlora_fp8_
   a.indices = indices;
   a.weights = weights;
   a.head = static_cast<int32_t*>(workspace);
+  a.count = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + sp.count);
+  a.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.sums);
   a.act = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + sp.act);
+  a.act_bytes = (uint32_t)(sp.total - sp.act);
   a.T = (int32_t)n_tokens;
   a.E = E;
   a.k = top_k;

@@ -2,6 +2,7 @@
 // their gradients, for gfx950 (MI355X).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "mlora_device.h"
 
@@ -13,8 +14,8 @@ namespace {
 //   r = residual_scale residual + y_scale gate n
 //   x = r R(r) (wx + offset)
 // One pass: a row's values stay in registers from the first load to the last
-// store, as fp32; r enters the second norm unrounded. 64, 256, 512 or 1024
-// threads hold a row, 8 or 16 values each; the two means are sums over them in a
+// store, as fp32; r enters the second norm unrounded. 64 to 1024 threads
+// hold a row, 8 values each (16 past 8192), and keep the weights from row to row; the two means are sums over them in a
 // fixed order. The gradients recompute r from the same inputs (which are read
 // for the norms' gradients anyway), so nothing is saved forward:
 //   g = d_x (wx + offset), h = r R(r)
@@ -28,7 +29,7 @@ namespace {
 enum GateForm { kNoGate, kChannel, kToken, kFull };
 constexpr int kMaxDim = 16384;
 constexpr int kSums = 3;          // wx, wy, gate per channel
-constexpr int kMaxGroups = 1024;  // groups of threads that write partial sums
+constexpr int kMaxGroups = 512;  // groups of threads that write partial sums
 
 struct NormArgs {
   mlora_norm_block b;
@@ -51,22 +52,34 @@ struct Cols {
   static constexpr int CH = VPT / V;
   static __device__ __forceinline__ int col(int ch, int tid) { return (ch * TPR + tid) * V; }
 
+  // A row as it is loaded, so that the next row's loads can be on their way.
+  typedef typename std::conditional<WIDE, u32x4, typename Row::elem>::type Piece;
+  struct Raw {
+    Piece v[CH];
+  };
+  static __device__ __forceinline__ void request(const void* base, int64_t off, int D, int tid, Raw& r) {
+    const typename Row::elem* p = static_cast<const typename Row::elem*>(base) + off;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      r.v[c] = {};
+      if (col(c, tid) < D)
+        r.v[c] = *reinterpret_cast<const Piece*>(p + col(c, tid));
+    }
+  }
+  static __device__ __forceinline__ void widen(const Raw& r, float (&f)[VPT]) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if constexpr (WIDE)
+        Row::widen16(r.v[c], f + c * V);
+      else
+        f[c] = Row::widen(r.v[c]);
+    }
+  }
   static __device__ __forceinline__ void load(const void* base, int64_t off, int D, int tid,
                                               float (&f)[VPT]) {
-    const typename Row::elem* p = static_cast<const typename Row::elem*>(base) + off;
-    if constexpr (WIDE) {
-      u32x4 v[CH];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        v[c] = u32x4{0, 0, 0, 0};
-        if (col(c, tid) < D) v[c] = *reinterpret_cast<const u32x4*>(p + col(c, tid));
-      }
-#pragma unroll
-      for (int c = 0; c < CH; ++c) Row::widen16(v[c], f + c * V);
-    } else {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) f[c] = col(c, tid) < D ? Row::widen(p[col(c, tid)]) : 0.f;
-    }
+    Raw r;
+    request(base, off, D, tid, r);
+    widen(r, f);
   }
   static __device__ __forceinline__ void store(void* base, int64_t off, int D, int tid,
                                                const float (&f)[VPT]) {
@@ -83,43 +96,47 @@ struct Cols {
   // fp32 vectors of the row's width
   static __device__ __forceinline__ void store_f32(float* p, int D, int tid, const float (&f)[VPT]) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (col(c, tid) + i < D) p[col(c, tid) + i] = f[c * V + i];
-  }
-  // norm weights plus offset, of either type; null: 1. Zeros past the row.
-  static __device__ __forceinline__ void load_weight(const void* w, int dtype, float offset, int D,
-                                                     int tid, float (&f)[VPT]) {
-#pragma unroll
     for (int c = 0; c < CH; ++c) {
+      if (col(c, tid) >= D) continue;
+      if constexpr (WIDE) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int at = col(c, tid) + i;
-        float v = 0.f;
-        if (at < D) {
-          if (!w)
-            v = 1.f;
-          else if (dtype == MLORA_F32)
-            v = static_cast<const float*>(w)[at] + offset;
-          else
-            v = Bf16Row::widen(static_cast<const uint16_t*>(w)[at]) + offset;
-        }
-        f[c * V + i] = v;
+        for (int i = 0; i < V; i += 4)
+          *reinterpret_cast<f32x4*>(p + col(c, tid) + i) =
+              f32x4{f[c * V + i], f[c * V + i + 1], f[c * V + i + 2], f[c * V + i + 3]};
+      } else {
+        p[col(c, tid)] = f[c];
       }
     }
   }
-  // the gate of each of the thread's values
-  static __device__ __forceinline__ void load_gate(const mlora_norm_block& b, int64_t row, int tid,
-                                                   float (&f)[VPT]) {
-    if (b.gate_form == kFull || b.gate_form == kChannel) {
-      load(b.gate, b.gate_form == kFull ? row * b.gate_ld : 0, b.dim, tid, f);
-    } else {
-      const float v = b.gate_form == kToken
-                          ? Row::widen(static_cast<const typename Row::elem*>(b.gate)[row * b.gate_ld])
-                          : 1.f;
+  // norm weights plus offset, of either type; null: 1. Zeros past the row.
+  template <typename W>
+  static __device__ __forceinline__ void load_weight_as(const void* w, float offset, int D, int tid,
+                                                        float (&f)[VPT]) {
+    const typename W::elem* p = static_cast<const typename W::elem*>(w);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) f[i] = v;
+    for (int c = 0; c < CH; ++c) {
+      typedef typename W::elem vec __attribute__((ext_vector_type(V)));
+      const bool in = col(c, tid) < D;
+      vec v = {};
+      if (in) v = *reinterpret_cast<const vec*>(p + col(c, tid));
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (V == 1)
+          f[c] = in ? W::widen(v[0]) + offset : 0.f;
+        else
+          f[c * V + i] = in ? W::widen(v[i]) + offset : 0.f;
+      }
+    }
+  }
+  static __device__ __forceinline__ void load_weight(const void* w, int dtype, float offset, int D,
+                                                     int tid, float (&f)[VPT]) {
+    if (!w) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) f[i] = col(i / V, tid) < D ? 1.f : 0.f;
+    } else if (dtype == MLORA_F32) {
+      load_weight_as<F32Row>(w, offset, D, tid, f);
+    } else {
+      load_weight_as<Bf16Row>(w, offset, D, tid, f);
     }
   }
 };
@@ -169,77 +186,120 @@ __device__ __forceinline__ float norm_y(const mlora_norm_block& b, const float (
   return R;
 }
 
-template <typename Row, int TPR, int VPT, bool WIDE>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_forward_kernel(NormArgs a) {
-  typedef Cols<Row, TPR, VPT, WIDE> C;
-  __shared__ float lds[2][TPR / 64];
+// Threads of a workgroup: one row's, or four waves with a row each.
+constexpr int threads_of(int tpr) { return tpr < 128 ? 256 : tpr; }
+constexpr int rows_of(int tpr) { return threads_of(tpr) / tpr; }
+
+// What a row's loads bring.
+template <typename C>
+struct RowIn {
+  typename C::Raw residual, y, gate, d_r, d_x;
+  float token_gate;
+};
+template <typename Row, typename C>
+__device__ __forceinline__ void request_row(const NormArgs& a, int64_t row, int tid, RowIn<C>& in) {
   const mlora_norm_block& b = a.b;
-  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-  const int tid = threadIdx.x & (TPR - 1);
-  const int64_t row = (int64_t)flat_group() * kRows + threadIdx.x / TPR;
-  if (row >= b.n_tokens) return;  // all of a row's threads (one wave, or the workgroup)
-  float r[VPT];
-  C::load(b.residual, row * b.residual_ld, b.dim, tid, r);
-  float wx[VPT];
-  if (a.x) C::load_weight(b.x_weight, b.w_dtype, b.weight_offset, b.dim, tid, wx);
-  if (b.y) {
-    float y[VPT], wy[VPT], gate[VPT], n[VPT];
-    C::load(b.y, row * b.y_ld, b.dim, tid, y);
-    if (b.y_weight) C::load_weight(b.y_weight, b.w_dtype, b.weight_offset, b.dim, tid, wy);
-    C::load_gate(b, row, tid, gate);
-    norm_y<C, TPR, VPT>(b, y, wy, lds[0], tid, n);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) r[i] = b.residual_scale * r[i] + b.y_scale * gate[i] * n[i];
+  C::request(b.residual, row * b.residual_ld, b.dim, tid, in.residual);
+  if (b.y) C::request(b.y, row * b.y_ld, b.dim, tid, in.y);
+  if (b.gate_form == kFull) C::request(b.gate, row * b.gate_ld, b.dim, tid, in.gate);
+  in.token_gate = 1.f;
+  if (b.gate_form == kToken)
+    in.token_gate = Row::widen(static_cast<const typename Row::elem*>(b.gate)[row * b.gate_ld]);
+  if (a.d_r) C::request(a.d_r, row * a.d_r_ld, b.dim, tid, in.d_r);
+  if (a.d_x) C::request(a.d_x, row * a.d_x_ld, b.dim, tid, in.d_x);
+}
+// The gate of each of the thread's values; a gate per channel is in in.gate already.
+template <typename C, int VPT>
+__device__ __forceinline__ void gate_of(const mlora_norm_block& b, const RowIn<C>& in,
+                                        float (&f)[VPT]) {
+  if (b.gate_form == kFull || b.gate_form == kChannel) {
+    C::widen(in.gate, f);
   } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) r[i] *= b.residual_scale;
+    for (int i = 0; i < VPT; ++i) f[i] = in.token_gate;
   }
-  if (a.r) C::store(a.r, row * a.r_ld, b.dim, tid, r);
-  if (!a.x) return;
-  float s[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) s[0] += r[i] * r[i];
-  row_sums<TPR, 1>(s, lds[1], tid);
-  const float R = inv_rms(s[0], b.dim, b.eps);
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) r[i] *= R * wx[i];
-  C::store(a.x, row * a.x_ld, b.dim, tid, r);
 }
 
 template <typename Row, int TPR, int VPT, bool WIDE>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_backward_kernel(NormArgs a) {
+__global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(NormArgs a) {
   typedef Cols<Row, TPR, VPT, WIDE> C;
   // of alternate rows: a wave may write the next row's sums while another reads
-  __shared__ float sums[2][5][TPR / 64];
+  __shared__ float sums[2][2][TPR / 64];
   const mlora_norm_block& b = a.b;
-  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-  const int tid = threadIdx.x & (TPR - 1);
-  const int D = b.dim;
-  const int64_t group = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-  const int64_t groups = (int64_t)gridDim.x * kRows;
+  const int tid = threadIdx.x & (TPR - 1), D = b.dim;
+  const int64_t groups = (int64_t)gridDim.x * rows_of(TPR);
+  float wx[VPT], wy[VPT];
+  RowIn<C> in;
+  if (a.x) C::load_weight(b.x_weight, b.w_dtype, b.weight_offset, D, tid, wx);
+  if (b.y_weight) C::load_weight(b.y_weight, b.w_dtype, b.weight_offset, D, tid, wy);
+  if (b.gate_form == kChannel) C::request(b.gate, 0, D, tid, in.gate);
+  int odd = 0;
+  // all of a row's threads (one wave, or the workgroup) leave together
+  for (int64_t row = (int64_t)blockIdx.x * rows_of(TPR) + threadIdx.x / TPR; row < b.n_tokens;
+       row += groups, odd ^= 1) {
+    request_row<Row, C>(a, row, tid, in);
+    float r[VPT];
+    C::widen(in.residual, r);
+    if (b.y) {
+      float y[VPT], gate[VPT], n[VPT];
+      C::widen(in.y, y);
+      gate_of<C, VPT>(b, in, gate);
+      norm_y<C, TPR, VPT>(b, y, wy, sums[odd][0], tid, n);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) r[i] = b.residual_scale * r[i] + b.y_scale * gate[i] * n[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) r[i] *= b.residual_scale;
+    }
+    if (a.r) C::store(a.r, row * a.r_ld, D, tid, r);
+    if (!a.x) continue;  // of the whole call
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) s[0] += r[i] * r[i];
+    row_sums<TPR, 1>(s, sums[odd][1], tid);
+    const float R = inv_rms(s[0], D, b.eps);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) r[i] *= R * wx[i];
+    C::store(a.x, row * a.x_ld, D, tid, r);
+  }
+}
+
+template <typename Row, int TPR, int VPT, bool WIDE>
+__global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs a) {
+  typedef Cols<Row, TPR, VPT, WIDE> C;
+  __shared__ float sums[2][5][TPR / 64];  // of alternate rows
+  const mlora_norm_block& b = a.b;
+  const int tid = threadIdx.x & (TPR - 1), D = b.dim;
+  const int64_t group = (int64_t)blockIdx.x * rows_of(TPR) + threadIdx.x / TPR;
+  const int64_t groups = (int64_t)gridDim.x * rows_of(TPR);
   float wx[VPT], wy[VPT], sum_wx[VPT], sum_wy[VPT], sum_gate[VPT];
   C::load_weight(b.x_weight, b.w_dtype, b.weight_offset, D, tid, wx);
   if (b.y_weight) C::load_weight(b.y_weight, b.w_dtype, b.weight_offset, D, tid, wy);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) sum_wx[i] = sum_wy[i] = sum_gate[i] = 0.f;
 
+  RowIn<C> in;
+  if (b.gate_form == kChannel) C::request(b.gate, 0, D, tid, in.gate);
+  if (group < b.n_tokens) request_row<Row, C>(a, group, tid, in);
   int odd = 0;
   for (int64_t row = group; row < b.n_tokens; row += groups, odd ^= 1) {
     float(*lds)[TPR / 64] = sums[odd];
     float r[VPT], y[VPT], d[VPT], g[VPT], gate[VPT], n[VPT];
-    C::load(b.residual, row * b.residual_ld, D, tid, r);
+    C::widen(in.residual, r);
     float Ry = 1.f;
     if (b.y) {
-      C::load(b.y, row * b.y_ld, D, tid, y);
-      C::load_gate(b, row, tid, gate);
+      C::widen(in.y, y);
+      gate_of<C, VPT>(b, in, gate);
     }
     if (a.d_r) {
-      C::load(a.d_r, row * a.d_r_ld, D, tid, d);
+      C::widen(in.d_r, d);
     } else {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) d[i] = 0.f;
     }
-    if (a.d_x) C::load(a.d_x, row * a.d_x_ld, D, tid, g);
+    if (a.d_x) C::widen(in.d_x, g);
+    // the next row's loads are on their way through this row's sums
+    if (row + groups < b.n_tokens) request_row<Row, C>(a, row + groups, tid, in);
     if (b.y) {
       Ry = norm_y<C, TPR, VPT>(b, y, wy, lds[0], tid, n);
 #pragma unroll
@@ -306,69 +366,83 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_backward_kernel(No
   if (a.partial[2]) C::store_f32(a.partial[2] + group * D, D, tid, sum_gate);
 }
 
-// Column sums of the groups' partial sums: 32 columns a workgroup, eight
-// threads a column.
+// Column sums of the groups' partial sums: 32 columns a workgroup, 32 threads a
+// column, four loads of each on their way.
 struct SumArgs {
   const float* partial[kSums];
   float* out[kSums];
   int32_t groups, dim;
 };
 
-__global__ void __launch_bounds__(256) norm_sum_kernel(SumArgs a) {
-  __shared__ float lds[8][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
-  const float* p = a.partial[blockIdx.y];
+__global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
+  __shared__ float lds[32][33];
+  const int c = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + c;
+  if (!a.out[blockIdx.y]) return;
+  const float* p = a.partial[blockIdx.y] + col;
   float s = 0.f;
-  if (a.out[blockIdx.y] && col < a.dim)
-    for (int g = part; g < a.groups; g += 8) s += p[(int64_t)g * a.dim + col];
-  lds[part][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (part > 0 || col >= a.dim || !a.out[blockIdx.y]) return;
+  if (col < a.dim) {
+    int g = part;
+    for (; g + 96 < a.groups; g += 128) {
+      float v[4];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s += lds[i][threadIdx.x & 31];
-  a.out[blockIdx.y][col] = s;
+      for (int i = 0; i < 4; ++i) v[i] = p[(int64_t)(g + 32 * i) * a.dim];
+      s += (v[0] + v[1]) + (v[2] + v[3]);
+    }
+    for (; g < a.groups; g += 32) s += p[(int64_t)g * a.dim];
+  }
+  lds[c][part] = s;
+  __syncthreads();
+  // column `part`'s 32 sums in the lanes of half a wave
+  s = group_sum<32>(lds[part][c]);
+  const int out_col = blockIdx.x * 32 + part;
+  if (c == 0 && out_col < a.dim) a.out[blockIdx.y][out_col] = s;
 }
 
-// Threads per row and values per thread: the fewest that hold the row.
+// Threads per row and values per thread: 8, as far as 1024 threads go.
 struct Shape {
   int tpr, vpt;
 };
 Shape shape_of(int dim) {
   if (dim <= 512) return {64, 8};
-  if (dim <= 1024) return {64, 16};
+  if (dim <= 1024) return {128, 8};
   if (dim <= 2048) return {256, 8};
-  if (dim <= 4096) return {256, 16};
-  if (dim <= 8192) return {512, 16};
+  if (dim <= 4096) return {512, 8};
+  if (dim <= 8192) return {1024, 8};
   return {1024, 16};
 }
-int64_t rows_per_group(Shape s) { return s.tpr < 256 ? 256 / s.tpr : 1; }
-// Workgroups of the gradient's kernel.
+// Workgroups that go through n_tokens rows, at most `most`, each about as many.
+int64_t grid_of(int64_t n_tokens, Shape h, int64_t most) {
+  const int64_t per = rows_of(h.tpr), groups = (n_tokens + per - 1) / per;
+  const int64_t turns = (groups + most - 1) / most;
+  return (groups + turns - 1) / turns;
+}
 int64_t backward_grid(int64_t n_tokens, int dim) {
-  const int64_t per = rows_per_group(shape_of(dim));
-  return std::min<int64_t>((n_tokens + per - 1) / per, kMaxGroups / per);
+  const Shape h = shape_of(dim);
+  return grid_of(n_tokens, h, kMaxGroups / rows_of(h.tpr));
 }
 
 template <typename Row, int TPR, int VPT, bool WIDE>
 void launch(const NormArgs& a, bool backward, hipStream_t s) {
-  constexpr int threads = TPR < 256 ? 256 : TPR;
-  if (backward) {
-    hipLaunchKernelGGL((norm_backward_kernel<Row, TPR, VPT, WIDE>),
-                       dim3((unsigned)backward_grid(a.b.n_tokens, a.b.dim)), dim3(threads), 0, s, a);
-  } else {
-    const int64_t per = threads / TPR;
-    hipLaunchKernelGGL((norm_forward_kernel<Row, TPR, VPT, WIDE>),
-                       flat_grid((a.b.n_tokens + per - 1) / per), dim3(threads), 0, s, a);
-  }
+  constexpr int threads = threads_of(TPR);
+  const int64_t grid = backward ? backward_grid(a.b.n_tokens, a.b.dim)
+                                : grid_of(a.b.n_tokens, Shape{TPR, VPT}, 256 * 2048 / threads);
+  if (backward)
+    hipLaunchKernelGGL((norm_backward_kernel<Row, TPR, VPT, WIDE>), dim3((unsigned)grid),
+                       dim3(threads), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_forward_kernel<Row, TPR, VPT, WIDE>), dim3((unsigned)grid),
+                       dim3(threads), 0, s, a);
 }
 
 template <typename Row, bool WIDE>
 void launch_shape(const NormArgs& a, bool backward, hipStream_t s) {
   const Shape h = shape_of(a.b.dim);
-  if (h.tpr == 64 && h.vpt == 8) return launch<Row, 64, 8, WIDE>(a, backward, s);
-  if (h.tpr == 64) return launch<Row, 64, 16, WIDE>(a, backward, s);
-  if (h.tpr == 256 && h.vpt == 8) return launch<Row, 256, 8, WIDE>(a, backward, s);
-  if (h.tpr == 256) return launch<Row, 256, 16, WIDE>(a, backward, s);
-  if (h.tpr == 512) return launch<Row, 512, 16, WIDE>(a, backward, s);
+  if (h.tpr == 64) return launch<Row, 64, 8, WIDE>(a, backward, s);
+  if (h.tpr == 128) return launch<Row, 128, 8, WIDE>(a, backward, s);
+  if (h.tpr == 256) return launch<Row, 256, 8, WIDE>(a, backward, s);
+  if (h.tpr == 512) return launch<Row, 512, 8, WIDE>(a, backward, s);
+  if (h.vpt == 8) return launch<Row, 1024, 8, WIDE>(a, backward, s);
   launch<Row, 1024, 16, WIDE>(a, backward, s);
 }
 
@@ -384,7 +458,8 @@ int32_t run(const char* who, const NormArgs& a, bool backward, hipStream_t s) {
        wide_rows(b.gate, b.gate_form == kFull ? b.gate_ld : 0, per)) &&
       wide_rows(a.r, a.r_ld, per) && wide_rows(a.x, a.x_ld, per) && wide_rows(a.d_r, a.d_r_ld, per) &&
       wide_rows(a.d_x, a.d_x_ld, per) && wide_rows(a.d_residual, a.d_residual_ld, per) &&
-      wide_rows(a.d_y, a.d_y_ld, per) &&
+      wide_rows(a.d_y, a.d_y_ld, per) && wide_rows(b.x_weight, 0, per) &&
+      wide_rows(b.y_weight, 0, per) &&
       (b.gate_form != kFull || wide_rows(a.d_gate, a.d_gate_ld, per));
   (void)hipGetLastError();
   if (b.dtype == MLORA_BF16) {
@@ -455,7 +530,7 @@ extern "C" int32_t mlora_block_norm(const mlora_norm_block* block, void* r, int6
 
 extern "C" uint64_t mlora_block_norm_backward_workspace_bytes(int64_t n_tokens, int32_t dim) {
   if (n_tokens < 1 || n_tokens > kMaxRows || dim < 1 || dim > kMaxDim) return 0;
-  const uint64_t groups = backward_grid(n_tokens, dim) * rows_per_group(shape_of(dim));
+  const uint64_t groups = backward_grid(n_tokens, dim) * rows_of(shape_of(dim).tpr);
   return (kSums * groups * dim * 4 + 255) / 256 * 256;
 }
 
@@ -502,7 +577,7 @@ extern "C" int32_t mlora_block_norm_backward(
     a.d_y_ld = d_y_ld;
     a.d_gate = d_gate;
     a.d_gate_ld = d_gate_ld;
-    sa.groups = (int32_t)(backward_grid(block->n_tokens, dim) * rows_per_group(shape_of(dim)));
+    sa.groups = (int32_t)(backward_grid(block->n_tokens, dim) * rows_of(shape_of(dim).tpr));
     for (int i = 0; i < kSums; ++i)
       if (sums[i])
         sa.partial[i] = a.partial[i] = static_cast<float*>(workspace) + (int64_t)i * sa.groups * dim;
@@ -512,7 +587,7 @@ extern "C" int32_t mlora_block_norm_backward(
     sa.dim = dim;
     for (int i = 0; i < kSums; ++i) sa.out[i] = sums[i];
     (void)hipGetLastError();
-    hipLaunchKernelGGL(norm_sum_kernel, dim3((dim + 31) / 32, kSums), dim3(256), 0, s, sa);
+    hipLaunchKernelGGL(norm_sum_kernel, dim3((dim + 31) / 32, kSums), dim3(1024), 0, s, sa);
     return launch_status(who);
   }
   clear_error();

@@ -42,6 +42,7 @@ struct NormArgs {
   void *d_residual, *d_y, *d_gate;
   int64_t d_residual_ld, d_y_ld, d_gate_ld;
   float* partial[kSums];  // [groups][dim], null: not wanted
+  bool past;              // the outputs are too large to be found in a cache later
 };
 
 // A thread's VPT values of a row: neighbours that fill 16 bytes (WIDE) or single
@@ -63,7 +64,7 @@ struct Cols {
     for (int c = 0; c < CH; ++c) {
       r.v[c] = {};
       if (col(c, tid) < D)
-        r.v[c] = *reinterpret_cast<const Piece*>(p + col(c, tid));
+        r.v[c] = __builtin_nontemporal_load(reinterpret_cast<const Piece*>(p + col(c, tid)));
     }
   }
   static __device__ __forceinline__ void widen(const Raw& r, float (&f)[VPT]) {
@@ -81,16 +82,23 @@ struct Cols {
     request(base, off, D, tid, r);
     widen(r, f);
   }
+  // past: past the caches' keep
   static __device__ __forceinline__ void store(void* base, int64_t off, int D, int tid,
-                                               const float (&f)[VPT]) {
+                                               const float (&f)[VPT], bool past) {
     typename Row::elem* p = static_cast<typename Row::elem*>(base) + off;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (col(c, tid) >= D) continue;
+      Piece v;
       if constexpr (WIDE)
-        *reinterpret_cast<u32x4*>(p + col(c, tid)) = Row::narrow16(f + c * V);
+        v = Row::narrow16(f + c * V);
       else
-        p[col(c, tid)] = Row::narrow(f[c]);
+        v = Row::narrow(f[c]);
+      Piece* to = reinterpret_cast<Piece*>(p + col(c, tid));
+      if (past)
+        __builtin_nontemporal_store(v, to);
+      else
+        *to = v;
     }
   }
   // fp32 vectors of the row's width
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(NormArgs 
 #pragma unroll
       for (int i = 0; i < VPT; ++i) r[i] *= b.residual_scale;
     }
-    if (a.r) C::store(a.r, row * a.r_ld, D, tid, r);
+    if (a.r) C::store(a.r, row * a.r_ld, D, tid, r, a.past);
     if (!a.x) continue;  // of the whole call
     float s[1] = {0.f};
 #pragma unroll
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(NormArgs 
     const float R = inv_rms(s[0], D, b.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) r[i] *= R * wx[i];
-    C::store(a.x, row * a.x_ld, D, tid, r);
+    C::store(a.x, row * a.x_ld, D, tid, r, a.past);
   }
 }
 
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs
       float out[VPT];
 #pragma unroll
       for (int i = 0; i < VPT; ++i) out[i] = b.residual_scale * d[i];
-      C::store(a.d_residual, row * a.d_residual_ld, D, tid, out);
+      C::store(a.d_residual, row * a.d_residual_ld, D, tid, out, a.past);
     }
     if (!b.y) continue;  // of the whole call
     float s[2] = {0.f, 0.f};
@@ -356,10 +364,10 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs
         for (int i = 0; i < VPT; ++i) d[i] = Ry * (d[i] - y[i] * mean);
       }
     }
-    if (a.d_y) C::store(a.d_y, row * a.d_y_ld, D, tid, d);
+    if (a.d_y) C::store(a.d_y, row * a.d_y_ld, D, tid, d, a.past);
     if (a.d_gate && b.gate_form == kToken && tid == 0)
       static_cast<float*>(a.d_gate)[row * a.d_gate_ld] = s[0];
-    if (a.d_gate && b.gate_form == kFull) C::store(a.d_gate, row * a.d_gate_ld, D, tid, n);
+    if (a.d_gate && b.gate_form == kFull) C::store(a.d_gate, row * a.d_gate_ld, D, tid, n, a.past);
   }
   if (a.partial[0]) C::store_f32(a.partial[0] + group * D, D, tid, sum_wx);
   if (a.partial[1]) C::store_f32(a.partial[1] + group * D, D, tid, sum_wy);
@@ -449,8 +457,11 @@ void launch_shape(const NormArgs& a, bool backward, hipStream_t s) {
 // Whether a matrix (null: any) allows 16-byte accesses.
 bool wide_rows(const void* p, int64_t ld, int per) { return !p || (ld % per == 0 && aligned(p, 16)); }
 
-int32_t run(const char* who, const NormArgs& a, bool backward, hipStream_t s) {
+// Rows past the size of the XCDs' L2s (8 of 4 MB) pass the caches by: 8192 rows of 4096
+// bf16 values 60 -> 56 us; smaller ones may still be there for the call that reads them.
+int32_t run(const char* who, NormArgs a, bool backward, hipStream_t s) {
   const mlora_norm_block& b = a.b;
+  a.past = b.n_tokens * b.dim * (b.dtype == MLORA_BF16 ? 2 : 4) > (32ll << 20);
   const int per = b.dtype == MLORA_BF16 ? 8 : 4;
   const bool wide =
       b.dim % per == 0 && wide_rows(b.residual, b.residual_ld, per) && wide_rows(b.y, b.y_ld, per) &&

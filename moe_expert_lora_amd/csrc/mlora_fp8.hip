@@ -87,7 +87,7 @@ struct QuantArgs {
   uint8_t* q;
   int64_t q_ld;
   float* scales;   // [groups][n_rows]
-  int64_t units;   // n_rows * groups
+  uint32_t units;  // n_rows * groups
   int32_t n_rows, K, groups;
 };
 
@@ -100,10 +100,10 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d)
 
 template <typename Row, bool SILU, bool WIDE>
 __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
-  const int64_t unit = (int64_t)flat_group() * 16 + (threadIdx.x >> 4);
+  const uint32_t unit = (uint32_t)flat_group() * 16 + (threadIdx.x >> 4);
   if (unit >= a.units) return;  // whole rows of 16 lanes: the reduction stays in them
-  const int row = (int)(unit / a.groups);
-  const int g = (int)(unit - (int64_t)row * a.groups);
+  const int row = (int)(unit / (uint32_t)a.groups);
+  const int g = (int)(unit - (uint32_t)row * (uint32_t)a.groups);
   const int k = g * 128 + (threadIdx.x & 15) * 8;
   float v[8];
   load8<Row, WIDE>(a.x, (int64_t)row * a.x_ld, k, a.K, v);
@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
     float u[8];
     load8<Row, WIDE>(a.up, (int64_t)row * a.up_ld, k, a.K, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + expf(-v[i])) * u[i];
+    // the reciprocal is exact to one unit, as the quotient's last bits are not kept
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * __builtin_amdgcn_rcpf(1.f + expf(-v[i])) * u[i];
   }
   uint32_t m = 0;
 #pragma unroll
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
 
 template <typename Row, bool SILU>
 void launch_quant(const QuantArgs& a, bool wide, hipStream_t s) {
-  const dim3 grid = flat_grid((a.units + 15) / 16);
+  const dim3 grid = flat_grid(((int64_t)a.units + 15) / 16);
   if (wide)
     hipLaunchKernelGGL((fp8_quant_kernel<Row, SILU, true>), grid, dim3(256), 0, s, a);
   else
@@ -334,12 +335,13 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a, bool w
 // piece p ^ (r / 2 % 8)), so that 8 lanes read one row whole and the 16 rows of an
 // operand come from all 64 banks.
 //
-// 8192 rows of 4096 by 4096 x 4096 take 124 us, 2.2 PFLOP/s (a library's product of
-// E4M3 with one scale: 102 us): the clock falls to 1.85 GHz, and a block takes 3280
-// cycles of which the matrix instructions fill 2048, the rest being the next block's
-// latency, which 128 KB of LDS allow to be requested one block ahead. Requesting it
-// between the matrix instructions instead of before them: 180 -> 176 us at that
-// stage; touching the lines of later blocks early made no difference.
+// 8192 rows of 4096 by 4096 x 4096 take 124 to 150 us, by the box's power (1.8 to 2.2
+// PFLOP/s; a library's product of E4M3 with one scale: 102 us on one of them): the
+// clock falls to 1.85 GHz, and a block takes 3280 cycles of which the matrix
+// instructions fill 2048, the rest being the next block's latency, which 128 KB of LDS
+// allow to be requested one block ahead. Where in a block it is requested, and which
+// waves go first, made no difference; touching the lines of later blocks early cost
+// 10% and more, as a CU's requests are near their limit.
 template <typename Row, int WM, int WN, int MT, int NT>
 struct Tile {
   static constexpr int W = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16;
@@ -356,10 +358,9 @@ __device__ __forceinline__ void to_lds(rsrc_t r, uint32_t lane_off, uint32_t off
 // One block of 128 k of a wave's pieces from a stage. The matrix instructions of one
 // column of pieces are issued between the multiply-adds of the column before, which
 // would wait for their results otherwise.
-template <typename Row, int MT, int NT, typename Request>
+template <typename Row, int MT, int NT>
 __device__ __forceinline__ void tile_block(const uint8_t* w, const uint8_t* x, int lane,
-                                           const float (&s)[MT], f32x4 (&acc)[MT][NT],
-                                           Request request) {
+                                           const float (&s)[MT], f32x4 (&acc)[MT][NT]) {
   const int row = lane & 15, piece = (lane >> 4) * 2;
   Fp8Frag xf[MT], wf[2];
   wf[0] = load_frag(w + lane * 16, 1024);
@@ -374,7 +375,6 @@ __device__ __forceinline__ void tile_block(const uint8_t* w, const uint8_t* x, i
   for (int j = 0; j <= NT; ++j) {
     __builtin_amdgcn_sched_barrier(0);
     if (j + 1 < NT) wf[(j + 1) & 1] = load_frag(w + (j + 1) * kFp8Tile + lane * 16, 1024);
-    if (j == 1) request();
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       if (j < NT) d[j & 1][i] = block_products<Row>(wf[j & 1], xf[i]);
@@ -464,9 +464,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
 #pragma unroll
     for (int i = 0; i < MT; ++i) s[i] = xs[i] * ws;
     // past the last block, the last one again (into the stage that nothing reads)
-    tile_block<Row, MT, NT>(
-        p + wn * NT * kFp8Tile, p + T::BN * 128 + wm * MT * 16 * 128, lane, s, acc,
-        [&] { request(min(kb + 1, a.KB - 1), stage + (~kb & 1) * T::kStage); });
+    request(min(kb + 1, a.KB - 1), stage + (~kb & 1) * T::kStage);
+    tile_block<Row, MT, NT>(p + wn * NT * kFp8Tile, p + T::BN * 128 + wm * MT * 16 * 128, lane, s, acc);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -534,7 +533,7 @@ int32_t launch_gemm(const char* who, const GemmArgs& a, bool wide, hipStream_t s
     return spans * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn);
   };
   if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row>(who, a, wide, s);
-  if (mean >= 128 && tiles(256, 256) >= 512) return launch_tile<Row, 4, 2, 4, 8>(who, a, wide, s);
+  if (mean >= 128 && tiles(256, 256) >= 384) return launch_tile<Row, 4, 2, 4, 8>(who, a, wide, s);
   if (mean >= 256 && tiles(128, 128) >= 512) return launch_tile<Row, 2, 2, 4, 4>(who, a, wide, s);
   if (mean >= 24 && tiles(64, 128) >= 256) return launch_tile<Row, 2, 2, 2, 4>(who, a, wide, s);
   return launch_tile<Row, 1, 4, 2, 2>(who, a, wide, s);
@@ -649,9 +648,9 @@ extern "C" int32_t mlora_fp8_quant(const void* x, int64_t x_ld, const void* up, 
   a.n_rows = (int32_t)n_rows;
   a.K = k;
   a.groups = (int32_t)blocks_of(k);
-  a.units = n_rows * a.groups;
-  if ((a.units + 15) / 16 > kMaxTiles)
+  if (n_rows * a.groups > 0xf0000000ll)
     return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
+  a.units = (uint32_t)(n_rows * a.groups);
   const int64_t per = dtype == MLORA_BF16 ? 8 : 4;
   const bool wide = k % 8 == 0 && x_ld % per == 0 && aligned(x, 16) &&
                     (!up || (up_ld % per == 0 && aligned(up, 16)));

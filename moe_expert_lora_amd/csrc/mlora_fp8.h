@@ -120,22 +120,15 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // 8 values of a row from column k on; zeros past K.
-template <typename Row, bool WIDE>
+template <typename Row>
 __device__ __forceinline__ void load8(const void* base, int64_t off, int k, int K, float* f) {
   const typename Row::elem* p = static_cast<const typename Row::elem*>(base) + off;
-  if constexpr (WIDE) {  // K is a multiple of 8, rows start on 16 bytes
-    u32x4 v[8 / Row::kPer16];
+  u32x4 v[8 / Row::kPer16];
 #pragma unroll
-    for (int i = 0; i < 8 / Row::kPer16; ++i) {
-      v[i] = u32x4{0, 0, 0, 0};
-      if (k < K) v[i] = *reinterpret_cast<const u32x4*>(p + k + i * Row::kPer16);
-    }
+  for (int i = 0; i < 8 / Row::kPer16; ++i)
+    v[i] = load16_any<Row>(p, k + i * Row::kPer16, K);
 #pragma unroll
-    for (int i = 0; i < 8 / Row::kPer16; ++i) Row::widen16(v[i], f + i * Row::kPer16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = k + i < K ? Row::widen(p[k + i]) : 0.f;
-  }
+  for (int i = 0; i < 8 / Row::kPer16; ++i) Row::widen16(v[i], f + i * Row::kPer16);
 }
 
 // MLORA_OK, or why the route is refused.

@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d)
   return (uint32_t)v;
 }
 
-template <typename Row, bool SILU, bool WIDE>
+template <typename Row, bool SILU>
 __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
   const uint32_t unit = (uint32_t)flat_group() * 16 + (threadIdx.x >> 4);
   if (unit >= a.units) return;  // whole rows of 16 lanes: the reduction stays in them
@@ -106,10 +106,10 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
   const int g = (int)(unit - (uint32_t)row * (uint32_t)a.groups);
   const int k = g * 128 + (threadIdx.x & 15) * 8;
   float v[8];
-  load8<Row, WIDE>(a.x, (int64_t)row * a.x_ld, k, a.K, v);
+  load8<Row>(a.x, (int64_t)row * a.x_ld, k, a.K, v);
   if constexpr (SILU) {
     float u[8];
-    load8<Row, WIDE>(a.up, (int64_t)row * a.up_ld, k, a.K, u);
+    load8<Row>(a.up, (int64_t)row * a.up_ld, k, a.K, u);
 #pragma unroll
     // the reciprocal is exact to one unit, as the quotient's last bits are not kept
     for (int i = 0; i < 8; ++i) v[i] = v[i] * __builtin_amdgcn_rcpf(1.f + expf(-v[i])) * u[i];
@@ -154,13 +154,13 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
     a.scales[(int64_t)g * a.n_rows + row] = bad ? __builtin_nanf("") : top / 448.f;
 }
 
-template <typename Row, bool SILU>
-void launch_quant(const QuantArgs& a, bool wide, hipStream_t s) {
+template <typename Row>
+void launch_quant(const QuantArgs& a, hipStream_t s) {
   const dim3 grid = flat_grid(((int64_t)a.units + 15) / 16);
-  if (wide)
-    hipLaunchKernelGGL((fp8_quant_kernel<Row, SILU, true>), grid, dim3(256), 0, s, a);
+  if (a.up)
+    hipLaunchKernelGGL((fp8_quant_kernel<Row, true>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((fp8_quant_kernel<Row, SILU, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((fp8_quant_kernel<Row, false>), grid, dim3(256), 0, s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -254,23 +254,21 @@ __device__ __forceinline__ int source_row(const GemmArgs& a, int r, int end) {
 
 // A lane's results from column n on, 4 or (a pair of tiles) 8 of them.
 template <typename Row, int C>
-__device__ __forceinline__ void store_columns(const GemmArgs& a, int64_t row, int n, const float* v,
-                                              bool wide) {
-  typename Row::elem* p = static_cast<typename Row::elem*>(a.out) + row * a.out_ld + n;
-  if (wide && n + C <= a.N) {
-    if constexpr (sizeof(typename Row::elem) == 4) {
+__device__ __forceinline__ void store_columns(const GemmArgs& a, int64_t row, int n, const float* v) {
+  typedef typename Row::elem elem;
+  elem* p = static_cast<elem*>(a.out) + row * a.out_ld + n;
+  if constexpr (C % Row::kPer16 == 0) {
 #pragma unroll
-      for (int i = 0; i < C; i += 4)
-        *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
-    } else if constexpr (C == 8) {
-      *reinterpret_cast<u32x4*>(p) = Row::narrow16(v);
-    } else {
-      *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-    }
+    for (int i = 0; i < C; i += Row::kPer16)
+      if (n + i < a.N) store16_any<Row>(p + i, a.N - n - i, Row::narrow16(v + i));
   } else {
+    if (n + 4 <= a.N) {
+      *reinterpret_cast<u32x2_any*>(p) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (n + i < a.N) p[i] = Row::narrow(v[i]);
+      for (int i = 0; i < 3; ++i)
+        if (n + i < a.N) p[i] = Row::narrow(v[i]);
+    }
   }
 }
 
@@ -287,7 +285,7 @@ __device__ __forceinline__ f32x4 block_products(const Fp8Frag& w, const Fp8Frag&
 // small to fill the chip with larger tiles. ks waves of a workgroup share a tile's
 // blocks and add their sums up in order.
 template <typename Row>
-__global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a, bool wide) {
+__global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
   __shared__ f32x4 part[8][64];
   const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
   const int nw = (int)(blockDim.x >> 6) / a.ks;
@@ -323,7 +321,7 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a, bool w
   }
   if (on && src >= 0) {
     const float v[4] = {acc[0], acc[1], acc[2], acc[3]};
-    store_columns<Row, 4>(a, row, fp8_column(nt, lane >> 4), v, wide);
+    store_columns<Row, 4>(a, row, fp8_column(nt, lane >> 4), v);
   }
 }
 
@@ -397,7 +395,7 @@ __device__ __forceinline__ void tile_block(const uint8_t* w, const uint8_t* x, i
 }
 
 template <typename Row, int WM, int WN, int MT, int NT>
-__global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs a, bool wide) {
+__global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs a) {
   typedef Tile<Row, WM, WN, MT, NT> T;
   extern __shared__ __attribute__((aligned(16))) uint8_t stage[];  // two
   const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
@@ -476,7 +474,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
       float v[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) v[c] = acc[i][j + c / 4][c % 4];
-      store_columns<Row, 8>(a, row, fp8_column(n0 + wn * NT + j, lane >> 4), v, wide);
+      store_columns<Row, 8>(a, row, fp8_column(n0 + wn * NT + j, lane >> 4), v);
     }
   }
 }
@@ -491,19 +489,19 @@ int64_t most_tiles(const GemmArgs& a, int size) {
 }
 
 template <typename Row, int WM, int WN, int MT, int NT>
-int32_t launch_tile(const char* who, GemmArgs a, bool wide, hipStream_t s) {
+int32_t launch_tile(const char* who, GemmArgs a, hipStream_t s) {
   typedef Tile<Row, WM, WN, MT, NT> T;
   const int64_t m_tiles = most_tiles(a, T::BM);
   a.n_groups = (a.NT * 16 + T::BN - 1) / T::BN;
   if (m_tiles * a.n_groups > kMaxTiles)
     return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
   hipLaunchKernelGGL((fp8_gemm_tile_kernel<Row, WM, WN, MT, NT>), flat_grid(m_tiles * a.n_groups + 7),
-                     dim3(64 * T::W), 2 * T::kStage, s, a, wide);
+                     dim3(64 * T::W), 2 * T::kStage, s, a);
   return launch_status(who);
 }
 
 template <typename Row>
-int32_t launch_stream(const char* who, GemmArgs a, bool wide, hipStream_t s) {
+int32_t launch_stream(const char* who, GemmArgs a, hipStream_t s) {
   const int64_t m_tiles = most_tiles(a, 16);
   a.ks = 1;
   while (a.ks < 8 && a.ks * 2 <= a.KB && m_tiles * a.NT * a.ks < 2048) a.ks *= 2;
@@ -512,7 +510,7 @@ int32_t launch_stream(const char* who, GemmArgs a, bool wide, hipStream_t s) {
   if (m_tiles * a.n_groups > kMaxTiles)
     return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
   hipLaunchKernelGGL((fp8_gemm_stream_kernel<Row>), flat_grid(m_tiles * a.n_groups + 7),
-                     dim3(64 * waves), 0, s, a, wide);
+                     dim3(64 * waves), 0, s, a);
   return launch_status(who);
 }
 
@@ -527,16 +525,16 @@ int32_t launch_stream(const char* who, GemmArgs a, bool wide, hipStream_t s) {
 //                        128: 259, 81, 62, 69, 67    256: 506, 151, 104, 103, 103
 //   768 -> 2048, 128 rows an expert: 249, 96, 78, 78, 73
 template <typename Row>
-int32_t launch_gemm(const char* who, const GemmArgs& a, bool wide, hipStream_t s) {
+int32_t launch_gemm(const char* who, const GemmArgs& a, hipStream_t s) {
   const int64_t spans = std::min(a.E, a.n_rows), mean = (a.n_rows + spans - 1) / spans;
   auto tiles = [&](int64_t bm, int64_t bn) {
     return spans * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn);
   };
-  if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row>(who, a, wide, s);
-  if (mean >= 128 && tiles(256, 256) >= 384) return launch_tile<Row, 4, 2, 4, 8>(who, a, wide, s);
-  if (mean >= 256 && tiles(128, 128) >= 512) return launch_tile<Row, 2, 2, 4, 4>(who, a, wide, s);
-  if (mean >= 24 && tiles(64, 128) >= 256) return launch_tile<Row, 2, 2, 2, 4>(who, a, wide, s);
-  return launch_tile<Row, 1, 4, 2, 2>(who, a, wide, s);
+  if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row>(who, a, s);
+  if (mean >= 128 && tiles(256, 256) >= 384) return launch_tile<Row, 4, 2, 4, 8>(who, a, s);
+  if (mean >= 256 && tiles(128, 128) >= 512) return launch_tile<Row, 2, 2, 4, 4>(who, a, s);
+  if (mean >= 24 && tiles(64, 128) >= 256) return launch_tile<Row, 2, 2, 2, 4>(who, a, s);
+  return launch_tile<Row, 1, 4, 2, 2>(who, a, s);
 }
 
 // Sizes of a route, or why they are refused.
@@ -651,22 +649,12 @@ extern "C" int32_t mlora_fp8_quant(const void* x, int64_t x_ld, const void* up, 
   if (n_rows * a.groups > 0xf0000000ll)
     return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
   a.units = (uint32_t)(n_rows * a.groups);
-  const int64_t per = dtype == MLORA_BF16 ? 8 : 4;
-  const bool wide = k % 8 == 0 && x_ld % per == 0 && aligned(x, 16) &&
-                    (!up || (up_ld % per == 0 && aligned(up, 16)));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (dtype == MLORA_BF16) {
-    if (up)
-      launch_quant<Bf16Row, true>(a, wide, s);
-    else
-      launch_quant<Bf16Row, false>(a, wide, s);
-  } else {
-    if (up)
-      launch_quant<F32Row, true>(a, wide, s);
-    else
-      launch_quant<F32Row, false>(a, wide, s);
-  }
+  if (dtype == MLORA_BF16)
+    launch_quant<Bf16Row>(a, s);
+  else
+    launch_quant<F32Row>(a, s);
   return launch_status(who);
 }
 
@@ -723,9 +711,8 @@ extern "C" int32_t mlora_fp8_gemm(const mlora_fp8_route* route, const uint8_t* q
   a.NB = (int32_t)blocks_of(route->n_out);
   a.KB = (int32_t)blocks_of(route->k_in);
   a.top_k = top_k;
-  const bool wide = out_ld % (out_dtype == MLORA_BF16 ? 8 : 4) == 0 && aligned(out, 16);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  return out_dtype == MLORA_BF16 ? launch_gemm<Bf16Row>(who, a, wide, s)
-                                 : launch_gemm<F32Row>(who, a, wide, s);
+  return out_dtype == MLORA_BF16 ? launch_gemm<Bf16Row>(who, a, s)
+                                 : launch_gemm<F32Row>(who, a, s);
 }

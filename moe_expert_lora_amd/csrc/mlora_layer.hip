@@ -127,7 +127,7 @@ __device__ __forceinline__ void choose_all(const LayerArgs& a, int* ids, float* 
 
 // XB: blocks of k a wave has at most, whose x it keeps in registers; 0: more, and x
 // is read again for each tile.
-template <typename Row, bool WIDE, int XB>
+template <typename Row, int XB>
 __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a) {
   extern __shared__ int lds[];
   constexpr int P = parts_of_x<Row>(), PA = parts_of_act<Row>();
@@ -151,13 +151,11 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = kb * 128 + g * 32 + j * 8;
-      if constexpr (P == 1 && WIDE) {
-        const uint16_t* x = static_cast<const uint16_t*>(a.x) + x_off + k;
-        xf[j][0] = u32x4{0, 0, 0, 0};
-        if (k < a.dim) xf[j][0] = *reinterpret_cast<const u32x4*>(x);
+      if constexpr (P == 1) {
+        xf[j][0] = load16_any<Row>(static_cast<const uint16_t*>(a.x) + x_off, k, a.dim);
       } else {
         float v[8];
-        load8<Row, WIDE>(a.x, x_off, k, a.dim, v);
+        load8<Row>(a.x, x_off, k, a.dim, v);
         split8<P>(v, xf[j]);
       }
     }
@@ -282,7 +280,7 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
 // splits write their sums past the caches, count themselves with an atomic, and only
 // the last one goes on (nothing waits).
 template <typename Row>
-__global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, int splits, bool wide) {
+__global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, int splits) {
   extern __shared__ int head[];
   __shared__ f32x4 part[kWaves][64];
   constexpr int PA = parts_of_act<Row>();
@@ -396,14 +394,16 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
   if (t >= a.T) return;
   const int n = fp8_column(nt, g);
   typename Row::elem* p = static_cast<typename Row::elem*>(a.out) + (int64_t)t * a.out_ld + n;
-  if (wide && n + 4 <= a.dim) {
-    if constexpr (sizeof(typename Row::elem) == 2)
-      *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])};
-    else
-      *reinterpret_cast<f32x4*>(p) = acc;
+  typedef typename Row::elem elem;
+  if (n + 4 <= a.dim) {
+    if constexpr (sizeof(elem) == 2) {
+      *reinterpret_cast<u32x2_any*>(p) = u32x2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])};
+    } else {
+      *reinterpret_cast<u32x4_any*>(p) = __builtin_bit_cast(u32x4, acc);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 3; ++i)
       if (n + i < a.dim) p[i] = Row::narrow(acc[i]);
   }
 }
@@ -454,7 +454,7 @@ int32_t check_layer(const char* who, int64_t n_tokens, int32_t n_experts, int32_
   return MLORA_OK;
 }
 
-template <typename Row, bool WIDE>
+template <typename Row>
 void launch_gate_up(const LayerArgs& a, hipStream_t s) {
   const Lds l = lds_of(a.T * a.k, a.E, a.max_active);
   const int64_t items = (int64_t)a.max_active * a.HB * 8;
@@ -465,26 +465,22 @@ void launch_gate_up(const LayerArgs& a, hipStream_t s) {
   const int blocks = (a.DB + kWaves - 1) / kWaves;  // a wave's
   constexpr bool kBf16 = sizeof(typename Row::elem) == 2;
   if (blocks <= 1)
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, WIDE, 1>), grid, block, l.total * 4, s, a);
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, 1>), grid, block, l.total * 4, s, a);
   else if (blocks <= 2)
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, WIDE, 2>), grid, block, l.total * 4, s, a);
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, 2>), grid, block, l.total * 4, s, a);
   else if (kBf16 && blocks <= 4)
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, WIDE, kBf16 ? 4 : 0>), grid, block, l.total * 4, s, a);
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, kBf16 ? 4 : 0>), grid, block, l.total * 4, s, a);
   else
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, WIDE, 0>), grid, block, l.total * 4, s, a);
+    hipLaunchKernelGGL((layer_gate_up_kernel<Row, 0>), grid, block, l.total * 4, s, a);
 }
 
 template <typename Row>
-int32_t launch_layer(const char* who, const LayerArgs& a, bool x_wide, bool out_wide,
-                     hipStream_t s) {
-  if (x_wide)
-    launch_gate_up<Row, true>(a, s);
-  else
-    launch_gate_up<Row, false>(a, s);
+int32_t launch_layer(const char* who, const LayerArgs& a, hipStream_t s) {
+  launch_gate_up<Row>(a, s);
   if (int32_t rc = launch_status(who)) return rc;
   const int splits = splits_of(a.T, a.E, a.k, a.dim, a.hidden);
   hipLaunchKernelGGL((layer_down_kernel<Row>), dim3(fp8_tiles(a.dim) * splits), dim3(64 * kWaves),
-                     (1 + a.max_active + a.max_active * (kTokens / 4)) * 4, s, a, splits, out_wide);
+                     (1 + a.max_active + a.max_active * (kTokens / 4)) * 4, s, a, splits);
   return launch_status(who);
 }
 
@@ -560,11 +556,8 @@ extern "C" int32_t mlora_moe_layer(const mlora_fp8_route* gate, const mlora_fp8_
   a.DB = (dim + 127) / 128;
   a.HB = (hidden + 127) / 128;
   a.max_active = std::min(E, a.T * top_k);
-  const int per = dtype == MLORA_BF16 ? 8 : 4;
-  const bool x_wide = dim % 8 == 0 && x_ld % per == 0 && aligned(x, 16);
-  const bool out_wide = out_ld % 4 == 0 && aligned(out, dtype == MLORA_BF16 ? 8 : 16);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  return dtype == MLORA_BF16 ? launch_layer<Bf16Row>(who, a, x_wide, out_wide, s)
-                             : launch_layer<F32Row>(who, a, x_wide, out_wide, s);
+  return dtype == MLORA_BF16 ? launch_layer<Bf16Row>(who, a, s)
+                             : launch_layer<F32Row>(who, a, s);
 }

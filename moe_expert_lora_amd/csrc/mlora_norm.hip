@@ -2,7 +2,6 @@
 // their gradients, for gfx950 (MI355X).
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "mlora_device.h"
 
@@ -15,9 +14,10 @@ namespace {
 //   x = r R(r) (wx + offset)
 // One pass: a row's values stay in registers from the first load to the last
 // store, as fp32; r enters the second norm unrounded. 64 to 1024 threads
-// hold a row, 8 values each (16 past 8192), and keep the weights from row to row; the two means are sums over them in a
-// fixed order. The gradients recompute r from the same inputs (which are read
-// for the norms' gradients anyway), so nothing is saved forward:
+// hold a row, 8 or 16 values each, and keep the weights from row to row; the two
+// means are sums over them in a fixed order. The gradients recompute r from the
+// same inputs (which are read for the norms' gradients anyway), so nothing is
+// saved forward:
 //   g = d_x (wx + offset), h = r R(r)
 //   d = d_r + R(r) (g - h mean(g h))              the gradient of r
 //   d_residual = residual_scale d, d_gate = y_scale d n, d_n = y_scale d gate
@@ -29,7 +29,6 @@ namespace {
 enum GateForm { kNoGate, kChannel, kToken, kFull };
 constexpr int kMaxDim = 16384;
 constexpr int kSums = 3;          // wx, wy, gate per channel
-constexpr int kMaxGroups = 512;  // groups of threads that write partial sums
 
 struct NormArgs {
   mlora_norm_block b;
@@ -45,76 +44,49 @@ struct NormArgs {
   bool past;              // the outputs are too large to be found in a cache later
 };
 
-// A thread's VPT values of a row: neighbours that fill 16 bytes (WIDE) or single
-// ones, threads in turn.
-template <typename Row, int TPR, int VPT, bool WIDE>
+// A thread's VPT values of a row: neighbours that fill 16 bytes, threads in turn.
+template <typename Row, int TPR, int VPT>
 struct Cols {
-  static constexpr int V = WIDE ? Row::kPer16 : 1;
+  typedef typename Row::elem elem;
+  static constexpr int V = Row::kPer16;
   static constexpr int CH = VPT / V;
   static __device__ __forceinline__ int col(int ch, int tid) { return (ch * TPR + tid) * V; }
 
   // A row as it is loaded, so that the next row's loads can be on their way.
-  typedef typename std::conditional<WIDE, u32x4, typename Row::elem>::type Piece;
   struct Raw {
-    Piece v[CH];
+    u32x4 v[CH];
   };
   static __device__ __forceinline__ void request(const void* base, int64_t off, int D, int tid, Raw& r) {
-    const typename Row::elem* p = static_cast<const typename Row::elem*>(base) + off;
+    const elem* p = static_cast<const elem*>(base) + off;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      r.v[c] = {};
-      if (col(c, tid) < D)
-        r.v[c] = __builtin_nontemporal_load(reinterpret_cast<const Piece*>(p + col(c, tid)));
-    }
+    for (int c = 0; c < CH; ++c) r.v[c] = load16_row<Row, true>(p, col(c, tid), D);
   }
-  static __device__ __forceinline__ void widen(const Raw& r, float (&f)[VPT]) {
+  static __device__ __forceinline__ void widen(const Raw& r, int D, int tid, float (&f)[VPT]) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if constexpr (WIDE)
-        Row::widen16(r.v[c], f + c * V);
-      else
-        f[c] = Row::widen(r.v[c]);
-    }
-  }
-  static __device__ __forceinline__ void load(const void* base, int64_t off, int D, int tid,
-                                              float (&f)[VPT]) {
-    Raw r;
-    request(base, off, D, tid, r);
-    widen(r, f);
+    for (int c = 0; c < CH; ++c) Row::widen16(row16_tail<Row>(r.v[c], col(c, tid), D), f + c * V);
   }
   // past: past the caches' keep
   static __device__ __forceinline__ void store(void* base, int64_t off, int D, int tid,
                                                const float (&f)[VPT], bool past) {
-    typename Row::elem* p = static_cast<typename Row::elem*>(base) + off;
+    elem* p = static_cast<elem*>(base) + off;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (col(c, tid) >= D) continue;
-      Piece v;
-      if constexpr (WIDE)
-        v = Row::narrow16(f + c * V);
-      else
-        v = Row::narrow(f[c]);
-      Piece* to = reinterpret_cast<Piece*>(p + col(c, tid));
+      const u32x4 v = Row::narrow16(f + c * V);
       if (past)
-        __builtin_nontemporal_store(v, to);
+        store16_any<Row, true>(p + col(c, tid), D - col(c, tid), v);
       else
-        *to = v;
+        store16_any<Row>(p + col(c, tid), D - col(c, tid), v);
     }
   }
   // fp32 vectors of the row's width
   static __device__ __forceinline__ void store_f32(float* p, int D, int tid, const float (&f)[VPT]) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (col(c, tid) >= D) continue;
-      if constexpr (WIDE) {
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int i = 0; i < V; i += 4)
-          *reinterpret_cast<f32x4*>(p + col(c, tid) + i) =
-              f32x4{f[c * V + i], f[c * V + i + 1], f[c * V + i + 2], f[c * V + i + 3]};
-      } else {
-        p[col(c, tid)] = f[c];
-      }
-    }
+      for (int i = 0; i < V; i += 4)
+        if (col(c, tid) + i < D)
+          store16_any<F32Row>(p + col(c, tid) + i, D - col(c, tid) - i, F32Row::narrow16(f + c * V + i));
   }
   // norm weights plus offset, of either type; null: 1. Zeros past the row.
   template <typename W>
@@ -123,24 +95,19 @@ struct Cols {
     const typename W::elem* p = static_cast<const typename W::elem*>(w);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      typedef typename W::elem vec __attribute__((ext_vector_type(V)));
-      const bool in = col(c, tid) < D;
-      vec v = {};
-      if (in) v = *reinterpret_cast<const vec*>(p + col(c, tid));
+      float g[V < W::kPer16 ? W::kPer16 : V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (V == 1)
-          f[c] = in ? W::widen(v[0]) + offset : 0.f;
-        else
-          f[c * V + i] = in ? W::widen(v[i]) + offset : 0.f;
-      }
+      for (int i = 0; i < V; i += W::kPer16)
+        W::widen16(load16_any<W>(p, col(c, tid) + i, D), g + i);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[c * V + i] = col(c, tid) + i < D ? g[i] + offset : 0.f;
     }
   }
   static __device__ __forceinline__ void load_weight(const void* w, int dtype, float offset, int D,
                                                      int tid, float (&f)[VPT]) {
     if (!w) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) f[i] = col(i / V, tid) < D ? 1.f : 0.f;
+      for (int i = 0; i < VPT; ++i) f[i] = col(i / V, tid) + i % V < D ? 1.f : 0.f;
     } else if (dtype == MLORA_F32) {
       load_weight_as<F32Row>(w, offset, D, tid, f);
     } else {
@@ -218,19 +185,19 @@ __device__ __forceinline__ void request_row(const NormArgs& a, int64_t row, int 
 }
 // The gate of each of the thread's values; a gate per channel is in in.gate already.
 template <typename C, int VPT>
-__device__ __forceinline__ void gate_of(const mlora_norm_block& b, const RowIn<C>& in,
+__device__ __forceinline__ void gate_of(const mlora_norm_block& b, const RowIn<C>& in, int tid,
                                         float (&f)[VPT]) {
   if (b.gate_form == kFull || b.gate_form == kChannel) {
-    C::widen(in.gate, f);
+    C::widen(in.gate, b.dim, tid, f);
   } else {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) f[i] = in.token_gate;
   }
 }
 
-template <typename Row, int TPR, int VPT, bool WIDE>
+template <typename Row, int TPR, int VPT>
 __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(NormArgs a) {
-  typedef Cols<Row, TPR, VPT, WIDE> C;
+  typedef Cols<Row, TPR, VPT> C;
   // of alternate rows: a wave may write the next row's sums while another reads
   __shared__ float sums[2][2][TPR / 64];
   const mlora_norm_block& b = a.b;
@@ -247,11 +214,11 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(NormArgs 
        row += groups, odd ^= 1) {
     request_row<Row, C>(a, row, tid, in);
     float r[VPT];
-    C::widen(in.residual, r);
+    C::widen(in.residual, b.dim, tid, r);
     if (b.y) {
       float y[VPT], gate[VPT], n[VPT];
-      C::widen(in.y, y);
-      gate_of<C, VPT>(b, in, gate);
+      C::widen(in.y, b.dim, tid, y);
+      gate_of<C, VPT>(b, in, tid, gate);
       norm_y<C, TPR, VPT>(b, y, wy, sums[odd][0], tid, n);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) r[i] = b.residual_scale * r[i] + b.y_scale * gate[i] * n[i];
@@ -272,9 +239,9 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(NormArgs 
   }
 }
 
-template <typename Row, int TPR, int VPT, bool WIDE>
+template <typename Row, int TPR, int VPT>
 __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs a) {
-  typedef Cols<Row, TPR, VPT, WIDE> C;
+  typedef Cols<Row, TPR, VPT> C;
   __shared__ float sums[2][5][TPR / 64];  // of alternate rows
   const mlora_norm_block& b = a.b;
   const int tid = threadIdx.x & (TPR - 1), D = b.dim;
@@ -288,26 +255,28 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs
 
   RowIn<C> in;
   if (b.gate_form == kChannel) C::request(b.gate, 0, D, tid, in.gate);
-  if (group < b.n_tokens) request_row<Row, C>(a, group, tid, in);
+  constexpr bool kAhead = VPT <= 8;  // 16 leave no registers for it
+  if (kAhead && group < b.n_tokens) request_row<Row, C>(a, group, tid, in);
   int odd = 0;
   for (int64_t row = group; row < b.n_tokens; row += groups, odd ^= 1) {
     float(*lds)[TPR / 64] = sums[odd];
+    if (!kAhead) request_row<Row, C>(a, row, tid, in);
     float r[VPT], y[VPT], d[VPT], g[VPT], gate[VPT], n[VPT];
-    C::widen(in.residual, r);
+    C::widen(in.residual, b.dim, tid, r);
     float Ry = 1.f;
     if (b.y) {
-      C::widen(in.y, y);
-      gate_of<C, VPT>(b, in, gate);
+      C::widen(in.y, b.dim, tid, y);
+      gate_of<C, VPT>(b, in, tid, gate);
     }
     if (a.d_r) {
-      C::widen(in.d_r, d);
+      C::widen(in.d_r, b.dim, tid, d);
     } else {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) d[i] = 0.f;
     }
-    if (a.d_x) C::widen(in.d_x, g);
+    if (a.d_x) C::widen(in.d_x, b.dim, tid, g);
     // the next row's loads are on their way through this row's sums
-    if (row + groups < b.n_tokens) request_row<Row, C>(a, row + groups, tid, in);
+    if (kAhead && row + groups < b.n_tokens) request_row<Row, C>(a, row + groups, tid, in);
     if (b.y) {
       Ry = norm_y<C, TPR, VPT>(b, y, wy, lds[0], tid, n);
 #pragma unroll
@@ -407,16 +376,17 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(SumArgs a) {
   if (c == 0 && out_col < a.dim) a.out[blockIdx.y][out_col] = s;
 }
 
-// Threads per row and values per thread: 8, as far as 1024 threads go.
+// Threads per row and values per thread: 8, as far as 1024 threads go; the gradients
+// hold twice as much a value, and take 16 in 512 threads rather than 8 in 1024.
 struct Shape {
   int tpr, vpt;
 };
-Shape shape_of(int dim) {
+Shape shape_of(int dim, bool backward) {
   if (dim <= 512) return {64, 8};
   if (dim <= 1024) return {128, 8};
   if (dim <= 2048) return {256, 8};
   if (dim <= 4096) return {512, 8};
-  if (dim <= 8192) return {1024, 8};
+  if (dim <= 8192) return backward ? Shape{512, 16} : Shape{1024, 8};
   return {1024, 16};
 }
 // Workgroups that go through n_tokens rows, at most `most`, each about as many.
@@ -425,65 +395,54 @@ int64_t grid_of(int64_t n_tokens, Shape h, int64_t most) {
   const int64_t turns = (groups + most - 1) / most;
   return (groups + turns - 1) / turns;
 }
+// Of the gradients: two waves a SIMD, since each group of threads writes sums of its own.
+// One, four and six a SIMD measured 45, 39 and 40 us where two take 32 (8192 rows of
+// 1024), 46, 45 and 45 for 37 (8000 rows of 300), 85, 89 and 103 for 85 (2000 rows of 8192).
 int64_t backward_grid(int64_t n_tokens, int dim) {
-  const Shape h = shape_of(dim);
-  return grid_of(n_tokens, h, kMaxGroups / rows_of(h.tpr));
+  const Shape h = shape_of(dim, true);
+  const int64_t waves = 2 * 4 * 256;
+  return grid_of(n_tokens, h, std::max<int64_t>(256, waves * 64 / threads_of(h.tpr)));
 }
 
-template <typename Row, int TPR, int VPT, bool WIDE>
+template <typename Row, int TPR, int VPT>
 void launch(const NormArgs& a, bool backward, hipStream_t s) {
   constexpr int threads = threads_of(TPR);
   const int64_t grid = backward ? backward_grid(a.b.n_tokens, a.b.dim)
                                 : grid_of(a.b.n_tokens, Shape{TPR, VPT}, 256 * 2048 / threads);
-  if (backward)
-    hipLaunchKernelGGL((norm_backward_kernel<Row, TPR, VPT, WIDE>), dim3((unsigned)grid),
-                       dim3(threads), 0, s, a);
-  else
-    hipLaunchKernelGGL((norm_forward_kernel<Row, TPR, VPT, WIDE>), dim3((unsigned)grid),
-                       dim3(threads), 0, s, a);
+  // shapes of one direction alone
+  constexpr bool kForward = !(TPR == 512 && VPT == 16), kBackward = !(TPR == 1024 && VPT == 8);
+  if constexpr (kBackward)
+    if (backward)
+      hipLaunchKernelGGL((norm_backward_kernel<Row, TPR, VPT>), dim3((unsigned)grid), dim3(threads),
+                         0, s, a);
+  if constexpr (kForward)
+    if (!backward)
+      hipLaunchKernelGGL((norm_forward_kernel<Row, TPR, VPT>), dim3((unsigned)grid), dim3(threads),
+                         0, s, a);
 }
 
-template <typename Row, bool WIDE>
+template <typename Row>
 void launch_shape(const NormArgs& a, bool backward, hipStream_t s) {
-  const Shape h = shape_of(a.b.dim);
-  if (h.tpr == 64) return launch<Row, 64, 8, WIDE>(a, backward, s);
-  if (h.tpr == 128) return launch<Row, 128, 8, WIDE>(a, backward, s);
-  if (h.tpr == 256) return launch<Row, 256, 8, WIDE>(a, backward, s);
-  if (h.tpr == 512) return launch<Row, 512, 8, WIDE>(a, backward, s);
-  if (h.vpt == 8) return launch<Row, 1024, 8, WIDE>(a, backward, s);
-  launch<Row, 1024, 16, WIDE>(a, backward, s);
+  const Shape h = shape_of(a.b.dim, backward);
+  if (h.tpr == 64) return launch<Row, 64, 8>(a, backward, s);
+  if (h.tpr == 128) return launch<Row, 128, 8>(a, backward, s);
+  if (h.tpr == 256) return launch<Row, 256, 8>(a, backward, s);
+  if (h.tpr == 512 && h.vpt == 8) return launch<Row, 512, 8>(a, backward, s);
+  if (h.tpr == 512) return launch<Row, 512, 16>(a, backward, s);
+  if (h.vpt == 8) return launch<Row, 1024, 8>(a, backward, s);
+  launch<Row, 1024, 16>(a, backward, s);
 }
-
-// Whether a matrix (null: any) allows 16-byte accesses.
-bool wide_rows(const void* p, int64_t ld, int per) { return !p || (ld % per == 0 && aligned(p, 16)); }
 
 // Rows past the size of the XCDs' L2s (8 of 4 MB) pass the caches by: 8192 rows of 4096
 // bf16 values 60 -> 56 us; smaller ones may still be there for the call that reads them.
 int32_t run(const char* who, NormArgs a, bool backward, hipStream_t s) {
   const mlora_norm_block& b = a.b;
   a.past = b.n_tokens * b.dim * (b.dtype == MLORA_BF16 ? 2 : 4) > (32ll << 20);
-  const int per = b.dtype == MLORA_BF16 ? 8 : 4;
-  const bool wide =
-      b.dim % per == 0 && wide_rows(b.residual, b.residual_ld, per) && wide_rows(b.y, b.y_ld, per) &&
-      (b.gate_form == kNoGate || b.gate_form == kToken ||
-       wide_rows(b.gate, b.gate_form == kFull ? b.gate_ld : 0, per)) &&
-      wide_rows(a.r, a.r_ld, per) && wide_rows(a.x, a.x_ld, per) && wide_rows(a.d_r, a.d_r_ld, per) &&
-      wide_rows(a.d_x, a.d_x_ld, per) && wide_rows(a.d_residual, a.d_residual_ld, per) &&
-      wide_rows(a.d_y, a.d_y_ld, per) && wide_rows(b.x_weight, 0, per) &&
-      wide_rows(b.y_weight, 0, per) &&
-      (b.gate_form != kFull || wide_rows(a.d_gate, a.d_gate_ld, per));
   (void)hipGetLastError();
-  if (b.dtype == MLORA_BF16) {
-    if (wide)
-      launch_shape<Bf16Row, true>(a, backward, s);
-    else
-      launch_shape<Bf16Row, false>(a, backward, s);
-  } else {
-    if (wide)
-      launch_shape<F32Row, true>(a, backward, s);
-    else
-      launch_shape<F32Row, false>(a, backward, s);
-  }
+  if (b.dtype == MLORA_BF16)
+    launch_shape<Bf16Row>(a, backward, s);
+  else
+    launch_shape<F32Row>(a, backward, s);
   return launch_status(who);
 }
 
@@ -541,7 +500,7 @@ extern "C" int32_t mlora_block_norm(const mlora_norm_block* block, void* r, int6
 
 extern "C" uint64_t mlora_block_norm_backward_workspace_bytes(int64_t n_tokens, int32_t dim) {
   if (n_tokens < 1 || n_tokens > kMaxRows || dim < 1 || dim > kMaxDim) return 0;
-  const uint64_t groups = backward_grid(n_tokens, dim) * rows_of(shape_of(dim).tpr);
+  const uint64_t groups = backward_grid(n_tokens, dim) * rows_of(shape_of(dim, true).tpr);
   return (kSums * groups * dim * 4 + 255) / 256 * 256;
 }
 
@@ -588,7 +547,7 @@ extern "C" int32_t mlora_block_norm_backward(
     a.d_y_ld = d_y_ld;
     a.d_gate = d_gate;
     a.d_gate_ld = d_gate_ld;
-    sa.groups = (int32_t)(backward_grid(block->n_tokens, dim) * rows_of(shape_of(dim).tpr));
+    sa.groups = (int32_t)(backward_grid(block->n_tokens, dim) * rows_of(shape_of(dim, true).tpr));
     for (int i = 0; i < kSums; ++i)
       if (sums[i])
         sa.partial[i] = a.partial[i] = static_cast<float*>(workspace) + (int64_t)i * sa.groups * dim;

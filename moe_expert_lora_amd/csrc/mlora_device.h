@@ -77,21 +77,24 @@ typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
 // 16 bytes of a row of `len` elements from element `at` on, as one access: past the
 // row's last 16 bytes those, which row16_tail moves to their place. So a row's loads
-// need no branch, and none waits for another. PAST: past the caches' keep.
-template <typename Row, bool PAST = false>
+// need no branch, and none waits for another. A row shorter than that (SHORT) goes an
+// element at a time. PAST: past the caches' keep.
+template <typename Row, bool SHORT, bool PAST = false>
 __device__ __forceinline__ u32x4 load16_row(const typename Row::elem* row, int at, int len) {
   constexpr int V = Row::kPer16;
-  if (len >= V) {
+  if constexpr (!SHORT) {
     const u32x4_any* p = reinterpret_cast<const u32x4_any*>(row + min(at, len - V));
     if constexpr (PAST) return __builtin_nontemporal_load(p);
     return *p;
-  }
-  u32x4 v = {0, 0, 0, 0};  // a row shorter than that, an element at a time
-  typedef typename std::conditional<V == 8, uint16_t, uint32_t>::type bits;
+  } else {
+    u32x4 v = {0, 0, 0, 0};
+    typedef typename std::conditional<V == 8, uint16_t, uint32_t>::type bits;
 #pragma unroll
-  for (int i = 0; i < V - 1; ++i)
-    if (at + i < len) v[i * 4 / V] |= (uint32_t)__builtin_bit_cast(bits, row[at + i]) << (16 * (i % (V / 4)));
-  return v;
+    for (int i = 0; i < V - 1; ++i)
+      if (at + i < len)
+        v[i * 4 / V] |= (uint32_t)__builtin_bit_cast(bits, row[at + i]) << (16 * (i % (V / 4)));
+    return v;
+  }
 }
 // What load16_row brought, with zeros for elements past the row.
 template <typename Row>
@@ -105,10 +108,6 @@ __device__ __forceinline__ u32x4 row16_tail(u32x4 v, int at, int len) {
   lo = s < 64 ? lo >> s | hi << (64 - s) : hi >> (s - 64);
   hi = s < 64 ? hi >> s : 0;
   return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
-template <typename Row>
-__device__ __forceinline__ u32x4 load16_any(const typename Row::elem* row, int at, int len) {
-  return row16_tail<Row>(load16_row<Row>(row, at, len), at, len);
 }
 // Stores a row's 16 bytes, of which `left` elements, at least one, are the row's.
 template <typename Row, bool PAST = false>

@@ -119,17 +119,38 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// 8 values of a row from column k on; zeros past K.
-template <typename Row>
-__device__ __forceinline__ void load8(const void* base, int64_t off, int k, int K, float* f) {
-  const typename Row::elem* p = static_cast<const typename Row::elem*>(base) + off;
-  u32x4 v[8 / Row::kPer16];
+// N times 8 neighbouring values of a row of K, the n-th from column k[n] on: asked
+// for, and with zeros past the row.
+template <typename Row, int N>
+struct Eights {
+  static constexpr int kVecs = 8 / Row::kPer16;
+  u32x4 v[N][kVecs];
+  template <bool SHORT>
+  __device__ __forceinline__ void request_as(const typename Row::elem* row, const int (&k)[N], int K) {
 #pragma unroll
-  for (int i = 0; i < 8 / Row::kPer16; ++i)
-    v[i] = load16_any<Row>(p, k + i * Row::kPer16, K);
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-  for (int i = 0; i < 8 / Row::kPer16; ++i) Row::widen16(v[i], f + i * Row::kPer16);
-}
+      for (int i = 0; i < kVecs; ++i)
+        v[n][i] = load16_row<Row, SHORT>(row, k[n] + i * Row::kPer16, K);
+  }
+  __device__ __forceinline__ void request(const void* row, const int (&k)[N], int K) {
+    const typename Row::elem* p = static_cast<const typename Row::elem*>(row);
+    if (K >= Row::kPer16)
+      request_as<false>(p, k, K);
+    else
+      request_as<true>(p, k, K);
+  }
+  __device__ __forceinline__ void finish(const int (&k)[N], int K) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) v[n][i] = row16_tail<Row>(v[n][i], k[n] + i * Row::kPer16, K);
+  }
+  __device__ __forceinline__ void widen(int n, float* f) const {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) Row::widen16(v[n][i], f + i * Row::kPer16);
+  }
+};
 
 // MLORA_OK, or why the route is refused.
 int32_t check_fp8_route(const char* who, const char* name, const mlora_fp8_route* r);

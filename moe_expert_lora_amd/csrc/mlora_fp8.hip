@@ -104,12 +104,18 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
   if (unit >= a.units) return;  // whole rows of 16 lanes: the reduction stays in them
   const int row = (int)(unit / (uint32_t)a.groups);
   const int g = (int)(unit - (uint32_t)row * (uint32_t)a.groups);
-  const int k = g * 128 + (threadIdx.x & 15) * 8;
+  typedef typename Row::elem elem;
+  const int k[1] = {g * 128 + (int)(threadIdx.x & 15) * 8};
+  Eights<Row, 1> x, up;
+  x.request(static_cast<const elem*>(a.x) + (int64_t)row * a.x_ld, k, a.K);
+  if constexpr (SILU) up.request(static_cast<const elem*>(a.up) + (int64_t)row * a.up_ld, k, a.K);
   float v[8];
-  load8<Row>(a.x, (int64_t)row * a.x_ld, k, a.K, v);
+  x.finish(k, a.K);
+  x.widen(0, v);
   if constexpr (SILU) {
     float u[8];
-    load8<Row>(a.up, (int64_t)row * a.up_ld, k, a.K, u);
+    up.finish(k, a.K);
+    up.widen(0, u);
 #pragma unroll
     // the reciprocal is exact to one unit, as the quotient's last bits are not kept
     for (int i = 0; i < 8; ++i) v[i] = v[i] * __builtin_amdgcn_rcpf(1.f + expf(-v[i])) * u[i];
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
   }
   u32x2 out = {pack_fp8(c[0], c[1], c[2], c[3]), pack_fp8(c[4], c[5], c[6], c[7])};
   if (bad) out = u32x2{0, 0};
-  *reinterpret_cast<u32x2*>(a.q + (int64_t)row * a.q_ld + k) = out;
+  *reinterpret_cast<u32x2*>(a.q + (int64_t)row * a.q_ld + k[0]) = out;
   if ((threadIdx.x & 15) == 0)
     a.scales[(int64_t)g * a.n_rows + row] = bad ? __builtin_nanf("") : top / 448.f;
 }

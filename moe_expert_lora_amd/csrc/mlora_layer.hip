@@ -147,24 +147,39 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
   const int t_col = lane & 15, g = lane >> 4;
   const int64_t x_off = (int64_t)min(t_col, a.T - 1) * a.x_ld;
   const int k0 = a.DB * wave / kWaves, k1 = a.DB * (wave + 1) / kWaves;
-  auto load_x = [&](int kb, u32x4 (&xf)[4][P]) {
+  typedef Eights<Row, 4> RawX;
+  const void* x = static_cast<const typename Row::elem*>(a.x) + x_off;
+  auto columns = [&](int kb, int (&k)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = kb * 128 + g * 32 + j * 8;
+  };
+  auto request_x = [&](int kb, RawX& raw) {
+    int k[4];
+    columns(kb, k);
+    raw.request(x, k, a.dim);
+  };
+  auto take_x = [&](int kb, RawX& raw, u32x4 (&xf)[4][P]) {
+    if (a.dim % 128 != 0) {
+      int k[4];
+      columns(kb, k);
+      raw.finish(k, a.dim);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int k = kb * 128 + g * 32 + j * 8;
       if constexpr (P == 1) {
-        xf[j][0] = load16_any<Row>(static_cast<const uint16_t*>(a.x) + x_off, k, a.dim);
+        xf[j][0] = raw.v[j][0];
       } else {
         float v[8];
-        load8<Row>(a.x, x_off, k, a.dim, v);
+        raw.widen(j, v);
         split8<P>(v, xf[j]);
       }
     }
   };
-  u32x4 xr[XB > 0 ? XB : 1][4][P];
+  RawX raw[XB > 0 ? XB : 1];
   auto request = [&] {
     if constexpr (XB > 0) {
 #pragma unroll
-      for (int b = 0; b < XB; ++b) load_x(min(k0 + b, a.DB - 1), xr[b]);
+      for (int b = 0; b < XB; ++b) request_x(min(k0 + b, a.DB - 1), raw[b]);
     }
   };
   if (a.E <= 128 && a.k <= 16)
@@ -200,6 +215,12 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
     for (int i = tid; i < active; i += 64 * kWaves) a.head[1 + i] = list[i];
     for (int i = tid; i < active * (kTokens / 4); i += 64 * kWaves)
       a.head[1 + a.max_active + i] = lds[l.slots + i];
+  }
+
+  u32x4 xr[XB > 0 ? XB : 1][4][P];
+  if constexpr (XB > 0) {
+#pragma unroll
+    for (int b = 0; b < XB; ++b) take_x(min(k0 + b, a.DB - 1), raw[b], xr[b]);
   }
 
   const int tiles = a.HB * 8;
@@ -238,7 +259,8 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
         const Fp8Frag gf = load_tile(gate_w, lane, in + kb * (8 * kFp8Tile));
         const Fp8Frag uf = load_tile(up_w, lane, in + kb * (8 * kFp8Tile));
         u32x4 xf[4][P];
-        load_x(kb, xf);
+        request_x(kb, raw[0]);
+        take_x(kb, raw[0], xf);
         add(kb, gf, uf, xf);
       }
     }

@@ -58,8 +58,13 @@ struct Cols {
   };
   static __device__ __forceinline__ void request(const void* base, int64_t off, int D, int tid, Raw& r) {
     const elem* p = static_cast<const elem*>(base) + off;
+    if (D >= V) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) r.v[c] = load16_row<Row, true>(p, col(c, tid), D);
+      for (int c = 0; c < CH; ++c) r.v[c] = load16_row<Row, false, true>(p, col(c, tid), D);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) r.v[c] = load16_row<Row, true>(p, col(c, tid), D);
+    }
   }
   static __device__ __forceinline__ void widen(const Raw& r, int D, int tid, float (&f)[VPT]) {
 #pragma unroll
@@ -93,12 +98,16 @@ struct Cols {
   static __device__ __forceinline__ void load_weight_as(const void* w, float offset, int D, int tid,
                                                         float (&f)[VPT]) {
     const typename W::elem* p = static_cast<const typename W::elem*>(w);
+    auto load = [&](const typename W::elem* p, int at) {
+      return D >= W::kPer16 ? row16_tail<W>(load16_row<W, false>(p, at, D), at, D)
+                            : load16_row<W, true>(p, at, D);
+    };
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float g[V < W::kPer16 ? W::kPer16 : V];
 #pragma unroll
       for (int i = 0; i < V; i += W::kPer16)
-        W::widen16(load16_any<W>(p, col(c, tid) + i, D), g + i);
+        W::widen16(load(p, col(c, tid) + i), g + i);
 #pragma unroll
       for (int i = 0; i < V; ++i) f[c * V + i] = col(c, tid) + i < D ? g[i] + offset : 0.f;
     }

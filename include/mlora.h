@@ -639,7 +639,11 @@ int32_t mlora_fp8_quant(const void* x, int64_t x_ld, const void* up, int64_t up_
  * sorted_ids == NULL: s = r (rows of an earlier product). expert_offsets == NULL:
  * one weight (n_experts == 1) for every row. Rows in no span, or whose s is
  * outside q, are left as they were. Offsets must be non-decreasing (other
- * contents stay in bounds but give unspecified rows).
+ * contents stay in bounds but give unspecified rows). For float32 results the
+ * products are exact and their sums fp32; for bf16 results eight neighbouring
+ * products are aligned to the largest of them and cut off below 2^-13 of its power
+ * of two before they are added, 1.5e-5 of the sum over random codes. A row's bits
+ * do not depend on the other rows' values. q spans 4 GiB at most.
  *   q         [q_rows, mlora_fp8_row_width(k_in)] codes and
  *   q_scales  [ceil(k_in / 128), q_rows], as mlora_fp8_quant writes them
  *   out       [n_rows, n_out] out_dtype */
@@ -659,7 +663,8 @@ uint64_t mlora_moe_layer_workspace_bytes(int64_t n_tokens, int32_t n_experts, in
  * e the j-th chosen expert and p its weight. gate and up are routes of
  * [hidden, dim], down of [dim, hidden]. Weights enter exactly, x is not
  * quantised; the activated row, times p, enters the last product to within 2^-16
- * (fp32: 2^-24) of each value; sums are fp32, one rounding. Values of x up to
+ * (fp32: 2^-24) of each value; sums are fp32, one rounding, and in an order that
+ * does not depend on the other tokens. Values of x up to
  * 2^117 in magnitude; a token with others, or with a NaN among its weights, gives
  * its own row no defined finite values, and other rows do not change.
  *   x, out      [n_tokens, dim] dtype
@@ -703,7 +708,7 @@ typedef struct mlora_norm_block {
  * x = r / rms(r) * (x_weight + offset), rms(v) = sqrt(mean(v^2) + eps), in fp32,
  * each output rounded once (x from the unrounded r). r, x [n_tokens, dim] dtype;
  * either may be NULL, and either may be the memory of residual or of y (with its
- * stride). */
+ * stride), but not both the same. */
 int32_t mlora_block_norm(const mlora_norm_block* block, void* r, int64_t r_ld, void* x,
                          int64_t x_ld, void* stream);
 
@@ -717,8 +722,9 @@ uint64_t mlora_block_norm_backward_workspace_bytes(int64_t n_tokens, int32_t dim
  *   d_x_weight, d_y_weight [dim] fp32, sums over the tokens (zeros for none)
  *   d_gate                 form 1: [dim] fp32, 2: one fp32 per token (d_gate_ld
  *                          apart), 3: [n_tokens, dim] dtype
- * The workspace (256-byte aligned) is needed for d_x_weight, d_y_weight and
- * d_gate of form 1; it needs no initialisation and is dead afterwards. */
+ * Two outputs may not be the same memory. The workspace (256-byte aligned) is
+ * needed for d_x_weight, d_y_weight and d_gate of form 1; it needs no
+ * initialisation, is dead afterwards, and calls that share it must be ordered. */
 int32_t mlora_block_norm_backward(const mlora_norm_block* block, const void* d_r, int64_t d_r_ld,
                                   const void* d_x, int64_t d_x_ld, void* d_residual,
                                   int64_t d_residual_ld, void* d_y, int64_t d_y_ld,

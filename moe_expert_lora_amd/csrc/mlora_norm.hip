@@ -545,6 +545,11 @@ extern "C" int32_t mlora_block_norm_backward(
                   (unsigned long long)(workspace ? workspace_bytes : 0), (unsigned long long)need);
     if (any && !aligned(workspace, 256))
       return fail(MLORA_ERR_INVALID, "%s: workspace must be 256-byte aligned", who);
+    const void* outputs[] = {d_residual, d_y, d_x_weight, d_y_weight, d_gate};
+    for (int i = 0; i < 5; ++i)
+      for (int j = 0; j < i; ++j)
+        if (outputs[i] && outputs[i] == outputs[j])
+          return fail(MLORA_ERR_INVALID, "%s: two outputs are the same memory", who);
     a.b = *block;
     a.d_r = d_r;
     a.d_r_ld = d_r_ld;

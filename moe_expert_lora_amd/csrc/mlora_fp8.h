@@ -118,6 +118,14 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
+// The same where loads write LDS: a workgroup fence would wait for all of them. The
+// wave's own LDS accesses are over; what the wave waited for, others may read.
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // LDS 0, the other counters at their maxima
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // N times 8 neighbouring values of a row of K, the n-th from column k[n] on: asked
 // for, and with zeros past the row.

@@ -195,67 +195,92 @@ struct GemmArgs {
 };
 
 // One tile: rows row .. end - 1 (as many as the tile takes of them) of expert e, and
-// the tile's number among the columns. e < 0: there are fewer tiles.
+// the tile's number among the columns. e < 0: there is none.
 struct Span {
   int e, row, end, n;
 };
 
-// Workgroup `group`'s tile among the spans' tiles of `size` rows by n_groups column
-// tiles, found by the wave together: 64 spans at a time, their tiles' prefix in the
-// lanes. The tiles of an XCD (every eighth workgroup) are neighbours, an eighth of
-// those that there are, so that they share rows and weights in its L2 and no XCD gets
-// more of them. Offsets past the rows count as the last row.
+// The spans, cut into tiles of `size` rows. Offsets past the rows count as the last row.
+struct Spans {
+  const int32_t* offsets;
+  int E, n_rows, size;
+};
+// Four times 64 spans in the lanes of a wave, all of them loaded at once.
+struct SpanRows {
+  static constexpr int kSpans = 256;
+  int lo[4], hi[4];
+  __device__ __forceinline__ void load(const Spans& s, int base) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = s.offsets[min(base + 64 * i + lane, s.E)];
+      hi[i] = s.offsets[min(base + 64 * i + lane + 1, s.E)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = min(max(lo[i], 0), s.n_rows);
+      hi[i] = base + 64 * i + lane < s.E ? min(max(hi[i], lo[i]), s.n_rows) : lo[i];
+    }
+  }
+  __device__ __forceinline__ int tiles(const Spans& s, int i) const {
+    return (hi[i] - lo[i] + s.size - 1) / s.size;
+  }
+};
+
+// Workgroup `group`'s tile, found by the wave together. The tiles of an XCD (every
+// eighth workgroup) are neighbours, an eighth of those that there are, so that they
+// share rows and weights in its L2 and no XCD gets more of them.
 __device__ __forceinline__ Span find_tile(const int32_t* offsets, int E, int n_rows, int size,
                                           int n_groups, int group) {
-  const int lane = threadIdx.x & 63;
-  auto span = [&](int e, int* lo, int* hi) {
-    *lo = *hi = 0;
-    if (e < E) {
-      *lo = min(max(offsets[e], 0), n_rows);
-      *hi = min(max(offsets[e + 1], *lo), n_rows);
-    }
-    return (*hi - *lo + size - 1) / size;
-  };
-  int total = 0, lo, hi;
-  if (!offsets) {
-    total = (n_rows + size - 1) / size;
-  } else {
-    for (int base = 0; base < E; base += 64) {
-      int sum;
-      wave_prefix(span(base + lane, &lo, &hi), &sum);
-      total += sum;
+  const Spans spans{offsets, E, n_rows, size};
+  SpanRows rows;
+  int total = (n_rows + size - 1) / size;
+  if (offsets) {
+    total = 0;
+    for (int base = 0; base < E; base += SpanRows::kSpans) {
+      rows.load(spans, base);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int sum;
+        wave_prefix(rows.tiles(spans, i), &sum);
+        total += sum;
+      }
     }
   }
   const int per = (int)(((int64_t)total * n_groups + 7) / 8);
   const int64_t at = (int64_t)(group % 8) * per + group / 8;
   if (group / 8 >= per || at >= (int64_t)total * n_groups) return Span{-1, 0, 0, 0};
-  int tile = (int)(at / n_groups);
-  const int n = (int)(at % n_groups);
+  int tile = (int)at / n_groups;
+  const int n = (int)at - tile * n_groups;
   if (!offsets) return Span{0, tile * size, n_rows, n};
-  for (int base = 0; base < E; base += 64) {
-    const int tiles = span(base + lane, &lo, &hi);
-    int sum;
-    const int before = wave_prefix(tiles, &sum);
-    if (tile < sum) {
-      const uint64_t here = __ballot(tile >= before && tile < before + tiles);
-      if (!here) break;  // sums past 32 bits, of offsets that are none
-      const int l = __builtin_ctzll(here);
-      const int row = __builtin_amdgcn_readlane(lo, l) +
-                      (tile - __builtin_amdgcn_readlane(before, l)) * size;
-      return Span{base + l, row, __builtin_amdgcn_readlane(hi, l), n};
+  for (int base = 0; base < E; base += SpanRows::kSpans) {
+    if (E > SpanRows::kSpans) rows.load(spans, base);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int sum;
+      const int tiles = rows.tiles(spans, i), before = wave_prefix(tiles, &sum);
+      if (tile >= 0 && tile < sum) {
+        const uint64_t here = __ballot(tile >= before && tile < before + tiles);
+        if (!here) return Span{-1, 0, 0, 0};  // sums past 32 bits, of offsets that are none
+        const int l = __builtin_ctzll(here);
+        const int row = __builtin_amdgcn_readlane(rows.lo[i], l) +
+                        (tile - __builtin_amdgcn_readlane(before, l)) * size;
+        return Span{base + 64 * i + l, row, __builtin_amdgcn_readlane(rows.hi[i], l), n};
+      }
+      tile -= sum;
     }
-    tile -= sum;
   }
   return Span{-1, 0, 0, 0};
 }
 
-// The q row that sorted row r reads; -1: none.
-__device__ __forceinline__ int source_row(const GemmArgs& a, int r, int end) {
-  if (r >= end) return -1;
-  if (!a.sorted_ids) return r < a.q_rows ? r : -1;
-  const int id = a.sorted_ids[r];
-  const int t = (int)((uint32_t)id / (uint32_t)a.top_k);
-  return id >= 0 && t < a.q_rows ? t : -1;
+// What names the q row that sorted row r reads (r past the rows: the last one's), and
+// that q row; -1: none.
+__device__ __forceinline__ int source_id(const GemmArgs& a, int r) {
+  return a.sorted_ids ? a.sorted_ids[min(r, a.n_rows - 1)] : r;
+}
+__device__ __forceinline__ int source_row(const GemmArgs& a, int id, int r, int end) {
+  const int t = a.sorted_ids ? (int)((uint32_t)id / (uint32_t)a.top_k) : id;
+  return r < end && id >= 0 && t < a.q_rows ? t : -1;
 }
 
 // A lane's results from column n on, 4 or (a pair of tiles) 8 of them.
@@ -301,7 +326,7 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
   const int nt = sp.n * nw + wave - kp * nw;
   const bool on = nt < a.NT;
   const int row = sp.row + (lane & 15);
-  const int src = source_row(a, row, sp.end);
+  const int src = source_row(a, source_id(a, row), row, sp.end);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   if (on) {
     const uint8_t* w =
@@ -333,25 +358,38 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
 
 // The same for spans of many rows: a workgroup of WM by WN waves makes a tile of
 // BM rows by BN columns, a wave MT by NT pieces of 16 by 16 of it. The blocks go
-// through two LDS stages: while one is multiplied the next is on its way, moved by
+// through LDS stages, two of rows and WS of weights: while one is multiplied the next is
+// on its way, the weights' (which are read from farthest) up to two blocks ahead, moved by
 // loads that write LDS themselves. Weights lie there as they are packed; a q row's
 // eight 16-byte pieces change places by the row's number (piece p of row r holds k
 // piece p ^ (r / 2 % 8)), so that 8 lanes read one row whole and the 16 rows of an
 // operand come from all 64 banks.
 //
-// 8192 rows of 4096 by 4096 x 4096 take 124 to 150 us, by the box's power (1.8 to 2.2
+// 8192 rows of 4096 by 4096 x 4096 take 124 to 140 us, by the box's power (2.0 to 2.2
 // PFLOP/s; a library's product of E4M3 with one scale: 102 us on one of them): the
 // clock falls to 1.85 GHz, and a block takes 3280 cycles of which the matrix
-// instructions fill 2048, the rest being the next block's latency, which 128 KB of LDS
-// allow to be requested one block ahead. Where in a block it is requested, and which
-// waves go first, made no difference; touching the lines of later blocks early cost
-// 10% and more, as a CU's requests are near their limit.
-template <typename Row, int WM, int WN, int MT, int NT>
+// instructions fill 2048, the rest being the next block's latency. The third stage of
+// weights, all that 160 KB of LDS have room for, took spans of 256 rows and 1024 columns
+// from 129 to 122 us. Where in a block it is requested, and which waves go first, made no
+// difference; touching the lines of later blocks early cost 10% and more, as a CU's
+// requests are near their limit. Of many spans a tile's start counts as well: its span
+// and its rows' numbers in one round trip each, shared through LDS, took 32768 rows of
+// 128 experts from 129 to 119 us, rows past a span's end that ask for nothing and are
+// not multiplied to 110 (by chance half of the spans have a tile of a few rows).
+// Workgroups that stay and ask for the next tile's first block before they store won
+// where tiles are alike (138 -> 137 us of the first case) and lost more where they are
+// not (2048 x 4096 weights: 196 -> 218), as they cannot take over from each other.
+template <typename Row, int WM, int WN, int MT, int NT, int WS>
 struct Tile {
   static constexpr int W = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16;
-  static constexpr int kStage = (BM + BN) * 128;  // bytes
+  static constexpr int kW = BN * 128, kX = BM * 128;  // bytes of a stage
+  static constexpr int kLds = WS * kW + 2 * kX;
   static constexpr int kWLoads = BN / 8 / W, kXLoads = BM / 8 / W;  // of 1 KB, a wave's
 };
+
+// The offset in q of a row that is not there: behind its end, where loads give zeros
+// without a request.
+constexpr uint32_t kNoRow = 0xffff8000u;
 
 // 16 bytes of each lane straight into LDS, lane l's at p + 16 l.
 __device__ __forceinline__ void to_lds(rsrc_t r, uint32_t lane_off, uint32_t off, uint8_t* p) {
@@ -400,15 +438,21 @@ __device__ __forceinline__ void tile_block(const uint8_t* w, const uint8_t* x, i
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <typename Row, int WM, int WN, int MT, int NT>
+template <typename Row, int WM, int WN, int MT, int NT, int WS>
 __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs a) {
-  typedef Tile<Row, WM, WN, MT, NT> T;
-  extern __shared__ __attribute__((aligned(16))) uint8_t stage[];  // two
-  const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
+  typedef Tile<Row, WM, WN, MT, NT, WS> T;
+  extern __shared__ __attribute__((aligned(16))) uint8_t stages[];  // of weights, then of rows
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i32(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const Span sp = find_tile(a.offsets, a.E, a.n_rows, T::BM, a.n_groups, flat_group());
   if (sp.e < 0) return;  // the whole workgroup
   const int n0 = sp.n * (T::BN / 16);  // in tiles of 16 columns
+
+  // the rows' q rows, one a thread, where the second block's rows go later
+  uint8_t* const x_stages = stages + WS * T::kW;
+  int* const source = reinterpret_cast<int*>(x_stages + T::kX);
+  if (tid < T::BM) source[tid] = source_row(a, source_id(a, sp.row + tid), sp.row + tid, sp.end);
+  __syncthreads();
 
   // what this wave moves: its share of the weights' and of the rows' kilobytes
   const int first = n0 / 8;  // block of 128 columns
@@ -426,27 +470,36 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
   uint32_t x_off[T::kXLoads];
 #pragma unroll
   for (int i = 0; i < T::kXLoads; ++i) {
-    const int r = (wave * T::kXLoads + i) * 8 + (lane >> 3);
-    const int src = max(source_row(a, sp.row + r, sp.end), 0);
-    x_off[i] = (uint32_t)src * (uint32_t)a.q_ld;
+    const int r = (wave * T::kXLoads + i) * 8 + (lane >> 3), src = source[r];
+    x_off[i] = src < 0 ? kNoRow : (uint32_t)src * (uint32_t)a.q_ld;
     asm volatile("" : "+v"(x_off[i]));  // else the sum takes two registers
     x_off[i] += ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
-  uint32_t s_off[MT];
+  uint32_t s_off[MT], there = 0;  // a bit for each of the pieces' rows that there are
   float xs[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    s_off[i] = 4u * max(source_row(a, sp.row + (wm * MT + i) * 16 + (lane & 15), sp.end), 0);
+  for (int i = 0; i < MT; ++i) {
+    const int src = source[(wm * MT + i) * 16 + (lane & 15)];
+    s_off[i] = 4u * max(src, 0);
+    there |= (src >= 0 ? 1u : 0u) << i;
+  }
   const float* w_scale =
       a.ws + ((int64_t)sp.e * a.NB + min((n0 + wn * NT) / 8, a.NB - 1)) * a.KB;
   float ws = 0.f;
-  auto request = [&](int kb, uint8_t* p) {
+  // past the last block, the last one again (into stages that nothing reads)
+  auto request_w = [&](int kb, int at) {
+    kb = min(kb, a.KB - 1);
 #pragma unroll
     for (int i = 0; i < T::kWLoads; ++i)
-      to_lds(w_buf, lane * 16, w_off[i] + kb * (8 * kFp8Tile), p + (wave * T::kWLoads + i) * 1024);
+      to_lds(w_buf, lane * 16, w_off[i] + kb * (8 * kFp8Tile),
+             stages + at * T::kW + (wave * T::kWLoads + i) * 1024);
+  };
+  auto request_x = [&](int kb) {
+    uint8_t* p = x_stages + (kb & 1) * T::kX;
+    kb = min(kb, a.KB - 1);
 #pragma unroll
     for (int i = 0; i < T::kXLoads; ++i)
-      to_lds(x_buf, x_off[i], kb * 128, p + T::BN * 128 + (wave * T::kXLoads + i) * 1024);
+      to_lds(x_buf, x_off[i], kb * 128, p + (wave * T::kXLoads + i) * 1024);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
       xs[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
@@ -459,22 +512,33 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  request(0, stage);
+  // a wave without rows leaves its matrix unit to the others (for fp32 results, whose
+  // products take twice as long, the branch costs more than it saves)
+  const bool live = sizeof(typename Row::elem) == 4 || sp.row + wm * MT * 16 < sp.end;
+  request_w(0, 0);
+  request_x(0);
+  __builtin_amdgcn_sched_barrier(0);  // the weights that need not be there are the last loads
+  if (WS == 3) request_w(1, 1);
+  int at = 0;  // the weights' stage
   for (int kb = 0; kb < a.KB; ++kb) {
-    wait_loads<0>();
-    lds_barrier();  // block kb has arrived, and the other stage is no longer read
-    const uint8_t* p = stage + (kb & 1) * T::kStage;
+    wait_loads<(WS - 2) * T::kWLoads>();
+    stage_barrier();  // block kb has arrived, and the stages to be filled are no longer read
     float s[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) s[i] = xs[i] * ws;
-    // past the last block, the last one again (into the stage that nothing reads)
-    request(min(kb + 1, a.KB - 1), stage + (~kb & 1) * T::kStage);
-    tile_block<Row, MT, NT>(p + wn * NT * kFp8Tile, p + T::BN * 128 + wm * MT * 16 * 128, lane, s, acc);
+    request_x(kb + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    request_w(kb + WS - 1, at == 0 ? WS - 1 : at - 1);
+    if (live)
+      tile_block<Row, MT, NT>(stages + at * T::kW + wn * NT * kFp8Tile,
+                              x_stages + (kb & 1) * T::kX + wm * MT * 16 * 128, lane, s, acc);
+    at = at == WS - 1 ? 0 : at + 1;
   }
+  wait_loads<0>();  // the stages are another workgroup's next
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int row = sp.row + (wm * MT + i) * 16 + (lane & 15);
-    if (source_row(a, row, sp.end) < 0) continue;
+    if (!(there >> i & 1)) continue;
 #pragma unroll
     for (int j = 0; j < NT; j += 2) {
       float v[8];
@@ -494,15 +558,15 @@ int64_t most_tiles(const GemmArgs& a, int size) {
   return (int64_t)a.n_rows / size + std::min(a.E, a.n_rows);
 }
 
-template <typename Row, int WM, int WN, int MT, int NT>
+template <typename Row, int WM, int WN, int MT, int NT, int WS>
 int32_t launch_tile(const char* who, GemmArgs a, hipStream_t s) {
-  typedef Tile<Row, WM, WN, MT, NT> T;
+  typedef Tile<Row, WM, WN, MT, NT, WS> T;
   const int64_t m_tiles = most_tiles(a, T::BM);
   a.n_groups = (a.NT * 16 + T::BN - 1) / T::BN;
   if (m_tiles * a.n_groups > kMaxTiles)
     return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<Row, WM, WN, MT, NT>), flat_grid(m_tiles * a.n_groups + 7),
-                     dim3(64 * T::W), 2 * T::kStage, s, a);
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<Row, WM, WN, MT, NT, WS>),
+                     flat_grid(m_tiles * a.n_groups + 7), dim3(64 * T::W), T::kLds, s, a);
   return launch_status(who);
 }
 
@@ -523,13 +587,14 @@ int32_t launch_stream(const char* who, GemmArgs a, hipStream_t s) {
 // The tile goes by the rows that a span has on average and by the tiles that they
 // make: large ones reuse more, but a span's last tile is half empty and the chip
 // wants two workgroups a CU. Measured, us, 16-row waves / tiles of 32, 64, 128 x 128
-// and 256 x 256 (bf16; one weight of 4096 x 4096, then 128 experts of 2048 x 768):
-//   rows of one weight   16: 5.8, 14, 17, 24, 46     64: 13, 21, 17, 25, 46
-//                        512: 80, 27, 27, 30, 50     2048: 291, 102, 61, 43, 55
-//                        8192: 1154, 526, 258, 159, 124
-//   rows of an expert    5: 31, 32, 32, 40, 57       32: 78, 41, 34, 45, 62
-//                        128: 259, 81, 62, 69, 67    256: 506, 151, 104, 103, 103
-//   768 -> 2048, 128 rows an expert: 249, 96, 78, 78, 73
+// and 256 x 256 (bf16, cold weights; one of 4096 x 4096, then 128 experts of 2048 x 768,
+// each token's experts by chance):
+//   rows of one weight   16: 6.1, 18, 18, 22, 32     64: 13, 18, 19, 23, 33
+//                        512: 78, 22, 23, 26, 53     2048: 290, 117, 63, 40, 57
+//                        8192: 1152, 542, 278, 171, 128
+//   rows of an expert    5: 42, 38, 37, 45, 49       32: 86, 51, 42, 49, 52
+//                        128: 264, 93, 73, 78, 66    256: 507, 157, 113, 109, 107
+//   768 -> 2048, 128 rows an expert: 246, 93, 77, 76, 74
 template <typename Row>
 int32_t launch_gemm(const char* who, const GemmArgs& a, hipStream_t s) {
   const int64_t spans = std::min(a.E, a.n_rows), mean = (a.n_rows + spans - 1) / spans;
@@ -537,10 +602,10 @@ int32_t launch_gemm(const char* who, const GemmArgs& a, hipStream_t s) {
     return spans * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn);
   };
   if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row>(who, a, s);
-  if (mean >= 128 && tiles(256, 256) >= 384) return launch_tile<Row, 4, 2, 4, 8>(who, a, s);
-  if (mean >= 256 && tiles(128, 128) >= 512) return launch_tile<Row, 2, 2, 4, 4>(who, a, s);
-  if (mean >= 24 && tiles(64, 128) >= 256) return launch_tile<Row, 2, 2, 2, 4>(who, a, s);
-  return launch_tile<Row, 1, 4, 2, 2>(who, a, s);
+  if (mean >= 128 && tiles(256, 256) >= 384) return launch_tile<Row, 4, 2, 4, 8, 3>(who, a, s);
+  if (mean >= 256 && tiles(128, 128) >= 512) return launch_tile<Row, 2, 2, 4, 4, 2>(who, a, s);
+  if (mean >= 24 && tiles(64, 128) >= 256) return launch_tile<Row, 2, 2, 2, 4, 2>(who, a, s);
+  return launch_tile<Row, 1, 4, 2, 2, 2>(who, a, s);
 }
 
 // Sizes of a route, or why they are refused.
@@ -696,7 +761,7 @@ extern "C" int32_t mlora_fp8_gemm(const mlora_fp8_route* route, const uint8_t* q
   if (!q || !q_scales || !out) return fail(MLORA_ERR_INVALID, "%s: NULL pointer", who);
   if (!aligned(q, 16)) return fail(MLORA_ERR_INVALID, "%s: q must be 16-byte aligned", who);
   const int64_t width = mlora_fp8_row_width(route->k_in);
-  if (q_ld > 0xffffffffll || (q_rows - 1) * q_ld + width > 0xffffffffll)
+  if (q_ld > kNoRow || (q_rows - 1) * q_ld + width > kNoRow)
     return fail(MLORA_ERR_INVALID, "%s: q spans more than 4 GiB; split the call", who);
   GemmArgs a{};
   a.q_bytes = (uint32_t)((q_rows - 1) * q_ld + width);

@@ -643,7 +643,7 @@ int32_t mlora_fp8_quant(const void* x, int64_t x_ld, const void* up, int64_t up_
  * products are exact and their sums fp32; for bf16 results eight neighbouring
  * products are aligned to the largest of them and cut off below 2^-13 of its power
  * of two before they are added, 1.5e-5 of the sum over random codes. A row's bits
- * do not depend on the other rows' values. q spans 4 GiB at most.
+ * do not depend on the other rows' values. q spans less than 4 GiB - 32 KB.
  *   q         [q_rows, mlora_fp8_row_width(k_in)] codes and
  *   q_scales  [ceil(k_in / 128), q_rows], as mlora_fp8_quant writes them
  *   out       [n_rows, n_out] out_dtype */

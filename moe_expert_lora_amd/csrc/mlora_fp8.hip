@@ -12,54 +12,81 @@ namespace {
 // ---------------------------------------------------------------------------
 //
 // A thread moves the 16 bytes of one lane and half (mlora_fp8.h). Forward, they
-// lie together in the source row; transposed, they are 16 rows of one column,
-// and 16 lanes of a wave read neighbouring columns.
+// lie together in the source row, at any address. Transposed, a workgroup takes one block of 128 x 128 through
+// LDS: rows of 128 neighbouring columns in, each thread's 16 bytes of a column out.
+// 128 weights of 2048 x 768 (201 MB each way): 77 to 96 us, transposed 76 (5.2 TB/s).
 
 struct Fp8PackArgs {
   const uint8_t* w;
   const float* scales;
   uint8_t* packed;
   float* packed_scales;
-  int64_t chunks, cells;  // 16-byte pieces of the weights, scales
+  int64_t cells;          // blocks, of as many scales
   int32_t N, K, NB, KB;   // of the packed (transposed) matrix
   int32_t transpose;
 };
 
-__global__ void __launch_bounds__(256) fp8_pack_kernel(Fp8PackArgs a) {
-  int64_t i = (int64_t)flat_group() * 256 + threadIdx.x;
-  if (i < a.chunks) {
-    const int lane = (int)(i & 63), half = (int)(i >> 6) & 1;
-    int64_t t = i >> 7;
-    const int part = (int)(t & 7);
-    t >>= 3;
-    const int kb = (int)(t % a.KB);
-    t /= a.KB;
-    const int nb = (int)(t % a.NB);
-    const int64_t e = t / a.NB;
-    const int r = lane & 15;
-    const int n = fp8_column(nb * 8 + part, r >> 2) + (r & 3), k = kb * 128 + (lane >> 4) * 32 + half * 16;
-    const uint8_t* src = a.w + e * a.N * a.K;
-    u32x4 v = {0, 0, 0, 0};
-    if (n < a.N && k < a.K) {
+typedef u32x4 u32x4_byte __attribute__((aligned(1)));
+
+// 16 bytes of a row of `len` from `at` on, zeros past it.
+__device__ __forceinline__ u32x4 load_codes(const uint8_t* row, int at, int len) {
+  u32x4 v = {0, 0, 0, 0};
+  if (at >= len) return v;
+  if (at + 16 <= len) return *reinterpret_cast<const u32x4_byte*>(row + at);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (k + j < a.K) {
-          const uint32_t b = a.transpose ? src[(int64_t)(k + j) * a.N + n] : src[(int64_t)n * a.K + k + j];
-          v[j / 4] |= b << (8 * (j % 4));
-        }
-      }
+  for (int j = 0; j < 15; ++j)
+    if (at + j < len) v[j / 4] |= (uint32_t)row[at + j] << (8 * (j % 4));
+  return v;
+}
+
+// Chunk c of a block of 128 x 128, 1024 of them: its column and its first k.
+__device__ __forceinline__ void pack_place(int c, int nb, int kb, int* n, int* k) {
+  const int lane = c & 63, half = (c >> 6) & 1, part = c >> 7, r = lane & 15;
+  *n = fp8_column(nb * 8 + part, r >> 2) + (r & 3);
+  *k = kb * 128 + (lane >> 4) * 32 + half * 16;
+}
+
+// One workgroup a block and its scale.
+__global__ void __launch_bounds__(256) fp8_pack_kernel(Fp8PackArgs a) {
+  __shared__ uint8_t tile[128][132];  // [k][n], transposed weights
+  const int64_t block = flat_group();
+  if (block >= a.cells) return;
+  const int tid = threadIdx.x;
+  const int kb = (int)(block % a.KB);
+  const int64_t t = block / a.KB;
+  const int nb = (int)(t % a.NB);
+  const int64_t e = t / a.NB;
+  const uint8_t* w = a.w + e * a.N * a.K;
+  if (tid == 0)
+    a.packed_scales[block] = a.scales[e * a.NB * a.KB + (a.transpose ? (int64_t)kb * a.NB + nb
+                                                                     : (int64_t)nb * a.KB + kb)];
+  uint8_t* out = a.packed + block * (8 * kFp8Tile);
+  if (a.transpose) {
+    const int n = tid % 8 * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = i * 32 + tid / 8;
+      u32x4 v = {0, 0, 0, 0};
+      if (kb * 128 + k < a.K)
+        v = load_codes(w + (int64_t)(kb * 128 + k) * a.N, nb * 128 + n, a.N);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(&tile[k][n + 4 * j]) = v[j];
     }
-    *reinterpret_cast<u32x4*>(a.packed + i * 16) = v;
-    return;
+    __syncthreads();
   }
-  i -= a.chunks;
-  if (i < a.cells) {
-    const int kb = (int)(i % a.KB);
-    const int64_t t = i / a.KB;
-    const int nb = (int)(t % a.NB);
-    const int64_t e = t / a.NB;
-    a.packed_scales[i] = a.scales[e * a.NB * a.KB + (a.transpose ? (int64_t)kb * a.NB + nb
-                                                                 : (int64_t)nb * a.KB + kb)];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = i * 256 + tid;
+    int n, k;
+    pack_place(c, nb, kb, &n, &k);
+    u32x4 v = {0, 0, 0, 0};
+    if (a.transpose) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j / 4] |= (uint32_t)tile[k % 128 + j][n % 128] << (8 * (j % 4));
+    } else if (n < a.N) {
+      v = load_codes(w + (int64_t)n * a.K, k, a.K);
+    }
+    *reinterpret_cast<u32x4*>(out + c * 16) = v;
   }
 }
 
@@ -667,14 +694,12 @@ extern "C" int32_t mlora_fp8_pack(const uint8_t* w, const float* scales, int32_t
   a.NB = (int32_t)blocks_of(n_out);
   a.KB = (int32_t)blocks_of(k_in);
   a.cells = (int64_t)n_experts * a.NB * a.KB;
-  a.chunks = a.cells * (8 * kFp8Tile / 16);
   a.packed = static_cast<uint8_t*>(packed);
-  a.packed_scales = reinterpret_cast<float*>(a.packed + a.chunks * 16);
+  a.packed_scales = reinterpret_cast<float*>(a.packed + a.cells * (8 * kFp8Tile));
   a.transpose = transpose != 0;
-  const int64_t groups = (a.chunks + a.cells + 255) / 256;
-  if (groups > kMaxRows) return fail(MLORA_ERR_INVALID, "%s: weights too large", who);
+  if (a.cells > kMaxRows) return fail(MLORA_ERR_INVALID, "%s: weights too large", who);
   (void)hipGetLastError();
-  hipLaunchKernelGGL(fp8_pack_kernel, flat_grid(groups), dim3(256), 0,
+  hipLaunchKernelGGL(fp8_pack_kernel, flat_grid(a.cells), dim3(256), 0,
                      reinterpret_cast<hipStream_t>(stream), a);
   if (int32_t rc = launch_status(who)) return rc;
   route->weights = a.packed;
@@ -762,7 +787,7 @@ extern "C" int32_t mlora_fp8_gemm(const mlora_fp8_route* route, const uint8_t* q
   if (!aligned(q, 16)) return fail(MLORA_ERR_INVALID, "%s: q must be 16-byte aligned", who);
   const int64_t width = mlora_fp8_row_width(route->k_in);
   if (q_ld > kNoRow || (q_rows - 1) * q_ld + width > kNoRow)
-    return fail(MLORA_ERR_INVALID, "%s: q spans more than 4 GiB; split the call", who);
+    return fail(MLORA_ERR_INVALID, "%s: q spans 4 GiB or nearly; split the call", who);
   GemmArgs a{};
   a.q_bytes = (uint32_t)((q_rows - 1) * q_ld + width);
   a.w = static_cast<const uint8_t*>(route->weights);

@@ -12,8 +12,9 @@ namespace {
 // ---------------------------------------------------------------------------
 //
 // A thread moves the 16 bytes of one lane and half (mlora_fp8.h). Forward, they
-// lie together in the source row, at any address. Transposed, a workgroup takes one block of 128 x 128 through
-// LDS: rows of 128 neighbouring columns in, each thread's 16 bytes of a column out.
+// lie together in the source row, at any address. Transposed, a workgroup takes its
+// block of 128 x 128 through LDS: rows of 128 neighbouring columns in, each thread's 16
+// bytes of a column out.
 // 128 weights of 2048 x 768 (201 MB each way): 77 to 96 us, transposed 76 (5.2 TB/s).
 
 struct Fp8PackArgs {
@@ -622,6 +623,10 @@ int32_t launch_stream(const char* who, GemmArgs a, hipStream_t s) {
 //   rows of an expert    5: 42, 38, 37, 45, 49       32: 86, 51, 42, 49, 52
 //                        128: 264, 93, 73, 78, 66    256: 507, 157, 113, 109, 107
 //   768 -> 2048, 128 rows an expert: 246, 93, 77, 76, 74
+// fp32 results take twice the matrix instructions, so small tiles go further (5 experts of
+// 1365 x 1000, 2001 rows: 31, 15.7, 17.9, 18.7, 43) and the largest has nothing left to
+// save (8192 rows of one 4096 x 4096: 263 of 128 x 128, 258 of 256 x 256 with registers
+// spilled): it is left out.
 template <typename Row>
 int32_t launch_gemm(const char* who, const GemmArgs& a, hipStream_t s) {
   const int64_t spans = std::min(a.E, a.n_rows), mean = (a.n_rows + spans - 1) / spans;
@@ -629,9 +634,12 @@ int32_t launch_gemm(const char* who, const GemmArgs& a, hipStream_t s) {
     return spans * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn);
   };
   if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row>(who, a, s);
-  if (mean >= 128 && tiles(256, 256) >= 384) return launch_tile<Row, 4, 2, 4, 8, 3>(who, a, s);
-  if (mean >= 256 && tiles(128, 128) >= 512) return launch_tile<Row, 2, 2, 4, 4, 2>(who, a, s);
-  if (mean >= 24 && tiles(64, 128) >= 256) return launch_tile<Row, 2, 2, 2, 4, 2>(who, a, s);
+  constexpr bool kBf16 = sizeof(typename Row::elem) == 2;
+  if constexpr (kBf16)
+    if (mean >= 128 && tiles(256, 256) >= 384) return launch_tile<Row, 4, 2, 4, 8, 3>(who, a, s);
+  if (mean >= 256 && tiles(128, 128) >= 448) return launch_tile<Row, 2, 2, 4, 4, 2>(who, a, s);
+  if (mean >= 24 && tiles(64, 128) >= (kBf16 ? 256 : 400))
+    return launch_tile<Row, 2, 2, 2, 4, 2>(who, a, s);
   return launch_tile<Row, 1, 4, 2, 2, 2>(who, a, s);
 }
 

@@ -96,12 +96,13 @@ __device__ __forceinline__ u32x4 load16_row(const typename Row::elem* row, int a
     return v;
   }
 }
-// What load16_row brought, with zeros for elements past the row.
-template <typename Row>
+// What load16_row brought, with zeros for elements past the row. LONG: the row is known
+// to have 16 bytes.
+template <typename Row, bool LONG = false>
 __device__ __forceinline__ u32x4 row16_tail(u32x4 v, int at, int len) {
   constexpr int V = Row::kPer16;
   const int past = at + V - len;  // elements past the row
-  if (past <= 0 || len < V) return v;
+  if (past <= 0 || (!LONG && len < V)) return v;
   if (past >= V) return u32x4{0, 0, 0, 0};
   const int s = past * (128 / V);
   uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;

@@ -50,6 +50,10 @@ struct Cols {
   typedef typename Row::elem elem;
   static constexpr int V = Row::kPer16;
   static constexpr int CH = VPT / V;
+  // More than 512 values a row (shape_of): no code for rows of less than a vector. Not of
+  // 1024 threads, whose few registers happen to be spilled worse without it (gradients of
+  // 2000 rows of 16384: 474 -> 630 us).
+  static constexpr bool kWide = TPR > 64 && TPR < 1024;
   static __device__ __forceinline__ int col(int ch, int tid) { return (ch * TPR + tid) * V; }
 
   // A row as it is loaded, so that the next row's loads can be on their way.
@@ -58,7 +62,7 @@ struct Cols {
   };
   static __device__ __forceinline__ void request(const void* base, int64_t off, int D, int tid, Raw& r) {
     const elem* p = static_cast<const elem*>(base) + off;
-    if (D >= V) {
+    if (kWide || D >= V) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) r.v[c] = load16_row<Row, false, true>(p, col(c, tid), D);
     } else {
@@ -68,7 +72,7 @@ struct Cols {
   }
   static __device__ __forceinline__ void widen(const Raw& r, int D, int tid, float (&f)[VPT]) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) Row::widen16(row16_tail<Row>(r.v[c], col(c, tid), D), f + c * V);
+    for (int c = 0; c < CH; ++c) Row::widen16(row16_tail<Row, kWide>(r.v[c], col(c, tid), D), f + c * V);
   }
   // past: past the caches' keep
   static __device__ __forceinline__ void store(void* base, int64_t off, int D, int tid,
@@ -99,7 +103,7 @@ struct Cols {
                                                         float (&f)[VPT]) {
     const typename W::elem* p = static_cast<const typename W::elem*>(w);
     auto load = [&](const typename W::elem* p, int at) {
-      return D >= W::kPer16 ? row16_tail<W>(load16_row<W, false>(p, at, D), at, D)
+      return kWide || D >= W::kPer16 ? row16_tail<W, kWide>(load16_row<W, false>(p, at, D), at, D)
                             : load16_row<W, true>(p, at, D);
     };
 #pragma unroll
@@ -189,6 +193,11 @@ __device__ __forceinline__ void request_row(const NormArgs& a, int64_t row, int 
   in.token_gate = 1.f;
   if (b.gate_form == kToken)
     in.token_gate = Row::widen(static_cast<const typename Row::elem*>(b.gate)[row * b.gate_ld]);
+}
+template <typename C>
+__device__ __forceinline__ void request_gradients(const NormArgs& a, int64_t row, int tid,
+                                                  RowIn<C>& in) {
+  const mlora_norm_block& b = a.b;
   if (a.d_r) C::request(a.d_r, row * a.d_r_ld, b.dim, tid, in.d_r);
   if (a.d_x) C::request(a.d_x, row * a.d_x_ld, b.dim, tid, in.d_x);
 }
@@ -264,8 +273,13 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs
 
   RowIn<C> in;
   if (b.gate_form == kChannel) C::request(b.gate, 0, D, tid, in.gate);
-  constexpr bool kAhead = VPT <= 8;  // 16 leave no registers for it
-  if (kAhead && group < b.n_tokens) request_row<Row, C>(a, group, tid, in);
+  // 8 values a thread leave registers for the next row's loads; 16 do not, nor for the
+  // gradients before they are needed (2000 rows of 8192 85 -> 74 us)
+  constexpr bool kAhead = VPT <= 8;
+  if (kAhead && group < b.n_tokens) {
+    request_row<Row, C>(a, group, tid, in);
+    request_gradients<C>(a, group, tid, in);
+  }
   int odd = 0;
   for (int64_t row = group; row < b.n_tokens; row += groups, odd ^= 1) {
     float(*lds)[TPR / 64] = sums[odd];
@@ -277,15 +291,21 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs
       C::widen(in.y, b.dim, tid, y);
       gate_of<C, VPT>(b, in, tid, gate);
     }
-    if (a.d_r) {
-      C::widen(in.d_r, b.dim, tid, d);
-    } else {
+    auto take_gradients = [&] {
+      if (a.d_r) {
+        C::widen(in.d_r, b.dim, tid, d);
+      } else {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) d[i] = 0.f;
-    }
-    if (a.d_x) C::widen(in.d_x, b.dim, tid, g);
+        for (int i = 0; i < VPT; ++i) d[i] = 0.f;
+      }
+      if (a.d_x) C::widen(in.d_x, b.dim, tid, g);
+    };
+    if (kAhead) take_gradients();
     // the next row's loads are on their way through this row's sums
-    if (kAhead && row + groups < b.n_tokens) request_row<Row, C>(a, row + groups, tid, in);
+    if (kAhead && row + groups < b.n_tokens) {
+      request_row<Row, C>(a, row + groups, tid, in);
+      request_gradients<C>(a, row + groups, tid, in);
+    }
     if (b.y) {
       Ry = norm_y<C, TPR, VPT>(b, y, wy, lds[0], tid, n);
 #pragma unroll
@@ -293,6 +313,10 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs
     } else {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) r[i] *= b.residual_scale;
+    }
+    if (!kAhead) {
+      request_gradients<C>(a, row, tid, in);
+      take_gradients();
     }
     if (a.d_x) {
       float s[2] = {0.f, 0.f};
@@ -405,8 +429,8 @@ int64_t grid_of(int64_t n_tokens, Shape h, int64_t most) {
   return (groups + turns - 1) / turns;
 }
 // Of the gradients: two waves a SIMD, since each group of threads writes sums of its own.
-// One, four and six a SIMD measured 45, 39 and 40 us where two take 32 (8192 rows of
-// 1024), 46, 45 and 45 for 37 (8000 rows of 300), 85, 89 and 103 for 85 (2000 rows of 8192).
+// One, two, four and six a SIMD measured 45, 32, 39 and 40 us (4096 rows of 2048), 46, 37,
+// 45 and 45 (8000 of 300), 71, 71, 89 and 103 (2000 of 8192) when this was chosen.
 int64_t backward_grid(int64_t n_tokens, int dim) {
   const Shape h = shape_of(dim, true);
   const int64_t waves = 2 * 4 * 256;

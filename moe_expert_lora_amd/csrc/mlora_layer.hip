@@ -126,8 +126,10 @@ __device__ __forceinline__ void choose_all(const LayerArgs& a, int* ids, float* 
 }
 
 // XB: blocks of k a wave has at most, whose x it keeps in registers; 0: more, and x
-// is read again for each tile.
-template <typename Row, int XB>
+// is read again for each tile. SHARE waves share a tile's blocks, and a workgroup takes
+// 8 / SHARE neighbouring tiles at a time: with fewer blocks than waves the others had
+// nothing to do (16 tokens, top 6 of 68, 154 -> 1153: 32 -> SHARED us).
+template <typename Row, int XB, int SHARE>
 __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a) {
   extern __shared__ int lds[];
   constexpr int P = parts_of_x<Row>(), PA = parts_of_act<Row>();
@@ -146,7 +148,9 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
 
   const int t_col = lane & 15, g = lane >> 4;
   const int64_t x_off = (int64_t)min(t_col, a.T - 1) * a.x_ld;
-  const int k0 = a.DB * wave / kWaves, k1 = a.DB * (wave + 1) / kWaves;
+  constexpr int kTiles = kWaves / SHARE;
+  const int sub = wave / SHARE, kp = wave % SHARE;
+  const int k0 = a.DB * kp / SHARE, k1 = a.DB * (kp + 1) / SHARE;
   typedef Eights<Row, 4> RawX;
   const void* x = static_cast<const typename Row::elem*>(a.x) + x_off;
   auto columns = [&](int kb, int (&k)[4]) {
@@ -223,12 +227,12 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
     for (int b = 0; b < XB; ++b) take_x(min(k0 + b, a.DB - 1), raw[b], xr[b]);
   }
 
-  const int tiles = a.HB * 8;
+  const int items = a.HB * 8 / kTiles;  // an expert's
   // One barrier an item: the sums of alternate items have LDS of their own, and half
   // of the waves finish an item while all go on to the next.
   int turn = 0;
-  for (int item = blockIdx.x; item < active * tiles; item += gridDim.x, turn ^= 1) {
-    const int at = item / tiles, nt = item - at * tiles;
+  for (int item = blockIdx.x; item < active * items; item += gridDim.x, turn ^= 1) {
+    const int at = item / items, nt0 = (item - at * items) * kTiles, nt = nt0 + sub;
     const int e = uniform_i32(list[at]);
     // a strip of 128 columns; a block past the wave's own is behind its end, and zeros
     const int64_t strip = ((int64_t)e * a.HB + nt / 8) * a.DB * (8 * kFp8Tile);
@@ -274,22 +278,26 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
     if ((wave >= kWaves / 2) == (turn == 1)) {
       const int id = tid & 255, t = id >> 4, c = id & 15;  // token and row of the tile
       const int src = (c & 3) * 64 + (c >> 2) * 16 + t;
-      float gate = 0.f, up = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        gate += p[(w * 2 + 0) * 256 + src];
-        up += p[(w * 2 + 1) * 256 + src];
-      }
       const int j = slots[at * kTokens + t];
-      if (j != kNone) {
-        const int slot = t * a.k + j;
-        float v = gate / (1.f + expf(-gate)) * up * wts[slot];
-        uint16_t* dst = a.act + (int64_t)slot * PA * (a.HB * 128) + fp8_column(nt, c >> 2) + (c & 3);
+      const int slot = t * a.k + j;
 #pragma unroll
-        for (int q = 0; q < PA; ++q) {
-          const uint16_t b = Bf16Row::narrow(v);
-          dst[(int64_t)q * (a.HB * 128)] = b;
-          v -= Bf16Row::widen(b);
+      for (int n = 0; n < kTiles; ++n) {
+        float gate = 0.f, up = 0.f;
+#pragma unroll
+        for (int w = n * SHARE; w < (n + 1) * SHARE; ++w) {
+          gate += p[(w * 2 + 0) * 256 + src];
+          up += p[(w * 2 + 1) * 256 + src];
+        }
+        if (j != kNone) {
+          float v = gate / (1.f + expf(-gate)) * up * wts[slot];
+          uint16_t* dst =
+              a.act + (int64_t)slot * PA * (a.HB * 128) + fp8_column(nt0 + n, c >> 2) + (c & 3);
+#pragma unroll
+          for (int q = 0; q < PA; ++q) {
+            const uint16_t b = Bf16Row::narrow(v);
+            dst[(int64_t)q * (a.HB * 128)] = b;
+            v -= Bf16Row::widen(b);
+          }
         }
       }
     }
@@ -476,24 +484,28 @@ int32_t check_layer(const char* who, int64_t n_tokens, int32_t n_experts, int32_
   return MLORA_OK;
 }
 
-template <typename Row>
-void launch_gate_up(const LayerArgs& a, hipStream_t s) {
+template <typename Row, int XB, int SHARE>
+void launch_gate_up_as(const LayerArgs& a, hipStream_t s) {
   const Lds l = lds_of(a.T * a.k, a.E, a.max_active);
-  const int64_t items = (int64_t)a.max_active * a.HB * 8;
+  const int64_t items = (int64_t)a.max_active * a.HB * SHARE;
   // Two workgroups a CU are there at once (16 of their waves hold their registers);
   // more would choose the experts again. Sixteen tokens, 256, 512, 768, 1024: the layer
   // 85, 82, 93, 95 us.
-  const dim3 grid((unsigned)std::min<int64_t>(items, 512)), block(64 * kWaves);
+  hipLaunchKernelGGL((layer_gate_up_kernel<Row, XB, SHARE>), dim3((unsigned)std::min<int64_t>(items, 512)),
+                     dim3(64 * kWaves), l.total * 4, s, a);
+}
+
+template <typename Row>
+void launch_gate_up(const LayerArgs& a, hipStream_t s) {
   const int blocks = (a.DB + kWaves - 1) / kWaves;  // a wave's
   constexpr bool kBf16 = sizeof(typename Row::elem) == 2;
-  if (blocks <= 1)
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, 1>), grid, block, l.total * 4, s, a);
-  else if (blocks <= 2)
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, 2>), grid, block, l.total * 4, s, a);
-  else if (kBf16 && blocks <= 4)
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, kBf16 ? 4 : 0>), grid, block, l.total * 4, s, a);
-  else
-    hipLaunchKernelGGL((layer_gate_up_kernel<Row, 0>), grid, block, l.total * 4, s, a);
+  if (a.DB == 1) return launch_gate_up_as<Row, 1, 1>(a, s);
+  if (a.DB == 2) return launch_gate_up_as<Row, 1, 2>(a, s);
+  if (a.DB <= 4) return launch_gate_up_as<Row, 1, 4>(a, s);
+  if (blocks <= 1) return launch_gate_up_as<Row, 1, 8>(a, s);
+  if (blocks <= 2) return launch_gate_up_as<Row, 2, 8>(a, s);
+  if (kBf16 && blocks <= 4) return launch_gate_up_as<Row, kBf16 ? 4 : 0, 8>(a, s);
+  launch_gate_up_as<Row, 0, 8>(a, s);
 }
 
 template <typename Row>

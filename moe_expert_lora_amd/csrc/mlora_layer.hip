@@ -128,7 +128,7 @@ __device__ __forceinline__ void choose_all(const LayerArgs& a, int* ids, float* 
 // XB: blocks of k a wave has at most, whose x it keeps in registers; 0: more, and x
 // is read again for each tile. SHARE waves share a tile's blocks, and a workgroup takes
 // 8 / SHARE neighbouring tiles at a time: with fewer blocks than waves the others had
-// nothing to do (16 tokens, top 6 of 68, 154 -> 1153: 32 -> SHARED us).
+// nothing to do (16 tokens, top 6 of 68, 154 -> 1153: the layer 34 -> 27 us).
 template <typename Row, int XB, int SHARE>
 __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a) {
   extern __shared__ int lds[];
@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
   bool more = active > 0;
   auto look = [&] {  // the wave's experts among the 64 from base on
     mine = base + lane < active ? list[base + lane] : 0;
-    first = (int)((uint32_t)(me - mine * a.HB + all * a.HB * kMaxExperts) % (uint32_t)all);
+    first = (int)(((uint32_t)(me - mine * a.HB) + (uint32_t)all * (uint32_t)a.HB * kMaxExperts) %
+                  (uint32_t)all);
     hits = __ballot(base + lane < active && first < a.HB);
   };
   auto next = [&] {  // the wave's next block, or more = false
@@ -416,10 +417,19 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
     if (uniform_i32(done) != splits - 1) return;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
     acc = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s)
+    constexpr int kTogether = 4;  // splits whose sums are on their way together
+    for (int s0 = 0; s0 < splits; s0 += kTogether) {
+      f32x4 v[kTogether];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[i] += __hip_atomic_load(&sums[s * 256 + i * 64 + lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int j = 0; j < kTogether; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[j][i] = __hip_atomic_load(&sums[min(s0 + j, splits - 1) * 256 + i * 64 + lane],
+                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j)
+        if (s0 + j < splits) acc += v[j];
+    }
   }
   if (t >= a.T) return;
   const int n = fp8_column(nt, g);
@@ -440,12 +450,13 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
 
 // Splits of the down product's blocks, so that there is a workgroup a CU, as long as
 // its waves have two blocks each. 128 tiles in 1, 2, 4 splits, the layer, us: one token
-// 20.7, 19.4, 20.3; sixteen 104, 82, 83; 448 tiles (dim 7168): 109, 110, 121.
+// 20.7, 19.4, 20.3; sixteen 104, 82, 83; 448 tiles (dim 7168): 109, 110, 121. Narrow
+// rows have few tiles (9 of 129 columns: 8 splits 18.6, 32 17.0).
 int splits_of(int64_t T, int64_t E, int64_t k, int64_t dim, int64_t hidden) {
   const int64_t tiles = fp8_tiles((int32_t)dim);
   const int64_t blocks = std::min(E, T * k) * ((hidden + 127) / 128);
   int s = 1;
-  while (s < 8 && tiles * s < 256 && blocks >= 2 * s * kWaves) s *= 2;
+  while (s < 32 && tiles * s < 256 && blocks >= 2 * s * kWaves) s *= 2;
   return s;
 }
 
@@ -459,7 +470,7 @@ LayerSpace space_of(int64_t T, int64_t E, int64_t k, int64_t dim, int64_t hidden
   LayerSpace s{};
   s.count = up((1 + active + active * (kTokens / 4)) * 4);
   s.sums = s.count + up(tiles * 4);
-  s.act = s.sums + tiles * 8 * 1024;
+  s.act = s.sums + tiles * splits_of(T, E, k, dim, hidden) * 1024;
   s.total = s.act + T * k * 3 * width * 2;
   return s;
 }
@@ -488,10 +499,13 @@ template <typename Row, int XB, int SHARE>
 void launch_gate_up_as(const LayerArgs& a, hipStream_t s) {
   const Lds l = lds_of(a.T * a.k, a.E, a.max_active);
   const int64_t items = (int64_t)a.max_active * a.HB * SHARE;
-  // Two workgroups a CU are there at once (16 of their waves hold their registers);
-  // more would choose the experts again. Sixteen tokens, 256, 512, 768, 1024: the layer
-  // 85, 82, 93, 95 us.
-  hipLaunchKernelGGL((layer_gate_up_kernel<Row, XB, SHARE>), dim3((unsigned)std::min<int64_t>(items, 512)),
+  // As many workgroups as are there at once: two a CU (16 of their waves hold their
+  // registers), one where x takes more than 128 registers. More would choose the experts
+  // again. Sixteen tokens, 256, 512, 768, 1024: the layer 85, 82, 93, 95 us; one fp32 token
+  // of 1834 -> 1010, 256 and 512: 25, 30.
+  constexpr int kXRegs = XB * (sizeof(typename Row::elem) == 2 ? 16 : 48);
+  hipLaunchKernelGGL((layer_gate_up_kernel<Row, XB, SHARE>),
+                     dim3((unsigned)std::min<int64_t>(items, kXRegs > 48 ? 256 : 512)),
                      dim3(64 * kWaves), l.total * 4, s, a);
 }
 

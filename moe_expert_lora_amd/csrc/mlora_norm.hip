@@ -23,8 +23,8 @@ namespace {
 //   d_residual = residual_scale d, d_gate = y_scale d n, d_n = y_scale d gate
 //   d_y = R(y) (u - v mean(u v)), u = d_n (wy + offset), v = y R(y)
 // Gradients of what all rows share (wx, wy, a gate per channel) are summed over a
-// thread's rows in registers, written once per group of threads, and added up by
-// a second kernel in a fixed order.
+// thread's rows in registers and over a workgroup's rows in LDS, written once per
+// workgroup, and added up by a second kernel in a fixed order.
 
 enum GateForm { kNoGate, kChannel, kToken, kFull };
 constexpr int kMaxDim = 16384;
@@ -40,7 +40,7 @@ struct NormArgs {
   int64_t d_r_ld, d_x_ld;
   void *d_residual, *d_y, *d_gate;
   int64_t d_residual_ld, d_y_ld, d_gate_ld;
-  float* partial[kSums];  // [groups][dim], null: not wanted
+  float* partial[kSums];  // [workgroups][dim], null: not wanted
   bool past;              // the outputs are too large to be found in a cache later
 };
 
@@ -371,9 +371,30 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(NormArgs
       static_cast<float*>(a.d_gate)[row * a.d_gate_ld] = s[0];
     if (a.d_gate && b.gate_form == kFull) C::store(a.d_gate, row * a.d_gate_ld, D, tid, n, a.past);
   }
-  if (a.partial[0]) C::store_f32(a.partial[0] + group * D, D, tid, sum_wx);
-  if (a.partial[1]) C::store_f32(a.partial[1] + group * D, D, tid, sum_wy);
-  if (a.partial[2]) C::store_f32(a.partial[2] + group * D, D, tid, sum_gate);
+  auto write_sum = [&](int which, float(&sum)[VPT]) {
+    if (!a.partial[which]) return;  // of the whole call
+    if constexpr (rows_of(TPR) > 1) {  // the workgroup's rows together, in their order
+      __shared__ float others[rows_of(TPR) - 1][VPT][TPR];
+      const int wave = threadIdx.x / TPR;
+      if (wave > 0) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) others[wave - 1][i][tid] = sum[i];
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int w = 0; w < rows_of(TPR) - 1; ++w)
+#pragma unroll
+          for (int i = 0; i < VPT; ++i) sum[i] += others[w][i][tid];
+      }
+      __syncthreads();
+      if (wave > 0) return;
+    }
+    C::store_f32(a.partial[which] + (int64_t)blockIdx.x * D, D, tid, sum);
+  };
+  write_sum(0, sum_wx);
+  write_sum(1, sum_wy);
+  write_sum(2, sum_gate);
 }
 
 // Column sums of the groups' partial sums: 32 columns a workgroup, 32 threads a
@@ -428,7 +449,7 @@ int64_t grid_of(int64_t n_tokens, Shape h, int64_t most) {
   const int64_t turns = (groups + most - 1) / most;
   return (groups + turns - 1) / turns;
 }
-// Of the gradients: two waves a SIMD, since each group of threads writes sums of its own.
+// Of the gradients: two waves a SIMD, since each workgroup writes sums of its own.
 // One, two, four and six a SIMD measured 45, 32, 39 and 40 us (4096 rows of 2048), 46, 37,
 // 45 and 45 (8000 of 300), 71, 71, 89 and 103 (2000 of 8192) when this was chosen.
 int64_t backward_grid(int64_t n_tokens, int dim) {
@@ -533,7 +554,7 @@ extern "C" int32_t mlora_block_norm(const mlora_norm_block* block, void* r, int6
 
 extern "C" uint64_t mlora_block_norm_backward_workspace_bytes(int64_t n_tokens, int32_t dim) {
   if (n_tokens < 1 || n_tokens > kMaxRows || dim < 1 || dim > kMaxDim) return 0;
-  const uint64_t groups = backward_grid(n_tokens, dim) * rows_of(shape_of(dim, true).tpr);
+  const uint64_t groups = backward_grid(n_tokens, dim);
   return (kSums * groups * dim * 4 + 255) / 256 * 256;
 }
 
@@ -585,7 +606,7 @@ extern "C" int32_t mlora_block_norm_backward(
     a.d_y_ld = d_y_ld;
     a.d_gate = d_gate;
     a.d_gate_ld = d_gate_ld;
-    sa.groups = (int32_t)(backward_grid(block->n_tokens, dim) * rows_of(shape_of(dim, true).tpr));
+    sa.groups = (int32_t)backward_grid(block->n_tokens, dim);
     for (int i = 0; i < kSums; ++i)
       if (sums[i])
         sa.partial[i] = a.partial[i] = static_cast<float*>(workspace) + (int64_t)i * sa.groups * dim;

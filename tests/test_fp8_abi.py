@@ -178,7 +178,7 @@ def test_norm_backward_refuses(lib, changed, bad):
 
 def test_norm_workspace(lib):
     need = ml.mlora_block_norm_backward_workspace_bytes(4, 64)
-    assert need % 256 == 0 and need >= 3 * 4 * 64 * 4
+    assert need % 256 == 0 and need >= 3 * 64 * 4  # three sums, of one workgroup at least
     b = _block()
     base = {**BACKWARD, "block": ctypes.byref(b)}
     _refused(lib, "mlora_block_norm_backward", base, dict(nbytes=need - 1), CAPACITY)

@@ -671,9 +671,9 @@ uint64_t mlora_moe_layer_workspace_bytes(int64_t n_tokens, int32_t n_experts, in
  *   logits      [n_tokens, n_experts] dtype
  *   indices, weights  [n_tokens, top_k]: the choice, as mlora_router_topk writes
  *               it; either may be NULL
- *   workspace   mlora_moe_layer_workspace_bytes bytes, 256-byte aligned; needs no
- *               initialisation, dead afterwards; calls that share it must be
- *               ordered */
+ *   workspace   mlora_moe_layer_workspace_bytes bytes (more tokens never need less),
+ *               256-byte aligned; needs no initialisation, dead afterwards; calls
+ *               that share it must be ordered */
 int32_t mlora_moe_layer(const mlora_fp8_route* gate, const mlora_fp8_route* up,
                         const mlora_fp8_route* down, const void* x, int64_t x_ld, int32_t dtype,
                         int64_t n_tokens, const void* logits, int64_t logits_ld, int32_t top_k,

@@ -1022,7 +1022,8 @@ def mlora_moe_layer(gate: Fp8Route, up: Fp8Route, down: Fp8Route, x, logits, out
                     stream=None) -> None:
     """A MoE layer of up to 16 tokens without adapters: the choice of
     mlora_router_topk from ``logits`` (written to ``indices`` and ``weights`` where
-    given), gate, up, silu, down and the weighted sum into ``out``."""
+    given), gate, up, silu, down and the weighted sum into ``out``. Calls that share
+    a workspace must be ordered; one of more tokens' size does for fewer."""
     (_bound or _load_native()).moe_layer(gate.address, up.address, down.address, x, logits, out,
                                          top_k, workspace, renormalize, indices, weights, stream)
 
@@ -1053,8 +1054,9 @@ def mlora_block_norm_backward(residual, d_r=None, d_x=None, d_residual=None, d_y
     """Gradients of mlora_block_norm for ``d_r`` and ``d_x`` (None: zeros) into the
     outputs that are given: ``d_residual`` and ``d_y`` (the rows' dtype, may be
     ``d_r`` or ``d_x``), ``d_x_weight`` and ``d_y_weight`` (float32), ``d_gate`` of
-    the gate's shape (float32; [n_tokens, dim]: the rows' dtype). The workspace is
-    needed for sums over the tokens."""
+    the gate's shape (float32; [n_tokens, dim]: the rows' dtype), no two of them the
+    same memory. The workspace is needed for sums over the tokens; calls that share it
+    must be ordered."""
     (_bound or _load_native()).block_norm_backward(
         residual, d_r, d_x, d_residual, d_y, d_x_weight, d_y_weight, d_gate, y, x_weight, y_weight,
         gate, residual_scale, y_scale, weight_offset, eps, workspace, stream)

@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
 // piece p ^ (r / 2 % 8)), so that 8 lanes read one row whole and the 16 rows of an
 // operand come from all 64 banks.
 //
-// 8192 rows of 4096 by 4096 x 4096 take 124 to 140 us, by the box's power (2.0 to 2.2
+// 8192 rows of 4096 by 4096 x 4096 take 124 to 140 us, by the card's power (2.0 to 2.2
 // PFLOP/s; a library's product of E4M3 with one scale: 102 us on one of them): the
 // clock falls to 1.85 GHz, and a block takes 3280 cycles of which the matrix
 // instructions fill 2048, the rest being the next block's latency. The third stage of

@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
     float* sums = a.sums + (int64_t)nt * splits * 256;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      __hip_atomic_store(&sums[split * 256 + i * 64 + lane], acc[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&sums[split * 256 + i * 64 + lane], acc[i], __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0: the sums are where every XCD sees them
     int done = 0;

@@ -60,7 +60,8 @@ struct Cols {
   struct Raw {
     u32x4 v[CH];
   };
-  static __device__ __forceinline__ void request(const void* base, int64_t off, int D, int tid, Raw& r) {
+  static __device__ __forceinline__ void request(const void* base, int64_t off, int D, int tid,
+                                                 Raw& r) {
     const elem* p = static_cast<const elem*>(base) + off;
     if (kWide || D >= V) {
 #pragma unroll
@@ -72,7 +73,8 @@ struct Cols {
   }
   static __device__ __forceinline__ void widen(const Raw& r, int D, int tid, float (&f)[VPT]) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) Row::widen16(row16_tail<Row, kWide>(r.v[c], col(c, tid), D), f + c * V);
+    for (int c = 0; c < CH; ++c)
+      Row::widen16(row16_tail<Row, kWide>(r.v[c], col(c, tid), D), f + c * V);
   }
   // past: past the caches' keep
   static __device__ __forceinline__ void store(void* base, int64_t off, int D, int tid,
@@ -95,7 +97,8 @@ struct Cols {
 #pragma unroll
       for (int i = 0; i < V; i += 4)
         if (col(c, tid) + i < D)
-          store16_any<F32Row>(p + col(c, tid) + i, D - col(c, tid) - i, F32Row::narrow16(f + c * V + i));
+          store16_any<F32Row>(p + col(c, tid) + i, D - col(c, tid) - i,
+                              F32Row::narrow16(f + c * V + i));
   }
   // norm weights plus offset, of either type; null: 1. Zeros past the row.
   template <typename W>

@@ -61,3 +61,11 @@ def test_norm_outputs_are_apart(lib, a, b):
             at["d_x_weight"], at["d_y_weight"], at["d_gate"], 64, P * 10, 1 << 40, None]
     assert lib.mlora_block_norm_backward(*args) == ml.MLORA_ERR_INVALID
     assert "same memory" in lib.mlora_last_error().decode()
+
+
+def test_layer_workspace_grows_with_the_tokens():
+    """One of 16 tokens' size does for fewer (the example's decode relies on it)."""
+    for E, k, dim, hidden in [(128, 8, 2048, 768), (12, 3, 1000, 365), (68, 6, 154, 1153),
+                              (1024, 64, 40, 24), (1, 1, 1, 1), (21, 4, 129, 1873)]:
+        sizes = [ml.mlora_moe_layer_workspace_bytes(t, E, k, dim, hidden) for t in range(1, 17)]
+        assert sizes == sorted(sizes)

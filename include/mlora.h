@@ -595,6 +595,7 @@ typedef struct mlora_fp8_route {
   int32_t n_experts;
   int32_t k_in;
   int32_t n_out;
+  int32_t fast_sums;  /* 0, as mlora_fp8_pack writes it, or 1: see mlora_fp8_gemm */
 } mlora_fp8_route;
 
 /* Bytes of the packed form; 0 for arguments mlora_fp8_pack refuses. */
@@ -639,11 +640,13 @@ int32_t mlora_fp8_quant(const void* x, int64_t x_ld, const void* up, int64_t up_
  * sorted_ids == NULL: s = r (rows of an earlier product). expert_offsets == NULL:
  * one weight (n_experts == 1) for every row. Rows in no span, or whose s is
  * outside q, are left as they were. Offsets must be non-decreasing (other
- * contents stay in bounds but give unspecified rows). For float32 results the
- * products are exact and their sums fp32; for bf16 results eight neighbouring
- * products are aligned to the largest of them and cut off below 2^-13 of its power
- * of two before they are added, 1.5e-5 of the sum over random codes. A row's bits
- * do not depend on the other rows' values. q spans less than 4 GiB - 32 KB.
+ * contents stay in bounds but give unspecified rows). The products are exact and
+ * their sums fp32. route->fast_sums == 1 (the caller sets it): for bf16 results
+ * the 8-bit matrix instruction adds, at twice the rate; of eight neighbouring
+ * products it keeps what is above 2^-13 of the largest one's power of two, so that
+ * a sum is off by 1.5e-5 of itself over random codes and by 7 * 2^-13 of the
+ * products' magnitudes at most. A row's bits do not depend on the other rows'
+ * values. q spans less than 4 GiB - 32 KB.
  *   q         [q_rows, mlora_fp8_row_width(k_in)] codes and
  *   q_scales  [ceil(k_in / 128), q_rows], as mlora_fp8_quant writes them
  *   out       [n_rows, n_out] out_dtype */

@@ -172,6 +172,7 @@ class Fp8Route(ctypes.Structure):
         ("n_experts", ctypes.c_int32),
         ("k_in", ctypes.c_int32),
         ("n_out", ctypes.c_int32),
+        ("fast_sums", ctypes.c_int32),
     ]
 
     @functools.cached_property
@@ -953,13 +954,18 @@ def mlora_fp8_row_width(k: int) -> int:
     return int(load().mlora_fp8_row_width(_i32(k, "k")))
 
 
-def make_fp8_route(w, scales, transpose: bool = False, stream=None) -> Fp8Route:
+def make_fp8_route(w, scales, transpose: bool = False, stream=None,
+                   fast_sums: bool = False) -> Fp8Route:
     """Packed route (mlora_fp8_pack) of 8-bit weights: ``w`` [n_experts, n_out,
     k_in] as float8_e4m3fn (or its bytes), ``scales`` float32 [n_experts,
     ceil(n_out / 128), ceil(k_in / 128)]. ``transpose``: of the transposed weights
     ([n_experts, n_out, k_in] holds the route's k_in before its n_out), for the
     gradient of the rows. The route keeps the packed tensor; the arguments are not
     needed once the call's work is done.
+
+    ``fast_sums``: bf16 results of mlora_fp8_gemm come from the 8-bit matrix
+    instruction, which adds eight neighbouring products in about 14 bits, at twice
+    the rate; without it, and for float32 results, sums are fp32.
 
     The packed tensor is written by and belongs to ``stream`` (None: the current
     one). Work on another stream has to wait for it, and ``stream`` for that work
@@ -989,6 +995,7 @@ def make_fp8_route(w, scales, transpose: bool = False, stream=None) -> Fp8Route:
                                ctypes.byref(route), _stream_handle(stream))
     if rc != MLORA_OK:
         raise _err(rc)
+    route.fast_sums = int(bool(fast_sums))
     route._keep = packed
     return route
 

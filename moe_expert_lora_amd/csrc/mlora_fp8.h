@@ -81,13 +81,14 @@ __device__ __forceinline__ Fp8Frag load_tile(rsrc_t r, int lane, uint32_t off) {
 }
 
 // 16 x 16 sums of 128 products of E4M3 codes; result i of lane l is row
-// 4 (l / 16) + i of the first operand by row l % 16 of the second. Either the
-// 8-bit instruction (block scales of 2^0): it aligns the products of 8 neighbouring
-// k to their largest and cuts them off below 2^-13 of its power of two, then adds in
-// fp32, so it is off by 1.5e-5 relative over random codes and by 7 * 2^-13 of the
-// sum of the products' magnitudes at most (measured), a fraction of a bf16 rounding.
-// Or, for fp32 results, bf16 values made of the codes (exact), at half the rate:
-// 9e-9 relative.
+// 4 (l / 16) + i of the first operand by row l % 16 of the second.
+// mfma_fp8: the 8-bit instruction (block scales of 2^0). It aligns the products of 8
+// neighbouring k to their largest and cuts them off below 2^-13 of its power of two,
+// then adds in fp32, so it is off by 1.5e-5 relative over random codes (the mean of the
+// errors is below 1e-7 of the magnitudes) and by 7 * 2^-13 of the sum of the products'
+// magnitudes at most (measured); the 8-bit forms without scales round the same.
+// mfma_fp8_as_bf16: bf16 values made of the codes (exact) and fp32 sums, 9e-9 relative,
+// at half the rate.
 __device__ __forceinline__ f32x4 mfma_fp8(const Fp8Frag& a, const Fp8Frag& b) {
   const i32x8 av = __builtin_bit_cast(i32x8, a), bv = __builtin_bit_cast(i32x8, b);
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,

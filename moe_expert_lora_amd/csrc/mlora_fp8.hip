@@ -331,10 +331,11 @@ __device__ __forceinline__ void store_columns(const GemmArgs& a, int64_t row, in
   }
 }
 
-// A block's products, as exact as the result's type asks for.
-template <typename Row>
+// A block's products: their sums in fp32, or (FAST, where the route asks for it) as the
+// 8-bit instruction makes them.
+template <bool FAST>
 __device__ __forceinline__ f32x4 block_products(const Fp8Frag& w, const Fp8Frag& q) {
-  if constexpr (sizeof(typename Row::elem) == 2)
+  if constexpr (FAST)
     return mfma_fp8(w, q);
   else
     return mfma_fp8_as_bf16(w, q);
@@ -343,7 +344,7 @@ __device__ __forceinline__ f32x4 block_products(const Fp8Frag& w, const Fp8Frag&
 // A wave makes 16 columns of 16 rows, operands straight from memory: for calls too
 // small to fill the chip with larger tiles. ks waves of a workgroup share a tile's
 // blocks and add their sums up in order.
-template <typename Row>
+template <typename Row, bool FAST>
 __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
   __shared__ f32x4 part[8][64];
   const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
       const Fp8Frag wf = load_frag(w + (int64_t)kb * (8 * kFp8Tile), 1024);
       const Fp8Frag qf = load_frag(q + kb * 128, 16);
       const float s = ws[kb] * qs[(int64_t)kb * a.q_rows];
-      const f32x4 p = block_products<Row>(wf, qf);
+      const f32x4 p = block_products<FAST>(wf, qf);
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[v] = fmaf(p[v], s, acc[v]);
     }
@@ -393,8 +394,9 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
 // piece p ^ (r / 2 % 8)), so that 8 lanes read one row whole and the 16 rows of an
 // operand come from all 64 banks.
 //
-// 8192 rows of 4096 by 4096 x 4096 take 124 to 140 us, by the card's power (2.0 to 2.2
-// PFLOP/s; a library's product of E4M3 with one scale: 102 us on one of them): the
+// 8192 rows of 4096 by 4096 x 4096 take 244 to 251 us with fp32 sums (128 x 128 tiles;
+// bf16 products of the library's rate would take 198). With fast sums (256 x 256 tiles)
+// they take 124 to 140 us, by the card's power (2.0 to 2.2 PFLOP/s; a library's product of E4M3 with one scale: 102 us on one of them): the
 // clock falls to 1.85 GHz, and a block takes 3280 cycles of which the matrix
 // instructions fill 2048, the rest being the next block's latency. The third stage of
 // weights, all that 160 KB of LDS have room for, took spans of 256 rows and 1024 columns
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
 // Workgroups that stay and ask for the next tile's first block before they store won
 // where tiles are alike (138 -> 137 us of the first case) and lost more where they are
 // not (2048 x 4096 weights: 196 -> 218), as they cannot take over from each other.
-template <typename Row, int WM, int WN, int MT, int NT, int WS>
+template <int WM, int WN, int MT, int NT, int WS>
 struct Tile {
   static constexpr int W = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16;
   static constexpr int kW = BN * 128, kX = BM * 128;  // bytes of a stage
@@ -428,7 +430,7 @@ __device__ __forceinline__ void to_lds(rsrc_t r, uint32_t lane_off, uint32_t off
 // One block of 128 k of a wave's pieces from a stage. The matrix instructions of one
 // column of pieces are issued between the multiply-adds of the column before, which
 // would wait for their results otherwise.
-template <typename Row, int MT, int NT>
+template <bool FAST, int MT, int NT>
 __device__ __forceinline__ void tile_block(const uint8_t* w, const uint8_t* x, int lane,
                                            const float (&s)[MT], f32x4 (&acc)[MT][NT]) {
   const int row = lane & 15, piece = (lane >> 4) * 2;
@@ -447,14 +449,14 @@ __device__ __forceinline__ void tile_block(const uint8_t* w, const uint8_t* x, i
     if (j + 1 < NT) wf[(j + 1) & 1] = load_frag(w + (j + 1) * kFp8Tile + lane * 16, 1024);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      if (j < NT) d[j & 1][i] = block_products<Row>(wf[j & 1], xf[i]);
+      if (j < NT) d[j & 1][i] = block_products<FAST>(wf[j & 1], xf[i]);
       if (j > 0) {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           acc[i][j - 1][v] = fmaf(d[(j - 1) & 1][i][v], s[i], acc[i][j - 1][v]);
       }
     }
-    if constexpr (sizeof(typename Row::elem) == 2) {
+    if constexpr (FAST) {
       if (j + 1 < NT) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -466,9 +468,9 @@ __device__ __forceinline__ void tile_block(const uint8_t* w, const uint8_t* x, i
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <typename Row, int WM, int WN, int MT, int NT, int WS>
+template <typename Row, bool FAST, int WM, int WN, int MT, int NT, int WS>
 __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs a) {
-  typedef Tile<Row, WM, WN, MT, NT, WS> T;
+  typedef Tile<WM, WN, MT, NT, WS> T;
   extern __shared__ __attribute__((aligned(16))) uint8_t stages[];  // of weights, then of rows
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i32(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -540,9 +542,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // a wave without rows leaves its matrix unit to the others (for fp32 results, whose
-  // products take twice as long, the branch costs more than it saves)
-  const bool live = sizeof(typename Row::elem) == 4 || sp.row + wm * MT * 16 < sp.end;
+  // a wave without rows leaves its matrix unit to the others (where a block's products
+  // take twice as long, the branch costs more than it saves)
+  const bool live = !FAST || sp.row + wm * MT * 16 < sp.end;
   request_w(0, 0);
   request_x(0);
   __builtin_amdgcn_sched_barrier(0);  // the weights that need not be there are the last loads
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
     __builtin_amdgcn_sched_barrier(0);
     request_w(kb + WS - 1, at == 0 ? WS - 1 : at - 1);
     if (live)
-      tile_block<Row, MT, NT>(stages + at * T::kW + wn * NT * kFp8Tile,
+      tile_block<FAST, MT, NT>(stages + at * T::kW + wn * NT * kFp8Tile,
                               x_stages + (kb & 1) * T::kX + wm * MT * 16 * 128, lane, s, acc);
     at = at == WS - 1 ? 0 : at + 1;
   }
@@ -586,19 +588,19 @@ int64_t most_tiles(const GemmArgs& a, int size) {
   return (int64_t)a.n_rows / size + std::min(a.E, a.n_rows);
 }
 
-template <typename Row, int WM, int WN, int MT, int NT, int WS>
+template <typename Row, bool FAST, int WM, int WN, int MT, int NT, int WS>
 int32_t launch_tile(const char* who, GemmArgs a, hipStream_t s) {
-  typedef Tile<Row, WM, WN, MT, NT, WS> T;
+  typedef Tile<WM, WN, MT, NT, WS> T;
   const int64_t m_tiles = most_tiles(a, T::BM);
   a.n_groups = (a.NT * 16 + T::BN - 1) / T::BN;
   if (m_tiles * a.n_groups > kMaxTiles)
     return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<Row, WM, WN, MT, NT, WS>),
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<Row, FAST, WM, WN, MT, NT, WS>),
                      flat_grid(m_tiles * a.n_groups + 7), dim3(64 * T::W), T::kLds, s, a);
   return launch_status(who);
 }
 
-template <typename Row>
+template <typename Row, bool FAST>
 int32_t launch_stream(const char* who, GemmArgs a, hipStream_t s) {
   const int64_t m_tiles = most_tiles(a, 16);
   a.ks = 1;
@@ -607,7 +609,7 @@ int32_t launch_stream(const char* who, GemmArgs a, hipStream_t s) {
   a.n_groups = (a.NT + waves / a.ks - 1) / (waves / a.ks);
   if (m_tiles * a.n_groups > kMaxTiles)
     return fail(MLORA_ERR_INVALID, "%s: too many rows for one call", who);
-  hipLaunchKernelGGL((fp8_gemm_stream_kernel<Row>), flat_grid(m_tiles * a.n_groups + 7),
+  hipLaunchKernelGGL((fp8_gemm_stream_kernel<Row, FAST>), flat_grid(m_tiles * a.n_groups + 7),
                      dim3(64 * waves), 0, s, a);
   return launch_status(who);
 }
@@ -615,7 +617,7 @@ int32_t launch_stream(const char* who, GemmArgs a, hipStream_t s) {
 // The tile goes by the rows that a span has on average and by the tiles that they
 // make: large ones reuse more, but a span's last tile is half empty and the chip
 // wants two workgroups a CU. Measured, us, 16-row waves / tiles of 32, 64, 128 x 128
-// and 256 x 256 (bf16, cold weights; one of 4096 x 4096, then 128 experts of 2048 x 768,
+// and 256 x 256 (bf16 with fast sums, cold weights; one of 4096 x 4096, then 128 experts of 2048 x 768,
 // each token's experts by chance):
 //   rows of one weight   16: 6.1, 18, 18, 22, 32     64: 13, 18, 19, 23, 33
 //                        512: 78, 22, 23, 26, 53     2048: 290, 117, 63, 40, 57
@@ -623,24 +625,25 @@ int32_t launch_stream(const char* who, GemmArgs a, hipStream_t s) {
 //   rows of an expert    5: 42, 38, 37, 45, 49       32: 86, 51, 42, 49, 52
 //                        128: 264, 93, 73, 78, 66    256: 507, 157, 113, 109, 107
 //   768 -> 2048, 128 rows an expert: 246, 93, 77, 76, 74
-// fp32 results take twice the matrix instructions, so small tiles go further (5 experts of
-// 1365 x 1000, 2001 rows: 31, 15.7, 17.9, 18.7, 43) and the largest has nothing left to
-// save (8192 rows of one 4096 x 4096: 263 of 128 x 128, 258 of 256 x 256 with registers
-// spilled): it is left out.
-template <typename Row>
+// fp32 sums take twice the matrix instructions, so small tiles go further (5 experts of
+// 1365 x 1000, 2001 rows, fp32 results: 31, 15.7, 17.9, 18.7, 43) and the largest has
+// nothing left to save (8192 rows of one 4096 x 4096, bf16: 244 of 128 x 128, 261 of 256 x
+// 256 with registers spilled): it is left out.
+template <typename Row, bool FAST>
 int32_t launch_gemm(const char* who, const GemmArgs& a, hipStream_t s) {
   const int64_t spans = std::min(a.E, a.n_rows), mean = (a.n_rows + spans - 1) / spans;
   auto tiles = [&](int64_t bm, int64_t bn) {
     return spans * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn);
   };
-  if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row>(who, a, s);
-  constexpr bool kBf16 = sizeof(typename Row::elem) == 2;
-  if constexpr (kBf16)
-    if (mean >= 128 && tiles(256, 256) >= 384) return launch_tile<Row, 4, 2, 4, 8, 3>(who, a, s);
-  if (mean >= 256 && tiles(128, 128) >= 448) return launch_tile<Row, 2, 2, 4, 4, 2>(who, a, s);
-  if (mean >= 24 && tiles(64, 128) >= (kBf16 ? 256 : 400))
-    return launch_tile<Row, 2, 2, 2, 4, 2>(who, a, s);
-  return launch_tile<Row, 1, 4, 2, 2, 2>(who, a, s);
+  if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row, FAST>(who, a, s);
+  if constexpr (FAST)
+    if (mean >= 128 && tiles(256, 256) >= 384)
+      return launch_tile<Row, FAST, 4, 2, 4, 8, 3>(who, a, s);
+  if (mean >= 256 && tiles(128, 128) >= 448)
+    return launch_tile<Row, FAST, 2, 2, 4, 4, 2>(who, a, s);
+  if (mean >= 24 && tiles(64, 128) >= (FAST ? 256 : 400))
+    return launch_tile<Row, FAST, 2, 2, 2, 4, 2>(who, a, s);
+  return launch_tile<Row, FAST, 1, 4, 2, 2, 2>(who, a, s);
 }
 
 // Sizes of a route, or why they are refused.
@@ -663,6 +666,9 @@ int32_t check_fp8_route(const char* who, const char* name, const mlora_fp8_route
   if (int32_t rc = check_sizes(who, r->n_experts, r->k_in, r->n_out)) return rc;
   if (!r->weights || !r->scales || !aligned(r->weights, 16) || !aligned(r->scales, 4))
     return fail(MLORA_ERR_INVALID, "%s: %s route without packed weights", who, name);
+  if (r->fast_sums != 0 && r->fast_sums != 1)
+    return fail(MLORA_ERR_INVALID, "%s: %s route's fast_sums=%d is neither 0 nor 1", who, name,
+                r->fast_sums);
   return MLORA_OK;
 }
 
@@ -715,6 +721,7 @@ extern "C" int32_t mlora_fp8_pack(const uint8_t* w, const float* scales, int32_t
   route->n_experts = n_experts;
   route->k_in = k_in;
   route->n_out = n_out;
+  route->fast_sums = 0;
   return MLORA_OK;
 }
 
@@ -817,6 +824,7 @@ extern "C" int32_t mlora_fp8_gemm(const mlora_fp8_route* route, const uint8_t* q
   a.top_k = top_k;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  return out_dtype == MLORA_BF16 ? launch_gemm<Bf16Row>(who, a, s)
-                                 : launch_gemm<F32Row>(who, a, s);
+  if (out_dtype == MLORA_F32) return launch_gemm<F32Row, false>(who, a, s);
+  return route->fast_sums ? launch_gemm<Bf16Row, true>(who, a, s)
+                          : launch_gemm<Bf16Row, false>(who, a, s);
 }

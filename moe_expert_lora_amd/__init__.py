@@ -328,6 +328,13 @@ def _err(code: int) -> MloraError:
     return MloraError(code, load().mlora_last_error().decode(errors="replace"))
 
 
+def _address(route, kind, name: str) -> int:
+    """Address of a route of the class whose memory the call reads."""
+    if not isinstance(route, kind):
+        raise TypeError(f"{name} must be a {kind.__name__}, not {type(route).__name__}")
+    return route.address
+
+
 def _arr(a, dtype) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=dtype))
 
@@ -935,8 +942,8 @@ def mlora_w4_gather_gemv(route: W4Route, x, out, ids=None, top_k: int = 1,
                          x_by_row: bool = False, stream=None) -> None:
     """``out[r]`` = W[ids[r]] x[r // top_k] (or x[r] with ``x_by_row``); rows with
     an id outside the route's experts get zeros. ``ids`` None: one weight."""
-    (_bound or _load_native()).w4_gather_gemv(route.address, x, out, ids, top_k, x_by_row,
-                                              stream)
+    at = _address(route, W4Route, "route")
+    (_bound or _load_native()).w4_gather_gemv(at, x, out, ids, top_k, x_by_row, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -1012,8 +1019,9 @@ def mlora_fp8_gemm(route: Fp8Route, q, q_scales, out, expert_offsets=None, sorte
     """``out[r]`` = W_e q[sorted_ids[r] // top_k] (``sorted_ids`` None: q[r]) for the
     rows of each expert's span of ``expert_offsets`` (None: one weight for all);
     rows in no span are left as they were."""
-    (_bound or _load_native()).fp8_gemm(route.address, q, q_scales, out, expert_offsets,
-                                        sorted_ids, top_k, stream)
+    at = _address(route, Fp8Route, "route")
+    (_bound or _load_native()).fp8_gemm(at, q, q_scales, out, expert_offsets, sorted_ids, top_k,
+                                        stream)
 
 
 def mlora_moe_layer_workspace_bytes(n_tokens: int, n_experts: int, top_k: int, dim: int,
@@ -1031,8 +1039,10 @@ def mlora_moe_layer(gate: Fp8Route, up: Fp8Route, down: Fp8Route, x, logits, out
     mlora_router_topk from ``logits`` (written to ``indices`` and ``weights`` where
     given), gate, up, silu, down and the weighted sum into ``out``. Calls that share
     a workspace must be ordered; one of more tokens' size does for fewer."""
-    (_bound or _load_native()).moe_layer(gate.address, up.address, down.address, x, logits, out,
-                                         top_k, workspace, renormalize, indices, weights, stream)
+    at = (_address(gate, Fp8Route, "gate"), _address(up, Fp8Route, "up"),
+          _address(down, Fp8Route, "down"))
+    (_bound or _load_native()).moe_layer(*at, x, logits, out, top_k, workspace, renormalize,
+                                         indices, weights, stream)
 
 
 def mlora_block_norm(residual, r=None, x=None, y=None, x_weight=None, y_weight=None, gate=None,

@@ -27,3 +27,27 @@ def test_sums_are_fast_or_not(lib, fast):
 def test_a_route_keeps_its_size():
     """The choice of sums takes what was padding."""
     assert ctypes.sizeof(ml.Fp8Route) == 32 and ml.Fp8Route.fast_sums.offset == 28
+
+
+# a route of another class, its address alone, nothing
+NOT_W4 = [ml.Fp8Route(P, P, 4, 256, 100), ml.ExpertRoute(), ml.MultiRoute(), P, None]
+NOT_FP8 = [ml.W4Route(P, P, None, 4, 256, 100, 64, ml.MLORA_BF16), ml.ExpertRoute(), P, None]
+
+
+@pytest.mark.parametrize("route", NOT_W4, ids=lambda r: type(r).__name__)
+def test_4_bit_products_take_4_bit_routes(route):
+    with pytest.raises(TypeError, match="route must be a W4Route"):
+        ml.mlora_w4_gather_gemv(route, None, None)
+
+
+@pytest.mark.parametrize("route", NOT_FP8, ids=lambda r: type(r).__name__)
+def test_8_bit_calls_take_8_bit_routes(route):
+    with pytest.raises(TypeError, match="route must be a Fp8Route"):
+        ml.mlora_fp8_gemm(route, None, None, None)
+    right = ml.Fp8Route(P, P, 4, 256, 100)
+    for i, name in enumerate(("gate", "up", "down")):
+        routes = [right] * 3
+        routes[i] = route
+        with pytest.raises(TypeError, match=name + " must be a Fp8Route"):
+            ml.mlora_moe_layer(*routes, None, None, None, 2, None)
+

@@ -716,7 +716,8 @@ int32_t mlora_block_norm(const mlora_norm_block* block, void* r, int64_t r_ld, v
                          int64_t x_ld, void* stream);
 
 /* Bytes of workspace for d_x_weight, d_y_weight and a gate per channel; 0 for
- * arguments that are refused and for no tokens. */
+ * arguments that are refused and for no tokens. More tokens of one dim never need
+ * less: a workspace of the largest batch's size does for every smaller one. */
 uint64_t mlora_block_norm_backward_workspace_bytes(int64_t n_tokens, int32_t dim);
 
 /* Gradients of mlora_block_norm for d_r and d_x (dtype; NULL: zeros, not both),

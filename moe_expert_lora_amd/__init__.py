@@ -1058,7 +1058,7 @@ def mlora_block_norm(residual, r=None, x=None, y=None, x_weight=None, y_weight=N
 
 
 def mlora_block_norm_backward_workspace_bytes(n_tokens: int, dim: int) -> int:
-    """Workspace bytes of mlora_block_norm_backward."""
+    """Workspace bytes of mlora_block_norm_backward; those of more tokens do for fewer."""
     return int(load().mlora_block_norm_backward_workspace_bytes(int(n_tokens), _i32(dim, "dim")))
 
 

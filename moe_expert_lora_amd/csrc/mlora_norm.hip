@@ -455,10 +455,18 @@ int64_t grid_of(int64_t n_tokens, Shape h, int64_t most) {
 // Of the gradients: two waves a SIMD, since each workgroup writes sums of its own.
 // One, two, four and six a SIMD measured 45, 32, 39 and 40 us (4096 rows of 2048), 46, 37,
 // 45 and 45 (8000 of 300), 71, 71, 89 and 103 (2000 of 8192) when this was chosen.
-int64_t backward_grid(int64_t n_tokens, int dim) {
-  const Shape h = shape_of(dim, true);
+int64_t backward_most(int dim) {
   const int64_t waves = 2 * 4 * 256;
-  return grid_of(n_tokens, h, std::max<int64_t>(256, waves * 64 / threads_of(h.tpr)));
+  return std::max<int64_t>(256, waves * 64 / threads_of(shape_of(dim, true).tpr));
+}
+int64_t backward_grid(int64_t n_tokens, int dim) {
+  return grid_of(n_tokens, shape_of(dim, true), backward_most(dim));
+}
+// What the workspace holds sums of: no fewer for more tokens, unlike the grid, whose
+// even turns take fewer workgroups just past a multiple of the most.
+int64_t backward_space(int64_t n_tokens, int dim) {
+  const int64_t per = rows_of(shape_of(dim, true).tpr);
+  return std::min((n_tokens + per - 1) / per, backward_most(dim));
 }
 
 template <typename Row, int TPR, int VPT>
@@ -557,7 +565,7 @@ extern "C" int32_t mlora_block_norm(const mlora_norm_block* block, void* r, int6
 
 extern "C" uint64_t mlora_block_norm_backward_workspace_bytes(int64_t n_tokens, int32_t dim) {
   if (n_tokens < 1 || n_tokens > kMaxRows || dim < 1 || dim > kMaxDim) return 0;
-  const uint64_t groups = backward_grid(n_tokens, dim);
+  const uint64_t groups = backward_space(n_tokens, dim);
   return (kSums * groups * dim * 4 + 255) / 256 * 256;
 }
 

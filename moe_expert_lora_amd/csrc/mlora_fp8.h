@@ -161,6 +161,15 @@ struct Eights {
   }
 };
 
+// v / (1 + e^-v). The exponential is of -|v|, so that it cannot overflow and the
+// denominator lies in [1, 2]: its reciprocal is never subnormal, and one step of Newton's
+// rounds it as a division would.
+__device__ __forceinline__ float silu(float v) {
+  const float e = expf(-fabsf(v)), d = 1.f + e;
+  const float r = __builtin_amdgcn_rcpf(d);
+  return (v < 0.f ? v * e : v) * fmaf(fmaf(-d, r, 1.f), r, r);
+}
+
 // MLORA_OK, or why the route is refused.
 int32_t check_fp8_route(const char* who, const char* name, const mlora_fp8_route* r);
 

@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(Fp8PackArgs a) {
 // have 8 bits each, so a quotient that is not half way between two codes stays
 // off that border by more than fp32's rounding. An fp32 x is divided in fp64,
 // and what the rounding to fp32 cut off is kept in its last bit, so that the
-// codes are those of the exact quotient too. silu(x) up is rounded to fp32 first.
+// codes are those of the exact quotient too. silu(x) up is an fp32 value of a few
+// roundings, and its quotient is rounded to fp32 before it is rounded to a code.
 // A group with an infinity or NaN gets a NaN as scale and codes of 0.
 
 struct QuantArgs {
@@ -145,8 +146,7 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(QuantArgs a) {
     up.finish(k, a.K);
     up.widen(0, u);
 #pragma unroll
-    // the reciprocal is exact to one unit, as the quotient's last bits are not kept
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * __builtin_amdgcn_rcpf(1.f + expf(-v[i])) * u[i];
+    for (int i = 0; i < 8; ++i) v[i] = silu(v[i]) * u[i];
   }
   uint32_t m = 0;
 #pragma unroll

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
           up += p[(w * 2 + 1) * 256 + src];
         }
         if (j != kNone) {
-          float v = gate / (1.f + expf(-gate)) * up * wts[slot];
+          float v = silu(gate) * up * wts[slot];
           uint16_t* dst =
               a.act + (int64_t)slot * PA * (a.HB * 128) + fp8_column(nt0 + n, c >> 2) + (c & 3);
 #pragma unroll

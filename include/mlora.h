@@ -584,7 +584,8 @@ int32_t mlora_w4_gather_gemv(const mlora_w4_route* route, const void* x, int64_t
  * point atomics). 8-bit values are OCP E4M3 codes (largest value 448, 0x7f and
  * 0xff NaN, no infinity). Weights have one fp32 scale for each block of 128 x 128,
  * rows one for each group of 128 values. Blocks and groups start at 0; the last
- * ones may be short. Any width from 1 to 2^20, 1024 experts.
+ * ones may be short. Any width from 1 to 2^20, 1024 experts, fewer than 2^30 blocks
+ * in all.
  */
 
 /* Device pointers of 8-bit expert weights as mlora_fp8_pack lays them out (the

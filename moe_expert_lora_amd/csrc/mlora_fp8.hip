@@ -646,6 +646,8 @@ int32_t launch_gemm(const char* who, const GemmArgs& a, hipStream_t s) {
   return launch_tile<Row, FAST, 1, 4, 2, 2, 2>(who, a, s);
 }
 
+int64_t blocks_of(int32_t v) { return ((int64_t)v + 127) / 128; }
+
 // Sizes of a route, or why they are refused.
 int32_t check_sizes(const char* who, int32_t n_experts, int32_t k_in, int32_t n_out) {
   if (n_experts < 1 || n_experts > kFp8MaxExperts)
@@ -654,10 +656,11 @@ int32_t check_sizes(const char* who, int32_t n_experts, int32_t k_in, int32_t n_
   if (k_in < 1 || k_in > kFp8MaxDim || n_out < 1 || n_out > kFp8MaxDim)
     return fail(MLORA_ERR_INVALID, "%s: k_in=%d, n_out=%d outside [1, %d]", who, k_in, n_out,
                 kFp8MaxDim);
+  if (n_experts * blocks_of(k_in) * blocks_of(n_out) > kMaxRows)
+    return fail(MLORA_ERR_INVALID, "%s: %d experts of %d x %d are too large", who, n_experts, n_out,
+                k_in);
   return MLORA_OK;
 }
-
-int64_t blocks_of(int32_t v) { return ((int64_t)v + 127) / 128; }
 
 }  // namespace
 
@@ -711,7 +714,6 @@ extern "C" int32_t mlora_fp8_pack(const uint8_t* w, const float* scales, int32_t
   a.packed = static_cast<uint8_t*>(packed);
   a.packed_scales = reinterpret_cast<float*>(a.packed + a.cells * (8 * kFp8Tile));
   a.transpose = transpose != 0;
-  if (a.cells > kMaxRows) return fail(MLORA_ERR_INVALID, "%s: weights too large", who);
   (void)hipGetLastError();
   hipLaunchKernelGGL(fp8_pack_kernel, flat_grid(a.cells), dim3(256), 0,
                      reinterpret_cast<hipStream_t>(stream), a);

@@ -51,3 +51,15 @@ def test_8_bit_calls_take_8_bit_routes(route):
         with pytest.raises(TypeError, match=name + " must be a Fp8Route"):
             ml.mlora_moe_layer(*routes, None, None, None, 2, None)
 
+
+def test_weights_too_large(lib):
+    """2^30 blocks and more: refused by the size query as by the call."""
+    wide = 1 << 20
+    assert ml.mlora_fp8_packed_bytes(16, wide, wide) == 0
+    assert ml.mlora_fp8_packed_bytes(15, wide, wide) > 0
+    for n in (16, 1024):
+        r = ml.Fp8Route()
+        assert lib.mlora_fp8_pack(P, P, n, wide, wide, 0, P, (1 << 64) - 1, ctypes.byref(r),
+                                  None) == ml.MLORA_ERR_INVALID
+        _refused(lib, "mlora_fp8_gemm", {**GEMM, "route": ctypes.byref(ml.Fp8Route(P, P, n, wide, wide))},
+                 dict(q_rows=4, q_ld=wide + 128, out_ld=wide))

@@ -642,7 +642,8 @@ int32_t mlora_fp8_quant(const void* x, int64_t x_ld, const void* up, int64_t up_
  * one weight (n_experts == 1) for every row. Rows in no span, or whose s is
  * outside q, are left as they were. Offsets must be non-decreasing (other
  * contents stay in bounds but give unspecified rows). The products are exact and
- * their sums fp32. route->fast_sums == 1 (the caller sets it): for bf16 results
+ * their sums fp32; the two scales' product is an fp32 value, which below 2^-126 is a
+ * multiple of 2^-149. route->fast_sums == 1 (the caller sets it): for bf16 results
  * the 8-bit matrix instruction adds, at twice the rate; of eight neighbouring
  * products it keeps what is above 2^-13 of the largest one's power of two, so that
  * a sum is off by 1.5e-5 of itself over random codes and by 7 * 2^-13 of the

@@ -19,7 +19,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import fp8  # noqa: E402
-from tests.fp8_cases import F32, U, close, product_error, to64  # noqa: E402
+from tests.fp8_cases import F32, U, close, product_error, to64, weights  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -77,6 +77,31 @@ def test_sums_are_fp32(ml, E, N, K, n, dtype):
         assert torch.equal(out[True], out[False])
     else:
         close(to64(out[True]), ref, product_error(ref, mag, K, "bf16"))
+
+
+@pytest.mark.parametrize("e", [-110, -118, -126])
+@pytest.mark.parametrize("E,N,K,n", SIZES[:4])
+def test_rows_of_small_values(ml, E, N, K, n, e):
+    """Rows of 2^e: their scales times the weights' 2^-12 or so fall below fp32's smallest
+    normal value, and enter to half of 2^-149 times the block's products."""
+    rng = np.random.default_rng(n)
+    w, ws = weights(rng, E, N, K)
+    x = torch.from_numpy(rng.normal(0, 1, (n, K)) * 2.0 ** e).to(DEV).float()
+    q = torch.zeros((n, ml.mlora_fp8_row_width(K)), dtype=torch.uint8, device=DEV)
+    s = torch.empty((-(-K // 128), n), device=DEV)
+    ml.mlora_fp8_quant(x, q, s)
+    off = np.linspace(0, n, E + 1).astype(np.int32)
+    out = torch.empty((n, N), device=DEV)
+    ml.mlora_fp8_gemm(ml.make_fp8_route(dev(w), dev(ws)), q, s, out, dev(off))
+    codes, qs = q.cpu().numpy(), s.cpu().numpy()
+    ref, mag = fp8.products(fp8.expand(w, ws), fp8.rows_of(codes, qs, K), off, None, 1,
+                            np.zeros((n, N)))
+    # the magnitudes without scales
+    _, units = fp8.products(fp8.expand(w, np.ones_like(ws)), fp8.rows_of(codes, np.ones_like(qs), K),
+                            off, None, 1, np.zeros((n, N)))
+    tiny = 2.0 ** -150
+    err = mag * (K + -(-K // 128) + 4) * F32 + units * tiny + (-(-K // 128) + 1) * tiny
+    close(to64(out), ref, err + (np.abs(ref) + err) * U["f32"])
 
 
 def test_packing_asks_for_fp32(ml):

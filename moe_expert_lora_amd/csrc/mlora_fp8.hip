@@ -2,6 +2,7 @@
 // block of 128 x 128), for gfx950 (MI355X): the weights' layout, the rows'
 // quantiser, and the product over rows sorted by expert.
 #include "mlora_fp8.h"
+#include "mlora_fp8_plan.h"
 #include <type_traits>
 
 namespace mlora {
@@ -614,35 +615,14 @@ int32_t launch_stream(const char* who, GemmArgs a, hipStream_t s) {
   return launch_status(who);
 }
 
-// The tile goes by the rows that a span has on average and by the tiles that they
-// make: large ones reuse more, but a span's last tile is half empty and the chip
-// wants two workgroups a CU. Measured, us, 16-row waves / tiles of 32, 64, 128 x 128
-// and 256 x 256 (bf16 with fast sums, cold weights; one of 4096 x 4096, then 128 experts of 2048 x 768,
-// each token's experts by chance):
-//   rows of one weight   16: 6.1, 18, 18, 22, 32     64: 13, 18, 19, 23, 33
-//                        512: 78, 22, 23, 26, 53     2048: 290, 117, 63, 40, 57
-//                        8192: 1152, 542, 278, 171, 128
-//   rows of an expert    5: 42, 38, 37, 45, 49       32: 86, 51, 42, 49, 52
-//                        128: 264, 93, 73, 78, 66    256: 507, 157, 113, 109, 107
-//   768 -> 2048, 128 rows an expert: 246, 93, 77, 76, 74
-// fp32 sums take twice the matrix instructions, so small tiles go further (5 experts of
-// 1365 x 1000, 2001 rows, fp32 results: 31, 15.7, 17.9, 18.7, 43) and the largest has
-// nothing left to save (8192 rows of one 4096 x 4096, bf16: 244 of 128 x 128, 261 of 256 x
-// 256 with registers spilled): it is left out.
 template <typename Row, bool FAST>
 int32_t launch_gemm(const char* who, const GemmArgs& a, hipStream_t s) {
-  const int64_t spans = std::min(a.E, a.n_rows), mean = (a.n_rows + spans - 1) / spans;
-  auto tiles = [&](int64_t bm, int64_t bn) {
-    return spans * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn);
-  };
-  if (mean <= 64 && tiles(32, 128) < 128) return launch_stream<Row, FAST>(who, a, s);
+  const Fp8Form form = plan_fp8(a.n_rows, a.E, a.N, FAST);
+  if (form == kFp8Stream) return launch_stream<Row, FAST>(who, a, s);
   if constexpr (FAST)
-    if (mean >= 128 && tiles(256, 256) >= 384)
-      return launch_tile<Row, FAST, 4, 2, 4, 8, 3>(who, a, s);
-  if (mean >= 256 && tiles(128, 128) >= 448)
-    return launch_tile<Row, FAST, 2, 2, 4, 4, 2>(who, a, s);
-  if (mean >= 24 && tiles(64, 128) >= (FAST ? 256 : 400))
-    return launch_tile<Row, FAST, 2, 2, 2, 4, 2>(who, a, s);
+    if (form == kFp8Rows256) return launch_tile<Row, FAST, 4, 2, 4, 8, 3>(who, a, s);
+  if (form == kFp8Rows128) return launch_tile<Row, FAST, 2, 2, 4, 4, 2>(who, a, s);
+  if (form == kFp8Rows64) return launch_tile<Row, FAST, 2, 2, 2, 4, 2>(who, a, s);
   return launch_tile<Row, FAST, 1, 4, 2, 2, 2>(who, a, s);
 }
 

@@ -157,6 +157,8 @@ class W4Route(ctypes.Structure):
         ("dtype", ctypes.c_int32),
     ]
 
+    device = None  # index of the packed weights' device, where a make_ function set it
+
     @functools.cached_property
     def address(self) -> int:
         """Of the struct (it stays where it is while the object lives)."""
@@ -174,6 +176,8 @@ class Fp8Route(ctypes.Structure):
         ("n_out", ctypes.c_int32),
         ("fast_sums", ctypes.c_int32),
     ]
+
+    device = None  # index of the packed weights' device, where a make_ function set it
 
     @functools.cached_property
     def address(self) -> int:
@@ -329,9 +333,12 @@ def _err(code: int) -> MloraError:
 
 
 def _address(route, kind, name: str) -> int:
-    """Address of a route of the class whose memory the call reads."""
+    """Address of a route of the class whose memory the call reads, its weights on the
+    current device, where the call runs."""
     if not isinstance(route, kind):
         raise TypeError(f"{name} must be a {kind.__name__}, not {type(route).__name__}")
+    if route.device is not None and route.device != _device():
+        raise ValueError(f"{name} must be on the current device")
     return route.address
 
 
@@ -934,7 +941,7 @@ def make_w4_route(q, scales, zeros, k_in: int, group: int, stream=None) -> W4Rou
                               ctypes.byref(route), _stream_handle(stream))
     if rc != MLORA_OK:
         raise _err(rc)
-    route._keep = packed
+    route._keep, route.device = packed, packed.device.index
     return route
 
 
@@ -1003,7 +1010,7 @@ def make_fp8_route(w, scales, transpose: bool = False, stream=None,
     if rc != MLORA_OK:
         raise _err(rc)
     route.fast_sums = int(bool(fast_sums))
-    route._keep = packed
+    route._keep, route.device = packed, packed.device.index
     return route
 
 

@@ -63,3 +63,21 @@ def test_weights_too_large(lib):
                                   None) == ml.MLORA_ERR_INVALID
         _refused(lib, "mlora_fp8_gemm", {**GEMM, "route": ctypes.byref(ml.Fp8Route(P, P, n, wide, wide))},
                  dict(q_rows=4, q_ld=wide + 128, out_ld=wide))
+
+
+def test_weights_of_another_device(monkeypatch):
+    """The tensors are on the current device already; the routes have to be as well."""
+    monkeypatch.setattr(ml, "_device", lambda: 0)
+    far4 = ml.W4Route(P, P, None, 4, 256, 100, 64, ml.MLORA_BF16)
+    near, far = ml.Fp8Route(P, P, 4, 256, 100), ml.Fp8Route(P, P, 4, 256, 100)
+    far4.device = far.device = 1
+    near.device = 0
+    with pytest.raises(ValueError, match="route must be on the current device"):
+        ml.mlora_w4_gather_gemv(far4, None, None)
+    with pytest.raises(ValueError, match="route must be on the current device"):
+        ml.mlora_fp8_gemm(far, None, None, None)
+    for i, name in enumerate(("gate", "up", "down")):
+        routes = [near] * 3
+        routes[i] = far
+        with pytest.raises(ValueError, match=name + " must be on the current device"):
+            ml.mlora_moe_layer(*routes, None, None, None, 2, None)

@@ -108,3 +108,10 @@ def test_packing_asks_for_fp32(ml):
     w, s = torch.zeros((1, 8, 8), dtype=torch.uint8, device=DEV), torch.ones((1, 1, 1), device=DEV)
     assert ml.make_fp8_route(w, s).fast_sums == 0
     assert ml.make_fp8_route(w, s, fast_sums=True).fast_sums == 1
+
+
+def test_routes_name_their_device(ml):
+    w, s = torch.zeros((1, 8, 8), dtype=torch.uint8, device=DEV), torch.ones((1, 1, 1), device=DEV)
+    assert ml.make_fp8_route(w, s).device == torch.cuda.current_device()
+    route = ml.make_w4_route(w, torch.ones((1, 8, 1), device=DEV), None, 16, 32)
+    assert route.device == torch.cuda.current_device()

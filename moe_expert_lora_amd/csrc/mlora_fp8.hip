@@ -395,21 +395,22 @@ __global__ void __launch_bounds__(512) fp8_gemm_stream_kernel(GemmArgs a) {
 // piece p ^ (r / 2 % 8)), so that 8 lanes read one row whole and the 16 rows of an
 // operand come from all 64 banks.
 //
-// 8192 rows of 4096 by 4096 x 4096 take 244 to 251 us with fp32 sums (128 x 128 tiles;
-// bf16 products of the library's rate would take 198). With fast sums (256 x 256 tiles)
-// they take 124 to 140 us, by the card's power (2.0 to 2.2 PFLOP/s; a library's product of E4M3 with one scale: 102 us on one of them): the
-// clock falls to 1.85 GHz, and a block takes 3280 cycles of which the matrix
-// instructions fill 2048, the rest being the next block's latency. The third stage of
-// weights, all that 160 KB of LDS have room for, took spans of 256 rows and 1024 columns
-// from 129 to 122 us. Where in a block it is requested, and which waves go first, made no
-// difference; touching the lines of later blocks early cost 10% and more, as a CU's
-// requests are near their limit. Of many spans a tile's start counts as well: its span
-// and its rows' numbers in one round trip each, shared through LDS, took 32768 rows of
-// 128 experts from 129 to 119 us, rows past a span's end that ask for nothing and are
-// not multiplied to 110 (by chance half of the spans have a tile of a few rows).
-// Workgroups that stay and ask for the next tile's first block before they store won
-// where tiles are alike (138 -> 137 us of the first case) and lost more where they are
-// not (2048 x 4096 weights: 196 -> 218), as they cannot take over from each other.
+// 8192 rows of 4096 by 4096 x 4096 take 244 to 251 us with fp32 sums, in tiles of 128 x
+// 128 (198 at the rate of the library's bf16 product). With fast sums, in tiles of 256 x
+// 256, they take 124 to 140, by the card's power (2.0 to 2.2 PFLOP/s; a library's product
+// of E4M3 with one scale: 102 us on one of them): the clock falls to 1.85 GHz, and a block
+// takes 3280 cycles of which the matrix instructions fill 2048, the rest being the next
+// block's latency. The rest of this is of fast sums too. The third stage of weights, all
+// that 160 KB of LDS have room for, took spans of 256 rows and 1024 columns from 129 to
+// 122 us. Where in a block it is requested, and which waves go first, made no difference;
+// touching the lines of later blocks early cost 10% and more, as a CU's requests are near
+// their limit. Of many spans a tile's start counts as well: its span and its rows' numbers
+// in one round trip each, shared through LDS, took 32768 rows of 128 experts from 129 to
+// 119 us, rows past a span's end that ask for nothing and are not multiplied to 110 (by
+// chance half of the spans have a tile of a few rows). Workgroups that stay and ask for
+// the next tile's first block before they store won where tiles are alike (138 -> 137 us
+// of the first case) and lost more where they are not (2048 x 4096 weights: 196 -> 218),
+// as they cannot take over from each other.
 template <int WM, int WN, int MT, int NT, int WS>
 struct Tile {
   static constexpr int W = WM * WN, BM = WM * MT * 16, BN = WN * NT * 16;
@@ -543,8 +544,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_gemm_tile_kernel(GemmArgs
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // a wave without rows leaves its matrix unit to the others (where a block's products
-  // take twice as long, the branch costs more than it saves)
+  // a wave without rows leaves its matrix unit to the others. With fp32 sums the branch
+  // costs as much as it saves (one weight, as above, 249 -> 259 us; 32768 skewed rows of 128
+  // experts 153 -> 149).
   const bool live = !FAST || sp.row + wm * MT * 16 < sp.end;
   request_w(0, 0);
   request_x(0);

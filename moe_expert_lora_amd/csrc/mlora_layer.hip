@@ -12,8 +12,10 @@ namespace {
 // weight rows by 16 tokens; every token of the call is a column of them, and the
 // ones that did not choose the expert are left out of the result. x stays as it
 // is: a bf16 value is one operand, an fp32 value three (24 bits). The activated
-// rows, times p, pass from kernel to kernel as two (three) bf16 parts, 2^-16
-// (2^-24) of the value. A block's sums enter the fp32 sums times its scale.
+// rows, times p, pass from kernel to kernel as two (three) bf16 parts, each rounded
+// to nearest: 2^-18 (2^-24) of the value, against the 2^-9 of the bf16 result. A third
+// part for bf16 costs a twentieth to a ninth of the layer (one token 18.4 -> 19.6 us,
+// sixteen 79 -> 88). A block's sums enter the fp32 sums times its scale.
 //
 // Kernel one: each workgroup chooses every token's experts itself (the logits
 // are a few KB), lists the experts that are chosen, and takes tiles of 16 hidden
@@ -309,6 +311,13 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
 // workgroup that finishes a tile's last split adds their sums up, in their order:
 // splits write their sums past the caches, count themselves with an atomic, and only
 // the last one goes on (nothing waits).
+//
+// What orders the sums before the count is the machine's rule, not the language's. On
+// gfx950 an access of agent scope (sc1) goes past the XCD's L2 to where all eight meet: a
+// store is acknowledged from there, and s_waitcnt vmcnt(0) waits for the acknowledgement,
+// so the count is raised after the sums have arrived; the last split's loads are of agent
+// scope too, and issued after the count's value came back. Agent fences would say this in
+// the language, but they write back and discard the whole L2 of the XCD: tens of us.
 template <typename Row>
 __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, int splits) {
   extern __shared__ int head[];
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
 }
 
 // Splits of the down product's blocks, so that there is a workgroup a CU, as long as
-// its waves have two blocks each. 128 tiles in 1, 2, 4 splits, the layer, us: one token
+// each of their waves has a block. 128 tiles in 1, 2, 4 splits, the layer, us: one token
 // 20.7, 19.4, 20.3; sixteen 104, 82, 83; 448 tiles (dim 7168): 109, 110, 121. Narrow
 // rows have few tiles (9 of 129 columns: 8 splits 18.6, 32 17.0).
 int splits_of(int64_t T, int64_t E, int64_t k, int64_t dim, int64_t hidden) {
@@ -500,9 +509,9 @@ template <typename Row, int XB, int SHARE>
 void launch_gate_up_as(const LayerArgs& a, hipStream_t s) {
   const Lds l = lds_of(a.T * a.k, a.E, a.max_active);
   const int64_t items = (int64_t)a.max_active * a.HB * SHARE;
-  // As many workgroups as are there at once: two a CU (16 of their waves hold their
-  // registers), one where x takes more than 128 registers. More would choose the experts
-  // again. Sixteen tokens, 256, 512, 768, 1024: the layer 85, 82, 93, 95 us; one fp32 token
+  // As many workgroups as are there at once: two a CU (a SIMD holds four of their waves'
+  // registers), one where a wave keeps more than 48 registers of x, with which it holds two
+  // or three. More would choose the experts again. Sixteen tokens, 256, 512, 768, 1024: the layer 85, 82, 93, 95 us; one fp32 token
   // of 1834 -> 1010, 256 and 512: 25, 30.
   constexpr int kXRegs = XB * (sizeof(typename Row::elem) == 2 ? 16 : 48);
   hipLaunchKernelGGL((layer_gate_up_kernel<Row, XB, SHARE>),

@@ -667,13 +667,12 @@ uint64_t mlora_moe_layer_workspace_bytes(int64_t n_tokens, int32_t n_experts, in
  *   out[t] = sum over j of p[t, j] down_e (silu(gate_e x[t]) * (up_e x[t])),
  * e the j-th chosen expert and p its weight. gate and up are routes of
  * [hidden, dim], down of [dim, hidden]. Weights enter exactly, x is not
- * quantised; the activated row, times p, enters the last product to within 2^-16
- * (fp32: 2^-24) of each value; sums are fp32, one rounding, and in an order that
- * goes by the sizes of the call, not by the other tokens. Values of x, and of the
- * activated row times p, up to 2^112 in magnitude (the 128 products of a block with
- * codes of up to 448 are added before its scale), fp32 ones to within 2^-126; a
- * token with others, or with a NaN among its weights, gives its own row no defined
- * finite values, and other rows do not change.
+ * quantised; the activated row, times p, is fp32; sums are fp32, one rounding, and
+ * in an order that goes by the sizes of the call, not by the other tokens. Values of
+ * x, and of the activated row times p, up to 2^112 in magnitude (the 128 products of
+ * a block with codes of up to 448 are added before its scale), fp32 ones to within
+ * 2^-126; a token with others, or with a NaN among its weights, gives its own row no
+ * defined finite values, and other rows do not change.
  *   x, out      [n_tokens, dim] dtype
  *   logits      [n_tokens, n_experts] dtype
  *   indices, weights  [n_tokens, top_k]: the choice, as mlora_router_topk writes

@@ -12,15 +12,13 @@ namespace {
 // weight rows by 16 tokens; every token of the call is a column of them, and the
 // ones that did not choose the expert are left out of the result. x stays as it
 // is: a bf16 value is one operand, an fp32 value three (24 bits). The activated
-// rows, times p, pass from kernel to kernel as two (three) bf16 parts, each rounded
-// to nearest: 2^-18 (2^-24) of the value, against the 2^-9 of the bf16 result. A third
-// part for bf16 costs a twentieth to a ninth of the layer (one token 18.4 -> 19.6 us,
-// sixteen 79 -> 88). A block's sums enter the fp32 sums times its scale.
+// rows, times p, pass from kernel to kernel in fp32 and become three operands there. A
+// block's sums enter the fp32 sums times its scale.
 //
 // Kernel one: each workgroup chooses every token's experts itself (the logits
 // are a few KB), lists the experts that are chosen, and takes tiles of 16 hidden
 // columns of them in turn; its waves share the blocks of k. Kernel two: a
-// workgroup owns 16 out columns and its waves share the experts' blocks, so that
+// workgroup owns 32 out columns and its waves share the experts' blocks, so that
 // the sum over the experts needs no atomics. Which wave takes a block goes by the
 // expert and the block alone: a token's sums have the same order, and its row the
 // same bits, whatever the other tokens choose.
@@ -43,15 +41,13 @@ struct LayerArgs {
   int32_t* head;     // workspace: count, experts [max_active], slots [max_active][16]
   int32_t* count;    // workspace: splits that are done, of each tile of out
   float* sums;       // workspace: [tiles of out][splits][4][64]
-  uint16_t* act;     // workspace: [T * k][parts][hidden, whole blocks]
+  float* act;        // workspace: [T * k][hidden, whole blocks]
   uint32_t act_bytes;
   int32_t T, E, k, renorm, dim, hidden, DB, HB, max_active;
 };
 
 template <typename Row>
 constexpr int parts_of_x() { return sizeof(typename Row::elem) == 2 ? 1 : 3; }
-template <typename Row>
-constexpr int parts_of_act() { return sizeof(typename Row::elem) == 2 ? 2 : 3; }
 
 // f as P bf16 values whose sum it is, the largest first.
 template <int P>
@@ -134,7 +130,7 @@ __device__ __forceinline__ void choose_all(const LayerArgs& a, int* ids, float* 
 template <typename Row, int XB, int SHARE>
 __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a) {
   extern __shared__ int lds[];
-  constexpr int P = parts_of_x<Row>(), PA = parts_of_act<Row>();
+  constexpr int P = parts_of_x<Row>();
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i32(tid >> 6);
   const int n = a.T * a.k;
   const Lds l = lds_of(n, a.E, a.max_active);
@@ -290,25 +286,22 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
           gate += p[(w * 2 + 0) * 256 + src];
           up += p[(w * 2 + 1) * 256 + src];
         }
-        if (j != kNone) {
-          float v = silu(gate) * up * wts[slot];
-          uint16_t* dst =
-              a.act + (int64_t)slot * PA * (a.HB * 128) + fp8_column(nt0 + n, c >> 2) + (c & 3);
-#pragma unroll
-          for (int q = 0; q < PA; ++q) {
-            const uint16_t b = Bf16Row::narrow(v);
-            dst[(int64_t)q * (a.HB * 128)] = b;
-            v -= Bf16Row::widen(b);
-          }
-        }
+        if (j != kNone)
+          a.act[(int64_t)slot * (a.HB * 128) + fp8_column(nt0 + n, c >> 2) + (c & 3)] =
+              silu(gate) * up * wts[slot];
       }
     }
   }
 }
 
-// Every wave of the call's `splits` workgroups a tile takes the blocks (e, b) with
-// (e HB + b) mod (8 splits) of its number, 64 experts of the list at a time. The
-// workgroup that finishes a tile's last split adds their sums up, in their order:
+// Every wave of the call's `splits` workgroups a pair of tiles takes the blocks (e, b)
+// with (e HB + b) mod (8 splits) of its number, 64 experts of the list at a time. A pair,
+// so that a block of the activated rows, which is read from the caches and cut into its
+// three operands by every wave that needs it, serves two tiles of weights: with one the
+// layer took 86 us instead of 73 (sixteen tokens; fp32 rows of eight 66, 59). Rows of two
+// bf16 parts, 18 bits, took 79 with one.
+//
+// The workgroup that finishes a tile's last split adds their sums up, in their order:
 // splits write their sums past the caches, count themselves with an atomic, and only
 // the last one goes on (nothing waits).
 //
@@ -321,10 +314,9 @@ __global__ void __launch_bounds__(64 * kWaves) layer_gate_up_kernel(LayerArgs a)
 template <typename Row>
 __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, int splits) {
   extern __shared__ int head[];
-  __shared__ f32x4 part[kWaves][64];
-  constexpr int PA = parts_of_act<Row>();
+  __shared__ f32x4 part[kWaves][2][64];
   const int lane = threadIdx.x & 63, wave = uniform_i32(threadIdx.x >> 6);
-  const int nt = blockIdx.x / splits, split = blockIdx.x - nt * splits;
+  const int pair = blockIdx.x / splits, split = blockIdx.x - pair * splits;
   const int t = lane & 15, g = lane >> 4;
   const int me = split * kWaves + wave, all = splits * kWaves;
   // the list and the slots, from kernel one
@@ -340,13 +332,13 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
   // there (no block, a token that did not choose the expert) lies behind its buffer's
   // end and arrives as zeros.
   struct Unit {
-    Fp8Frag w;
-    u32x4 x[4][PA];
+    Fp8Frag w[2];
+    u32x4 x[4][2];  // 8 fp32 values of each step
     float scale;
     bool on, live;
   };
   const rsrc_t act = buffer(a.act, a.act_bytes);
-  const uint32_t row_bytes = (uint32_t)a.HB * 256;  // of a part
+  const uint32_t row_bytes = (uint32_t)a.HB * 512;
   int base = 0, mine = 0, first = 0, at = 0, e = 0, b = a.HB;
   uint64_t hits = 0;
   bool more = active > 0;
@@ -378,25 +370,38 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
   auto request = [&](Unit& u) {
     if (more) next();
     u.live = more;
-    const int64_t strip = (int64_t)e * a.DB + nt / 8;
+    const int64_t strip = (int64_t)e * a.DB + pair / 4;
     const rsrc_t w = buffer(a.down + strip * a.HB * (8 * kFp8Tile), more ? a.HB * (8 * kFp8Tile) : 0);
     const int in_strip = more ? b : 0;
-    u.w = load_tile(w, lane, (in_strip * 8 + nt % 8) * kFp8Tile);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      u.w[n] = load_tile(w, lane, (in_strip * 8 + pair % 4 * 2 + n) * kFp8Tile);
     u.scale = a.down_s[strip * a.HB + in_strip];
     const int j = slots[at * kTokens + t];
     u.on = j != kNone;
-    const uint32_t x = u.on && more ? (uint32_t)(t * a.k + j) * PA * row_bytes + g * 64 : 0xffff0000u;
+    const uint32_t x = u.on && more ? (uint32_t)(t * a.k + j) * row_bytes + g * 128 : 0xffff0000u;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int p = 0; p < PA; ++p)
-        u.x[i][p] = buffer_load16(act, x, p * row_bytes + in_strip * 256 + i * 16);
+      for (int h = 0; h < 2; ++h)
+        u.x[i][h] = buffer_load16(act, x, in_strip * 512 + i * 32 + h * 16);
   };
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   auto add = [&](const Unit& u) {
-    const f32x4 s = block_sum<PA>(u.w, u.x);
+    u32x4 x[4][3];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = u.on ? fmaf(s[i], u.scale, acc[i]) : acc[i];
+    for (int i = 0; i < 4; ++i) {
+      float v[8];
+      F32Row::widen16(u.x[i][0], v);
+      F32Row::widen16(u.x[i][1], v + 4);
+      split8<3>(v, x[i]);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const f32x4 s = block_sum<3>(u.w[n], x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = u.on ? fmaf(s[i], u.scale, acc[n][i]) : acc[n][i];
+    }
   };
   if (more) look();
   Unit u0, u1;
@@ -408,16 +413,20 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
     request(u0);
     add(u1);
   }
-  part[wave][lane] = acc;
-  __syncthreads();
-  if (wave > 0) return;
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) acc += part[w][lane];
+  for (int n = 0; n < 2; ++n) part[wave][n][lane] = acc[n];
+  __syncthreads();
+  if (wave > 1) return;
+  // waves 0 and 1 finish a tile each
+  const int nt = 2 * pair + wave;
+  f32x4 sum = part[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) sum += part[w][wave][lane];
   if (splits > 1) {
     float* sums = a.sums + (int64_t)nt * splits * 256;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      __hip_atomic_store(&sums[split * 256 + i * 64 + lane], acc[i], __ATOMIC_RELAXED,
+      __hip_atomic_store(&sums[split * 256 + i * 64 + lane], sum[i], __ATOMIC_RELAXED,
                          __HIP_MEMORY_SCOPE_AGENT);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0: the sums are where every XCD sees them
@@ -426,7 +435,7 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
       done = __hip_atomic_fetch_add(&a.count[nt], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (uniform_i32(done) != splits - 1) return;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    sum = f32x4{0.f, 0.f, 0.f, 0.f};
     constexpr int kTogether = 4;  // splits whose sums are on their way together
     for (int s0 = 0; s0 < splits; s0 += kTogether) {
       f32x4 v[kTogether];
@@ -438,7 +447,7 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
       for (int j = 0; j < kTogether; ++j)
-        if (s0 + j < splits) acc += v[j];
+        if (s0 + j < splits) sum += v[j];
     }
   }
   if (t >= a.T) return;
@@ -447,26 +456,26 @@ __global__ void __launch_bounds__(64 * kWaves) layer_down_kernel(LayerArgs a, in
   typedef typename Row::elem elem;
   if (n + 4 <= a.dim) {
     if constexpr (sizeof(elem) == 2) {
-      *reinterpret_cast<u32x2_any*>(p) = u32x2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])};
+      *reinterpret_cast<u32x2_any*>(p) = u32x2{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
     } else {
-      *reinterpret_cast<u32x4_any*>(p) = __builtin_bit_cast(u32x4, acc);
+      *reinterpret_cast<u32x4_any*>(p) = __builtin_bit_cast(u32x4, sum);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 3; ++i)
-      if (n + i < a.dim) p[i] = Row::narrow(acc[i]);
+      if (n + i < a.dim) p[i] = Row::narrow(sum[i]);
   }
 }
 
 // Splits of the down product's blocks, so that there is a workgroup a CU, as long as
-// each of their waves has a block. 128 tiles in 1, 2, 4 splits, the layer, us: one token
-// 20.7, 19.4, 20.3; sixteen 104, 82, 83; 448 tiles (dim 7168): 109, 110, 121. Narrow
-// rows have few tiles (9 of 129 columns: 8 splits 18.6, 32 17.0).
+// each of their waves has a block. 64 pairs of tiles in 2, 4, 8 splits, the layer, us: two
+// tokens 28.2, 25.6, 28.5; sixteen 92, 74, 78; 224 pairs (dim 7168) in 1, 2, 4: 98, 101,
+// 109. Narrow rows have few pairs (154 columns: 8 splits 30, 32 24.8).
 int splits_of(int64_t T, int64_t E, int64_t k, int64_t dim, int64_t hidden) {
-  const int64_t tiles = fp8_tiles((int32_t)dim);
+  const int64_t pairs = fp8_tiles((int32_t)dim) / 2;
   const int64_t blocks = std::min(E, T * k) * ((hidden + 127) / 128);
   int s = 1;
-  while (s < 32 && tiles * s < 256 && blocks >= 2 * s * kWaves) s *= 2;
+  while (s < 32 && pairs * s < 256 && blocks >= 2 * s * kWaves) s *= 2;
   return s;
 }
 
@@ -481,7 +490,7 @@ LayerSpace space_of(int64_t T, int64_t E, int64_t k, int64_t dim, int64_t hidden
   s.count = up((1 + active + active * (kTokens / 4)) * 4);
   s.sums = s.count + up(tiles * 4);
   s.act = s.sums + tiles * splits_of(T, E, k, dim, hidden) * 1024;
-  s.total = s.act + T * k * 3 * width * 2;
+  s.total = s.act + T * k * width * 4;
   return s;
 }
 
@@ -499,7 +508,7 @@ int32_t check_layer(const char* who, int64_t n_tokens, int32_t n_experts, int32_
     return fail(MLORA_ERR_INVALID, "%s: dim=%d, hidden=%d outside [1, %d]", who, dim, hidden,
                 kFp8MaxDim);
   // the activated rows are read with 32-bit offsets
-  if (n_tokens * top_k * 6 * (((int64_t)hidden + 127) / 128 * 128) >= 0xff000000ll)
+  if (n_tokens * top_k * 4 * (((int64_t)hidden + 127) / 128 * 128) >= 0xff000000ll)
     return fail(MLORA_ERR_INVALID, "%s: hidden=%d is too wide for %lld rows", who, hidden,
                 (long long)(n_tokens * top_k));
   return MLORA_OK;
@@ -537,7 +546,7 @@ int32_t launch_layer(const char* who, const LayerArgs& a, hipStream_t s) {
   launch_gate_up<Row>(a, s);
   if (int32_t rc = launch_status(who)) return rc;
   const int splits = splits_of(a.T, a.E, a.k, a.dim, a.hidden);
-  hipLaunchKernelGGL((layer_down_kernel<Row>), dim3(fp8_tiles(a.dim) * splits), dim3(64 * kWaves),
+  hipLaunchKernelGGL((layer_down_kernel<Row>), dim3(fp8_tiles(a.dim) / 2 * splits), dim3(64 * kWaves),
                      (1 + a.max_active + a.max_active * (kTokens / 4)) * 4, s, a, splits);
   return launch_status(who);
 }
@@ -603,7 +612,7 @@ extern "C" int32_t mlora_moe_layer(const mlora_fp8_route* gate, const mlora_fp8_
   a.head = static_cast<int32_t*>(workspace);
   a.count = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + sp.count);
   a.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.sums);
-  a.act = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + sp.act);
+  a.act = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.act);
   a.act_bytes = (uint32_t)(sp.total - sp.act);
   a.T = (int32_t)n_tokens;
   a.E = E;

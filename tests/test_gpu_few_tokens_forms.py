@@ -96,3 +96,45 @@ def test_smallest_x(ml, dim, e):
                                                  + np.abs(fp8.silu(g @ x[t])) * ue + 2 * ge * ue))
     err = mag * (dim + 72 + 96 + 1) * F32 + lost
     close(to64(c.out), ref, err + (np.abs(ref) + err) * U["f32"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_activated_rows_keep_24_bits(ml, dtype):
+    """Two hidden columns whose activations differ in their 17th bit or so cancel in the
+    last product, so that what is left shows their last bits.
+
+    x has two values, gate's rows are alike and up's differ in one small code, so every
+    value before the last product is a handful of roundings: up one sum and its scale,
+    silu(gate) shared, times up and p; then three parts of each column and the scale.
+    Column by column (4 + 3 + 1) roundings, 6 shared ones: 16 times 2^-24 of the two
+    columns' magnitudes covers them. Rows of 18 bits are off by up to 64."""
+    dim, hidden, T, E = 128, 2, 16, 24
+    rng = np.random.default_rng(3)
+    code = lambda v: fp8.e4m3_round(np.asarray(v, dtype=np.float64))  # noqa: E731
+    gate, up, down = np.zeros((E, 2, dim)), np.zeros((E, 2, dim)), np.zeros((E, dim, 2))
+    gate[:, :, :2] = rng.uniform(100, 400, (E, 1, 2))
+    up[:, :, 0] = rng.uniform(300, 448, (E, 1))
+    up[:, 1, 1] = rng.uniform(0.25, 2, E)
+    down[:, :, 0] = rng.uniform(100, 448, (E, dim))
+    down[:, :, 1] = -down[:, :, 0]
+    made = [(code(w), rng.uniform(0.002, 0.004, (E, 1, 1)).astype(np.float32))
+            for w in (gate, up, down)]
+    for seed in range(8):
+        c = Case(ml, seed, T, E, 1, dim, hidden, dtype)
+        c.routes = [ml.make_fp8_route(dev(w), dev(s)) for w, s in made]
+        c.full = [fp8.expand(w, s) for w, s in made]
+        c.x.zero_()
+        c.x[:, 0] = dev(rng.uniform(1, 2, T)).to(c.x.dtype)
+        c.x[:, 1] = dev(rng.uniform(1, 2, T) * 2.0 ** -8).to(c.x.dtype)
+        c.run(renorm=False)
+        x = to64(c.x)
+        ref, idx, w, _ = fp8.layer(x, to64(c.logits), *c.full, 1, False)
+        mag = np.zeros_like(ref)
+        for t in range(T):
+            g, u, d = (m[idx[t, 0]] for m in c.full)
+            mag[t] = np.abs(d) @ np.abs(w[t, 0] * fp8.silu(g @ x[t]) * (u @ x[t]))
+        # the weights are the kernel's own: a few units of the exponential
+        close(to64(c.w), w, w * 64 * F32)
+        ref, mag = ref * to64(c.w) / w, mag * to64(c.w) / w
+        err = mag * 16 * F32
+        close(to64(c.out), ref, err + (np.abs(ref) + err) * U[dtype])

@@ -161,13 +161,12 @@ struct Eights {
   }
 };
 
-// v / (1 + e^-v). The exponential is of -|v|, so that it cannot overflow and the
-// denominator lies in [1, 2]: its reciprocal is never subnormal, and one step of Newton's
-// rounds it as a division would.
+// v / (1 + e^-v), each step rounded to fp32. Where e^-v would be infinite (e^88.7 is not)
+// the 1 is far below it, and the quotient is v e^v.
 __device__ __forceinline__ float silu(float v) {
-  const float e = expf(-fabsf(v)), d = 1.f + e;
-  const float r = __builtin_amdgcn_rcpf(d);
-  return (v < 0.f ? v * e : v) * fmaf(fmaf(-d, r, 1.f), r, r);
+  const bool far = v < -88.7f;
+  const float e = expf(far ? v : -v);
+  return far ? v * e : v / (1.f + e);
 }
 
 // MLORA_OK, or why the route is refused.

@@ -621,11 +621,10 @@ int32_t mlora_fp8_pack(const uint8_t* w, const float* scales, int32_t n_experts,
 int32_t mlora_fp8_row_width(int32_t k);
 
 /* Quantises rows: x, or silu(x) * up (x / (1 + e^-x) * up, rounded to fp32 after
- * each operation) where up is given. Of each group
- * of 128 values, m = the largest magnitude or 448 * 2^-126, whichever is larger:
- * scale = m / 448, code = 448 x / m to the nearest E4M3 value, ties to even. A
- * group with an infinity or NaN gets a NaN scale and codes of 0 (its product rows
- * are NaN; other rows do not change).
+ * each operation) where up is given. Of each group of 128 values, m = the largest
+ * magnitude or 448 * 2^-126, whichever is larger: scale = m / 448, code = 448 x / m
+ * to the nearest E4M3 value, ties to even. A group with an infinity or NaN gets a
+ * NaN scale and codes of 0 (its product rows are NaN; other rows do not change).
  *   x, up     [n_rows, k] dtype
  *   q         [n_rows, mlora_fp8_row_width(k)] codes, zeros from k to the end of
  *             its block; 16-byte aligned, q_ld (bytes) a multiple of 16
